@@ -54,7 +54,9 @@ typedef enum {
     FA_ERR_TIMEOUT = -6,     /* a device-side wait gave up (device status word) */
     FA_ERR_WORKSPACE = -7,   /* workspace missing or smaller than the problem needs */
     FA_ERR_SEQLENS = -8,     /* packed batch: cu_seqlens inconsistent (device status word) */
-    FA_ERR_ARG = -9          /* an argument is outside its range (dropout probability) */
+    FA_ERR_ARG = -9,         /* an argument is outside its range (dropout probability, cache format) */
+    FA_ERR_PAGE = -10,       /* 8-bit cache: a page table entry is no page (device status word) */
+    FA_ERR_VALUE = -11       /* 8-bit cache: a value written was infinite or NaN (device status word) */
 } fa_status;
 
 /* bf16 Q/K/V/out, fp32 accumulation. d in {64, 128}. */
@@ -217,6 +219,88 @@ int fa_fwd_splitkv_fp16(const void *q, const void *k, const void *v, void *out, 
 int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *out, float *lse, int B, int H,
                            int Nq, int Nk, int d, float scale, int causal, int n_splits, void *stream);
 
+/* ---- 8-bit key/value cache ---------------------------------------------------
+ * A paged cache of K and V in 8 bits with one scale for each page and head:
+ *   k_codes, v_codes : [n_pages][Hkv][page][d] bytes (int8, or e4m3 as in torch.float8_e4m3fn)
+ *   k_scale, v_scale : float [n_pages][Hkv], >= 0 and finite
+ *   page_table       : int32 [nseq][max_pages]
+ * Position t of sequence s is slot t % page of page page_table[s][t / page]; its values are
+ * code * scale. page is 16, 32, 64 or 128, d 64 or 128, format FA_KVQ8_INT8 or FA_KVQ8_E4M3.
+ * All are caller-owned DEVICE pointers (codes 16-byte aligned, the rest 4). e4m3 codes must not
+ * be NaN (0x7f, 0xff); fa_kvq8_append writes none.
+ * The tables and lengths are read on the device. A length that is negative or does not fit (below)
+ * counts as 0 and records FA_ERR_SEQLENS in the device status word; a page table entry outside
+ * [0, n_pages) that a call needs records FA_ERR_PAGE, and its tokens are left out: not written, not
+ * read, not attended to. Entries that no token needs are not looked at.
+ *
+ * fa_kvq8_append quantises new tokens into the cache: tokens [cu_seqlens[s], cu_seqlens[s+1]) of
+ * k, v (element strides between tokens and between heads, multiples of 8; a row's d values are
+ * contiguous) go to positions cache_lens[s], cache_lens[s] + 1, ... of sequence s. cu_seqlens is
+ * int32 [nseq + 1] as for fa_fwd_varlen; cache_lens, int32 [nseq], is the count of tokens held
+ * before the call and is not changed. At most max_new tokens per sequence (host-side bound).
+ * With QMAX = 127 (int8) or 448 (e4m3), a page's scale is the smallest power of two s in
+ * [2^-110, 2^120] with |x| <= QMAX s for all its tokens, 0 while all are 0, and codes are x / s
+ * rounded to nearest even, saturated. A page that held tokens before keeps its scale or, where
+ * the new tokens need a larger one, takes that; then its earlier codes are rounded to it. A page
+ * that starts empty needs no initial scale. Slots past the last token are not touched. Infinite
+ * and NaN values are written as 0 and record FA_ERR_VALUE. A page that takes tokens must belong
+ * to one sequence only: a page shared by two that both append to it in one call (the same page
+ * twice) gets undefined contents.
+ *
+ * fa_kvq8_read gives tokens back: positions first[s] .. first[s] + n - 1 (first NULL: 0), with
+ * n = cu_seqlens[s+1] - cu_seqlens[s] <= max_len, as rows cu_seqlens[s] .. of k, v
+ * [total][Hkv][d], code * scale rounded to the 16-bit type. Other rows are not touched.
+ *
+ * fa_fwd_kvq8 is the decoding forward over the cache: q, out [B][H][Nq][d], lse float [B][H][Nq],
+ * 1 <= Nq <= 16, Hkv dividing H (heads shared as in fa_fwd_gqa). Sequence b attends to its first
+ * kv_lens[b] positions, 0 <= kv_lens[b] <= max_len <= max_pages * page (max_len: host-side bound).
+ * causal != 0 aligns the last query with the last key: query i sees keys j <= i + kv_lens[b] - Nq.
+ * A row that sees no key gets out = 0 and lse = -inf. Codes, scores, sums and accumulators are
+ * not rounded below fp32; the softmax weights are rounded to fp16 before they multiply V (bf16
+ * queries enter the products exactly down to 2^-24 of their row's largest magnitude). The keys are
+ * cut into at most n_splits chunks of equal length, whose summaries go through the workspace
+ * (256-byte aligned, at least fa_kvq8_workspace_bytes(B, H, Nq, d, n_splits) bytes, contents on
+ * entry irrelevant, not shared by overlapping calls; it may be NULL when n_splits is 1). The result
+ * does not depend on timing: two calls on the same inputs give the same bits.
+ * Other errors as for fa_fwd_splitkv; FA_ERR_UNSUPPORTED for another page or d, FA_ERR_ARG for
+ * another format, FA_ERR_SHAPE for strides that are no multiples of 8. */
+enum { FA_KVQ8_INT8 = 0, FA_KVQ8_E4M3 = 1 };
+
+int fa_kvq8_append(const void *k, const void *v, long long k_token_stride, long long k_head_stride,
+                   long long v_token_stride, long long v_head_stride, const int *cu_seqlens, const int *cache_lens,
+                   int nseq, int total, int max_new, void *k_codes, void *v_codes, float *k_scale, float *v_scale,
+                   const int *page_table, int n_pages, int max_pages, int page, int Hkv, int d, int format,
+                   void *stream);
+int fa_kvq8_append_fp16(const void *k, const void *v, long long k_token_stride, long long k_head_stride,
+                        long long v_token_stride, long long v_head_stride, const int *cu_seqlens,
+                        const int *cache_lens, int nseq, int total, int max_new, void *k_codes, void *v_codes,
+                        float *k_scale, float *v_scale, const int *page_table, int n_pages, int max_pages, int page,
+                        int Hkv, int d, int format, void *stream);
+
+int fa_kvq8_read(const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
+                 const int *page_table, int n_pages, int max_pages, int page, const int *cu_seqlens,
+                 const int *first_or_null, int nseq, int total, int max_len, void *k, void *v, int Hkv, int d,
+                 int format, void *stream);
+int fa_kvq8_read_fp16(const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
+                      const int *page_table, int n_pages, int max_pages, int page, const int *cu_seqlens,
+                      const int *first_or_null, int nseq, int total, int max_len, void *k, void *v, int Hkv, int d,
+                      int format, void *stream);
+
+/* A split count that gives the GPU enough independent chunks (>= 1), or a negative status. */
+int fa_kvq8_num_splits(int B, int H, int Hkv, int Nq, int max_len, int d);
+/* Workspace bytes fa_fwd_kvq8 needs, or a negative status. */
+long long fa_kvq8_workspace_bytes(int B, int H, int Nq, int d, int n_splits);
+
+int fa_fwd_kvq8(const void *q, const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
+                const int *page_table, int n_pages, int max_pages, int page, const int *kv_lens, void *out,
+                float *lse, int B, int H, int Hkv, int Nq, int max_len, int d, int format, float scale, int causal,
+                int n_splits, void *workspace, unsigned long long workspace_bytes, void *stream);
+int fa_fwd_kvq8_fp16(const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
+                     const float *v_scale, const int *page_table, int n_pages, int max_pages, int page,
+                     const int *kv_lens, void *out, float *lse, int B, int H, int Hkv, int Nq, int max_len, int d,
+                     int format, float scale, int causal, int n_splits, void *workspace,
+                     unsigned long long workspace_bytes, void *stream);
+
 /* ---- packed variable-length batch ------------------------------------------
  * The same attention for nseq independent sequences packed back to back
  * ("IO-aware exact attention", section "Tile order and on-chip capacity":
@@ -273,7 +357,7 @@ int fa_bwd_fp16(const void *q, const void *k, const void *v, const void *out, co
 const char *fa_status_string(int status);
 
 /* Synchronises `stream`, returns the device status word of the current device
- * (FA_OK, FA_ERR_TIMEOUT or FA_ERR_SEQLENS) and clears it. Returns FA_ERR_LAUNCH if the
+ * (FA_OK, FA_ERR_TIMEOUT, FA_ERR_SEQLENS, FA_ERR_PAGE or FA_ERR_VALUE; the last one recorded) and clears it. Returns FA_ERR_LAUNCH if the
  * synchronisation itself fails. */
 int fa_get_device_status(void *stream);
 

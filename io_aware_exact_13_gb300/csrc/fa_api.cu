@@ -15,6 +15,7 @@
 #include "../../include/fa.h"
 #include "fa_launch.cuh"
 #include "fa_bwd.cuh"
+#include "fa_kvq8.cuh"
 #include "fa_splitkv.cuh"
 
 namespace fa {
@@ -374,6 +375,138 @@ int splitkv_common(bool fp16, const void *q, const void *k, const void *v, void 
     return fa::launch_splitkv(a, fp16);
 }
 
+int check_kvq8_cache(const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
+                     const int *page_table, int n_pages, int max_pages, int page, int Hkv, int d, int format) {
+    if (!k_codes || !v_codes || !k_scale || !v_scale || !page_table) return FA_ERR_NULL;
+    if (!aligned(k_codes, 16) || !aligned(v_codes, 16) || !aligned(k_scale, 4) || !aligned(v_scale, 4) ||
+        !aligned(page_table, 4))
+        return FA_ERR_ALIGN;
+    if (n_pages < 1 || max_pages < 1 || Hkv < 1) return FA_ERR_SHAPE;
+    if (page != 16 && page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (format != FA_KVQ8_INT8 && format != FA_KVQ8_E4M3) return FA_ERR_ARG;
+    if (static_cast<int64_t>(max_pages) * page > (1 << 30)) return FA_ERR_SHAPE;  // positions stay below 2^31
+    return FA_OK;
+}
+
+fa::Kvq8Cache kvq8_cache(const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
+                         const int *page_table, int n_pages, int max_pages, int page, int Hkv, int d, int format) {
+    fa::Kvq8Cache c;
+    c.k_codes = static_cast<uint8_t *>(const_cast<void *>(k_codes));
+    c.v_codes = static_cast<uint8_t *>(const_cast<void *>(v_codes));
+    c.k_scale = const_cast<float *>(k_scale);
+    c.v_scale = const_cast<float *>(v_scale);
+    c.page_table = page_table;
+    c.n_pages = n_pages;
+    c.max_pages = max_pages;
+    c.page = page;
+    c.Hkv = Hkv;
+    c.d = d;
+    c.format = format;
+    return c;
+}
+
+int kvq8_append_common(bool fp16, const void *k, const void *v, long long kt, long long kh, long long vt, long long vh,
+                       const int *cu_seqlens, const int *cache_lens, int nseq, int total, int max_new, void *k_codes,
+                       void *v_codes, float *k_scale, float *v_scale, const int *page_table, int n_pages,
+                       int max_pages, int page, int Hkv, int d, int format, void *stream) {
+    if (!k || !v || !cu_seqlens || !cache_lens) return FA_ERR_NULL;
+    int rc = check_kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    if (rc != FA_OK) return rc;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_seqlens, 4) || !aligned(cache_lens, 4)) return FA_ERR_ALIGN;
+    if (nseq < 1 || total < 1 || max_new < 1) return FA_ERR_SHAPE;
+    if (kt % 8 || kh % 8 || vt % 8 || vh % 8) return FA_ERR_SHAPE;  // 16-byte rows
+    DeviceInfo *di = device_info();
+    if (!di) return FA_ERR_LAUNCH;
+    fa::Kvq8AppendArgs a;
+    a.c = kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    a.k = k;
+    a.v = v;
+    a.k_token = kt;
+    a.k_head = kh;
+    a.v_token = vt;
+    a.v_head = vh;
+    a.cu_seqlens = cu_seqlens;
+    a.cache_lens = cache_lens;
+    a.nseq = nseq;
+    a.total = total;
+    a.max_new = max_new;
+    a.status = di->status;
+    a.stream = static_cast<cudaStream_t>(stream);
+    log_call("8-bit cache append %s format=%d page=%d d=%d nseq=%d total=%d max_new=%d Hkv=%d", fp16 ? "fp16" : "bf16",
+             format, page, d, nseq, total, max_new, Hkv);
+    return fa::launch_kvq8_append(a, fp16);
+}
+
+int kvq8_read_common(bool fp16, const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
+                     const int *page_table, int n_pages, int max_pages, int page, const int *cu_seqlens,
+                     const int *first, int nseq, int total, int max_len, void *k, void *v, int Hkv, int d, int format,
+                     void *stream) {
+    if (!k || !v || !cu_seqlens) return FA_ERR_NULL;
+    int rc = check_kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    if (rc != FA_OK) return rc;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_seqlens, 4) || (first && !aligned(first, 4)))
+        return FA_ERR_ALIGN;
+    if (nseq < 1 || total < 1 || max_len < 1 || max_len > (1 << 30)) return FA_ERR_SHAPE;
+    DeviceInfo *di = device_info();
+    if (!di) return FA_ERR_LAUNCH;
+    fa::Kvq8ReadArgs a;
+    a.c = kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    a.k = k;
+    a.v = v;
+    a.cu_seqlens = cu_seqlens;
+    a.first = first;
+    a.nseq = nseq;
+    a.total = total;
+    a.max_len = max_len;
+    a.status = di->status;
+    a.stream = static_cast<cudaStream_t>(stream);
+    log_call("8-bit cache read %s format=%d page=%d d=%d nseq=%d total=%d max_len=%d Hkv=%d", fp16 ? "fp16" : "bf16",
+             format, page, d, nseq, total, max_len, Hkv);
+    return fa::launch_kvq8_read(a, fp16);
+}
+
+int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
+                     const float *v_scale, const int *page_table, int n_pages, int max_pages, int page,
+                     const int *kv_lens, void *out, float *lse, int B, int H, int Hkv, int Nq, int max_len, int d,
+                     int format, float scale, int causal, int n_splits, void *workspace,
+                     unsigned long long workspace_bytes, void *stream) {
+    if (!q || !kv_lens || !out || !lse) return FA_ERR_NULL;
+    int rc = check_kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    if (rc != FA_OK) return rc;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4)) return FA_ERR_ALIGN;
+    if (B < 1 || H < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq) return FA_ERR_SHAPE;
+    if (max_len < 1 || max_len > static_cast<int64_t>(max_pages) * page) return FA_ERR_SHAPE;
+    if (n_splits < 1 || n_splits > max_len) return FA_ERR_SHAPE;
+    const int64_t rows = static_cast<int64_t>(B) * H * Nq;
+    if (rows > INT32_MAX) return FA_ERR_SHAPE;
+    const size_t need = n_splits > 1 ? fa::splitkv_workspace_bytes(rows, d, n_splits) : 0;
+    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+    DeviceInfo *di = device_info();
+    if (!di) return FA_ERR_LAUNCH;
+    fa::Kvq8AttnArgs a;
+    a.c = kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.kv_lens = kv_lens;
+    a.B = B;
+    a.H = H;
+    a.Nq = Nq;
+    a.max_len = max_len;
+    a.scale = scale;
+    a.causal = causal ? 1 : 0;
+    a.n_splits = n_splits;
+    const size_t o_bytes = ((static_cast<size_t>(n_splits) * rows * d * sizeof(float) + 255) / 256) * 256;
+    a.o_part = need ? static_cast<float *>(workspace) : nullptr;
+    a.lse_part = need ? reinterpret_cast<float *>(static_cast<char *>(workspace) + o_bytes) : nullptr;
+    a.status = di->status;
+    a.stream = static_cast<cudaStream_t>(stream);
+    log_call("8-bit cache attention %s format=%d page=%d d=%d causal=%d B=%d H=%d Hkv=%d Nq=%d max_len=%d splits=%d",
+             fp16 ? "fp16" : "bf16", format, page, d, a.causal, B, H, Hkv, Nq, max_len, n_splits);
+    return fa::launch_kvq8_attention(a, fp16);
+}
+
 int varlen_common(bool fp16, const void *q, const void *k, const void *v, void *out, float *lse,
                   const int *cu_seqlens, int nseq, int total, int max_seqlen, int H, int Hkv, int d, float scale,
                   int causal, void *stream) {
@@ -638,6 +771,63 @@ int fa_fwd_gqa_fp16(const void *q, const void *k, const void *v, const float *ma
     return fwd_common(Type::FP16, q, k, v, mask_or_null, out, lse, B, H, N, d, scale, causal, stream, Hkv);
 }
 
+#define FA_APPEND_ARGS                                                                                                 \
+    const void *k, const void *v, long long kt, long long kh, long long vt, long long vh, const int *cu_seqlens,       \
+        const int *cache_lens, int nseq, int total, int max_new, void *k_codes, void *v_codes, float *k_scale,         \
+        float *v_scale, const int *page_table, int n_pages, int max_pages, int page, int Hkv, int d, int format,       \
+        void *stream
+int fa_kvq8_append(FA_APPEND_ARGS) {
+    return kvq8_append_common(false, k, v, kt, kh, vt, vh, cu_seqlens, cache_lens, nseq, total, max_new, k_codes,
+                              v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format, stream);
+}
+int fa_kvq8_append_fp16(FA_APPEND_ARGS) {
+    return kvq8_append_common(true, k, v, kt, kh, vt, vh, cu_seqlens, cache_lens, nseq, total, max_new, k_codes,
+                              v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format, stream);
+}
+#undef FA_APPEND_ARGS
+
+#define FA_READ_ARGS                                                                                                   \
+    const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale, const int *page_table,       \
+        int n_pages, int max_pages, int page, const int *cu_seqlens, const int *first, int nseq, int total,            \
+        int max_len, void *k, void *v, int Hkv, int d, int format, void *stream
+int fa_kvq8_read(FA_READ_ARGS) {
+    return kvq8_read_common(false, k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page,
+                            cu_seqlens, first, nseq, total, max_len, k, v, Hkv, d, format, stream);
+}
+int fa_kvq8_read_fp16(FA_READ_ARGS) {
+    return kvq8_read_common(true, k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page,
+                            cu_seqlens, first, nseq, total, max_len, k, v, Hkv, d, format, stream);
+}
+#undef FA_READ_ARGS
+
+int fa_kvq8_num_splits(int B, int H, int Hkv, int Nq, int max_len, int d) {
+    if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || max_len < 1) return FA_ERR_SHAPE;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    DeviceInfo *di = device_info();
+    return fa::kvq8_num_splits(B, Hkv, H / Hkv * Nq, max_len, d, di ? di->num_sms : 148);
+}
+
+long long fa_kvq8_workspace_bytes(int B, int H, int Nq, int d, int n_splits) {
+    return fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits);
+}
+
+#define FA_KVQ8_ARGS                                                                                                   \
+    const void *q, const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,               \
+        const int *page_table, int n_pages, int max_pages, int page, const int *kv_lens, void *out, float *lse, int B, \
+        int H, int Hkv, int Nq, int max_len, int d, int format, float scale, int causal, int n_splits,                 \
+        void *workspace, unsigned long long workspace_bytes, void *stream
+int fa_fwd_kvq8(FA_KVQ8_ARGS) {
+    return kvq8_attn_common(false, q, k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page,
+                            kv_lens, out, lse, B, H, Hkv, Nq, max_len, d, format, scale, causal, n_splits, workspace,
+                            workspace_bytes, stream);
+}
+int fa_fwd_kvq8_fp16(FA_KVQ8_ARGS) {
+    return kvq8_attn_common(true, q, k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page,
+                            kv_lens, out, lse, B, H, Hkv, Nq, max_len, d, format, scale, causal, n_splits, workspace,
+                            workspace_bytes, stream);
+}
+#undef FA_KVQ8_ARGS
+
 int fa_fwd_varlen(const void *q, const void *k, const void *v, void *out, float *lse, const int *cu_seqlens,
                   int nseq, int total, int max_seqlen, int H, int Hkv, int d, float scale, int causal, void *stream) {
     return varlen_common(false, q, k, v, out, lse, cu_seqlens, nseq, total, max_seqlen, H, Hkv, d, scale, causal,
@@ -693,7 +883,10 @@ const char *fa_status_string(int status) {
         case FA_ERR_TIMEOUT: return "a device-side pipeline wait timed out";
         case FA_ERR_WORKSPACE: return "workspace missing or smaller than the problem needs";
         case FA_ERR_SEQLENS: return "cu_seqlens inconsistent with total or max_seqlen (device status)";
-        case FA_ERR_ARG: return "an argument is outside its range (dropout: the drop probability keeps nothing)";
+        case FA_ERR_ARG:
+            return "an argument is outside its range (dropout: the drop probability keeps nothing; cache: no such format)";
+        case FA_ERR_PAGE: return "a page table entry is outside the cache (device status)";
+        case FA_ERR_VALUE: return "an infinite or NaN value was written to the 8-bit cache as 0 (device status)";
         default: return "unknown status";
     }
 }

@@ -1,0 +1,97 @@
+// fa_kvq8.cuh -- the 8-bit key/value cache: its layout, host-side arguments, and the
+// device helpers its three kernels (append, read, attention) share.
+//
+// A cache is n_pages pages of `page` tokens (16, 32, 64 or 128). Codes are
+// [n_pages][Hkv][page][d] bytes, scales [n_pages][Hkv] floats, K and V apart; a value is
+// code * scale. Sequence s keeps position t in page page_table[s][t / page], slot t % page.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fa {
+
+constexpr int kKvq8Int8 = 0, kKvq8E4m3 = 1;  // FA_KVQ8_INT8, FA_KVQ8_E4M3
+constexpr int kStatusSeqlensQ8 = -8;         // FA_ERR_SEQLENS
+constexpr int kStatusPage = -10;             // FA_ERR_PAGE
+constexpr int kStatusValue = -11;            // FA_ERR_VALUE
+constexpr int kKvq8MaxNq = 16;
+
+struct Kvq8Cache {
+    uint8_t *k_codes, *v_codes;
+    float *k_scale, *v_scale;
+    const int *page_table;  // [nseq][max_pages]
+    int n_pages, max_pages, page, Hkv, d, format;
+};
+
+struct Kvq8AppendArgs {
+    Kvq8Cache c;
+    const void *k, *v;  // [total][Hkv][d] with element strides between tokens and heads
+    long long k_token, k_head, v_token, v_head;
+    const int *cu_seqlens, *cache_lens;
+    int nseq, total, max_new;
+    int *status;
+    cudaStream_t stream;
+};
+
+struct Kvq8ReadArgs {
+    Kvq8Cache c;
+    void *k, *v;  // [total][Hkv][d]
+    const int *cu_seqlens, *first;  // first: position of each sequence's first token read, or NULL (0)
+    int nseq, total, max_len;
+    int *status;
+    cudaStream_t stream;
+};
+
+struct Kvq8AttnArgs {
+    Kvq8Cache c;
+    const void *q;
+    void *out;
+    float *lse;
+    const int *kv_lens;
+    int B, H, Nq, max_len;
+    float scale;
+    int causal, n_splits;
+    float *o_part, *lse_part;  // workspace: [n_splits][B*H*Nq][d], [n_splits][B*H*Nq]
+    int *status;
+    cudaStream_t stream;
+};
+
+int launch_kvq8_append(const Kvq8AppendArgs &a, bool fp16);
+int launch_kvq8_read(const Kvq8ReadArgs &a, bool fp16);
+int launch_kvq8_attention(const Kvq8AttnArgs &a, bool fp16);
+// Keys per split for n_splits splits of at most max_len keys (a multiple of the 16-key tiles).
+int kvq8_split_len(int max_len, int n_splits);
+// A split count for the problem; rows = (H / Hkv) * Nq query rows share a K/V head.
+int kvq8_num_splits(int B, int Hkv, int rows, int max_len, int d, int num_sms);
+
+// Four int8 codes -> two pairs of fp16, exact: code + 128 under the exponent of 1024 is the
+// fp16 number 1152 + code.
+__device__ __forceinline__ void int8x4_to_half2(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    const uint32_t u = w ^ 0x80808080u;
+    const uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2 *>(&a), bias);
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2 *>(&b), bias);
+    lo = *reinterpret_cast<const uint32_t *>(&x);
+    hi = *reinterpret_cast<const uint32_t *>(&y);
+}
+// Four e4m3 codes -> two pairs of fp16 (every e4m3 number is an fp16 number).
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+}
+template <int FMT>
+__device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t &lo, uint32_t &hi) {
+    if constexpr (FMT == kKvq8Int8) int8x4_to_half2(w, lo, hi);
+    else e4m3x4_to_half2(w, lo, hi);
+}
+
+// 8 bytes of the cache per asynchronous copy (zero-filled when src_bytes is 0).
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
+}  // namespace fa

@@ -10,16 +10,20 @@ Names follow the C ABI: ``fa_fwd`` (bf16), ``fa_fwd_fp16``, ``fa_fwd_fp32``,
 ``fa_fwd_dropout`` / ``fa_fwd_dropout_fp16`` (dropout on the probabilities),
 ``fa_fwd_splitkv`` / ``fa_fwd_splitkv_fp16`` (decoding), ``fa_bwd`` /
 ``fa_bwd_fp16`` (backward by recomputation), ``fa_fwd_varlen`` /
-``fa_fwd_varlen_fp16`` (packed variable-length batches), their sizing helpers,
+``fa_fwd_varlen_fp16`` (packed variable-length batches), ``fa_fwd_kvq8`` /
+``fa_fwd_kvq8_fp16`` (decoding over an 8-bit cache), their sizing helpers,
 ``fa_status_string``, ``fa_get_device_status``, ``fa_num_sms``. ``attention``,
-``attention_decode``, ``attention_varlen`` and ``attention_backward`` are convenience wrappers that allocate outputs (and
-the split-KV workspace) with torch and pick the entry point from the dtype.
+``attention_decode``, ``attention_varlen``, ``attention_kvq8`` and ``attention_backward`` are convenience wrappers
+that allocate outputs (and the workspaces) with torch and pick the entry point from the dtype; ``kvq8_append`` and
+``kvq8_read`` write and read the 8-bit cache (``KVCacheQ8``, allocated by ``kv_cache_q8``).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
+from typing import NamedTuple
 
 import torch
 
@@ -40,6 +44,8 @@ FA_ERR_TIMEOUT = -6
 FA_ERR_WORKSPACE = -7
 FA_ERR_SEQLENS = -8
 FA_ERR_ARG = -9
+FA_ERR_PAGE = -10
+FA_ERR_VALUE = -11
 
 # Every symbol the header declares, with its ctypes signature.
 _vp = ctypes.c_void_p
@@ -76,6 +82,8 @@ SIGNATURES = {
                                [ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp]),
     "fa_fwd_varlen": (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _vp]),
     "fa_fwd_varlen_fp16": (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _vp]),
+    "fa_kvq8_num_splits": (ctypes.c_int, [ctypes.c_int] * 6),
+    "fa_kvq8_workspace_bytes": (ctypes.c_longlong, [ctypes.c_int] * 5),
     "fa_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_ulonglong, _vp]),
     "fa_fwd_host": (ctypes.c_int, [_vp] * 10 + [ctypes.c_int] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp]),
     "fa_fwd_host_fp16": (ctypes.c_int, [_vp] * 10 + [ctypes.c_int] * 4 +
@@ -86,6 +94,14 @@ SIGNATURES = {
     "fa_bwd_fp16": (ctypes.c_int, [_vp] * 9 + [ctypes.c_int] * 4 + [ctypes.c_float, ctypes.c_int, _vp,
                                                                       ctypes.c_ulonglong, _vp]),
 }
+_KVQ8_APPEND = [_vp] * 2 + [ctypes.c_longlong] * 4 + [_vp] * 2 + [ctypes.c_int] * 3 + [_vp] * 5 + [ctypes.c_int] * 6 + [_vp]
+_KVQ8_READ = [_vp] * 5 + [ctypes.c_int] * 3 + [_vp] * 2 + [ctypes.c_int] * 3 + [_vp] * 2 + [ctypes.c_int] * 3 + [_vp]
+_KVQ8_FWD = ([_vp] * 6 + [ctypes.c_int] * 3 + [_vp] * 3 + [ctypes.c_int] * 7 + [ctypes.c_float] + [ctypes.c_int] * 2 +
+             [_vp, ctypes.c_ulonglong, _vp])
+for _suffix in ("", "_fp16"):
+    SIGNATURES["fa_kvq8_append" + _suffix] = (ctypes.c_int, _KVQ8_APPEND)
+    SIGNATURES["fa_kvq8_read" + _suffix] = (ctypes.c_int, _KVQ8_READ)
+    SIGNATURES["fa_fwd_kvq8" + _suffix] = (ctypes.c_int, _KVQ8_FWD)
 for _name, (_res, _args) in SIGNATURES.items():
     _f = getattr(lib, _name)
     _f.restype = _res
@@ -423,6 +439,197 @@ def attention_decode(q, k, v, scale=None, causal=False, n_splits=None, stream=No
     lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     fn = {torch.bfloat16: fa_fwd_splitkv, torch.float16: fa_fwd_splitkv_fp16}[q.dtype]
     fn(q, k, v, out, lse, scale, causal, n_splits, ws, stream)
+    return out, lse
+
+
+# ---------------------------------------------------------------- 8-bit key/value cache
+class KVCacheQ8(NamedTuple):
+    """A paged cache of K and V in 8 bits: codes [n_pages, Hkv, page, d] (torch.int8 or torch.float8_e4m3fn) and
+    scales [n_pages, Hkv] (float32); a value is code * scale. Which pages a sequence owns is the caller's page table."""
+    k_codes: torch.Tensor
+    v_codes: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+
+_KVQ8_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
+_FP16_SUFFIX = {torch.bfloat16: "", torch.float16: "_fp16"}
+
+
+def kv_cache_q8(n_pages, Hkv, page, d, dtype=torch.int8, device="cuda") -> KVCacheQ8:
+    """An empty cache of ``n_pages`` pages of ``page`` tokens (16, 32, 64 or 128), codes in ``dtype``."""
+    if dtype not in _KVQ8_FORMATS:
+        raise ValueError("codes are torch.int8 or torch.float8_e4m3fn")
+    codes = [torch.zeros((n_pages, Hkv, page, d), dtype=torch.uint8, device=device).view(dtype) for _ in range(2)]
+    scales = [torch.zeros((n_pages, Hkv), dtype=torch.float32, device=device) for _ in range(2)]
+    return KVCacheQ8(*codes, *scales)
+
+
+def _on(device, stream):
+    """Context in which ``device`` is current and torch allocates for ``stream`` (None: the device's current one)."""
+    if stream is not None:
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    if device.index != torch.cuda.current_device():
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _check_ints(name, t, shape, device):
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+
+
+def _check_kvq8(cache, page_table):
+    """The cache's (device, page, Hkv, d) after checking its tensors against each other and the page table's form."""
+    kc = cache.k_codes
+    if kc.dtype not in _KVQ8_FORMATS or kc.dim() != 4:
+        raise ValueError("cache codes must be int8 or float8_e4m3fn tensors [n_pages, Hkv, page, d]")
+    if not kc.is_cuda:
+        raise ValueError("the cache must be on a CUDA device")
+    n_pages, Hkv, page, d = kc.shape
+    for name, t, dtype, shape in (("k_codes", kc, kc.dtype, kc.shape), ("v_codes", cache.v_codes, kc.dtype, kc.shape),
+                                  ("k_scale", cache.k_scale, torch.float32, (n_pages, Hkv)),
+                                  ("v_scale", cache.v_scale, torch.float32, (n_pages, Hkv))):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != kc.device:
+            raise ValueError(f"cache {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {kc.device}")
+    if page_table.dim() != 2:
+        raise ValueError("page_table must be int32 [nseq, max_pages]")
+    _check_ints("page_table", page_table, page_table.shape, kc.device)
+    return kc.device, page, Hkv, d
+
+
+def _kvq8_ptrs(cache):
+    return [_ptr(t) for t in cache]
+
+
+def kvq8_append(cache, k, v, page_table, cu_seqlens, cache_lens, max_new, stream=None):
+    """Quantise new tokens' ``k``, ``v`` [total, Hkv, d] (bf16 or fp16; any strides of tokens and heads that are
+    multiples of 8, rows contiguous) into ``cache``: tokens [cu_seqlens[s], cu_seqlens[s+1]) go to positions
+    cache_lens[s], ... of sequence s, at most ``max_new`` per sequence. ``cache_lens`` is left as it is."""
+    device, page, Hkv, d = _check_kvq8(cache, page_table)
+    nseq, max_pages = page_table.shape
+    total = k.shape[0]
+    strides = []
+    for name, t in (("k", k), ("v", v)):
+        if t.dtype != k.dtype or t.dtype not in _FP16_SUFFIX or t.device != device or t.shape != (total, Hkv, d):
+            raise ValueError(f"{name} must be a bf16 or fp16 tensor [total, {Hkv}, {d}] on {device}, k and v alike")
+        if t.stride(2) != 1:
+            raise ValueError(f"{name}: the head dimension must be contiguous")
+        strides += [t.stride(0) if total > 1 else 0, t.stride(1) if Hkv > 1 else 0]
+    _check_ints("cu_seqlens", cu_seqlens, (nseq + 1,), device)
+    _check_ints("cache_lens", cache_lens, (nseq,), device)
+    name = "fa_kvq8_append" + _FP16_SUFFIX[k.dtype]
+    with _on(device, stream):
+        rc = getattr(lib, name)(_ptr(k), _ptr(v), *strides, _ptr(cu_seqlens), _ptr(cache_lens), nseq, total,
+                                int(max_new), *_kvq8_ptrs(cache), _ptr(page_table), cache.k_codes.shape[0], max_pages,
+                                page, Hkv, d, _KVQ8_FORMATS[cache.k_codes.dtype],
+                                ctypes.c_void_p(_stream_handle(stream)))
+    if rc != FA_OK:
+        raise FAError(rc, name)
+
+
+def kvq8_read(cache, page_table, cu_seqlens, total, max_len, first=None, dtype=torch.bfloat16, k=None, v=None,
+              stream=None):
+    """Cached tokens back as packed K, V [total, Hkv, d]: rows [cu_seqlens[s], cu_seqlens[s+1]) (at most ``max_len``)
+    are positions first[s], first[s] + 1, ... of sequence s (``first`` None: from 0). Rows that no sequence covers are
+    not written; ``k`` and ``v`` are allocated unless given."""
+    device, page, Hkv, d = _check_kvq8(cache, page_table)
+    nseq, max_pages = page_table.shape
+    _check_ints("cu_seqlens", cu_seqlens, (nseq + 1,), device)
+    if first is not None:
+        _check_ints("first", first, (nseq,), device)
+    if dtype not in _FP16_SUFFIX:
+        raise ValueError(f"unsupported dtype {dtype}")
+    name = "fa_kvq8_read" + _FP16_SUFFIX[dtype]
+    with _on(device, stream):
+        k = torch.empty((total, Hkv, d), dtype=dtype, device=device) if k is None else k
+        v = torch.empty((total, Hkv, d), dtype=dtype, device=device) if v is None else v
+        for n, t in (("k", k), ("v", v)):
+            if t.dtype != dtype or t.shape != (total, Hkv, d) or not t.is_contiguous() or t.device != device:
+                raise ValueError(f"{n} must be a contiguous {dtype} tensor [{total}, {Hkv}, {d}] on {device}")
+        rc = getattr(lib, name)(*_kvq8_ptrs(cache), _ptr(page_table), cache.k_codes.shape[0], max_pages, page,
+                                _ptr(cu_seqlens), _ptr(first), nseq, int(total), int(max_len), _ptr(k), _ptr(v), Hkv,
+                                d, _KVQ8_FORMATS[cache.k_codes.dtype], ctypes.c_void_p(_stream_handle(stream)))
+    if rc != FA_OK:
+        raise FAError(rc, name)
+    return k, v
+
+
+def fa_kvq8_num_splits(B, H, Hkv, Nq, max_len, d) -> int:
+    n = int(lib.fa_kvq8_num_splits(int(B), int(H), int(Hkv), int(Nq), int(max_len), int(d)))
+    if n < 0:
+        raise FAError(n, "fa_kvq8_num_splits")
+    return n
+
+
+def fa_kvq8_workspace_bytes(B, H, Nq, d, n_splits) -> int:
+    n = int(lib.fa_kvq8_workspace_bytes(int(B), int(H), int(Nq), int(d), int(n_splits)))
+    if n < 0:
+        raise FAError(n, "fa_kvq8_workspace_bytes")
+    return n
+
+
+def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_splits, workspace,
+              stream):
+    device, page, Hkv, d = _check_kvq8(cache, page_table)
+    for name, t in (("q", q), ("out", out)):
+        if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != 4 or t.shape != q.shape:
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor [B, H, Nq, d] on {device}")
+    B, H, Nq, dq = q.shape
+    if dq != d or H % Hkv or page_table.shape[0] != B:
+        raise ValueError("q: [B, H, Nq, d] with the cache's d, its Hkv dividing H and one page table row per b")
+    if lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous() or lse.shape != (B, H, Nq):
+        raise ValueError(f"lse must be a contiguous float32 [B, H, Nq] tensor on {device}")
+    _check_ints("kv_lens", kv_lens, (B,), device)
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    with _on(device, stream):
+        rc = getattr(lib, fn_name)(_ptr(q), *_kvq8_ptrs(cache), _ptr(page_table), cache.k_codes.shape[0],
+                                   page_table.shape[1], page, _ptr(kv_lens), _ptr(out), _ptr(lse), B, H, Hkv, Nq,
+                                   int(max_len), d, _KVQ8_FORMATS[cache.k_codes.dtype], float(scale),
+                                   int(bool(causal)), int(n_splits), _ptr(workspace), nbytes,
+                                   ctypes.c_void_p(_stream_handle(stream)))
+    if rc != FA_OK:
+        raise FAError(rc, fn_name)
+
+
+def fa_fwd_kvq8(q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_splits, workspace, stream=None):
+    """bf16 forward of 1 to 16 query rows per sequence over an 8-bit cache, into ``out`` and ``lse``."""
+    _raw_kvq8("fa_fwd_kvq8", torch.bfloat16, q, cache, page_table, kv_lens, out, lse, scale, causal, max_len,
+              n_splits, workspace, stream)
+
+
+def fa_fwd_kvq8_fp16(q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_splits, workspace,
+                     stream=None):
+    """fp16 forward over an 8-bit cache (see ``fa_fwd_kvq8``)."""
+    _raw_kvq8("fa_fwd_kvq8_fp16", torch.float16, q, cache, page_table, kv_lens, out, lse, scale, causal, max_len,
+              n_splits, workspace, stream)
+
+
+def attention_kvq8(q, cache, page_table, kv_lens, scale=None, causal=False, max_len=None, n_splits=None, stream=None):
+    """O [B, H, Nq, d] and lse [B, H, Nq] of 1 to 16 query rows per sequence over its first kv_lens[b] cached tokens.
+    ``max_len`` bounds every length (the page table's reach unless given); the workspace is a torch allocation."""
+    B, H, Nq, d = q.shape
+    if q.dtype not in _FP16_SUFFIX:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    if max_len is None:
+        max_len = page_table.shape[1] * cache.k_codes.shape[2]
+    with _on(q.device, stream) if q.is_cuda else contextlib.nullcontext():
+        if n_splits is None:
+            n_splits = fa_kvq8_num_splits(B, H, cache.k_codes.shape[1], Nq, max_len, d)
+        ws = None
+        if n_splits > 1:
+            ws = torch.empty(fa_kvq8_workspace_bytes(B, H, Nq, d, n_splits), dtype=torch.uint8, device=q.device)
+        out = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    _raw_kvq8("fa_fwd_kvq8" + _FP16_SUFFIX[q.dtype], q.dtype, q, cache, page_table, kv_lens, out, lse, scale, causal,
+              max_len, n_splits, ws, stream)
     return out, lse
 
 
