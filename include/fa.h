@@ -257,11 +257,12 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *ou
  * causal != 0 aligns the last query with the last key: query i sees keys j <= i + kv_lens[b] - Nq.
  * A row that sees no key gets out = 0 and lse = -inf. Codes, scores, sums and accumulators are
  * not rounded below fp32; the softmax weights are rounded to fp16 before they multiply V (bf16
- * queries enter the products exactly down to 2^-24 of their row's largest magnitude). The keys are
- * cut into at most n_splits chunks of equal length, whose summaries go through the workspace
- * (256-byte aligned, at least fa_kvq8_workspace_bytes(B, H, Nq, d, n_splits) bytes, contents on
- * entry irrelevant, not shared by overlapping calls; it may be NULL when n_splits is 1). The result
- * does not depend on timing: two calls on the same inputs give the same bits.
+ * queries enter the products exactly down to 2^-24 of their row's largest magnitude). All sequences'
+ * keys are cut, as one line, into n_parts equal stretches, whatever the lengths are; the summaries
+ * of sequences that more than one part shares go through the workspace (256-byte aligned, at least
+ * fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) bytes, contents on entry irrelevant, not shared by
+ * overlapping calls). The result does not depend on timing: two calls on the same inputs, with the
+ * same n_parts, give the same bits.
  * Other errors as for fa_fwd_splitkv; FA_ERR_UNSUPPORTED for another page or d, FA_ERR_ARG for
  * another format, FA_ERR_SHAPE for strides that are no multiples of 8. */
 enum { FA_KVQ8_INT8 = 0, FA_KVQ8_E4M3 = 1 };
@@ -286,19 +287,19 @@ int fa_kvq8_read_fp16(const void *k_codes, const void *v_codes, const float *k_s
                       const int *first_or_null, int nseq, int total, int max_len, void *k, void *v, int Hkv, int d,
                       int format, void *stream);
 
-/* A split count that gives the GPU enough independent chunks (>= 1), or a negative status. */
-int fa_kvq8_num_splits(int B, int H, int Hkv, int Nq, int max_len, int d);
+/* A part count that fills the GPU once, without parts of less than 64 keys (>= 1), or a negative status. */
+int fa_kvq8_num_parts(int B, int H, int Hkv, int Nq, int max_len, int d);
 /* Workspace bytes fa_fwd_kvq8 needs, or a negative status. */
-long long fa_kvq8_workspace_bytes(int B, int H, int Nq, int d, int n_splits);
+long long fa_kvq8_workspace_bytes(int H, int Hkv, int Nq, int d, int n_parts);
 
 int fa_fwd_kvq8(const void *q, const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
                 const int *page_table, int n_pages, int max_pages, int page, const int *kv_lens, void *out,
                 float *lse, int B, int H, int Hkv, int Nq, int max_len, int d, int format, float scale, int causal,
-                int n_splits, void *workspace, unsigned long long workspace_bytes, void *stream);
+                int n_parts, void *workspace, unsigned long long workspace_bytes, void *stream);
 int fa_fwd_kvq8_fp16(const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
                      const float *v_scale, const int *page_table, int n_pages, int max_pages, int page,
                      const int *kv_lens, void *out, float *lse, int B, int H, int Hkv, int Nq, int max_len, int d,
-                     int format, float scale, int causal, int n_splits, void *workspace,
+                     int format, float scale, int causal, int n_parts, void *workspace,
                      unsigned long long workspace_bytes, void *stream);
 
 /* ---- packed variable-length batch ------------------------------------------

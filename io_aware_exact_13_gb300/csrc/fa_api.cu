@@ -469,7 +469,7 @@ int kvq8_read_common(bool fp16, const void *k_codes, const void *v_codes, const 
 int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
                      const float *v_scale, const int *page_table, int n_pages, int max_pages, int page,
                      const int *kv_lens, void *out, float *lse, int B, int H, int Hkv, int Nq, int max_len, int d,
-                     int format, float scale, int causal, int n_splits, void *workspace,
+                     int format, float scale, int causal, int n_parts, void *workspace,
                      unsigned long long workspace_bytes, void *stream) {
     if (!q || !kv_lens || !out || !lse) return FA_ERR_NULL;
     int rc = check_kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
@@ -477,11 +477,12 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4)) return FA_ERR_ALIGN;
     if (B < 1 || H < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq) return FA_ERR_SHAPE;
     if (max_len < 1 || max_len > static_cast<int64_t>(max_pages) * page) return FA_ERR_SHAPE;
-    if (n_splits < 1 || n_splits > max_len) return FA_ERR_SHAPE;
-    const int64_t rows = static_cast<int64_t>(B) * H * Nq;
-    if (rows > INT32_MAX) return FA_ERR_SHAPE;
-    const size_t need = n_splits > 1 ? fa::splitkv_workspace_bytes(rows, d, n_splits) : 0;
-    if (need && (!workspace || !aligned(workspace, 256) || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+    if (n_parts < 1 || n_parts > (1 << 20)) return FA_ERR_SHAPE;
+    if (static_cast<int64_t>(B) * H * Nq > INT32_MAX) return FA_ERR_SHAPE;
+    const int rows = H / Hkv * Nq;
+    if (fa::kvq8_tiles(B, Hkv, rows, max_len) > (1 << 30)) return FA_ERR_SHAPE;
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < fa::kvq8_workspace_bytes(rows, d, n_parts))
+        return FA_ERR_WORKSPACE;
     DeviceInfo *di = device_info();
     if (!di) return FA_ERR_LAUNCH;
     fa::Kvq8AttnArgs a;
@@ -496,14 +497,12 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     a.max_len = max_len;
     a.scale = scale;
     a.causal = causal ? 1 : 0;
-    a.n_splits = n_splits;
-    const size_t o_bytes = ((static_cast<size_t>(n_splits) * rows * d * sizeof(float) + 255) / 256) * 256;
-    a.o_part = need ? static_cast<float *>(workspace) : nullptr;
-    a.lse_part = need ? reinterpret_cast<float *>(static_cast<char *>(workspace) + o_bytes) : nullptr;
+    a.parts = n_parts;
+    a.workspace = static_cast<float *>(workspace);
     a.status = di->status;
     a.stream = static_cast<cudaStream_t>(stream);
-    log_call("8-bit cache attention %s format=%d page=%d d=%d causal=%d B=%d H=%d Hkv=%d Nq=%d max_len=%d splits=%d",
-             fp16 ? "fp16" : "bf16", format, page, d, a.causal, B, H, Hkv, Nq, max_len, n_splits);
+    log_call("8-bit cache attention %s format=%d page=%d d=%d causal=%d B=%d H=%d Hkv=%d Nq=%d max_len=%d parts=%d",
+             fp16 ? "fp16" : "bf16", format, page, d, a.causal, B, H, Hkv, Nq, max_len, n_parts);
     return fa::launch_kvq8_attention(a, fp16);
 }
 
@@ -800,30 +799,32 @@ int fa_kvq8_read_fp16(FA_READ_ARGS) {
 }
 #undef FA_READ_ARGS
 
-int fa_kvq8_num_splits(int B, int H, int Hkv, int Nq, int max_len, int d) {
+int fa_kvq8_num_parts(int B, int H, int Hkv, int Nq, int max_len, int d) {
     if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || max_len < 1) return FA_ERR_SHAPE;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     DeviceInfo *di = device_info();
-    return fa::kvq8_num_splits(B, Hkv, H / Hkv * Nq, max_len, d, di ? di->num_sms : 148);
+    return fa::kvq8_num_parts(B, Hkv, H / Hkv * Nq, max_len, di ? di->num_sms : 148);
 }
 
-long long fa_kvq8_workspace_bytes(int B, int H, int Nq, int d, int n_splits) {
-    return fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits);
+long long fa_kvq8_workspace_bytes(int H, int Hkv, int Nq, int d, int n_parts) {
+    if (H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || n_parts < 1) return FA_ERR_SHAPE;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    return static_cast<long long>(fa::kvq8_workspace_bytes(H / Hkv * Nq, d, n_parts));
 }
 
 #define FA_KVQ8_ARGS                                                                                                   \
     const void *q, const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,               \
         const int *page_table, int n_pages, int max_pages, int page, const int *kv_lens, void *out, float *lse, int B, \
-        int H, int Hkv, int Nq, int max_len, int d, int format, float scale, int causal, int n_splits,                 \
+        int H, int Hkv, int Nq, int max_len, int d, int format, float scale, int causal, int n_parts,                  \
         void *workspace, unsigned long long workspace_bytes, void *stream
 int fa_fwd_kvq8(FA_KVQ8_ARGS) {
     return kvq8_attn_common(false, q, k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page,
-                            kv_lens, out, lse, B, H, Hkv, Nq, max_len, d, format, scale, causal, n_splits, workspace,
+                            kv_lens, out, lse, B, H, Hkv, Nq, max_len, d, format, scale, causal, n_parts, workspace,
                             workspace_bytes, stream);
 }
 int fa_fwd_kvq8_fp16(FA_KVQ8_ARGS) {
     return kvq8_attn_common(true, q, k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page,
-                            kv_lens, out, lse, B, H, Hkv, Nq, max_len, d, format, scale, causal, n_splits, workspace,
+                            kv_lens, out, lse, B, H, Hkv, Nq, max_len, d, format, scale, causal, n_parts, workspace,
                             workspace_bytes, stream);
 }
 #undef FA_KVQ8_ARGS

@@ -51,8 +51,8 @@ struct Kvq8AttnArgs {
     const int *kv_lens;
     int B, H, Nq, max_len;
     float scale;
-    int causal, n_splits;
-    float *o_part, *lse_part;  // workspace: [n_splits][B*H*Nq][d], [n_splits][B*H*Nq]
+    int causal, parts;
+    float *workspace;
     int *status;
     cudaStream_t stream;
 };
@@ -60,10 +60,11 @@ struct Kvq8AttnArgs {
 int launch_kvq8_append(const Kvq8AppendArgs &a, bool fp16);
 int launch_kvq8_read(const Kvq8ReadArgs &a, bool fp16);
 int launch_kvq8_attention(const Kvq8AttnArgs &a, bool fp16);
-// Keys per split for n_splits splits of at most max_len keys (a multiple of the 16-key tiles).
-int kvq8_split_len(int max_len, int n_splits);
-// A split count for the problem; rows = (H / Hkv) * Nq query rows share a K/V head.
-int kvq8_num_splits(int B, int Hkv, int rows, int max_len, int d, int num_sms);
+// 16-key tiles of B sequences of max_len keys, over K/V heads and tiles of the `rows` = (H / Hkv) * Nq query rows
+// that share one; a part count for them, and the workspace that it takes.
+long long kvq8_tiles(int B, int Hkv, int rows, int max_len);
+int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int num_sms);
+size_t kvq8_workspace_bytes(int rows, int d, int parts);
 
 // Four int8 codes -> two pairs of fp16, exact: code + 128 under the exponent of 1024 is the
 // fp16 number 1152 + code.
@@ -89,7 +90,13 @@ __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t &lo, uint32_
     else e4m3x4_to_half2(w, lo, hi);
 }
 
-// 8 bytes of the cache per asynchronous copy (zero-filled when src_bytes is 0).
+// Asynchronous copies of 16 or 8 bytes per thread; with src_bytes = 0 nothing is read and zeros are written.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, uint32_t src_bytes) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }

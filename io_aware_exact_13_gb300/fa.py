@@ -82,7 +82,7 @@ SIGNATURES = {
                                [ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp]),
     "fa_fwd_varlen": (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _vp]),
     "fa_fwd_varlen_fp16": (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _vp]),
-    "fa_kvq8_num_splits": (ctypes.c_int, [ctypes.c_int] * 6),
+    "fa_kvq8_num_parts": (ctypes.c_int, [ctypes.c_int] * 6),
     "fa_kvq8_workspace_bytes": (ctypes.c_longlong, [ctypes.c_int] * 5),
     "fa_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_ulonglong, _vp]),
     "fa_fwd_host": (ctypes.c_int, [_vp] * 10 + [ctypes.c_int] * 4 + [ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp]),
@@ -559,21 +559,21 @@ def kvq8_read(cache, page_table, cu_seqlens, total, max_len, first=None, dtype=t
     return k, v
 
 
-def fa_kvq8_num_splits(B, H, Hkv, Nq, max_len, d) -> int:
-    n = int(lib.fa_kvq8_num_splits(int(B), int(H), int(Hkv), int(Nq), int(max_len), int(d)))
+def fa_kvq8_num_parts(B, H, Hkv, Nq, max_len, d) -> int:
+    n = int(lib.fa_kvq8_num_parts(int(B), int(H), int(Hkv), int(Nq), int(max_len), int(d)))
     if n < 0:
-        raise FAError(n, "fa_kvq8_num_splits")
+        raise FAError(n, "fa_kvq8_num_parts")
     return n
 
 
-def fa_kvq8_workspace_bytes(B, H, Nq, d, n_splits) -> int:
-    n = int(lib.fa_kvq8_workspace_bytes(int(B), int(H), int(Nq), int(d), int(n_splits)))
+def fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) -> int:
+    n = int(lib.fa_kvq8_workspace_bytes(int(H), int(Hkv), int(Nq), int(d), int(n_parts)))
     if n < 0:
         raise FAError(n, "fa_kvq8_workspace_bytes")
     return n
 
 
-def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_splits, workspace,
+def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_parts, workspace,
               stream):
     device, page, Hkv, d = _check_kvq8(cache, page_table)
     for name, t in (("q", q), ("out", out)):
@@ -592,26 +592,26 @@ def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, ca
         rc = getattr(lib, fn_name)(_ptr(q), *_kvq8_ptrs(cache), _ptr(page_table), cache.k_codes.shape[0],
                                    page_table.shape[1], page, _ptr(kv_lens), _ptr(out), _ptr(lse), B, H, Hkv, Nq,
                                    int(max_len), d, _KVQ8_FORMATS[cache.k_codes.dtype], float(scale),
-                                   int(bool(causal)), int(n_splits), _ptr(workspace), nbytes,
+                                   int(bool(causal)), int(n_parts), _ptr(workspace), nbytes,
                                    ctypes.c_void_p(_stream_handle(stream)))
     if rc != FA_OK:
         raise FAError(rc, fn_name)
 
 
-def fa_fwd_kvq8(q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_splits, workspace, stream=None):
+def fa_fwd_kvq8(q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_parts, workspace, stream=None):
     """bf16 forward of 1 to 16 query rows per sequence over an 8-bit cache, into ``out`` and ``lse``."""
     _raw_kvq8("fa_fwd_kvq8", torch.bfloat16, q, cache, page_table, kv_lens, out, lse, scale, causal, max_len,
-              n_splits, workspace, stream)
+              n_parts, workspace, stream)
 
 
-def fa_fwd_kvq8_fp16(q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_splits, workspace,
+def fa_fwd_kvq8_fp16(q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_parts, workspace,
                      stream=None):
     """fp16 forward over an 8-bit cache (see ``fa_fwd_kvq8``)."""
     _raw_kvq8("fa_fwd_kvq8_fp16", torch.float16, q, cache, page_table, kv_lens, out, lse, scale, causal, max_len,
-              n_splits, workspace, stream)
+              n_parts, workspace, stream)
 
 
-def attention_kvq8(q, cache, page_table, kv_lens, scale=None, causal=False, max_len=None, n_splits=None, stream=None):
+def attention_kvq8(q, cache, page_table, kv_lens, scale=None, causal=False, max_len=None, n_parts=None, stream=None):
     """O [B, H, Nq, d] and lse [B, H, Nq] of 1 to 16 query rows per sequence over its first kv_lens[b] cached tokens.
     ``max_len`` bounds every length (the page table's reach unless given); the workspace is a torch allocation."""
     B, H, Nq, d = q.shape
@@ -621,15 +621,14 @@ def attention_kvq8(q, cache, page_table, kv_lens, scale=None, causal=False, max_
     if max_len is None:
         max_len = page_table.shape[1] * cache.k_codes.shape[2]
     with _on(q.device, stream) if q.is_cuda else contextlib.nullcontext():
-        if n_splits is None:
-            n_splits = fa_kvq8_num_splits(B, H, cache.k_codes.shape[1], Nq, max_len, d)
-        ws = None
-        if n_splits > 1:
-            ws = torch.empty(fa_kvq8_workspace_bytes(B, H, Nq, d, n_splits), dtype=torch.uint8, device=q.device)
+        if n_parts is None:
+            n_parts = fa_kvq8_num_parts(B, H, cache.k_codes.shape[1], Nq, max_len, d)
+        ws = torch.empty(fa_kvq8_workspace_bytes(H, cache.k_codes.shape[1], Nq, d, n_parts), dtype=torch.uint8,
+                         device=q.device)
         out = torch.empty_like(q)
         lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
     _raw_kvq8("fa_fwd_kvq8" + _FP16_SUFFIX[q.dtype], q.dtype, q, cache, page_table, kv_lens, out, lse, scale, causal,
-              max_len, n_splits, ws, stream)
+              max_len, n_parts, ws, stream)
     return out, lse
 
 

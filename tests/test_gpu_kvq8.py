@@ -270,7 +270,7 @@ def check_attention(q, cache, table, lens, out, lse, scale, causal):
 
 
 ATTEND = [
-    # fmt, dtype, page, H, Hkv, Nq, d, lens, causal, n_splits
+    # fmt, dtype, page, H, Hkv, Nq, d, lens, causal, n_parts
     ("int8", "bf16", 16, 1, 1, 1, 64, [1], False, None),
     ("int8", "bf16", 16, 8, 2, 1, 128, [509, 16, 17, 0], False, None),
     ("e4m3", "fp16", 64, 4, 4, 1, 64, [64, 63, 65], False, 1),
@@ -286,13 +286,13 @@ ATTEND = [
 ]
 
 
-@pytest.mark.parametrize("fmt,dtype,page,H,Hkv,Nq,d,lens,causal,n_splits", ATTEND)
-def test_attention_matches_the_definition(fa, fmt, dtype, page, H, Hkv, Nq, d, lens, causal, n_splits):
+@pytest.mark.parametrize("fmt,dtype,page,H,Hkv,Nq,d,lens,causal,n_parts", ATTEND)
+def test_attention_matches_the_definition(fa, fmt, dtype, page, H, Hkv, Nq, d, lens, causal, n_parts):
     rng = np.random.default_rng(H * 100 + Nq + sum(lens))
     table, n_pages = random_table(rng, lens, page)
     cache = filled(fa, rng, fmt, n_pages, Hkv, page, d)
     q = torch.from_numpy(rng.standard_normal((len(lens), H, Nq, d))).to(DT[dtype]).to(DEV)
-    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints(lens), causal=causal, n_splits=n_splits,
+    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints(lens), causal=causal, n_parts=n_parts,
                                  max_len=max(lens))
     status_ok(fa)
     check_attention(q, cache, table, lens, out, lse, 1 / math.sqrt(d), causal)
@@ -313,7 +313,7 @@ def test_attention_scales_and_growing_scores(fa, fmt, d, scale):
     q = torch.from_numpy(rng.standard_normal((1, H, 3, d))).bfloat16().to(DEV)
     if scale == 0.4:
         q *= 0.5
-    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([n]), scale=scale, causal=True, n_splits=3)
+    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([n]), scale=scale, causal=True, n_parts=3)
     status_ok(fa)
     check_attention(q, cache, table, [n], out, lse, scale, True)
 
@@ -331,10 +331,24 @@ def test_attention_page_scales_far_apart(fa, fmt, dtype):
     cache.k_scale[table[0, 4]] = 0.0
     cache.k_scale[table[0, 5], 1] = 0.01337
     q = torch.from_numpy(rng.standard_normal((1, 4, 1, d))).to(DT[dtype]).to(DEV)
-    for n_splits in (1, 4):
-        out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([n]), n_splits=n_splits)
+    for n_parts in (1, 4):
+        out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([n]), n_parts=n_parts)
         status_ok(fa)
         check_attention(q, cache, table, [n], out, lse, 1 / math.sqrt(d), False)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_attention_pages_of_zeros_before_keys_a_row_does_not_see(fa, fmt):
+    """Early causal rows that see nothing but values of zero, then tiles in which they see no key."""
+    rng = np.random.default_rng(31)
+    table, n_pages = random_table(rng, [60], 16)
+    cache = filled(fa, rng, fmt, n_pages, 1, 16, 64)
+    cache.v_scale[table[0, :3]] = 0.0
+    q = torch.from_numpy(rng.standard_normal((1, 2, 16, 64))).half().to(DEV)
+    for n_parts in (1, 2):
+        out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([60]), causal=True, n_parts=n_parts)
+        status_ok(fa)
+        check_attention(q, cache, table, [60], out, lse, 0.125, True)
 
 
 def test_attention_all_values_zero_and_wide_queries(fa):
@@ -385,7 +399,7 @@ def test_attention_bad_pages_and_lengths(fa):
     cache = filled(fa, rng, "int8", 12, 1, page, d)
     table = np.array([[0, 1, 2, 3], [4, 5, 77, 6], [7, 8, 9, 10], [-1, 11, 11, 11]])
     q = torch.from_numpy(rng.standard_normal((4, 2, 1, d))).bfloat16().to(DEV)
-    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([64, 60, 65, 10]), n_splits=2)
+    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([64, 60, 65, 10]), n_parts=2)
     torch.cuda.synchronize()
     assert fa.fa_get_device_status() in (fa.FA_ERR_PAGE, fa.FA_ERR_SEQLENS)
     check_attention(q[:1], cache, table[:1], [64], out[:1], lse[:1], 1 / 8, False)
@@ -395,14 +409,14 @@ def test_attention_bad_pages_and_lengths(fa):
     status_ok(fa)
 
 
-def test_attention_repeats_bit_for_bit_and_split_counts_agree(fa):
+def test_attention_repeats_bit_for_bit_and_part_counts_agree(fa):
     rng = np.random.default_rng(26)
     lens, page, d = [3000, 700], 64, 128
     table, n_pages = random_table(rng, lens, page)
     cache = filled(fa, rng, "int8", n_pages, 2, page, d)
     q = torch.from_numpy(rng.standard_normal((2, 8, 1, d))).bfloat16().to(DEV)
-    for n_splits in (1, 2, 5, 47, 3000):
-        got = [fa.attention_kvq8(q, cache, ints(table.tolist()), ints(lens), n_splits=n_splits, max_len=3000)
+    for n_parts in (1, 2, 5, 47, 3000):
+        got = [fa.attention_kvq8(q, cache, ints(table.tolist()), ints(lens), n_parts=n_parts, max_len=3000)
                for _ in range(2)]
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
         check_attention(q, cache, table, lens, *got[0], 1 / math.sqrt(d), False)
@@ -438,10 +452,10 @@ def test_streams_and_concurrent_calls(fa):
     cache = filled(fa, rng, "e4m3", n_pages, 2, page, d)
     tab, ln = ints(table.tolist()), ints(lens)
     qs = [torch.from_numpy(rng.standard_normal((2, 4, 2, d))).half().to(DEV) for _ in range(6)]
-    want = [fa.attention_kvq8(q, cache, tab, ln, causal=True, n_splits=9) for q in qs]
+    want = [fa.attention_kvq8(q, cache, tab, ln, causal=True, n_parts=9) for q in qs]
     torch.cuda.synchronize()
     streams = [torch.cuda.Stream() for _ in range(3)]
-    got = [fa.attention_kvq8(q, cache, tab, ln, causal=True, n_splits=9,
+    got = [fa.attention_kvq8(q, cache, tab, ln, causal=True, n_parts=9,
                              stream=streams[i % 3] if i < 3 else streams[i % 3].cuda_stream)
            for i, q in enumerate(qs)]
     torch.cuda.synchronize()
@@ -467,7 +481,7 @@ def test_decoding_loop_in_a_graph(fa):
 
     def step():
         fa.kvq8_append(cache, k, v, tab, cu1, held, 1)
-        got = fa.attention_kvq8(q, cache, tab, seen, n_splits=2)
+        got = fa.attention_kvq8(q, cache, tab, seen, n_parts=2)
         held.add_(1)
         seen.add_(1)
         return got

@@ -43,12 +43,12 @@ def read(fa, ptrs=None, first=None, nseq=2, total=5, max_len=4, name="fa_kvq8_re
                                  c["d"], c["format"], None)
 
 
-def attend(fa, ptrs=None, B=2, H=4, Nq=1, max_len=64, n_splits=1, ws=0, ws_bytes=0, name="fa_fwd_kvq8", **kw):
+def attend(fa, ptrs=None, B=2, H=4, Nq=1, max_len=64, n_parts=1, ws=0x100000, ws_bytes=1 << 20, name="fa_fwd_kvq8", **kw):
     c = {**CACHE, **kw}
     p = [0x10000 * (i + 1) for i in range(9)] if ptrs is None else ptrs
     p = [ctypes.c_void_p(x) if x else None for x in p]
     return getattr(fa.lib, name)(*p[:6], c["n_pages"], c["max_pages"], c["page"], p[6], p[7], p[8], B, H, c["Hkv"], Nq,
-                                 max_len, c["d"], c["format"], ctypes.c_float(0.1), 0, n_splits,
+                                 max_len, c["d"], c["format"], ctypes.c_float(0.1), 0, n_parts,
                                  ctypes.c_void_p(ws) if ws else None, ws_bytes, None)
 
 
@@ -87,17 +87,20 @@ def test_append_and_read_sizes_are_refused(fa):
 
 def test_attention_sizes_and_workspace_are_refused(fa):
     for kw in (dict(B=0), dict(H=0), dict(H=3), dict(Nq=0), dict(Nq=17), dict(max_len=0), dict(max_len=65),
-               dict(n_splits=0), dict(n_splits=65)):
+               dict(n_parts=0), dict(n_parts=(1 << 20) + 1), dict(B=1 << 20, H=1 << 12),
+               dict(B=1 << 18, max_pages=1 << 14, max_len=1 << 18)):
         assert attend(fa, **kw) == fa.FA_ERR_SHAPE, kw
-    need = fa.fa_kvq8_workspace_bytes(2, 4, 1, 64, 2)
-    assert attend(fa, n_splits=2) == fa.FA_ERR_WORKSPACE
-    assert attend(fa, n_splits=2, ws=0x100010, ws_bytes=need) == fa.FA_ERR_WORKSPACE
-    assert attend(fa, n_splits=2, ws=0x100000, ws_bytes=need - 1) == fa.FA_ERR_WORKSPACE
-    assert fa.lib.fa_kvq8_num_splits(1, 4, 3, 1, 100, 64) == fa.FA_ERR_SHAPE
-    assert fa.lib.fa_kvq8_num_splits(1, 4, 2, 1, 100, 80) == fa.FA_ERR_UNSUPPORTED
+    need = fa.fa_kvq8_workspace_bytes(4, 2, 1, 64, 2)
+    assert attend(fa, n_parts=2, ws=0) == fa.FA_ERR_WORKSPACE
+    assert attend(fa, n_parts=2, ws=0x100010, ws_bytes=need) == fa.FA_ERR_WORKSPACE
+    assert attend(fa, n_parts=2, ws_bytes=need - 1) == fa.FA_ERR_WORKSPACE
+    assert fa.lib.fa_kvq8_num_parts(1, 4, 3, 1, 100, 64) == fa.FA_ERR_SHAPE
+    assert fa.lib.fa_kvq8_num_parts(1, 4, 2, 1, 100, 80) == fa.FA_ERR_UNSUPPORTED
+    assert fa.lib.fa_kvq8_workspace_bytes(4, 3, 1, 64, 1) == fa.FA_ERR_SHAPE
+    assert fa.lib.fa_kvq8_workspace_bytes(4, 2, 1, 96, 1) == fa.FA_ERR_UNSUPPORTED
     for B, Hkv, n in ((1, 1, 1), (1, 8, 100000), (300, 8, 5000), (4, 2, 63)):
-        s = fa.fa_kvq8_num_splits(B, 4 * Hkv, Hkv, 1, n, 128)
-        assert 1 <= s <= n
+        s = fa.fa_kvq8_num_parts(B, 4 * Hkv, Hkv, 1, n, 128)
+        assert 1 <= s <= B * Hkv * ((n + 63) // 64)
 
 
 def test_binding_refuses(fa):
@@ -111,7 +114,7 @@ def test_binding_refuses(fa):
     with pytest.raises(ValueError):
         fa.kvq8_read(cache, table, cu, 3, 3)
     with pytest.raises(ValueError):
-        fa.attention_kvq8(torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16), cache, table, lens, n_splits=1)
+        fa.attention_kvq8(torch.zeros(1, 2, 1, 64, dtype=torch.bfloat16), cache, table, lens, n_parts=1)
     with pytest.raises(ValueError):
         fa.attention_kvq8(torch.zeros(1, 2, 1, 64), cache, table, lens)  # fp32 queries
     with pytest.raises(ValueError):
