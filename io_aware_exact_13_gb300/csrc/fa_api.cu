@@ -480,7 +480,7 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     if (n_parts < 1 || n_parts > (1 << 20)) return FA_ERR_SHAPE;
     if (static_cast<int64_t>(B) * H * Nq > INT32_MAX) return FA_ERR_SHAPE;
     const int rows = H / Hkv * Nq;
-    if (fa::kvq8_tiles(B, Hkv, rows, max_len) > (1 << 30)) return FA_ERR_SHAPE;
+    if (fa::kvq8_tiles(B, Hkv, rows, max_len, d) > (1 << 30)) return FA_ERR_SHAPE;
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < fa::kvq8_workspace_bytes(rows, d, n_parts))
         return FA_ERR_WORKSPACE;
     DeviceInfo *di = device_info();
@@ -803,7 +803,7 @@ int fa_kvq8_num_parts(int B, int H, int Hkv, int Nq, int max_len, int d) {
     if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || max_len < 1) return FA_ERR_SHAPE;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     DeviceInfo *di = device_info();
-    return fa::kvq8_num_parts(B, Hkv, H / Hkv * Nq, max_len, di ? di->num_sms : 148);
+    return fa::kvq8_num_parts(B, Hkv, H / Hkv * Nq, max_len, d, di ? di->num_sms : 148);
 }
 
 long long fa_kvq8_workspace_bytes(int H, int Hkv, int Nq, int d, int n_parts) {

@@ -62,8 +62,8 @@ int launch_kvq8_read(const Kvq8ReadArgs &a, bool fp16);
 int launch_kvq8_attention(const Kvq8AttnArgs &a, bool fp16);
 // 16-key tiles of B sequences of max_len keys, over K/V heads and tiles of the `rows` = (H / Hkv) * Nq query rows
 // that share one; a part count for them, and the workspace that it takes.
-long long kvq8_tiles(int B, int Hkv, int rows, int max_len);
-int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int num_sms);
+long long kvq8_tiles(int B, int Hkv, int rows, int max_len, int d);
+int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int d, int num_sms);
 size_t kvq8_workspace_bytes(int rows, int d, int parts);
 
 // Four int8 codes -> two pairs of fp16, exact: code + 128 under the exponent of 1024 is the

@@ -14,8 +14,11 @@
 //   - The order of the contraction index, and of the rows of A, is free as long as both sides
 //     agree. So a lane loads 16 contiguous codes of a key (K: dims 64 j + 16 c.., four MMA steps'
 //     worth; V: dims 16 g.. of four keys), and the fragments are cut from its own registers: no
-//     lane ever needs another's codes. Each lane therefore copies into its own slots of shared
-//     memory (cp.async, kStages tiles deep) and waits for its own copies only.
+//     lane ever needs another's codes and nothing passes through shared memory. (A ring of
+//     asynchronous copies in shared memory was slower, 272 us against 214 on the large case below:
+//     its loads and copies crowd the pipe that the shuffles use.) The next tile's K is loaded into
+//     the registers as soon as the scores have read them, its V at the end of the step; bringing
+//     tiles further ahead to L2 first was slower too (219 to 271 us).
 //   - The page scales multiply scores, which are few (16 keys x 8 rows per tile and warp): ks goes
 //     into the score, log2 vs into the exponent of the weights that multiply Vc. Those weights,
 //     w_j = s_j log2 e + log2 vs(j), keep a running maximum of their own: the fp16 rounding of the
@@ -25,9 +28,15 @@
 // range, which is exact down to 2^-24 of the row's largest magnitude. P (the weights) are rounded
 // to fp16, 2^-11 relative.
 //
-// A CTA takes one chunk of keys of one (sequence, K/V head, row tile); its four warps take every
-// fourth 16-key tile and merge at the end. A sequence that needs one chunk is finished by its CTA;
-// otherwise the chunks' summaries go to the workspace and fa_kvq8_combine merges them.
+// Ragged batches: all sequences' tiles are one line (sequence by sequence, head by head) that the warps of one
+// wave of CTAs cut into equal stretches, whatever the lengths are; each warp finds its place by adding the
+// lengths up. (A CTA per fixed chunk of keys left most of a second wave idle: 51 us against 38 on the ragged
+// case below.) A unit that one warp does alone is written at once; the warps of a CTA merge theirs in shared
+// memory; what several CTAs share goes through the workspace to fa_kvq8_combine.
+//
+// Measured on one GB300 (copy rate 6.80 TB/s): B 64, H 64 / 8, d 128, e4m3, ragged up to 16384 keys 211 us (92 % of
+// the copy rate); B 16, H 32 / 8, d 128, int8, ragged up to 8192 keys 42 us (60 %); time is about bytes / rate + 15 us,
+// of which launch and lengths are 2.3, the merge kernel 5.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,14 +58,31 @@ constexpr float kTau = 8.0f;  // log2 units by which a reference maximum may be 
 constexpr float kNone = -1e30f;  // reference maximum of a row that has seen no key
 constexpr float kLn2 = 0.6931471805599453f;
 
+// Resident CTAs per SM that the kernel is compiled for: 128, 168 or 255 registers per thread.
+__host__ __device__ constexpr int q8_ctas(int D, int NT) { return NT == 1 ? 4 : NT == 2 && D == 64 ? 3 : 2; }
+
 template <int D, int NT>
 struct Q8Cfg {
     static constexpr int KB = D / 64;                   // 16-byte units of a K row per lane
     static constexpr int VB = D / 8;                    // bytes of a V row per lane
     static constexpr int VW = VB / 4;                   // words of a V row per lane
-    static constexpr int PITCH = D + 8;  // floats per row of the merge buffer
+    static constexpr int KS = D / 16;    // MMA steps over the head dimension
+    static constexpr int MT = D / 16;    // 16-row tiles of O^T
     static constexpr int RT = 8 * NT;    // query rows per unit
-    static constexpr int CTAS = NT == 1 ? 4 : 3;  // per SM: 128 or 168 registers per thread
+    static constexpr int DEPTH = D == 64 || NT == 2 ? 2 : 1;  // tiles in flight per warp: 4 KB (8 KB where CTAs are few)
+    static constexpr int PITCH = D + 4;  // floats per row of a shared stretch's summary
+    static constexpr int CTAS = q8_ctas(D, NT);
+    static constexpr int SM_O = 0;                                           // [2 kWarps][RT][PITCH] floats
+    static constexpr int SM_ML = SM_O + 2 * kWarps * RT * PITCH * 4;         // m, l: [2 kWarps][RT] floats each
+    static constexpr int SM_SEG = SM_ML + 2 * 2 * kWarps * RT * 4;           // Q8Stretch[2 kWarps]
+    static constexpr int SMEM = SM_SEG + 2 * kWarps * 32;
+};
+
+// What a warp left in shared memory of a unit that it did not do alone: tiles [beg, end) of the unit's [first, last).
+struct Q8Stretch {
+    int unit;  // b * units + unit, or -1
+    int first, last, beg, end;
+    int pad[3];
 };
 
 struct Q8Params {
@@ -67,6 +93,7 @@ struct Q8Params {
     const float *k_scale, *v_scale;
     const int *page_table, *kv_lens;
     float *o_part, *lse_part;  // [parts][2][RT][d], [parts][2][RT]
+    int4 *shared;              // [parts]: the unit that holds the part's first tile, if it began in an earlier part
     int *status;
     int B, H, Hkv, Nq, rows, row_tiles;  // rows = (H / Hkv) Nq query rows share a K/V head, in row_tiles tiles
     int n_pages, max_pages, page_shift;
@@ -89,19 +116,6 @@ __device__ __forceinline__ int q8_len(const Q8Params &p, int b, bool &bad) {
     return bad ? 0 : len;
 }
 __device__ __forceinline__ int q8_tiles(int len) { return (len + kTileKeys - 1) / kTileKeys; }
-
-// Sum over the CTA (THREADS threads, sum[] of THREADS / 32 ints in shared memory); ends with a barrier.
-template <int THREADS>
-__device__ __forceinline__ int cta_sum(int v, int *sum) {
-    v = __reduce_add_sync(0xffffffffu, v);
-    if ((threadIdx.x & 31) == 0) sum[threadIdx.x >> 5] = v;
-    __syncthreads();
-    int s = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) s += sum[w];
-    __syncthreads();
-    return s;
-}
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
@@ -127,9 +141,14 @@ __device__ __forceinline__ void load_codes(const uint8_t *src, uint32_t (&w)[N])
     }
 }
 template <typename T>
-__device__ __forceinline__ float to_float(T x) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) return __bfloat162float(x);
-    else return __half2float(x);
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
 }
 template <typename T>
 __device__ __forceinline__ T from_float(float x) {
@@ -140,74 +159,72 @@ __device__ __forceinline__ T from_float(float x) {
 template <typename T, int D, int FMT, int NT, bool CAUSAL>
 __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_partial(const Q8Params p) {
     using C = Q8Cfg<D, NT>;
-    constexpr int KS = D / 16;   // MMA steps over the head dimension
-    constexpr int MT = D / 16;   // 16-row tiles of O^T
-    constexpr int RT = C::RT;
-    __shared__ float sm_m[kWarps * RT], sm_l[kWarps * RT];
-    __shared__ __align__(16) float sm_o[kWarps * RT * C::PITCH];
-    __shared__ int sm_scan[kWarps];
+    constexpr int KS = C::KS, MT = C::MT, RT = C::RT;
+    extern __shared__ __align__(128) uint8_t sm[];
+    float *sm_o = reinterpret_cast<float *>(sm + C::SM_O), *sm_m = reinterpret_cast<float *>(sm + C::SM_ML);
+    float *sm_l = sm_m + 2 * kWarps * RT;
+    Q8Stretch *seg = reinterpret_cast<Q8Stretch *>(sm + C::SM_SEG);
     grid_launch_dependents();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;
     const int page_mask = (1 << p.page_shift) - 1;
     const int units = p.Hkv * p.row_tiles;  // per sequence
 
-    // ---------------------------------------------------------------- this CTA's stretch of the line
-    int cur, end, b = 0, base = 0, len = 0;  // base: first tile of sequence b
+    // ---------------------------------------------------------------- this warp's stretch of the line
+    // Each warp adds the lengths up for itself: no barrier between the lengths' arrival and the first page's read.
+    int cur, end, b = 0, base = 0, len = 0, per;  // base: first tile of sequence b
     {
-        int mine = 0, first = 0;  // first: the tiles of this thread's first sequence
-        for (int s = threadIdx.x; s < p.B; s += kWarps * 32) {
+        int total = 0, first_len = 0, s_bad = 0;  // first_len: the length of this lane's first sequence
+#pragma unroll 4
+        for (int s = lane; s < p.B; s += 32) {
             bool bad;
-            const int n = q8_tiles(q8_len(p, s, bad)) * units;
-            if (bad && blockIdx.x == 0) atomicExch(p.status, kStatusSeqlensQ8);
-            if (s == threadIdx.x) first = n;
-            mine += n;
+            const int n = q8_len(p, s, bad);
+            s_bad |= bad;
+            if (s == lane) first_len = n;
+            total += q8_tiles(n) * units;
         }
-        const int total = cta_sum<kWarps * 32>(mine, sm_scan);
-        const int per = q8_part_tiles(total, p.parts);
+        total = __reduce_add_sync(0xffffffffu, total);
+        per = q8_part_tiles(total, p.parts);
+        if (s_bad && blockIdx.x == 0 && warp == 0) atomicExch(p.status, kStatusSeqlensQ8);
+        // sequences without keys: zeros, by the CTAs in turn
+        for (int s = blockIdx.x; s < p.B; s += gridDim.x) {
+            bool bad;
+            if (q8_len(p, s, bad) != 0) continue;
+            const size_t rows = (size_t)p.H * p.Nq;
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + s * rows * D);
+            for (size_t i = threadIdx.x; i < rows * (D / 8); i += kWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (size_t i = threadIdx.x; i < rows; i += kWarps * 32) p.lse[s * rows + i] = -INFINITY;
+        }
+        if (threadIdx.x == 0) p.shared[blockIdx.x] = make_int4(-1, 0, 0, 0);
         if ((long long)blockIdx.x * per >= total) return;
-        cur = blockIdx.x * per;
-        end = min(total, cur + per);
-        // the sequence that holds tile cur: blocks of 128 sequences, each scanned by the CTA
-        for (int s0 = 0;; s0 += kWarps * 32) {
-            int n = first;
-            if (s0 > 0) {
-                bool bad;
-                n = s0 + (int)threadIdx.x < p.B ? q8_tiles(q8_len(p, s0 + threadIdx.x, bad)) * units : 0;
-            }
+        cur = blockIdx.x * per + warp * (per / kWarps);
+        end = min(total, cur + per / kWarps);
+        if (lane < 2) seg[2 * warp + lane].unit = -1;
+        // the sequence that holds tile cur, 32 at a time
+        for (int s0 = 0; cur < total; s0 += 32) {
+            bool bad;
+            const int l = s0 == 0 ? first_len : s0 + lane < p.B ? q8_len(p, s0 + lane, bad) : 0;
+            const int n = q8_tiles(l) * units;
             int incl = n;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, d);
                 if (lane >= d) incl += v;
             }
-            if (lane == 31) sm_scan[warp] = incl;
-            __syncthreads();
-            int before = base, all = base;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                before += w < warp ? sm_scan[w] : 0;
-                all += sm_scan[w];
+            const uint32_t past = __ballot_sync(0xffffffffu, cur < base + incl);
+            if (past != 0) {
+                const int at = __ffs(past) - 1;
+                b = s0 + at;
+                base += __shfl_sync(0xffffffffu, incl - n, at);
+                len = __shfl_sync(0xffffffffu, l, at);
+                break;
             }
-            __syncthreads();
-            if (cur >= all) {  // the same for every thread; cur < total, so some block holds it
-                base = all;
-                continue;
-            }
-            const int from = before + incl - n;
-            if (cur >= from && cur < from + n) {  // one thread
-                sm_scan[0] = s0 + threadIdx.x;
-                sm_scan[1] = from;
-            }
-            __syncthreads();
-            b = sm_scan[0];
-            base = sm_scan[1];
-            break;
+            base += __shfl_sync(0xffffffffu, incl, 31);
         }
-        bool bad;
-        len = q8_len(p, b, bad);
+        __syncwarp();
     }
-    const int start = cur;
+    const int start = blockIdx.x * per;  // of the CTA
+    const int warp_start = cur;
 
     while (cur < end) {
         int seq_tiles = q8_tiles(len);
@@ -221,23 +238,29 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
         const int tile0 = cur - base - unit * seq_tiles;
         const int n_tiles = min(seq_tiles - tile0, end - cur);
         const bool whole = n_tiles == seq_tiles;
-        const int part_slot = 2 * blockIdx.x + (cur == start ? 0 : 1);
+        const int slot = 2 * warp + (cur == warp_start ? 0 : 1);  // a stretch that is not whole is the first or the last
+        if (!whole && lane == 0) {
+            seg[slot].unit = b * units + unit;
+            seg[slot].first = base + unit * seq_tiles;
+            seg[slot].last = base + (unit + 1) * seq_tiles;
+            seg[slot].beg = cur;
+            seg[slot].end = cur + n_tiles;
+        }
         cur += n_tiles;
         const int kvh = unit / p.row_tiles, rt = unit - kvh * p.row_tiles;
         const int k0 = tile0 * kTileKeys, k1 = min(len, k0 + n_tiles * kTileKeys);
         const int row0 = rt * RT;  // first of the unit's rows among the rows of the K/V head
         const size_t row_base = ((size_t)b * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq;
-        const int my_tiles = n_tiles > warp ? (n_tiles - warp + kWarps - 1) / kWarps : 0;
 
-        // Lane i looks after tile 32 n + i of this warp: its page and scales. The page numbers are read a window
+        // Lane i looks after tile 32 n + i of the stretch: its page and scales. The page numbers are read a window
         // of 32 tiles ahead.
         const int *table = p.page_table + (size_t)b * p.max_pages;
-        const int lane_key = k0 + (warp + lane * kWarps) * kTileKeys;  // + 32 kWarps kTileKeys per window
+        const int lane_key = k0 + lane * kTileKeys;  // + 32 kTileKeys per window
         int ahead = lane_key < k1 ? __ldg(table + (lane_key >> p.page_shift)) : -1;
         int pg = -1;
         float pg_ks = 0.f, pg_lv = -INFINITY;
         auto load_pages = [&](int it0) {  // the window that starts at tile it0 (a multiple of 32)
-            const int key = lane_key + it0 * kWarps * kTileKeys;
+            const int key = lane_key + it0 * kTileKeys;
             pg = -1;
             if (key < k1) {
                 if (ahead >= 0 && ahead < p.n_pages) {
@@ -249,67 +272,64 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                     atomicExch(p.status, kStatusPage);
                 }
             }
-            const int next = key + 32 * kWarps * kTileKeys;
+            const int next = key + 32 * kTileKeys;
             ahead = next < k1 ? __ldg(table + (next >> p.page_shift)) : -1;
         };
         // This lane's codes of one tile: K rows g and g + 8 (dims 64 j + 16 c ..), V rows 2c, 2c + 1, 2c + 8,
         // 2c + 9 (dims VB g ..). Keys past the stretch and pages that are none are read as zeros; only a
-        // stretch's last tile looks at single keys.
-        uint32_t kw[2][C::KB][4], vw[4][C::VW];
+        // stretch's last tile looks at single keys. DEPTH tiles are in flight.
+        struct Tile {
+            uint32_t kw[2][C::KB][4], vw[4][C::VW];
+            size_t off;    // byte offset of its codes
+            int n_keys;    // how many of its keys there are to read
+            float ks, lv;  // scale log2 e times the page's K scale, log2 of its V scale
+        };
+        Tile buf[C::DEPTH];
         const uint8_t *k_lane = p.k_codes + g * D + c * 16, *v_lane = p.v_codes + 2 * c * D + g * C::VB;
-        size_t off = 0;  // byte offset of the tile whose K was loaded last
-        int n_keys = 0;  // how many of its keys there are to read
-        auto load_k = [&](int it) {
+        auto load_k = [&](Tile &b, int it) {
             const int page = __shfl_sync(0xffffffffu, pg, it & 31);
-            const int key0 = k0 + (warp + it * kWarps) * kTileKeys;
-            off = ((((size_t)(page >= 0 ? page : 0) * p.Hkv + kvh) << p.page_shift) + (size_t)(key0 & page_mask)) * D;
-            n_keys = page >= 0 ? k1 - key0 : 0;
-            const uint8_t *src = k_lane + off;
-            if (n_keys >= kTileKeys) {
+            b.ks = __shfl_sync(0xffffffffu, pg_ks, it & 31);
+            b.lv = __shfl_sync(0xffffffffu, pg_lv, it & 31);
+            const int key0 = k0 + it * kTileKeys;
+            b.off = ((((size_t)(page >= 0 ? page : 0) * p.Hkv + kvh) << p.page_shift) + (size_t)(key0 & page_mask)) * D;
+            b.n_keys = page >= 0 ? k1 - key0 : 0;
+            const uint8_t *src = k_lane + b.off;
+            if (b.n_keys >= kTileKeys) {
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
-                    for (int j = 0; j < C::KB; ++j) load_codes(src + 8 * r * D + j * 64, kw[r][j]);
+                    for (int j = 0; j < C::KB; ++j) load_codes(src + 8 * r * D + j * 64, b.kw[r][j]);
             } else {
 #pragma unroll
                 for (int r = 0; r < 2; ++r)
 #pragma unroll
                     for (int j = 0; j < C::KB; ++j) {
-                        kw[r][j][0] = kw[r][j][1] = kw[r][j][2] = kw[r][j][3] = 0u;
-                        if (g + 8 * r < n_keys) load_codes(src + 8 * r * D + j * 64, kw[r][j]);
+                        b.kw[r][j][0] = b.kw[r][j][1] = b.kw[r][j][2] = b.kw[r][j][3] = 0u;
+                        if (g + 8 * r < b.n_keys) load_codes(src + 8 * r * D + j * 64, b.kw[r][j]);
                     }
             }
         };
-        auto load_v = [&]() {
-            const uint8_t *src = v_lane + off;
-            if (n_keys >= kTileKeys) {
+        auto load_v = [&](Tile &b) {
+            const uint8_t *src = v_lane + b.off;
+            if (b.n_keys >= kTileKeys) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) load_codes(src + ((i & 1) + (i >> 1) * 8) * D, vw[i]);
+                for (int i = 0; i < 4; ++i) load_codes(src + ((i & 1) + (i >> 1) * 8) * D, b.vw[i]);
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int key = (i & 1) + (i >> 1) * 8;
 #pragma unroll
-                    for (int e = 0; e < C::VW; ++e) vw[i][e] = 0u;
-                    if (2 * c + key < n_keys) load_codes(src + key * D, vw[i]);
+                    for (int e = 0; e < C::VW; ++e) b.vw[i][e] = 0u;
+                    if (2 * c + key < b.n_keys) load_codes(src + key * D, b.vw[i]);
                 }
             }
         };
-        load_pages(0);
-        if (my_tiles > 0) {
-            load_k(0);
-            load_v();
-        }
-
         // Q as B fragments: column g of tile t is row row0 + 8 t + g, contraction index in the order of the K codes
         uint32_t qb[NT][KS][2];
-        float qmul[NT][2];  // what the rows 2c, 2c + 1 of tile t were divided by
-        int lim[NT][2];     // causal: last visible key of those rows
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int row = row0 + 8 * t + g;
             const T *src = static_cast<const T *>(p.q) + (row_base + row) * D;
-            float mul = 1.0f;
 #pragma unroll
             for (int j = 0; j < C::KB; ++j) {
                 uint4 w[2] = {make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u)};
@@ -323,13 +343,27 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                     qb[t][4 * j + e][1] = e == 0 ? w[0].y : e == 1 ? w[0].w : e == 2 ? w[1].y : w[1].w;
                 }
             }
+        }
+        load_pages(0);
+#pragma unroll
+        for (int i = 0; i < C::DEPTH; ++i)
+            if (i < n_tiles) {
+                load_k(buf[i], i);
+                load_v(buf[i]);
+            }
+
+        float qmul[NT][2];  // what the rows 2c, 2c + 1 of a tile were divided by
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            uint32_t (&qt)[KS][2] = qb[t];
+            float mul = 1.0f;
             if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                 uint32_t most = 0;
 #pragma unroll
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        most = max(most, max(qb[t][s][e] & 0x7FFFu, (qb[t][s][e] >> 16) & 0x7FFFu));
+                        most = max(most, max(qt[s][e] & 0x7FFFu, (qt[s][e] >> 16) & 0x7FFFu));
                 most = max(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 most = max(most, __shfl_xor_sync(0xffffffffu, most, 2));
                 const uint32_t ex = min(most >> 7, 253u);  // biased exponent of the row's largest magnitude
@@ -339,18 +373,14 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                 for (int s = 0; s < KS; ++s)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&qb[t][s][e]);
+                        const __nv_bfloat162 h = *reinterpret_cast<const __nv_bfloat162 *>(&qt[s][e]);
                         const float2 f = __bfloat1622float2(h);
                         const __half2 o = __floats2half2_rn(f.x * inv, f.y * inv);
-                        qb[t][s][e] = *reinterpret_cast<const uint32_t *>(&o);
+                        qt[s][e] = *reinterpret_cast<const uint32_t *>(&o);
                     }
             }
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                qmul[t][e] = __shfl_sync(0xffffffffu, mul, 8 * c + 4 * e);  // lane of column 2c + e
-                if constexpr (CAUSAL) lim[t][e] = len - p.Nq + (row0 + 8 * t + 2 * c + e) % p.Nq;
-                else lim[t][e] = len - 1;
-            }
+            for (int e = 0; e < 2; ++e) qmul[t][e] = __shfl_sync(0xffffffffu, mul, 8 * c + 4 * e);  // of column 2c + e
         }
 
         float o[NT][MT][4], m[NT][2], mw[NT][2], l[NT][2];
@@ -365,11 +395,10 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
             }
         }
 
-        for (int it = 0; it < my_tiles; ++it) {
+        auto step = [&](Tile &b, int it) {
             float x[NT][4];
-            const float ks = __shfl_sync(0xffffffffu, pg_ks, it & 31), lv = __shfl_sync(0xffffffffu, pg_lv, it & 31);
-            const int key0 = k0 + (warp + it * kWarps) * kTileKeys;
-            const int in_tile = n_keys;  // of this tile
+            const float ks = b.ks, lv = b.lv;
+            const int key0 = k0 + it * kTileKeys, in_tile = b.n_keys;
             // S^T = Kc Q^T
 #pragma unroll
             for (int t = 0; t < NT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
@@ -378,29 +407,34 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t a[4];
-                    codes_to_half2<FMT>(kw[0][j][e], a[0], a[2]);
-                    codes_to_half2<FMT>(kw[1][j][e], a[1], a[3]);
+                    codes_to_half2<FMT>(b.kw[0][j][e], a[0], a[2]);
+                    codes_to_half2<FMT>(b.kw[1][j][e], a[1], a[3]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mma_f16(x[t], a, qb[t][4 * j + e][0], qb[t][4 * j + e][1]);
                 }
-            // the next tile's K, in flight during the rest of this step
-            const bool next = it + 1 < my_tiles;
-            if (next) {
-                if (((it + 1) & 31) == 0) load_pages(it + 1);
-                load_k(it + 1);
+            // K of the tile that takes this one's registers, in flight from here on; its V at the end
+            const bool more = it + C::DEPTH < n_tiles;
+            if (more) {
+                if (((it + C::DEPTH) & 31) == 0) load_pages(it + C::DEPTH);
+                load_k(b, it + C::DEPTH);
             }
             // scores in log2 units, with the range, page and causal limits
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[t][e] *= ks * qmul[t][e & 1];
+            for (int t = 0; t < NT; ++t) {
+                const float2 mul = make_float2(ks * qmul[t][0], ks * qmul[t][1]);
+                x[t][0] *= mul.x;
+                x[t][1] *= mul.y;
+                x[t][2] *= mul.x;
+                x[t][3] *= mul.y;
+            }
             if (in_tile < kTileKeys || (CAUSAL && key0 + kTileKeys - 1 > len - p.Nq)) {
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int r = g + (e >> 1) * 8;
-                        if (r >= in_tile || key0 + r > lim[t][e & 1]) x[t][e] = -INFINITY;
+                        const int last = CAUSAL ? len - p.Nq + (row0 + 8 * t + 2 * c + (e & 1)) % p.Nq : len;
+                        if (r >= in_tile || key0 + r > last) x[t][e] = -INFINITY;
                     }
             }
             bool need = false;
@@ -455,20 +489,26 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
 #pragma unroll
             for (int i = 0; i < C::VW; ++i) {
                 uint32_t a[4];
-                codes_to_half2<FMT>(__byte_perm(vw[0][i], vw[1][i], 0x5140), a[0], a[1]);
-                codes_to_half2<FMT>(__byte_perm(vw[2][i], vw[3][i], 0x5140), a[2], a[3]);
+                codes_to_half2<FMT>(__byte_perm(b.vw[0][i], b.vw[1][i], 0x5140), a[0], a[1]);
+                codes_to_half2<FMT>(__byte_perm(b.vw[2][i], b.vw[3][i], 0x5140), a[2], a[3]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * i], a, pb[t][0], pb[t][1]);
-                codes_to_half2<FMT>(__byte_perm(vw[0][i], vw[1][i], 0x7362), a[0], a[1]);
-                codes_to_half2<FMT>(__byte_perm(vw[2][i], vw[3][i], 0x7362), a[2], a[3]);
+                codes_to_half2<FMT>(__byte_perm(b.vw[0][i], b.vw[1][i], 0x7362), a[0], a[1]);
+                codes_to_half2<FMT>(__byte_perm(b.vw[2][i], b.vw[3][i], 0x7362), a[2], a[3]);
 #pragma unroll
                 for (int t = 0; t < NT; ++t) mma_f16(o[t][2 * i + 1], a, pb[t][0], pb[t][1]);
             }
-            if (next) load_v();
-        }
+            if (more) load_v(b);
+        };
+        for (int it = 0; it < n_tiles; it += C::DEPTH)
+#pragma unroll
+            for (int i = 0; i < C::DEPTH; ++i)
+                if (i == 0 || it + i < n_tiles) step(buf[i], it + i);
 
-        // merge the warps: l over the lanes of a row, O relative to m
-        #pragma unroll
+
+        // Lane (g, c) holds head columns VB g .. VB g + VB - 1 of rows 2c, 2c + 1 of every tile: value (i, e2) is
+        // column VB g + 2 i + e2. A whole unit is written out, any other stretch left for the CTA's merge.
+#pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -477,119 +517,175 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                 ls += __shfl_xor_sync(0xffffffffu, ls, 8);
                 ls += __shfl_xor_sync(0xffffffffu, ls, 16);
                 const int r = 8 * t + 2 * c + e;
-                if (g == 0) {
-                    sm_m[warp * RT + r] = m[t][e];
-                    sm_l[warp * RT + r] = ls;
+                float f = ex2_approx(mw[t][e] - m[t][e]);  // 0 where every weight was (mw = kNone)
+                if (whole) {
+                    f = ls > 0.f ? f / ls : 0.f;
+                    if (row0 + r < p.rows) {
+                        uint32_t w[MT];
+#pragma unroll
+                        for (int i = 0; i < MT; ++i) w[i] = pack16<T>(o[t][i][e] * f, o[t][i][e + 2] * f);
+                        T *dst = static_cast<T *>(p.out) + (row_base + row0 + r) * D + C::VB * g;
+#pragma unroll
+                        for (int i = 0; i < MT; i += 4) st_global_v4(dst + 2 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
+                        if (g == 0) p.lse[row_base + row0 + r] = ls > 0.f ? (m[t][e] + lg2_approx(ls)) * kLn2 : -INFINITY;
+                    }
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(sm_o + (slot * RT + r) * C::PITCH + C::VB * g);
+#pragma unroll
+                    for (int i = 0; i < MT; i += 2)
+                        dst[i / 2] = make_float4(o[t][i][e] * f, o[t][i][e + 2] * f, o[t][i + 1][e] * f, o[t][i + 1][e + 2] * f);
+                    if (g == 0) {
+                        sm_m[slot * RT + r] = m[t][e];
+                        sm_l[slot * RT + r] = ls;
+                    }
                 }
-                const float f = ex2_approx(mw[t][e] - m[t][e]);  // 0 where every weight was (mw = kNone)
-                // value (i, e2) of lane g is head column (D / 8) g + 2 i + e2, kept at 16 i + 2 g + e2
-                float *dst = sm_o + (warp * RT + r) * C::PITCH + 2 * g;
-#pragma unroll
-                for (int i = 0; i < MT; ++i)
-                    *reinterpret_cast<float2 *>(dst + 16 * i) = make_float2(o[t][i][e] * f, o[t][i][e + 2] * f);
             }
-        __syncthreads();
-        for (int idx = threadIdx.x; idx < RT * D; idx += kWarps * 32) {
-            const int r = idx / D, dim = idx % D;
-            const int row = row0 + r;
-            if (row >= p.rows) continue;
-            const int at = ((dim % C::VB) >> 1) * 16 + (dim / C::VB) * 2 + (dim & 1);
-            float M = kNone;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[w * RT + r]);
-            float L = 0.f, A = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = ex2_approx(sm_m[w * RT + r] - M);  // 0 for a warp that saw nothing, unless none did
-                L += f * sm_l[w * RT + r];
-                A += f * sm_o[(w * RT + r) * C::PITCH + at];
+    }
+
+    // ---------------------------------------------------------------- units shared by warps or CTAs
+    // Neighbouring stretches of one unit are merged. Where they are all of it the rows are written, otherwise the
+    // CTA's summary: slot 0 of the part for the unit that holds the CTA's first tile, slot 1 for its last one.
+    __syncthreads();
+    for (int a = 0; a < 2 * kWarps;) {
+        const int uid = seg[a].unit;
+        if (uid < 0) {
+            ++a;
+            continue;
+        }
+        int z = a, next = a + 1;  // stretches a .. z (some slots between may be empty)
+        for (; next < 2 * kWarps && (seg[next].unit < 0 || seg[next].unit == uid); ++next)
+            if (seg[next].unit == uid) z = next;
+        const bool all = seg[a].beg == seg[a].first && seg[z].end == seg[z].last;
+        const size_t part = 2 * (size_t)blockIdx.x + (seg[a].first <= start ? 0 : 1);
+        if (threadIdx.x == 0 && seg[a].first < start) p.shared[blockIdx.x] = make_int4(uid, seg[a].first, seg[a].last, per);
+        const int ub = uid / units, unit = uid - ub * units;
+        const int kvh = unit / p.row_tiles, row0 = (unit - kvh * p.row_tiles) * RT;
+        const size_t row_base = ((size_t)ub * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq + row0;
+        for (int idx = threadIdx.x; idx < RT * D / 4; idx += kWarps * 32) {
+            const int r = idx / (D / 4), e4 = idx % (D / 4);
+            if (row0 + r >= p.rows) break;
+            float M = kNone, L = 0.f;
+            float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int s = a; s <= z; ++s)
+                if (seg[s].unit >= 0) M = fmaxf(M, sm_m[s * RT + r]);
+            for (int s = a; s <= z; ++s) {
+                if (seg[s].unit < 0) continue;
+                const float f = ex2_approx(sm_m[s * RT + r] - M);  // 0 for a stretch that saw nothing, unless none did
+                const float4 v = *reinterpret_cast<const float4 *>(sm_o + (s * RT + r) * C::PITCH + 4 * e4);
+                L += f * sm_l[s * RT + r];
+                A.x = fmaf(f, v.x, A.x);
+                A.y = fmaf(f, v.y, A.y);
+                A.z = fmaf(f, v.z, A.z);
+                A.w = fmaf(f, v.w, A.w);
             }
-            const float val = L > 0.f ? A / L : 0.f;
+            const float inv = L > 0.f ? 1.0f / L : 0.f;
             const float lse = L > 0.f ? (M + lg2_approx(L)) * kLn2 : -INFINITY;
-            if (whole) {
-                static_cast<T *>(p.out)[(row_base + row) * D + dim] = from_float<T>(val);
-                if (dim == 0) p.lse[row_base + row] = lse;
+            if (all) {
+                uint2 w;
+                w.x = pack16<T>(A.x * inv, A.y * inv);
+                w.y = pack16<T>(A.z * inv, A.w * inv);
+                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * e4) = w;
+                if (e4 == 0) p.lse[row_base + r] = lse;
             } else {
-                const size_t at_part = (size_t)part_slot * RT + r;
-                p.o_part[at_part * D + dim] = val;
-                if (dim == 0) p.lse_part[at_part] = lse;
+                *reinterpret_cast<float4 *>(p.o_part + (part * RT + r) * D + 4 * e4) =
+                    make_float4(A.x * inv, A.y * inv, A.z * inv, A.w * inv);
+                if (e4 == 0) p.lse_part[part * RT + r] = lse;
             }
         }
-        __syncthreads();  // the merge buffer is free
+        a = next;
     }
 }
 
-// One CTA per query row: the summaries of the parts that share its unit, merged onto their common maximum
-// (fa_splitkv.cu's rule), the parts spread over the CTA's groups of D / 4 threads. A unit that one part did alone is
-// written already; one without keys gets out = 0, lse = -inf.
-constexpr int kCombineThreads = 256;
+// The units that several parts share: their summaries merged onto their common maximum (fa_splitkv.cu's rule). A unit
+// that n parts share is merged by the CTAs of its parts but the first, each doing every (n - 1)-th row; where a CTA has
+// few rows, several groups of threads share a row's summaries out.
+constexpr int kCombineThreads = 512;
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kCombineThreads) fa_kvq8_combine(const Q8Params p) {
-    constexpr int LANES = D / 4, GROUPS = kCombineThreads / LANES;
-    __shared__ int sm_sum[kCombineThreads / 32];
-    __shared__ float sm_max[kCombineThreads / 32], sm_w[GROUPS];
-    __shared__ float4 sm_a[GROUPS][LANES];
-    const int units = p.Hkv * p.row_tiles;
-    const int heads_rows = p.rows;  // rows of one K/V head
-    const int b = blockIdx.x / (p.Hkv * heads_rows), in_seq = blockIdx.x - b * p.Hkv * heads_rows;
-    const int kvh = in_seq / heads_rows, row = in_seq - kvh * heads_rows;
-    const int unit = kvh * p.row_tiles + row / RT, r = row % RT;
-    int before = 0, after = 0;
-    for (int s = threadIdx.x; s < p.B; s += kCombineThreads) {
-        bool bad;
-        const int n = q8_tiles(q8_len(p, s, bad)) * units;
-        if (s < b) before += n;
-        else after += n;
-    }
-    before = cta_sum<kCombineThreads>(before, sm_sum);
-    const int total = before + cta_sum<kCombineThreads>(after, sm_sum);
-    const int per = q8_part_tiles(total, p.parts);
-    bool bad;
-    const int tiles = q8_tiles(q8_len(p, b, bad));
-    const int first = before + unit * tiles;
-    const int p0 = first / per, n = tiles > 0 ? (first + tiles - 1) / per - p0 + 1 : 0;
+    constexpr int LANES = D / 4, SLOTS = kCombineThreads / LANES;  // four columns of a row per thread
+    constexpr int AHEAD = 8;                                      // summaries loaded before the first is used
+    static_assert(RT <= SLOTS, "a slot for each row");
+    __shared__ float4 sm_a[SLOTS][LANES];
+    __shared__ float sm_m[SLOTS], sm_w[SLOTS];
     grid_dependency_wait();
-    if (n == 1) return;
+    const int4 d = p.shared[blockIdx.x];
+    if (d.x < 0) return;
+    const int first = d.y, per = d.w, p0 = first / per, n = (d.z - 1) / per - p0 + 1;
+    const int units = p.Hkv * p.row_tiles;
+    const int b = d.x / units, unit = d.x - b * units, kvh = unit / p.row_tiles, rt = unit - kvh * p.row_tiles;
+    const size_t row_base = ((size_t)b * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq + rt * RT;
+    const int mine = (int)blockIdx.x - p0 - 1, n_rows = min(RT, p.rows - rt * RT);
+    if (mine >= n_rows) return;
+    const int rows = (n_rows - mine + n - 2) / (n - 1);  // rows mine, mine + (n - 1), ...
+    int groups = 1;
+    while (2 * groups * rows <= SLOTS && groups < n) groups *= 2;
     // part p0 may begin in an earlier unit; every later one begins in this one
     const int slot0 = 2 * p0 + (p0 * per >= first ? 0 : 1);
-    auto at = [&](int s) { return (size_t)(s == 0 ? slot0 : 2 * (p0 + s)) * RT + r; };
-    float M = -INFINITY;
-    for (int s = threadIdx.x; s < n; s += kCombineThreads) M = fmaxf(M, p.lse_part[at(s)]);
-#pragma unroll
-    for (int d = 16; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-    if ((threadIdx.x & 31) == 0) sm_max[threadIdx.x >> 5] = M;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kCombineThreads / 32; ++w) M = fmaxf(M, sm_max[w]);
-    const int group = threadIdx.x / LANES, lane = threadIdx.x % LANES;
-    float W = 0.f;
+    const int slot = threadIdx.x / LANES, lane = threadIdx.x % LANES, group = slot % groups;
+    const int r = mine + slot / groups * (n - 1);
+    float M = -INFINITY, W = 0.f;
     float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
-#pragma unroll 4
-        for (int s = group; s < n; s += GROUPS) {
-            const size_t i = at(s);
-            const float w = __expf(p.lse_part[i] - M);  // 0 for a part that saw no key
-            const float4 v = *reinterpret_cast<const float4 *>(p.o_part + i * D + 4 * lane);
-            W += w;
-            A.x = fmaf(w, v.x, A.x);
-            A.y = fmaf(w, v.y, A.y);
-            A.z = fmaf(w, v.z, A.z);
-            A.w = fmaf(w, v.w, A.w);
+    if (slot < groups * rows) {
+        for (int s0 = group; s0 < n; s0 += AHEAD * groups) {
+            float l[AHEAD];
+            float4 v[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const int s = s0 + k * groups;
+                const size_t at = (size_t)(s == 0 ? slot0 : 2 * (p0 + s)) * RT + r;
+                l[k] = -INFINITY;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (s < n) {
+                    l[k] = p.lse_part[at];
+                    v[k] = *reinterpret_cast<const float4 *>(p.o_part + at * D + 4 * lane);
+                }
+            }
+            float m = M;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) m = fmaxf(m, l[k]);
+            if (m == -INFINITY) continue;  // parts that saw no key
+            const float f = __expf(M - m);
+            W *= f;
+            A.x *= f, A.y *= f, A.z *= f, A.w *= f;
+            M = m;
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const float w = __expf(l[k] - m);
+                W += w;
+                A.x = fmaf(w, v[k].x, A.x);
+                A.y = fmaf(w, v[k].y, A.y);
+                A.z = fmaf(w, v[k].z, A.z);
+                A.w = fmaf(w, v[k].w, A.w);
+            }
+        }
+        sm_a[slot][lane] = A;
+        if (lane == 0) {
+            sm_m[slot] = M;
+            sm_w[slot] = W;
         }
     }
-    sm_a[group][lane] = A;
-    if (lane == 0) sm_w[group] = W;
     __syncthreads();
-    if (threadIdx.x >= D) return;
-    float sum = 0.f, den = 0.f;
-#pragma unroll
-    for (int i = 0; i < GROUPS; ++i) {
-        sum += reinterpret_cast<const float *>(sm_a[i])[threadIdx.x];
-        den += sm_w[i];
+    if (group != 0 || slot >= groups * rows) return;
+    for (int i = 1; i < groups; ++i) M = fmaxf(M, sm_m[slot + i]);
+    W = 0.f;
+    A = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (M != -INFINITY) {
+        for (int i = 0; i < groups; ++i) {
+            const float f = __expf(sm_m[slot + i] - M);
+            const float4 v = sm_a[slot + i][lane];
+            W += f * sm_w[slot + i];
+            A.x = fmaf(f, v.x, A.x);
+            A.y = fmaf(f, v.y, A.y);
+            A.z = fmaf(f, v.z, A.z);
+            A.w = fmaf(f, v.w, A.w);
+        }
     }
-    const size_t out_row = (size_t)blockIdx.x;  // rows are in the order of q
-    static_cast<T *>(p.out)[out_row * D + threadIdx.x] = from_float<T>(den > 0.f ? sum / den : 0.f);
-    if (threadIdx.x == 0) p.lse[out_row] = den > 0.f ? M + __logf(den) : -INFINITY;
+    const float inv = W > 0.f ? 1.0f / W : 0.f;
+    uint2 o;
+    o.x = pack16<T>(A.x * inv, A.y * inv);
+    o.y = pack16<T>(A.z * inv, A.w * inv);
+    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * lane) = o;
+    if (lane == 0) p.lse[row_base + r] = W > 0.f ? M + __logf(W) : -INFINITY;
 }
 
 int page_log2(int page) {
@@ -598,12 +694,20 @@ int page_log2(int page) {
     return s;
 }
 
-// Row tiles of the kernel: 8 query rows per MMA column tile, one tile or two.
-int rows_per_unit(int rows) { return rows <= 8 ? 8 : 16; }
+// Query rows that share a K/V head, in 8-row MMA tiles: as few units as the accumulators' registers allow (two
+// tiles at d = 128, four at d = 64), the tiles spread evenly over them.
+int tiles_per_unit(int rows, int d) {
+    const int most = d == 64 ? 4 : 2, n = (rows + 7) / 8;
+    const int units = (n + most - 1) / most;
+    return (n + units - 1) / units;
+}
+int units_per_head(int rows, int d) { return (rows + 8 * tiles_per_unit(rows, d) - 1) / (8 * tiles_per_unit(rows, d)); }
 
 template <typename T, int D, int FMT, int NT, bool CAUSAL>
 int launch_q8(const Kvq8AttnArgs &a) {
     using C = Q8Cfg<D, NT>;
+    auto kern = fa_kvq8_partial<T, D, FMT, NT, CAUSAL>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -5;
     Q8Params p;
     p.q = a.q;
     p.out = a.out;
@@ -616,32 +720,42 @@ int launch_q8(const Kvq8AttnArgs &a) {
     p.kv_lens = a.kv_lens;
     p.o_part = a.workspace;
     p.lse_part = a.workspace + (size_t)a.parts * 2 * C::RT * D;
+    p.shared = reinterpret_cast<int4 *>(a.workspace + (size_t)a.parts * 2 * C::RT * (D + 1));
     p.status = a.status;
     p.B = a.B;
     p.H = a.H;
     p.Hkv = a.c.Hkv;
     p.Nq = a.Nq;
     p.rows = a.H / a.c.Hkv * a.Nq;
-    p.row_tiles = (p.rows + C::RT - 1) / C::RT;
+    p.row_tiles = units_per_head(p.rows, D);
     p.n_pages = a.c.n_pages;
     p.max_pages = a.c.max_pages;
     p.page_shift = page_log2(a.c.page);
     p.max_len = a.max_len;
     p.parts = a.parts;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
-    fa_kvq8_partial<T, D, FMT, NT, CAUSAL><<<a.parts, kWarps * 32, 0, a.stream>>>(p);
+    // (not as a programmatic dependent: its CTAs would take their places beside those of the kernel ahead, and
+    // the one wave that the parts are sized for would become two)
+    kern<<<a.parts, kWarps * 32, C::SMEM, a.stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -5;
-    return launch_dependent(fa_kvq8_combine<T, D, C::RT>, dim3(a.B * a.H * a.Nq), dim3(kCombineThreads), 0,
+    if (a.parts == 1) return 0;
+    return launch_dependent(fa_kvq8_combine<T, D, C::RT>, dim3(a.parts), dim3(kCombineThreads), 0,
                             a.stream, p) == cudaSuccess
                ? 0
                : -5;
 }
 
+template <typename T, int D, int FMT, int NT>
+int launch_q8_causal(const Kvq8AttnArgs &a) {
+    return a.causal ? launch_q8<T, D, FMT, NT, true>(a) : launch_q8<T, D, FMT, NT, false>(a);
+}
 template <typename T, int D, int FMT>
 int launch_q8_rows(const Kvq8AttnArgs &a) {
-    const int rows = a.H / a.c.Hkv * a.Nq;
-    if (rows <= 8) return a.causal ? launch_q8<T, D, FMT, 1, true>(a) : launch_q8<T, D, FMT, 1, false>(a);
-    return a.causal ? launch_q8<T, D, FMT, 2, true>(a) : launch_q8<T, D, FMT, 2, false>(a);
+    const int nt = tiles_per_unit(a.H / a.c.Hkv * a.Nq, D);
+    if (nt == 1) return launch_q8_causal<T, D, FMT, 1>(a);
+    if (nt == 2) return launch_q8_causal<T, D, FMT, 2>(a);
+    if constexpr (D == 64) return nt == 3 ? launch_q8_causal<T, D, FMT, 3>(a) : launch_q8_causal<T, D, FMT, 4>(a);
+    return -4;
 }
 
 template <typename T>
@@ -654,20 +768,20 @@ int launch_q8_t(const Kvq8AttnArgs &a) {
 
 }  // namespace
 
-long long kvq8_tiles(int B, int Hkv, int rows, int max_len) {
-    const int rt = rows_per_unit(rows);
-    return (long long)B * Hkv * ((rows + rt - 1) / rt) * ((max_len + kTileKeys - 1) / kTileKeys);
+long long kvq8_tiles(int B, int Hkv, int rows, int max_len, int d) {
+    return (long long)B * Hkv * units_per_head(rows, d) * ((max_len + kTileKeys - 1) / kTileKeys);
 }
 
-int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int num_sms) {
+int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int d, int num_sms) {
     // one part for each CTA that can be resident, and at least one tile for each of a CTA's warps
-    const long long slots = (long long)(rows <= 8 ? Q8Cfg<128, 1>::CTAS : Q8Cfg<128, 2>::CTAS) * num_sms;
-    const long long by_len = (kvq8_tiles(B, Hkv, rows, max_len) + kWarps - 1) / kWarps;
+    const int nt = tiles_per_unit(rows, d);
+    const long long slots = (long long)q8_ctas(d, nt) * num_sms;
+    const long long by_len = (kvq8_tiles(B, Hkv, rows, max_len, d) + kWarps - 1) / kWarps;
     return (int)(by_len < slots ? by_len : slots);
 }
 
 size_t kvq8_workspace_bytes(int rows, int d, int parts) {
-    return (size_t)parts * 2 * rows_per_unit(rows) * (d + 1) * sizeof(float);
+    return (size_t)parts * (2 * 8 * tiles_per_unit(rows, d) * (d + 1) * sizeof(float) + sizeof(int4));
 }
 
 int launch_kvq8_attention(const Kvq8AttnArgs &a, bool fp16) {
