@@ -354,6 +354,37 @@ int fa_bwd_fp16(const void *q, const void *k, const void *v, const void *out, co
                 void *dq, void *dk, void *dv, int B, int H, int N, int d, float scale, int causal,
                 void *workspace, unsigned long long workspace_bytes, void *stream);
 
+/* ---- keys of another sequence (cross attention) -----------------------------
+ * The forward and its gradients for queries and keys of different lengths, as when a
+ * decoder attends to an encoder's states:
+ *   q, out, dout, dq : [B][H][Nq][d]      k, v, dk, dv : [B][Hkv][Nk][d]      lse : float [B][H][Nq]
+ * Hkv divides H; consecutive query heads share a K/V head as in fa_fwd_gqa, and dk, dv are summed
+ * over the heads that share one. No mask and not causal: every query of batch index b sees keys
+ * 0 .. kv_lens[b] - 1 (int32 [B] in DEVICE memory, 4-byte aligned; NULL: all Nk). What K and V hold
+ * past them does not matter, NaN and infinities included. kv_lens[b] = 0 gives out = 0, lse = -inf
+ * and gradients of 0, and dk, dv are 0 for the keys past kv_lens[b]. A length below 0 or above Nk
+ * counts as 0 and records FA_ERR_SEQLENS in the device status word. d in {64, 128}.
+ * Forward: with few query rows the keys of a head are cut into n_splits runs (1 <= n_splits <=
+ * ceil(Nk / 128); fa_cross_num_splits gives a count that fills the GPU), whose summaries go
+ * through the workspace and are merged as in fa_fwd_splitkv: 256-byte aligned, at least
+ * fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits) bytes; it may be NULL when n_splits is 1.
+ * Backward: out and lse are the forward's; the workspace is fa_bwd_workspace_bytes(B, H, Nq, d)
+ * bytes, as for fa_bwd; dq is accumulated in fp32 in an order that varies from call to call.
+ * Calls that share a workspace must not overlap on the GPU. Errors as for fa_fwd_gqa and fa_bwd. */
+int fa_cross_num_splits(int B, int H, int Nq, int Nk);
+int fa_fwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, void *out, float *lse, int B,
+                 int H, int Hkv, int Nq, int Nk, int d, float scale, int n_splits, void *workspace,
+                 unsigned long long workspace_bytes, void *stream);
+int fa_fwd_cross_fp16(const void *q, const void *k, const void *v, const int *kv_lens_or_null, void *out, float *lse,
+                      int B, int H, int Hkv, int Nq, int Nk, int d, float scale, int n_splits, void *workspace,
+                      unsigned long long workspace_bytes, void *stream);
+int fa_bwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, const void *out,
+                 const void *dout, const float *lse, void *dq, void *dk, void *dv, int B, int H, int Hkv, int Nq, int Nk,
+                 int d, float scale, void *workspace, unsigned long long workspace_bytes, void *stream);
+int fa_bwd_cross_fp16(const void *q, const void *k, const void *v, const int *kv_lens_or_null, const void *out,
+                      const void *dout, const float *lse, void *dq, void *dk, void *dv, int B, int H, int Hkv, int Nq,
+                      int Nk, int d, float scale, void *workspace, unsigned long long workspace_bytes, void *stream);
+
 /* Static text for a status code (never NULL). */
 const char *fa_status_string(int status);
 

@@ -506,6 +506,75 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     return fa::launch_kvq8_attention(a, fp16);
 }
 
+// Splits of each work unit's keys for the forward over keys of another length: with fewer units (256 query rows of a
+// head) than half the SMs, as many as fill the GPU once, each of at least two 128-key blocks (a split costs a launch and
+// about 3 us of start and merge, a block 0.5 us).
+int cross_num_splits(int B, int H, int Nq, int Nk, int num_sms) {
+    const int64_t units = static_cast<int64_t>(B) * H * ((static_cast<int64_t>(Nq) + 255) / 256);
+    const int64_t blocks = (static_cast<int64_t>(Nk) + 127) / 128;
+    int64_t n = num_sms / units;
+    if (n > blocks / 2) n = blocks / 2;
+    return n < 1 ? 1 : static_cast<int>(n);
+}
+
+int check_cross(const void *q, const void *k, const void *v, const int *kv_lens, const void *out, const float *lse,
+                int B, int H, int Hkv, int Nq, int Nk, int d) {
+    int rc = check_args(Type::BF16, q, k, v, nullptr, out, lse, B, H, Nq, d);
+    if (rc != FA_OK) return rc;
+    if (kv_lens && !aligned(kv_lens, 4)) return FA_ERR_ALIGN;
+    if (Hkv < 1 || H % Hkv != 0 || Nk < 1) return FA_ERR_SHAPE;
+    if (static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Nk) + 127) / 128) > INT32_MAX) return FA_ERR_SHAPE;
+    return FA_OK;
+}
+
+int cross_common(Type ty, const void *q, const void *k, const void *v, const int *kv_lens, void *out, float *lse,
+                 int B, int H, int Hkv, int Nq, int Nk, int d, float scale, int n_splits, void *workspace,
+                 unsigned long long workspace_bytes, void *stream) {
+    int rc = check_cross(q, k, v, kv_lens, out, lse, B, H, Hkv, Nq, Nk, d);
+    if (rc != FA_OK) return rc;
+    if (n_splits < 1 || n_splits > (static_cast<int64_t>(Nk) + 127) / 128) return FA_ERR_SHAPE;
+    const int64_t rows = static_cast<int64_t>(B) * H * Nq;
+    if (n_splits > 1) {
+        if (rows > INT32_MAX) return FA_ERR_SHAPE;  // one merge CTA per row
+        if (!workspace || !aligned(workspace, 256) || workspace_bytes < fa::splitkv_workspace_bytes(rows, d, n_splits))
+            return FA_ERR_WORKSPACE;
+    }
+    log_call("forward over keys of another length %s d=%d B=%d H=%d Hkv=%d Nq=%d Nk=%d lens=%s splits=%d",
+             ty == Type::BF16 ? "bf16" : "fp16", d, B, H, Hkv, Nq, Nk, kv_lens ? "given" : "all", n_splits);
+    DeviceInfo *di = device_info();
+    if (!di || !encoder()) return FA_ERR_LAUNCH;
+    fa::LaunchArgs a;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.mask = nullptr;
+    a.out = out;
+    a.lse = lse;
+    a.B = B;
+    a.H = H;
+    a.N = Nq;
+    a.d = d;
+    a.Hkv = Hkv;
+    a.scale = scale;
+    a.causal = 0;
+    a.stream = static_cast<cudaStream_t>(stream);
+    a.status = di->status;
+    a.num_sms = di->num_sms;
+    a.timeout_ns = kDefaultTimeoutNs;
+    a.Nk = Nk;
+    a.kv_lens = kv_lens;
+    a.n_splits = n_splits;
+    if (n_splits > 1) {
+        const size_t o_bytes = ((static_cast<size_t>(n_splits) * rows * d * sizeof(float) + 255) / 256) * 256;
+        a.o_part = static_cast<float *>(workspace);
+        a.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) + o_bytes);
+    }
+    rc = ty == Type::BF16 ? fa::launch_fwd_cross_bf16(a) : fa::launch_fwd_cross_fp16(a);
+    if (rc != 0 || n_splits == 1) return rc;
+    return fa::launch_splitkv_merge(a.o_part, a.lse_part, out, lse, static_cast<int>(rows), d, n_splits,
+                                    ty == Type::FP16, a.stream);
+}
+
 int varlen_common(bool fp16, const void *q, const void *k, const void *v, void *out, float *lse,
                   const int *cu_seqlens, int nseq, int total, int max_seqlen, int H, int Hkv, int d, float scale,
                   int causal, void *stream) {
@@ -547,7 +616,8 @@ int varlen_common(bool fp16, const void *q, const void *k, const void *v, void *
 
 int bwd_common(bool fp16, const void *q, const void *k, const void *v, const void *out, const void *dout,
                const float *lse, void *dq, void *dk, void *dv, int B, int H, int N, int d, float scale, int causal,
-               void *workspace, unsigned long long workspace_bytes, void *stream) {
+               void *workspace, unsigned long long workspace_bytes, void *stream, bool cross = false, int Hkv = 0,
+               int Nk = 0, const int *kv_lens = nullptr) {
     if (!q || !k || !v || !out || !dout || !lse || !dq || !dk || !dv) return FA_ERR_NULL;
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(dout, 16) ||
         !aligned(dq, 16) || !aligned(dk, 16) || !aligned(dv, 16) || !aligned(lse, 4))
@@ -558,6 +628,10 @@ int bwd_common(bool fp16, const void *q, const void *k, const void *v, const voi
     const int64_t npad = fa::bwd_padded_rows(N);
     if (bh * (npad / fa::kBwdRows) > INT32_MAX) return FA_ERR_SHAPE;  // one CTA per (head, 128-key block)
     if (bh * npad > (int64_t(1) << 36)) return FA_ERR_SHAPE;           // row-statistics grid
+    if (cross) {
+        const int rc = check_cross(q, k, v, kv_lens, out, lse, B, H, Hkv, N, Nk, d);
+        if (rc != FA_OK) return rc;
+    }
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     const size_t need = fa::bwd_workspace_bytes(bh, N, d);
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FA_ERR_WORKSPACE;
@@ -588,6 +662,14 @@ int bwd_common(bool fp16, const void *q, const void *k, const void *v, const voi
     a.stream = static_cast<cudaStream_t>(stream);
     a.status = di->status;
     a.timeout_ns = kDefaultTimeoutNs;
+    if (cross) {
+        a.Hkv = Hkv;
+        a.Nk = Nk;
+        a.kv_lens = kv_lens;
+        log_call("backward over keys of another length %s d=%d B=%d H=%d Hkv=%d Nq=%d Nk=%d lens=%s", fp16 ? "fp16" : "bf16",
+                 d, B, H, Hkv, N, Nk, kv_lens ? "given" : "all");
+        return fa::launch_bwd_cross(a, fp16);
+    }
     log_call("backward %s d=%d (%s kernel) causal=%d B=%d H=%d N=%d", fp16 ? "fp16" : "bf16", d,
              d == 64 ? "half-block" : "serial", a.causal, B, H, N);
     return fa::launch_bwd(a, fp16);
@@ -860,6 +942,40 @@ int fa_bwd_fp16(const void *q, const void *k, const void *v, const void *out, co
                 unsigned long long workspace_bytes, void *stream) {
     return bwd_common(true, q, k, v, out, dout, lse, dq, dk, dv, B, H, N, d, scale, causal, workspace,
                       workspace_bytes, stream);
+}
+
+int fa_cross_num_splits(int B, int H, int Nq, int Nk) {
+    if (B < 1 || H < 1 || Nq < 1 || Nk < 1) return FA_ERR_SHAPE;
+    DeviceInfo *di = device_info();
+    return cross_num_splits(B, H, Nq, Nk, di ? di->num_sms : 148);
+}
+
+int fa_fwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, void *out, float *lse, int B,
+                 int H, int Hkv, int Nq, int Nk, int d, float scale, int n_splits, void *workspace,
+                 unsigned long long workspace_bytes, void *stream) {
+    return cross_common(Type::BF16, q, k, v, kv_lens_or_null, out, lse, B, H, Hkv, Nq, Nk, d, scale, n_splits,
+                        workspace, workspace_bytes, stream);
+}
+
+int fa_fwd_cross_fp16(const void *q, const void *k, const void *v, const int *kv_lens_or_null, void *out, float *lse,
+                      int B, int H, int Hkv, int Nq, int Nk, int d, float scale, int n_splits, void *workspace,
+                      unsigned long long workspace_bytes, void *stream) {
+    return cross_common(Type::FP16, q, k, v, kv_lens_or_null, out, lse, B, H, Hkv, Nq, Nk, d, scale, n_splits,
+                        workspace, workspace_bytes, stream);
+}
+
+int fa_bwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, const void *out,
+                 const void *dout, const float *lse, void *dq, void *dk, void *dv, int B, int H, int Hkv, int Nq, int Nk,
+                 int d, float scale, void *workspace, unsigned long long workspace_bytes, void *stream) {
+    return bwd_common(false, q, k, v, out, dout, lse, dq, dk, dv, B, H, Nq, d, scale, 0, workspace, workspace_bytes,
+                      stream, true, Hkv, Nk, kv_lens_or_null);
+}
+
+int fa_bwd_cross_fp16(const void *q, const void *k, const void *v, const int *kv_lens_or_null, const void *out,
+                      const void *dout, const float *lse, void *dq, void *dk, void *dv, int B, int H, int Hkv, int Nq,
+                      int Nk, int d, float scale, void *workspace, unsigned long long workspace_bytes, void *stream) {
+    return bwd_common(true, q, k, v, out, dout, lse, dq, dk, dv, B, H, Nq, d, scale, 0, workspace, workspace_bytes,
+                      stream, true, Hkv, Nk, kv_lens_or_null);
 }
 
 int fa_selftest_wait_timeout(unsigned long long timeout_ns, void *stream) {

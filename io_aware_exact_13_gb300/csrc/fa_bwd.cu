@@ -97,7 +97,53 @@ struct BwdParams {
     int BH, N, Npad;
     float scale, scale_log2;
     uint64_t timeout_ns;
+    // CROSS: N, Npad and the statistics are the queries'; K and V have Nk rows for each of the B * Hkv heads (BH above),
+    // of which batch index b uses the first kv_lens[b] (nullptr: all), and `group` query heads share one
+    const int *kv_lens;
+    int Nk, Hkv, group;
 };
+
+// CROSS (keys of another sequence, heads shared by `group` query heads): the CTA of a key block visits the query blocks
+// of every head that shares its keys, head by head, so dK and dV of shared heads are summed in the same accumulators.
+// Iteration it is query block it % n_qblk of head it / n_qblk of the group, and the row statistics of the group's heads
+// follow each other, so theirs is simply block it.
+struct CrossBlock {
+    int len, row;   // keys of the batch index; first key row of the block
+    bool none;      // the block lies past them
+};
+__device__ __forceinline__ CrossBlock cross_block(const BwdParams &p, int bh, int j) {
+    CrossBlock c;
+    c.len = p.Nk;
+    if (p.kv_lens != nullptr) {
+        c.len = __ldg(p.kv_lens + bh / p.Hkv);
+        if (c.len < 0 || c.len > p.Nk) {
+            if (threadIdx.x == 0) atomicExch(p.status, -8);  // FA_ERR_SEQLENS: counts as 0
+            c.len = 0;
+        }
+    }
+    c.row = j * kBlk;
+    c.none = c.row >= c.len;
+    return c;
+}
+// dK and dV of a key block that no query sees.
+template <typename T, int D>
+__device__ __forceinline__ void zero_block(const BwdParams &p, int bh, int row) {
+    const int rows = min(kBlk, p.Nk - row);
+    const size_t at = ((size_t)bh * p.Nk + (size_t)row) * D;
+    for (int i = threadIdx.x; i < rows * D / 8; i += kBwdThreads) {
+        st_global_v4(reinterpret_cast<T *>(p.dk) + at + 8 * i, 0u, 0u, 0u, 0u);
+        st_global_v4(reinterpret_cast<T *>(p.dv) + at + 8 * i, 0u, 0u, 0u, 0u);
+    }
+}
+// Rows [first, 128) of a 128-row tile of NCH swizzle chunks set to zero by one warp: K and V rows past a sequence's
+// keys may hold anything, and 0 times NaN would reach dQ. Every issuing warp does it before its own products; they
+// write the same zeros, so a product of one may overlap the other's writes.
+template <int NCH, int CHUNK>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane) {
+    for (int u = first * 8 + lane; u < 128 * 8; u += 32)
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) st_shared_v4(tile + c * CHUNK + u * 16, 0u, 0u, 0u, 0u);
+}
 
 __device__ __forceinline__ bool bwd_wait(uint32_t bar, uint32_t parity, const BwdParams &p) {
     if (mbar_try_wait(bar, parity)) return true;
@@ -195,7 +241,7 @@ __device__ __forceinline__ void stage_and_reduce_dq(const CUtensorMap *tm_dq, ui
     }
 }
 
-template <typename T, int D, bool CAUSAL>
+template <typename T, int D, bool CAUSAL, bool CROSS = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -226,8 +272,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int j = blockIdx.x / p.BH;
     const int n_qblk = p.Npad / kBlk;
     const int i0 = CAUSAL ? j : 0;  // first query block that sees key block j
-    const int n_it = n_qblk - i0;   // >= 1
+    const int n_it = CROSS ? n_qblk * p.group : n_qblk - i0;  // >= 1
     grid_launch_dependents();       // fa_bwd_post may be scheduled once every CTA has started
+    int n_keys = p.N;               // keys of the sequence
+    if constexpr (CROSS) {
+        const CrossBlock cb = cross_block(p, bh, j);
+        n_keys = cb.len;
+        if (cb.none) {  // (fa_bwd_post must not start before fa_bwd_pre is done, so wait for it here too)
+            zero_block<T, D>(p, bh, cb.row);
+            grid_dependency_wait();
+            return;
+        }
+    }
+    const int qh0 = CROSS ? bh * p.group : bh;  // first query head of the group
 
     if (threadIdx.x == 0) {
         mbar_init(bar_kv, 1);
@@ -269,16 +326,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int it = 0; it < n_it; ++it) {
                 const int s = it % ST;
                 const uint32_t dst = smem_u32(smem + C::SMEM_QD + s * 2 * C::TILE);
-                const int row0 = (i0 + it) * kBlk;
+                const int row0 = (CROSS ? it % n_qblk : i0 + it) * kBlk;
+                const int qh = CROSS ? qh0 + it / n_qblk : bh;
                 if (!bwd_wait(bar_q_empty(s), ((it / ST) & 1u) ^ 1u, p)) break;
                 mbar_arrive_expect_tx(bar_q_full(s), C::TILE);
-                for (int c = 0; c < C::NCH; ++c) tma_load_3d(dst + c * C::CHUNK, &tm_q, bar_q_full(s), c * 64, row0, bh, pol);
+                for (int c = 0; c < C::NCH; ++c) tma_load_3d(dst + c * C::CHUNK, &tm_q, bar_q_full(s), c * 64, row0, qh, pol);
                 issued_q = it + 1;
                 // dO's half also held the dQ tiles of the stage's last block until they were read
                 if (!bwd_wait(bar_do_empty(s), ((it / ST) & 1u) ^ 1u, p)) break;
                 mbar_arrive_expect_tx(bar_do_full(s), C::TILE);
                 for (int c = 0; c < C::NCH; ++c)
-                    tma_load_3d(dst + C::TILE + c * C::CHUNK, &tm_do, bar_do_full(s), c * 64, row0, bh, pol);
+                    tma_load_3d(dst + C::TILE + c * C::CHUNK, &tm_do, bar_do_full(s), c * 64, row0, qh, pol);
                 issued_do = it + 1;
             }
             // Before the CTA may exit, every copy into its shared memory must have
@@ -303,6 +361,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint64_t k_mn = smem_desc_sw128(smem_u32(smem + C::SMEM_K), C::CHUNK, 1024);   // K_j as B, N-major
         const uint64_t ds_mn = smem_desc_sw128(smem_u32(smem + C::SMEM_DS), C::CHUNK, 1024); // dS as A, M-major
         bool ok = bwd_wait_warp(bar_kv, 0, p);
+        if (CROSS && ok && (j + 1) * kBlk > n_keys && n_keys < p.Nk) {
+            zero_rows<C::NCH, C::CHUNK>(smem_u32(smem + C::SMEM_K), n_keys - j * kBlk, lane);
+            zero_rows<C::NCH, C::CHUNK>(smem_u32(smem + C::SMEM_V), n_keys - j * kBlk, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
         for (int it = 0; ok && it < n_it; ++it) {
             const int s = it % ST;
             ok = bwd_wait_warp(bar_q_full(s), (it / ST) & 1u, p) && bwd_wait_warp(bar_do_full(s), (it / ST) & 1u, p);
@@ -351,20 +415,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const int r = w * 32 + lane;               // TMEM lane: key r of block j, later query row r of block i
         const uint32_t lane_base = (uint32_t)(w * 32) << 16;
         const int key = j * kBlk + r;
-        const bool key_ok = key < p.N;
+        const bool key_ok = key < n_keys;
         const uint32_t ds_base = smem_u32(smem + C::SMEM_DS);
         const uint32_t stats = smem_u32(smem + C::SMEM_STATS);
         // this warp's 4 KB of the dS buffer (its 32 key rows of chunk g), reused to stage dQ tiles
         const uint32_t stage = ds_base + g * C::CHUNK + w * 4096;
         // one statistic per thread: -lse2 (group 0) or -D (group 1) of query row r of the block
-        const float *stat_src = (g == 0 ? p.lse2 : p.dsum) + (size_t)bh * p.Npad + r;
+        const float *stat_src = (g == 0 ? p.lse2 : p.dsum) + (size_t)qh0 * p.Npad + r;
         grid_dependency_wait();  // statistics and the zeroed dQ accumulator are written by fa_bwd_pre
         float stat_next = -__ldg(stat_src + i0 * kBlk);
-        const bool ragged_keys = (j + 1) * kBlk > p.N;
+        const bool ragged_keys = (j + 1) * kBlk > n_keys;
         bool ok = true;
         for (int it = 0; ok && it < n_it; ++it) {
             const int i = i0 + it;
-            const int row0 = i * kBlk;
+            const int row0 = (CROSS ? it % n_qblk : i) * kBlk;
+            const int qh = CROSS ? qh0 + it / n_qblk : bh;
             // hand over the block's statistics (their last readers passed p_full of the previous block)
             st_shared_f32(stats + (g * 128 + r) * 4, stat_next);
             mbar_arrive(bar_stats);
@@ -442,7 +507,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) {
-                    tma_reduce_add_3d(&tm_dq, box, g * COLS + 32 * t, row0 + w * 32, bh);
+                    tma_reduce_add_3d(&tm_dq, box, g * COLS + 32 * t, row0 + w * 32, qh);
                     bulk_commit_group();
                 }
             }
@@ -453,13 +518,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (ok) {
             tc_fence_after();
             const float mul = g == 0 ? 1.0f : p.scale;
-            T *dst = reinterpret_cast<T *>(g == 0 ? p.dv : p.dk) + ((size_t)bh * p.N + (size_t)(key_ok ? key : 0)) * D;
+            const int k_rows = CROSS ? p.Nk : p.N;  // rows past the sequence's keys get their zeros
+            const bool store = key < k_rows;
+            T *dst = reinterpret_cast<T *>(g == 0 ? p.dv : p.dk) + ((size_t)bh * k_rows + (size_t)(store ? key : 0)) * D;
             const uint32_t src_col = 256u + (uint32_t)(g * D);
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 64) {
                 uint32_t a[32], b[32];
                 tmem_ld32x2_wait(tmem + lane_base + src_col + c0, a, tmem + lane_base + src_col + c0 + 32, b);
-                if (key_ok) {
+                if (store) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
                         st_global_v4(dst + c0 + c, pk2<T>(__uint_as_float(a[c]) * mul, __uint_as_float(a[c + 1]) * mul),
@@ -530,7 +597,7 @@ struct BwdCfgH64 {
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-template <typename T, bool CAUSAL>
+template <typename T, bool CAUSAL, bool CROSS = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel_h64(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -557,8 +624,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int j = blockIdx.x / p.BH;
     const int n_qblk = p.Npad / kBlk;
     const int i0 = CAUSAL ? j : 0;
-    const int n_it = n_qblk - i0;  // >= 1
+    const int n_it = CROSS ? n_qblk * p.group : n_qblk - i0;  // >= 1
     grid_launch_dependents();      // fa_bwd_post may be scheduled once every CTA has started
+    int n_keys = p.N;              // keys of the sequence
+    if constexpr (CROSS) {
+        const CrossBlock cb = cross_block(p, bh, j);
+        n_keys = cb.len;
+        if (cb.none) {  // (as in fa_bwd_kernel)
+            zero_block<T, 64>(p, bh, cb.row);
+            grid_dependency_wait();
+            return;
+        }
+    }
+    const int qh0 = CROSS ? bh * p.group : bh;  // first query head of the group
 
     if (threadIdx.x == 0) {
         mbar_init(bar_kv, 1);
@@ -600,9 +678,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (!bwd_wait(bar_qd_empty(s), ((it / ST) & 1u) ^ 1u, p)) break;
                 const uint32_t dst = smem_u32(smem + C::SMEM_QD + s * 2 * C::CHUNK);
                 mbar_arrive_expect_tx(bar_qd_full(s), 2 * C::CHUNK);
-                const int row0 = (i0 + it) * kBlk;
-                tma_load_3d(dst, &tm_q, bar_qd_full(s), 0, row0, bh, pol);
-                tma_load_3d(dst + C::CHUNK, &tm_do, bar_qd_full(s), 0, row0, bh, pol);
+                const int row0 = (CROSS ? it % n_qblk : i0 + it) * kBlk;
+                const int qh = CROSS ? qh0 + it / n_qblk : bh;
+                tma_load_3d(dst, &tm_q, bar_qd_full(s), 0, row0, qh, pol);
+                tma_load_3d(dst + C::CHUNK, &tm_do, bar_qd_full(s), 0, row0, qh, pol);
                 issued = it + 1;
             }
             bwd_wait(bar_kv, 0, p);  // every copy into this CTA's shared memory lands before exit
@@ -623,6 +702,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint64_t v_km = smem_desc_sw128(smem_u32(smem + C::SMEM_V), 16, 1024);
         const uint64_t k_mn = smem_desc_sw128(smem_u32(smem + C::SMEM_K), C::CHUNK, 1024);
         bool ok = bwd_wait_warp(bar_kv, 0, p);
+        if (CROSS && ok && (j + 1) * kBlk > n_keys && n_keys < p.Nk) {
+            zero_rows<1, C::CHUNK>(smem_u32(smem + C::SMEM_K), n_keys - j * kBlk, lane);
+            zero_rows<1, C::CHUNK>(smem_u32(smem + C::SMEM_V), n_keys - j * kBlk, lane);
+            fence_proxy_async_smem();
+            __syncwarp();
+        }
         if (warp == 1) {
             // S_h^T = K_j Q_h^T, dP_h^T = V_j dO_h^T of block it (query rows 64h.. of the stage = +8 KB)
             auto issue_s = [&](int it, int h) {
@@ -715,15 +800,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t lane_base = (uint32_t)(w * 32) << 16;
         const uint32_t s_col = tmem + lane_base + 128u * g;  // S_g; dP_g at +64
         const int key = j * kBlk + r;
-        const bool key_ok = key < p.N;
-        const bool ragged_keys = (j + 1) * kBlk > p.N;
+        const bool key_ok = key < n_keys;
+        const bool ragged_keys = (j + 1) * kBlk > n_keys;
         const uint32_t ds_row0 = smem_u32(smem + C::SMEM_DS) + g * C::CHUNK + r * 128;  // + (block & 1) * 32 KB
         // dQ of block b is staged in this warp's own 32 rows of b's dS buffer: dK(b) and dQ(b) have read it by
         // the time dQ(b) is read out, and this warp writes those rows again only in the pass of block b + 2
         const uint32_t box0 = smem_u32(smem + C::SMEM_DS) + g * C::CHUNK + w * 4096;  // + (block & 1) * 32 KB
         const uint32_t stats0 = smem_u32(smem + C::SMEM_STATS) + g * 1024;  // + buffer * 512
         // thread r hands over -lse2 (r < 64) or -D (r >= 64) of query row 64g + (r & 63)
-        const float *stat_src = (r < 64 ? p.lse2 : p.dsum) + (size_t)bh * p.Npad + 64 * g + (r & 63);
+        const float *stat_src = (r < 64 ? p.lse2 : p.dsum) + (size_t)qh0 * p.Npad + 64 * g + (r & 63);
         grid_dependency_wait();  // statistics and the zeroed dQ accumulator are written by fa_bwd_pre
         float stat_next = -__ldg(stat_src + i0 * kBlk);
         bool ok = true;
@@ -735,7 +820,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_fence_before();
             mbar_arrive(bar_dq_free);
             const uint32_t box = box0 + ((blk - i0) & 1) * 2 * C::CHUNK;
-            stage_and_reduce_dq(&tm_dq, box, qv, p.scale, lane, 32 * g, blk * kBlk + w * 32, bh);
+            stage_and_reduce_dq(&tm_dq, box, qv, p.scale, lane, 32 * g, (CROSS ? blk % n_qblk : blk) * kBlk + w * 32,
+                                CROSS ? qh0 + blk / n_qblk : bh);
             return true;
         };
         for (int it = 0; ok && it < n_it; ++it) {
@@ -787,10 +873,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (ok) {  // the last dq_full covers every dV and dK product
             tc_fence_after();
             const float mul = g == 0 ? 1.0f : p.scale;
-            T *dst = reinterpret_cast<T *>(g == 0 ? p.dv : p.dk) + ((size_t)bh * p.N + (size_t)(key_ok ? key : 0)) * 64;
+            const int k_rows = CROSS ? p.Nk : p.N;  // rows past the sequence's keys get their zeros
+            const bool store = key < k_rows;
+            T *dst = reinterpret_cast<T *>(g == 0 ? p.dv : p.dk) + ((size_t)bh * k_rows + (size_t)(store ? key : 0)) * 64;
             uint32_t a[32], b[32];
             tmem_ld32x2_wait(tmem + lane_base + 320 + 64 * g, a, tmem + lane_base + 320 + 64 * g + 32, b);
-            if (key_ok) {
+            if (store) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 8) {
                     st_global_v4(dst + c, pk2<T>(__uint_as_float(a[c]) * mul, __uint_as_float(a[c + 1]) * mul),
@@ -873,12 +961,12 @@ __global__ void __launch_bounds__(256) fa_bwd_post(const float *__restrict__ dq_
     reinterpret_cast<uint2 *>(dq)[i] = o;
 }
 
-template <typename T, int D, bool CAUSAL>
+template <typename T, int D, bool CAUSAL, bool CROSS = false>
 int launch_bwd_variant(const BwdArgs &a) {
     // d = 64 runs the overlapped half-block kernel; d = 128 (tensor memory full) the serial one
     auto kern = [] {
-        if constexpr (D == 64) return fa_bwd_kernel_h64<T, CAUSAL>;
-        else return fa_bwd_kernel<T, D, CAUSAL>;
+        if constexpr (D == 64) return fa_bwd_kernel_h64<T, CAUSAL, CROSS>;
+        else return fa_bwd_kernel<T, D, CAUSAL, CROSS>;
     }();
     constexpr int smem_bytes = D == 64 ? BwdCfgH64<T>::SMEM_BYTES : BwdCfg<T, D>::SMEM_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess)
@@ -893,8 +981,9 @@ int launch_bwd_variant(const BwdArgs &a) {
     if (cudaGetLastError() != cudaSuccess) return -5;
     CUtensorMap tq, tk, tv, tdo;
     if (!encode_rows_map(&tq, Elem<T>::tma, 2, a.q, D, a.N, BH, kBlk)) return -5;
-    if (!encode_rows_map(&tk, Elem<T>::tma, 2, a.k, D, a.N, BH, kBlk)) return -5;
-    if (!encode_rows_map(&tv, Elem<T>::tma, 2, a.v, D, a.N, BH, kBlk)) return -5;
+    const int BHkv = CROSS ? a.B * a.Hkv : BH, Nk = CROSS ? a.Nk : a.N;
+    if (!encode_rows_map(&tk, Elem<T>::tma, 2, a.k, D, Nk, BHkv, kBlk)) return -5;
+    if (!encode_rows_map(&tv, Elem<T>::tma, 2, a.v, D, Nk, BHkv, kBlk)) return -5;
     if (!encode_rows_map(&tdo, Elem<T>::tma, 2, a.dout, D, a.N, BH, kBlk)) return -5;
     CUtensorMap tdq;  // fp32 dQ accumulator, 32 x 32 boxes (128-byte rows), reduced into
     if (!encode_rows_map(&tdq, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, a.dq_acc, D, a.N, BH, 32)) return -5;
@@ -905,13 +994,17 @@ int launch_bwd_variant(const BwdArgs &a) {
     p.dk = a.dk;
     p.dv = a.dv;
     p.status = a.status;
-    p.BH = BH;
+    p.BH = BHkv;
+    p.kv_lens = CROSS ? a.kv_lens : nullptr;
+    p.Nk = Nk;
+    p.Hkv = CROSS ? a.Hkv : a.H;
+    p.group = CROSS ? a.H / a.Hkv : 1;
     p.N = a.N;
     p.Npad = Npad;
     p.scale = a.scale;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
-    const int64_t grid = static_cast<int64_t>(BH) * (Npad / kBlk);
+    const int64_t grid = static_cast<int64_t>(BHkv) * (bwd_padded_rows(Nk) / kBlk);
     // programmatic dependents: the backward's copies of K, V, Q, dO start while fa_bwd_pre drains (its
     // gradient warps wait for the statistics), and fa_bwd_post's launch overlaps the backward's tail
     if (launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), smem_bytes, a.stream, tq, tk,
@@ -925,6 +1018,13 @@ int launch_bwd_variant(const BwdArgs &a) {
 }
 
 template <typename T>
+int launch_bwd_cross_t(const BwdArgs &a) {
+    if (a.d == 128) return launch_bwd_variant<T, 128, false, true>(a);
+    if (a.d == 64) return launch_bwd_variant<T, 64, false, true>(a);
+    return -4;
+}
+
+template <typename T>
 int launch_bwd_t(const BwdArgs &a) {
     if (a.d == 128) return a.causal ? launch_bwd_variant<T, 128, true>(a) : launch_bwd_variant<T, 128, false>(a);
     if (a.d == 64) return a.causal ? launch_bwd_variant<T, 64, true>(a) : launch_bwd_variant<T, 64, false>(a);
@@ -932,6 +1032,10 @@ int launch_bwd_t(const BwdArgs &a) {
 }
 
 }  // namespace
+
+int launch_bwd_cross(const BwdArgs &a, bool fp16) {
+    return fp16 ? launch_bwd_cross_t<__half>(a) : launch_bwd_cross_t<__nv_bfloat16>(a);
+}
 
 int launch_bwd(const BwdArgs &a, bool fp16) { return fp16 ? launch_bwd_t<__half>(a) : launch_bwd_t<__nv_bfloat16>(a); }
 

@@ -20,6 +20,9 @@ struct BwdArgs {
     cudaStream_t stream;
     int *status;
     uint64_t timeout_ns;
+    // keys of another sequence (launch_bwd_cross): k, v, dk, dv [B][Hkv][Nk][d], N query rows
+    int Hkv = 0, Nk = 0;
+    const int *kv_lens = nullptr;  // [B] keys in use, or nullptr (Nk)
 };
 
 inline int64_t bwd_padded_rows(int N) { return ((static_cast<int64_t>(N) + kBwdRows - 1) / kBwdRows) * kBwdRows; }
@@ -33,5 +36,6 @@ inline size_t bwd_workspace_bytes(int64_t BH, int N, int d) {
 }
 
 int launch_bwd(const BwdArgs &a, bool fp16);
+int launch_bwd_cross(const BwdArgs &a, bool fp16);
 
 }  // namespace fa

@@ -160,6 +160,47 @@ __device__ __forceinline__ void philox4x64_10(uint64_t c0, uint64_t c1, uint64_t
     w[4] = (uint32_t)c2, w[5] = (uint32_t)(c2 >> 32), w[6] = (uint32_t)c3, w[7] = (uint32_t)(c3 >> 32);
 }
 
+// CROSS: the keys of a work unit. Units are numbered (unit of the plain schedule) * n_splits + run; the unit's keys
+// [first, first + n) are blocks [run nb / n_splits, (run + 1) nb / n_splits) of its nb blocks.
+struct CrossRun {
+    int run, first, n;
+};
+__device__ __forceinline__ CrossRun cross_run(const FwdParams &p, int bh, int run) {
+    const int b = bh / p.H;
+    int len = p.Nk;
+    if (p.kv_lens != nullptr) {
+        len = __ldg(p.kv_lens + b);
+        if (len < 0 || len > p.Nk) len = 0;  // reported by the softmax warps
+    }
+    const int nb = (len + kBK128 - 1) / kBK128;
+    const int b0 = (int)((long long)run * nb / p.n_splits), b1 = (int)((long long)(run + 1) * nb / p.n_splits);
+    CrossRun r;
+    r.run = run;
+    r.first = b0 * kBK128;
+    r.n = min(len, b1 * kBK128) - r.first;
+    return r;
+}
+// The work list of the dense kernels: plain, or (CROSS) each unit n_splits times with its run of keys.
+template <bool VARLEN, bool CROSS>
+struct Items128 : ItemIter<VARLEN> {
+    using ItemIter<VARLEN>::ItemIter;
+    CrossRun keys = {0, 0, 0};
+    int unit = 0;
+    __device__ __forceinline__ bool next_item(const FwdParams &p, Item &it, bool &ok) {
+        if constexpr (!CROSS) {
+            return this->next(p, it, ok);
+        } else {
+            const long long u = (long long)unit++ * gridDim.x + blockIdx.x;
+            if (u >= (long long)p.n_items * p.n_splits) return false;
+            const int item = (int)(u / p.n_splits);
+            it = get_item(p, item);
+            keys = cross_run(p, it.bh, (int)(u - (long long)item * p.n_splits));
+            it.n = keys.n;
+            return true;
+        }
+    }
+};
+
 // MASK: an additive [B][N][N] mask whose entries are all 0 or -inf, in its packed form
 // (p.mask_bits, one bit per entry, set = -inf; see fa_mask_pack.cu). Thread r reads the 16
 // bytes of its row and key block from global memory (L2: the packed mask of a batch index is
@@ -168,12 +209,19 @@ __device__ __forceinline__ void philox4x64_10(uint64_t c0, uint64_t c1, uint64_t
 // names the variant). The softmax keeps the row maximum and sum of the undropped scores (lse
 // is unchanged); P is stored with dropped keys set to 0, and the epilogue multiplies O by
 // 1 / q. The keep bytes of a 32-key group come from one Philox block (see FwdParams).
-template <typename T, int D, bool CAUSAL, bool VARLEN, bool MASK = false, bool DROP = false>
+// CROSS: keys of another sequence ("IO-aware exact attention", section "Tile order and on-chip capacity": lengths
+// add bounds and indexing). N query rows against the first kv_lens[b] of Nk keys. K and V past a sequence's keys
+// may hold anything, NaN included: their scores are replaced before any arithmetic, and the V rows that share a
+// 16-key MMA step with the last key are set to zero in shared memory by the warps that issue the step (0 times NaN
+// would reach O); later steps are not issued. With few work units the keys of a unit are cut into n_splits runs of
+// whole blocks, and each run leaves (O / l, lse) in fp32 for the split-KV merge.
+template <typename T, int D, bool CAUSAL, bool VARLEN, bool MASK = false, bool DROP = false, bool CROSS = false>
 __global__ void __launch_bounds__(kThreads, 1)
     fa_fwd_bk128_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
     static_assert(!(VARLEN && MASK), "no mask in a packed batch");
     static_assert(!(DROP && (VARLEN || MASK)), "dropout with dense unmasked inputs only");
+    static_assert(!(CROSS && (CAUSAL || VARLEN || MASK || DROP)), "keys of another sequence: dense, unmasked");
     using C = Cfg128<T, D>;
     constexpr int RK = C::RK, RV = C::RV;
     if constexpr (MASK) {
@@ -261,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t pol_q = policy_evict_first();
             uint32_t qcount[2] = {0, 0};
             uint32_t kpos = 0, vpos = 0;
-            int kv_y = 0, kv_z = 0, tok0 = 0;
+            int kv_y = 0, kv_z = 0, tok0 = 0, key0 = 0;
             bool ok = true;
             auto load_kv = [&](bool is_v, int blk) -> bool {
                 uint32_t &pos = is_v ? vpos : kpos;
@@ -276,14 +324,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int c = 0; c < C::NCH; ++c)
                         tma_load_3d(dst + c * C::KV_CHUNK, is_v ? &tm_v : &tm_k, full, c * C::CHUNK_ELEMS,
-                                    VARLEN ? kv_y : blk * kBK128, VARLEN ? tok0 + blk * kBK128 : kv_z, pol_kv);
+                                    VARLEN ? kv_y : key0 + blk * kBK128, VARLEN ? tok0 + blk * kBK128 : kv_z, pol_kv);
                 }
                 __syncwarp();
                 ++pos;
                 return true;
             };
-            ItemIter<VARLEN> iter(p, abort_flag, ring);
-            for (Item itm; ok && iter.next(p, itm, ok);) {
+            Items128<VARLEN, CROSS> iter(p, abort_flag, ring);
+            for (Item itm; ok && iter.next_item(p, itm, ok);) {
                 const int q0 = itm.q0, cur_bh = itm.bh;
                 const int kv_h = (cur_bh % p.H) / p.kv_group;  // grouped-query: kv_group query heads per K/V head
                 if (VARLEN) {
@@ -291,6 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tok0 = itm.tok0;
                 } else {
                     kv_z = (cur_bh / p.H) * (p.H / p.kv_group) + kv_h;
+                    if constexpr (CROSS) key0 = iter.keys.first;
                 }
                 const int n0 = tile_nkv<CAUSAL, kBK128>(itm, 0), n1 = tile_nkv<CAUSAL, kBK128>(itm, 1);
                 const int nmax = max(n0, n1);
@@ -345,8 +394,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t qcount[2] = {0, 0}, kpos = 0, s_issued = 0;
             uint32_t sg[2] = {0, 0};  // S products of each tile so far
             bool ok = true;
-            ItemIter<VARLEN> iter(p, abort_flag, ring);
-            for (Item itm; ok && iter.next(p, itm, ok);) {
+            Items128<VARLEN, CROSS> iter(p, abort_flag, ring);
+            for (Item itm; ok && iter.next_item(p, itm, ok);) {
                 const int nt[2] = {tile_nkv<CAUSAL, kBK128>(itm, 0), tile_nkv<CAUSAL, kBK128>(itm, 1)};
                 const int nmax = max(nt[0], nt[1]);
 #pragma unroll
@@ -399,8 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             constexpr uint64_t KVT16 = C::KV_TILE >> 4;
             uint32_t vpos = 0, pcount = 0;
             bool ok = true;
-            ItemIter<VARLEN> iter(p, abort_flag, ring);
-            for (Item itm; ok && iter.next(p, itm, ok);) {
+            Items128<VARLEN, CROSS> iter(p, abort_flag, ring);
+            for (Item itm; ok && iter.next_item(p, itm, ok);) {
                 const int nt = tile_nkv<CAUSAL, kBK128>(itm, t);
                 const int nmax = max(tile_nkv<CAUSAL, kBK128>(itm, 0), tile_nkv<CAUSAL, kBK128>(itm, 1));
                 for (int j = 0; ok && j < nmax; ++j) {
@@ -421,10 +470,27 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     const uint64_t b0 = vd0 + slot * KVT16;
+                    const int rem = itm.n - j * kBK128;  // keys from this block on
+                    if (CROSS && rem < kBK128) {
+                        // The last block ends inside the tile. Both issuers write the same zeros, each before its own
+                        // product; the other's product then reads zeros whichever of the two wrote them.
+                        const int steps = (rem + 15) / 16, n0 = (steps * 16 - rem) * C::NCH * 8;  // 16-byte units
+                        const uint32_t v0 = smem_u32(smem + C::SMEM_V) + slot * C::KV_TILE + rem * 128;
+                        for (int u = lane; u < n0; u += 32)  // unit u % 8 of row u / 8 % rows, swizzle chunk above
+                            st_shared_v4(v0 + (u / ((steps * 16 - rem) * 8)) * C::KV_CHUNK +
+                                             (u % ((steps * 16 - rem) * 8)) * 16,
+                                         0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        for (int k = 0; k < steps; ++k)
+                            mma_ts(d_o, a_p + k * 8, b0 + (uint64_t)((k * C::V_KSTEP_BYTES) >> 4), C::IDESC_PV,
+                                   (k > 0 || j > 0) ? 1u : 0u, issue);
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < C::KSTEPS_PV; ++k)
-                        mma_ts(d_o, a_p + k * 8, b0 + (uint64_t)((k * C::V_KSTEP_BYTES) >> 4), C::IDESC_PV,
-                               (k > 0 || j > 0) ? 1u : 0u, issue);
+                        for (int k = 0; k < C::KSTEPS_PV; ++k)
+                            mma_ts(d_o, a_p + k * 8, b0 + (uint64_t)((k * C::V_KSTEP_BYTES) >> 4), C::IDESC_PV,
+                                   (k > 0 || j > 0) ? 1u : 0u, issue);
+                    }
                     tc_commit(sy.pv_done(t, (pcount - 1) & 1u), issue);
                     tc_commit(sy.v_empty(slot), issue);
                 }
@@ -465,10 +531,26 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t scount = 0;  // S products of this tile consumed (all items)
         uint32_t g = 0;       // P blocks produced (all items) = P V products of this tile
         bool ok = true;
-        ItemIter<VARLEN> iter(p, abort_flag, ring);
-        for (Item itm; ok && iter.next(p, itm, ok);) {
+        Items128<VARLEN, CROSS> iter(p, abort_flag, ring);
+        for (Item itm; ok && iter.next_item(p, itm, ok);) {
             const int bh = itm.bh, q0 = itm.q0, n = itm.n;
             const int nt = tile_nkv<CAUSAL, kBK128>(itm, t);
+            const int rows_end = CROSS ? itm.nrow : n;  // rows at or past it are not written
+            if constexpr (CROSS) {
+                if (r == 0 && t == 0 && p.kv_lens != nullptr && (unsigned)__ldg(p.kv_lens + bh / p.H) > (unsigned)p.Nk)
+                    atomicExch(p.status, -8);  // FA_ERR_SEQLENS
+                if (nt == 0 && q0 + t * kBQ + r < rows_end) {  // a run without keys: an empty summary, or the empty row
+                    const size_t at = (size_t)bh * p.N + (size_t)(q0 + t * kBQ + r);
+                    if (p.n_splits > 1) {
+                        const size_t part = (size_t)iter.keys.run * p.B * p.H * p.N + at;
+                        for (int c = 0; c < D; c += 4) st_global_v4(p.o_part + part * D + c, 0u, 0u, 0u, 0u);
+                        p.lse_part[part] = -INFINITY;
+                    } else {
+                        for (int c = 0; c < D; c += 8) st_global_v4(reinterpret_cast<T *>(p.out) + at * D + c, 0u, 0u, 0u, 0u);
+                        p.lse[at] = -INFINITY;
+                    }
+                }
+            }
             if (nt == 0) continue;
             const int row = q0 + t * kBQ + r;  // query row within the sequence (may be >= n in a ragged tail)
             const int tile_row0 = q0 + t * kBQ;
@@ -614,11 +696,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t orow_idx = VARLEN ? ((size_t)(itm.tok0 + row) * p.H + (size_t)(bh % p.H))
                                            : ((size_t)bh * p.N + (size_t)row);
             T *orow = reinterpret_cast<T *>(p.out) + orow_idx * D;
+            const size_t part = CROSS ? (size_t)iter.keys.run * p.B * p.H * p.N + orow_idx : 0;
 #pragma unroll
             for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t ov[32];
                 tmem_ld32_wait(o_addr + c0, ov);
-                if (row < n) {
+                if (CROSS && p.n_splits > 1) {
+                    if (row < rows_end) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            st_global_v4(p.o_part + part * D + c0 + c, __float_as_uint(__uint_as_float(ov[c]) * inv),
+                                         __float_as_uint(__uint_as_float(ov[c + 1]) * inv),
+                                         __float_as_uint(__uint_as_float(ov[c + 2]) * inv),
+                                         __float_as_uint(__uint_as_float(ov[c + 3]) * inv));
+                    }
+                } else if (row < rows_end) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8)
                         st_global_v4(orow + c0 + c,
@@ -629,8 +721,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             tc_fence_before();  // the O reads above come before the next item's first P V (after p_full)
-            if (row < n)  // lse: [B][H][N], or [H][total] for a packed batch
-                p.lse[VARLEN ? (size_t)(bh % p.H) * p.total + itm.tok0 + row : (size_t)bh * p.N + row] =
+            float *lse_out = CROSS && p.n_splits > 1 ? p.lse_part + (part - orow_idx) : p.lse;
+            if (row < rows_end)  // lse: [B][H][N], or [H][total] for a packed batch
+                lse_out[VARLEN ? (size_t)(bh % p.H) * p.total + itm.tok0 + row : (size_t)bh * p.N + row] =
                     (l > 0.0f) ? (m_ref + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
         }
     }

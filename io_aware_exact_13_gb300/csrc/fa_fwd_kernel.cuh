@@ -146,6 +146,12 @@ struct FwdParams {
     uint64_t drop_seed, drop_offset;
     int drop_threshold;
     float drop_scale;
+    // Keys of another sequence (128-key kernel, CROSS): N query rows, K and V of Nk rows of which batch index b uses
+    // the first kv_lens[b] (nullptr: all); with n_splits > 1 a work unit covers every n_splits-th part of its keys and
+    // leaves its summary in o_part [n_splits][B*H*N][d], lse_part [n_splits][B*H*N].
+    const int *kv_lens = nullptr;
+    int Nk = 0, n_splits = 1;
+    float *o_part = nullptr, *lse_part = nullptr;
 };
 
 // Static schedule: CTA c takes item w*G + c in even waves w and w*G + (G-1-c)

@@ -34,6 +34,10 @@ struct LaunchArgs {
     // dropout: keep threshold 1..256 (0 = no dropout), Philox key and counter offset
     int drop_threshold = 0;
     uint64_t drop_seed = 0, drop_offset = 0;
+    // keys of another sequence: Nk rows of K and V, kv_lens[b] of them in use (nullptr: all), in n_splits runs
+    int Nk = 0, n_splits = 1;
+    const int *kv_lens = nullptr;
+    float *o_part = nullptr, *lse_part = nullptr;
 };
 
 // Defined in fa_mask_pack.cu: bytes of the packed form of a [rows][nk] mask, and the packing pass
@@ -126,11 +130,11 @@ int launch_variant(const LaunchArgs &a) {
 
 // The 128-key-block kernel: dense [B][H][N][d] tensors, or a packed batch; MASK: a shared
 // [B][N][N] mask in its packed one-bit form; DROP: dropout (dense, no mask).
-template <typename T, int D, bool CAUSAL, bool VARLEN, bool MASK = false, bool DROP = false>
+template <typename T, int D, bool CAUSAL, bool VARLEN, bool MASK = false, bool DROP = false, bool CROSS = false>
 int launch_bk128(const LaunchArgs &a) {
     static_assert(!(VARLEN && MASK), "no mask in a packed batch");
     using C = Cfg128<T, D>;
-    auto kern = fa_fwd_bk128_kernel<T, D, CAUSAL, VARLEN, MASK, DROP>;
+    auto kern = fa_fwd_bk128_kernel<T, D, CAUSAL, VARLEN, MASK, DROP, CROSS>;
     if (MASK && (a.mask_bits == nullptr || a.mask_kind == nullptr)) return -5;
     if (DROP && (a.drop_threshold < 1 || a.drop_threshold > 256)) return -5;
     // The register split between warpgroups assumes 128 registers per thread at
@@ -147,8 +151,9 @@ int launch_bk128(const LaunchArgs &a) {
         if (!encode_tokens_map(&tv, Elem<T>::tma, sizeof(T), a.v, D, a.Hkv, a.total, kBK128)) return -5;
     } else {
         if (!encode_rows_map(&tq, Elem<T>::tma, sizeof(T), a.q, D, a.N, a.B * a.H, kBQ)) return -5;
-        if (!encode_rows_map(&tk, Elem<T>::tma, sizeof(T), a.k, D, a.N, a.B * a.Hkv, kBK128)) return -5;
-        if (!encode_rows_map(&tv, Elem<T>::tma, sizeof(T), a.v, D, a.N, a.B * a.Hkv, kBK128)) return -5;
+        const int nk = CROSS ? a.Nk : a.N;
+        if (!encode_rows_map(&tk, Elem<T>::tma, sizeof(T), a.k, D, nk, a.B * a.Hkv, kBK128)) return -5;
+        if (!encode_rows_map(&tv, Elem<T>::tma, sizeof(T), a.v, D, nk, a.B * a.Hkv, kBK128)) return -5;
     }
     FwdParams p;
     p.out = a.out;
@@ -182,7 +187,18 @@ int launch_bk128(const LaunchArgs &a) {
     p.drop_offset = DROP ? a.drop_offset : 0;
     p.drop_threshold = DROP ? a.drop_threshold : 256;
     p.drop_scale = DROP ? static_cast<float>(256.0 / a.drop_threshold) : 1.0f;
-    const int grid = p.n_items < a.num_sms ? p.n_items : a.num_sms;
+    if (CROSS) {
+        p.Nk = a.Nk;
+        p.kv_lens = a.kv_lens;
+        p.n_splits = a.n_splits;
+        p.o_part = a.o_part;
+        p.lse_part = a.lse_part;
+        if (a.n_splits > 1) {  // single tiles do not pay for themselves here: the splits fill the grid
+            p.n_items = p.n_pair = a.B * a.H * p.n_qblk;
+        }
+    }
+    const long long units = static_cast<long long>(p.n_items) * (CROSS ? a.n_splits : 1);
+    const int grid = units < a.num_sms ? static_cast<int>(units) : a.num_sms;
     // a programmatic dependent of the work ahead (MASK: the packing pass, whose verdict and bits it waits
     // for; otherwise whatever ran before, waited for before any global access)
     return launch_dependent(kern, dim3(grid), dim3(kThreads), C::SMEM_BYTES, a.stream, tq, tk, tv, p) == cudaSuccess
@@ -219,6 +235,17 @@ int launch_fwd_mask_bf16(const LaunchArgs &a);  // fa_fwd_mask_bf16.cu
 int launch_fwd_mask_fp16(const LaunchArgs &a);  // fa_fwd_mask_fp16.cu
 int launch_fwd_drop_bf16(const LaunchArgs &a);  // fa_fwd_drop_bf16.cu
 int launch_fwd_drop_fp16(const LaunchArgs &a);  // fa_fwd_drop_fp16.cu
+
+int launch_fwd_cross_bf16(const LaunchArgs &a);  // fa_fwd_cross_bf16.cu
+int launch_fwd_cross_fp16(const LaunchArgs &a);  // fa_fwd_cross_fp16.cu
+
+// A forward over keys of another length (dense, no mask, not causal).
+template <typename T>
+int launch_cross_fwd(const LaunchArgs &a) {
+    if (a.d == 128) return launch_bk128<T, 128, false, false, false, false, true>(a);
+    if (a.d == 64) return launch_bk128<T, 64, false, false, false, false, true>(a);
+    return -4;
+}
 
 // A forward with dropout (dense, no mask).
 template <typename T, int D>

@@ -470,6 +470,22 @@ int launch_sk_t(const SplitKVArgs &a) {
 
 int splitkv_blocks_per_sm(int d, int Nq) { return d == 64 ? occupancy_d<64>(Nq) : occupancy_d<128>(Nq); }
 
+int launch_splitkv_merge(const float *o_part, const float *lse_part, void *out, float *lse, int rows, int d,
+                         int n_splits, bool fp16, cudaStream_t stream) {
+    auto go = [&](auto *typed, auto kern, int threads) {
+        return launch_dependent(kern, dim3(rows), dim3(threads), 0, stream, o_part, lse_part, typed, lse, rows,
+                                n_splits) == cudaSuccess
+                   ? 0
+                   : -5;
+    };
+    if (fp16) {
+        __half *o = static_cast<__half *>(out);
+        return d == 64 ? go(o, fa_splitkv_combine<__half, 64>, 64) : go(o, fa_splitkv_combine<__half, 128>, 128);
+    }
+    __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(out);
+    return d == 64 ? go(o, fa_splitkv_combine<__nv_bfloat16, 64>, 64) : go(o, fa_splitkv_combine<__nv_bfloat16, 128>, 128);
+}
+
 int launch_splitkv(const SplitKVArgs &a, bool fp16) {
     return fp16 ? launch_sk_t<__half>(a) : launch_sk_t<__nv_bfloat16>(a);
 }

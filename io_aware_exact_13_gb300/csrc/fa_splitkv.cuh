@@ -29,6 +29,11 @@ inline size_t splitkv_workspace_bytes(int64_t rows, int d, int n_splits) {
 
 int launch_splitkv(const SplitKVArgs &a, bool fp16);
 
+// The merge of the splits' summaries ([n_splits][rows][d] and [n_splits][rows] fp32), as a programmatic dependent of
+// the kernel that writes them.
+int launch_splitkv_merge(const float *o_part, const float *lse_part, void *out, float *lse, int rows, int d,
+                         int n_splits, bool fp16, cudaStream_t stream);
+
 // Resident CTAs per SM of the partial kernel used for (d, Nq) (bf16 variant).
 int splitkv_blocks_per_sm(int d, int Nq);
 // FA_LOG=1: one line per call to stderr (defined in fa_api.cu).

@@ -11,9 +11,11 @@ Names follow the C ABI: ``fa_fwd`` (bf16), ``fa_fwd_fp16``, ``fa_fwd_fp32``,
 ``fa_fwd_splitkv`` / ``fa_fwd_splitkv_fp16`` (decoding), ``fa_bwd`` /
 ``fa_bwd_fp16`` (backward by recomputation), ``fa_fwd_varlen`` /
 ``fa_fwd_varlen_fp16`` (packed variable-length batches), ``fa_fwd_kvq8`` /
-``fa_fwd_kvq8_fp16`` (decoding over an 8-bit cache), their sizing helpers,
+``fa_fwd_kvq8_fp16`` (decoding over an 8-bit cache), ``fa_fwd_cross`` / ``fa_bwd_cross`` and their ``_fp16`` forms
+(keys of another length), their sizing helpers,
 ``fa_status_string``, ``fa_get_device_status``, ``fa_num_sms``. ``attention``,
-``attention_decode``, ``attention_varlen``, ``attention_kvq8`` and ``attention_backward`` are convenience wrappers
+``attention_decode``, ``attention_varlen``, ``attention_kvq8``, ``attention_cross``,
+``attention_cross_backward`` and ``attention_backward`` are convenience wrappers
 that allocate outputs (and the workspaces) with torch and pick the entry point from the dtype; ``kvq8_append`` and
 ``kvq8_read`` write and read the 8-bit cache (``KVCacheQ8``, allocated by ``kv_cache_q8``).
 """
@@ -82,6 +84,7 @@ SIGNATURES = {
                                [ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp]),
     "fa_fwd_varlen": (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _vp]),
     "fa_fwd_varlen_fp16": (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _vp]),
+    "fa_cross_num_splits": (ctypes.c_int, [ctypes.c_int] * 4),
     "fa_kvq8_num_parts": (ctypes.c_int, [ctypes.c_int] * 6),
     "fa_kvq8_workspace_bytes": (ctypes.c_longlong, [ctypes.c_int] * 5),
     "fa_selftest_wait_timeout": (ctypes.c_int, [ctypes.c_ulonglong, _vp]),
@@ -102,6 +105,10 @@ for _suffix in ("", "_fp16"):
     SIGNATURES["fa_kvq8_append" + _suffix] = (ctypes.c_int, _KVQ8_APPEND)
     SIGNATURES["fa_kvq8_read" + _suffix] = (ctypes.c_int, _KVQ8_READ)
     SIGNATURES["fa_fwd_kvq8" + _suffix] = (ctypes.c_int, _KVQ8_FWD)
+    SIGNATURES["fa_fwd_cross" + _suffix] = (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 +
+                                            [ctypes.c_float, ctypes.c_int, _vp, ctypes.c_ulonglong, _vp])
+    SIGNATURES["fa_bwd_cross" + _suffix] = (ctypes.c_int, [_vp] * 10 + [ctypes.c_int] * 6 +
+                                            [ctypes.c_float, _vp, ctypes.c_ulonglong, _vp])
 for _name, (_res, _args) in SIGNATURES.items():
     _f = getattr(lib, _name)
     _f.restype = _res
@@ -724,6 +731,122 @@ def attention_backward(q, k, v, out, dout, lse, scale=None, causal=False, worksp
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
     fn = {torch.bfloat16: fa_bwd, torch.float16: fa_bwd_fp16}[q.dtype]
     fn(q, k, v, out, dout, lse, dq, dk, dv, scale, causal, workspace, stream)
+    return dq, dk, dv
+
+
+# ---------------------------------------------------------------- keys of another sequence
+def fa_cross_num_splits(B, H, Nq, Nk) -> int:
+    n = int(lib.fa_cross_num_splits(int(B), int(H), int(Nq), int(Nk)))
+    if n < 0:
+        raise FAError(n, "fa_cross_num_splits")
+    return n
+
+
+def _check_cross(q, k, v, kv_lens, like_q, like_k, lse, dtype):
+    """(B, H, Hkv, Nq, Nk, d) after checking every tensor; like_q, like_k: (name, tensor) pairs shaped like q and k."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q must be [B, H, Nq, d] and k, v [B, Hkv, Nk, d]")
+    B, H, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    if k.shape != (B, Hkv, Nk, d) or Hkv < 1 or H % Hkv:
+        raise ValueError("k, v must be [B, Hkv, Nk, d] with q's B and d, and Hkv dividing H")
+    device = q.device
+    for pairs, shape in (([("q", q)] + like_q, q.shape), ([("k", k), ("v", v)] + like_k, k.shape)):
+        for name, t in pairs:
+            if t.dtype != dtype or not t.is_cuda or t.device != device or not t.is_contiguous() or t.shape != shape:
+                raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, all on one device")
+    if lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous() or lse.shape != (B, H, Nq):
+        raise ValueError("lse must be a contiguous float32 [B, H, Nq] tensor on q's device")
+    if kv_lens is not None:
+        _check_ints("kv_lens", kv_lens, (B,), device)
+    return B, H, Hkv, Nq, Nk, d
+
+
+def _check_workspace(workspace, device):
+    if workspace is None:
+        return 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+    return workspace.numel() * workspace.element_size()
+
+
+def _raw_cross(fn_name, dtype, q, k, v, kv_lens, out, lse, scale, n_splits, workspace, stream):
+    B, H, Hkv, Nq, Nk, d = _check_cross(q, k, v, kv_lens, [("out", out)], [], lse, dtype)
+    nbytes = _check_workspace(workspace, q.device)
+    with _on(q.device, stream):
+        rc = getattr(lib, fn_name)(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(out), _ptr(lse), B, H, Hkv, Nq, Nk, d,
+                                   float(scale), int(n_splits), _ptr(workspace), nbytes,
+                                   ctypes.c_void_p(_stream_handle(stream)))
+    if rc != FA_OK:
+        raise FAError(rc, fn_name)
+
+
+def fa_fwd_cross(q, k, v, kv_lens, out, lse, scale, n_splits=1, workspace=None, stream=None):
+    """bf16 forward of q [B, H, Nq, d] over k, v [B, Hkv, Nk, d]; batch index b uses its first kv_lens[b] keys
+    (int32 [B]; None: all), whatever lies behind them. ``workspace`` as for ``fa_fwd_splitkv`` when n_splits > 1."""
+    _raw_cross("fa_fwd_cross", torch.bfloat16, q, k, v, kv_lens, out, lse, scale, n_splits, workspace, stream)
+
+
+def fa_fwd_cross_fp16(q, k, v, kv_lens, out, lse, scale, n_splits=1, workspace=None, stream=None):
+    """fp16 forward over keys of another length (see ``fa_fwd_cross``)."""
+    _raw_cross("fa_fwd_cross_fp16", torch.float16, q, k, v, kv_lens, out, lse, scale, n_splits, workspace, stream)
+
+
+def attention_cross(q, k, v, kv_lens=None, scale=None, n_splits=None, stream=None):
+    """O [B, H, Nq, d] and lse [B, H, Nq] of queries over the keys of another sequence; allocates the outputs and, when
+    the keys are split, the workspace."""
+    if q.dtype not in _FP16_SUFFIX:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    B, H, Nq, d = q.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(q.device, stream) if q.is_cuda else contextlib.nullcontext():
+        n_splits = fa_cross_num_splits(B, H, Nq, k.shape[2]) if n_splits is None else n_splits
+        ws = None
+        if n_splits > 1:
+            ws = torch.empty(fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits), dtype=torch.uint8, device=q.device)
+        out = torch.empty_like(q)
+        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+    _raw_cross("fa_fwd_cross" + _FP16_SUFFIX[q.dtype], q.dtype, q, k, v, kv_lens, out, lse, scale, n_splits, ws, stream)
+    return out, lse
+
+
+def _raw_bwd_cross(fn_name, dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream):
+    B, H, Hkv, Nq, Nk, d = _check_cross(q, k, v, kv_lens, [("out", out), ("dout", dout), ("dq", dq)],
+                                        [("dk", dk), ("dv", dv)], lse, dtype)
+    nbytes = _check_workspace(workspace, q.device)
+    with _on(q.device, stream):
+        rc = getattr(lib, fn_name)(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq),
+                                   _ptr(dk), _ptr(dv), B, H, Hkv, Nq, Nk, d, float(scale), _ptr(workspace), nbytes,
+                                   ctypes.c_void_p(_stream_handle(stream)))
+    if rc != FA_OK:
+        raise FAError(rc, fn_name)
+
+
+def fa_bwd_cross(q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream=None):
+    """bf16 gradients of ``fa_fwd_cross`` into ``dq`` (like q) and ``dk``, ``dv`` (like k, summed over the query heads
+    that share them; 0 past kv_lens); ``workspace`` of ``fa_bwd_workspace_bytes(B, H, Nq, d)`` bytes."""
+    _raw_bwd_cross("fa_bwd_cross", torch.bfloat16, q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream)
+
+
+def fa_bwd_cross_fp16(q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream=None):
+    """fp16 gradients of ``fa_fwd_cross_fp16`` (see ``fa_bwd_cross``)."""
+    _raw_bwd_cross("fa_bwd_cross_fp16", torch.float16, q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace,
+                   stream)
+
+
+def attention_cross_backward(q, k, v, out, dout, lse, kv_lens=None, scale=None, workspace=None, stream=None):
+    """(dq, dk, dv) of sum(dout * out) for out, lse from ``attention_cross``; allocates the outputs and, unless given,
+    the workspace with torch."""
+    if q.dtype not in _FP16_SUFFIX:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    B, H, Nq, d = q.shape
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    with _on(q.device, stream) if q.is_cuda else contextlib.nullcontext():
+        if workspace is None:
+            workspace = torch.empty(fa_bwd_workspace_bytes(B, H, Nq, d), dtype=torch.uint8, device=q.device)
+        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    _raw_bwd_cross("fa_bwd_cross" + _FP16_SUFFIX[q.dtype], q.dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale,
+                   workspace, stream)
     return dq, dk, dv
 
 
