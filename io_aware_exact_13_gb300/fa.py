@@ -21,7 +21,6 @@ that allocate outputs (and the workspaces) with torch and pick the entry point f
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 import os
@@ -472,69 +471,98 @@ def kv_cache_q8(n_pages, Hkv, page, d, dtype=torch.int8, device="cuda") -> KVCac
     return KVCacheQ8(*codes, *scales)
 
 
-def _on(device, stream):
-    """Context in which ``device`` is current and torch allocates for ``stream`` (None: the device's current one)."""
-    if stream is not None:
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=device)
-        if stream.device != device:
-            raise ValueError(f"the stream belongs to {stream.device}, the tensors are on {device}")
-        return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
-    return contextlib.nullcontext()
+# The checks below run on every call, in a decoding loop beside kernels of a few microseconds: they ask each tensor as
+# little as possible (get_device() is the index, -1 off the GPU).
+def _on(index, stream):
+    """Context in which device ``index`` is current and torch allocates for ``stream`` (None: the device's current one)."""
+    if stream is None:
+        return _NOTHING if index == torch.cuda.current_device() else torch.cuda.device(index)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
+    if stream.device.index != index:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors are on cuda:{index}")
+    return torch.cuda.stream(stream)
 
 
-def _check_ints(name, t, shape, device):
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {tuple(shape)} on {device}")
+class _Nothing:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_NOTHING = _Nothing()
+
+
+def _raw_stream(index, stream):
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(index)
+    return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _check_tensor(name, t, dtype, shape, index):
+    if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
+
+
+def _nbytes(workspace, index):
+    if workspace is None:
+        return 0
+    if workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return workspace.numel() * workspace.element_size()
 
 
 def _check_kvq8(cache, page_table):
-    """The cache's (device, page, Hkv, d) after checking its tensors against each other and the page table's form."""
-    kc = cache.k_codes
-    if kc.dtype not in _KVQ8_FORMATS or kc.dim() != 4:
+    """(device index, codes' shape, arguments of the cache for the C call) after checking its tensors against each
+    other, and the page table's form."""
+    kc, vc, ks, vs = cache
+    fmt = _KVQ8_FORMATS.get(kc.dtype)
+    shape = kc.shape
+    if fmt is None or len(shape) != 4:
         raise ValueError("cache codes must be int8 or float8_e4m3fn tensors [n_pages, Hkv, page, d]")
-    if not kc.is_cuda:
+    index = kc.get_device()
+    if index < 0:
         raise ValueError("the cache must be on a CUDA device")
-    n_pages, Hkv, page, d = kc.shape
-    for name, t, dtype, shape in (("k_codes", kc, kc.dtype, kc.shape), ("v_codes", cache.v_codes, kc.dtype, kc.shape),
-                                  ("k_scale", cache.k_scale, torch.float32, (n_pages, Hkv)),
-                                  ("v_scale", cache.v_scale, torch.float32, (n_pages, Hkv))):
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.device != kc.device:
-            raise ValueError(f"cache {name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {kc.device}")
-    if page_table.dim() != 2:
+    _check_tensor("k_codes", kc, kc.dtype, shape, index)
+    _check_tensor("v_codes", vc, kc.dtype, shape, index)
+    scales = shape[:2]
+    _check_tensor("k_scale", ks, torch.float32, scales, index)
+    _check_tensor("v_scale", vs, torch.float32, scales, index)
+    table = page_table.shape
+    if len(table) != 2:
         raise ValueError("page_table must be int32 [nseq, max_pages]")
-    _check_ints("page_table", page_table, page_table.shape, kc.device)
-    return kc.device, page, Hkv, d
-
-
-def _kvq8_ptrs(cache):
-    return [_ptr(t) for t in cache]
+    _check_tensor("page_table", page_table, torch.int32, table, index)
+    ptrs = (kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), page_table.data_ptr())
+    return index, fmt, shape, table, ptrs
 
 
 def kvq8_append(cache, k, v, page_table, cu_seqlens, cache_lens, max_new, stream=None):
     """Quantise new tokens' ``k``, ``v`` [total, Hkv, d] (bf16 or fp16; any strides of tokens and heads that are
     multiples of 8, rows contiguous) into ``cache``: tokens [cu_seqlens[s], cu_seqlens[s+1]) go to positions
     cache_lens[s], ... of sequence s, at most ``max_new`` per sequence. ``cache_lens`` is left as it is."""
-    device, page, Hkv, d = _check_kvq8(cache, page_table)
-    nseq, max_pages = page_table.shape
-    total = k.shape[0]
+    index, fmt, (n_pages, Hkv, page, d), (nseq, max_pages), cache_ptrs = _check_kvq8(cache, page_table)
+    dtype, shape = k.dtype, k.shape
+    suffix = _FP16_SUFFIX.get(dtype)
+    if suffix is None or len(shape) != 3 or shape[1] != Hkv or shape[2] != d:
+        raise ValueError(f"k, v must be bf16 or fp16 tensors [total, {Hkv}, {d}]")
+    total = shape[0]
     strides = []
     for name, t in (("k", k), ("v", v)):
-        if t.dtype != k.dtype or t.dtype not in _FP16_SUFFIX or t.device != device or t.shape != (total, Hkv, d):
-            raise ValueError(f"{name} must be a bf16 or fp16 tensor [total, {Hkv}, {d}] on {device}, k and v alike")
-        if t.stride(2) != 1:
+        if t.dtype is not dtype or t.get_device() != index or t.shape != shape:
+            raise ValueError(f"{name} must be a {dtype} tensor [total, {Hkv}, {d}] on cuda:{index}, k and v alike")
+        s0, s1, s2 = t.stride()
+        if s2 != 1:
             raise ValueError(f"{name}: the head dimension must be contiguous")
-        strides += [t.stride(0) if total > 1 else 0, t.stride(1) if Hkv > 1 else 0]
-    _check_ints("cu_seqlens", cu_seqlens, (nseq + 1,), device)
-    _check_ints("cache_lens", cache_lens, (nseq,), device)
-    name = "fa_kvq8_append" + _FP16_SUFFIX[k.dtype]
-    with _on(device, stream):
-        rc = getattr(lib, name)(_ptr(k), _ptr(v), *strides, _ptr(cu_seqlens), _ptr(cache_lens), nseq, total,
-                                int(max_new), *_kvq8_ptrs(cache), _ptr(page_table), cache.k_codes.shape[0], max_pages,
-                                page, Hkv, d, _KVQ8_FORMATS[cache.k_codes.dtype],
-                                ctypes.c_void_p(_stream_handle(stream)))
+        strides += (s0 if total > 1 else 0, s1 if Hkv > 1 else 0)
+    _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), index)
+    _check_tensor("cache_lens", cache_lens, torch.int32, (nseq,), index)
+    name = "fa_kvq8_append" + suffix
+    with _on(index, stream):
+        rc = getattr(lib, name)(k.data_ptr(), v.data_ptr(), *strides, cu_seqlens.data_ptr(), cache_lens.data_ptr(),
+                                nseq, total, int(max_new), *cache_ptrs, n_pages, max_pages, page, Hkv, d, fmt,
+                                _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, name)
 
@@ -544,23 +572,23 @@ def kvq8_read(cache, page_table, cu_seqlens, total, max_len, first=None, dtype=t
     """Cached tokens back as packed K, V [total, Hkv, d]: rows [cu_seqlens[s], cu_seqlens[s+1]) (at most ``max_len``)
     are positions first[s], first[s] + 1, ... of sequence s (``first`` None: from 0). Rows that no sequence covers are
     not written; ``k`` and ``v`` are allocated unless given."""
-    device, page, Hkv, d = _check_kvq8(cache, page_table)
-    nseq, max_pages = page_table.shape
-    _check_ints("cu_seqlens", cu_seqlens, (nseq + 1,), device)
+    index, fmt, (n_pages, Hkv, page, d), (nseq, max_pages), cache_ptrs = _check_kvq8(cache, page_table)
+    _check_tensor("cu_seqlens", cu_seqlens, torch.int32, (nseq + 1,), index)
     if first is not None:
-        _check_ints("first", first, (nseq,), device)
-    if dtype not in _FP16_SUFFIX:
+        _check_tensor("first", first, torch.int32, (nseq,), index)
+    suffix = _FP16_SUFFIX.get(dtype)
+    if suffix is None:
         raise ValueError(f"unsupported dtype {dtype}")
-    name = "fa_kvq8_read" + _FP16_SUFFIX[dtype]
-    with _on(device, stream):
-        k = torch.empty((total, Hkv, d), dtype=dtype, device=device) if k is None else k
-        v = torch.empty((total, Hkv, d), dtype=dtype, device=device) if v is None else v
-        for n, t in (("k", k), ("v", v)):
-            if t.dtype != dtype or t.shape != (total, Hkv, d) or not t.is_contiguous() or t.device != device:
-                raise ValueError(f"{n} must be a contiguous {dtype} tensor [{total}, {Hkv}, {d}] on {device}")
-        rc = getattr(lib, name)(*_kvq8_ptrs(cache), _ptr(page_table), cache.k_codes.shape[0], max_pages, page,
-                                _ptr(cu_seqlens), _ptr(first), nseq, int(total), int(max_len), _ptr(k), _ptr(v), Hkv,
-                                d, _KVQ8_FORMATS[cache.k_codes.dtype], ctypes.c_void_p(_stream_handle(stream)))
+    name = "fa_kvq8_read" + suffix
+    shape, device = (int(total), Hkv, d), cache.k_codes.device
+    with _on(index, stream):
+        k = torch.empty(shape, dtype=dtype, device=device) if k is None else k
+        v = torch.empty(shape, dtype=dtype, device=device) if v is None else v
+        _check_tensor("k", k, dtype, shape, index)
+        _check_tensor("v", v, dtype, shape, index)
+        rc = getattr(lib, name)(*cache_ptrs, n_pages, max_pages, page, cu_seqlens.data_ptr(),
+                                None if first is None else first.data_ptr(), nseq, int(total), int(max_len),
+                                k.data_ptr(), v.data_ptr(), Hkv, d, fmt, _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, name)
     return k, v
@@ -582,27 +610,35 @@ def fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) -> int:
 
 def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_parts, workspace,
               stream):
-    device, page, Hkv, d = _check_kvq8(cache, page_table)
-    for name, t in (("q", q), ("out", out)):
-        if t.dtype != dtype or t.device != device or not t.is_contiguous() or t.dim() != 4 or t.shape != q.shape:
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor [B, H, Nq, d] on {device}")
-    B, H, Nq, dq = q.shape
-    if dq != d or H % Hkv or page_table.shape[0] != B:
+    """``out``, ``lse`` None: allocated; ``max_len``, ``n_parts``, ``workspace`` None: chosen and allocated."""
+    index, fmt, (n_pages, Hkv, page, d), (nseq, max_pages), cache_ptrs = _check_kvq8(cache, page_table)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B, H, Nq, d]")
+    B, H, Nq, dq = shape
+    if dq != d or H % Hkv or nseq != B:
         raise ValueError("q: [B, H, Nq, d] with the cache's d, its Hkv dividing H and one page table row per b")
-    if lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous() or lse.shape != (B, H, Nq):
-        raise ValueError(f"lse must be a contiguous float32 [B, H, Nq] tensor on {device}")
-    _check_ints("kv_lens", kv_lens, (B,), device)
-    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    with _on(device, stream):
-        rc = getattr(lib, fn_name)(_ptr(q), *_kvq8_ptrs(cache), _ptr(page_table), cache.k_codes.shape[0],
-                                   page_table.shape[1], page, _ptr(kv_lens), _ptr(out), _ptr(lse), B, H, Hkv, Nq,
-                                   int(max_len), d, _KVQ8_FORMATS[cache.k_codes.dtype], float(scale),
-                                   int(bool(causal)), int(n_parts), _ptr(workspace), nbytes,
-                                   ctypes.c_void_p(_stream_handle(stream)))
+    _check_tensor("q", q, dtype, shape, index)
+    _check_tensor("kv_lens", kv_lens, torch.int32, (B,), index)
+    max_len = max_pages * page if max_len is None else int(max_len)
+    with _on(index, stream):
+        if out is None:
+            out = torch.empty_like(q)
+            lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+        else:
+            _check_tensor("out", out, dtype, shape, index)
+            _check_tensor("lse", lse, torch.float32, shape[:3], index)
+        if n_parts is None:
+            n_parts = fa_kvq8_num_parts(B, H, Hkv, Nq, max_len, d)
+        if workspace is None:
+            workspace = torch.empty(fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts), dtype=torch.uint8, device=q.device)
+        rc = getattr(lib, fn_name)(q.data_ptr(), *cache_ptrs, n_pages, max_pages, page, kv_lens.data_ptr(),
+                                   out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, max_len, d, fmt, scale, bool(causal),
+                                   n_parts, workspace.data_ptr(), _nbytes(workspace, index),
+                                   _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, fn_name)
+    return out, lse
 
 
 def fa_fwd_kvq8(q, cache, page_table, kv_lens, out, lse, scale, causal, max_len, n_parts, workspace, stream=None):
@@ -621,22 +657,12 @@ def fa_fwd_kvq8_fp16(q, cache, page_table, kv_lens, out, lse, scale, causal, max
 def attention_kvq8(q, cache, page_table, kv_lens, scale=None, causal=False, max_len=None, n_parts=None, stream=None):
     """O [B, H, Nq, d] and lse [B, H, Nq] of 1 to 16 query rows per sequence over its first kv_lens[b] cached tokens.
     ``max_len`` bounds every length (the page table's reach unless given); the workspace is a torch allocation."""
-    B, H, Nq, d = q.shape
-    if q.dtype not in _FP16_SUFFIX:
+    suffix = _FP16_SUFFIX.get(q.dtype)
+    if suffix is None:
         raise ValueError(f"unsupported dtype {q.dtype}")
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    if max_len is None:
-        max_len = page_table.shape[1] * cache.k_codes.shape[2]
-    with _on(q.device, stream) if q.is_cuda else contextlib.nullcontext():
-        if n_parts is None:
-            n_parts = fa_kvq8_num_parts(B, H, cache.k_codes.shape[1], Nq, max_len, d)
-        ws = torch.empty(fa_kvq8_workspace_bytes(H, cache.k_codes.shape[1], Nq, d, n_parts), dtype=torch.uint8,
-                         device=q.device)
-        out = torch.empty_like(q)
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    _raw_kvq8("fa_fwd_kvq8" + _FP16_SUFFIX[q.dtype], q.dtype, q, cache, page_table, kv_lens, out, lse, scale, causal,
-              max_len, n_parts, ws, stream)
-    return out, lse
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    return _raw_kvq8("fa_fwd_kvq8" + suffix, q.dtype, q, cache, page_table, kv_lens, None, None, scale, causal, max_len,
+                     n_parts, None, stream)
 
 
 # ---------------------------------------------------------------- packed variable-length batch
@@ -742,43 +768,48 @@ def fa_cross_num_splits(B, H, Nq, Nk) -> int:
     return n
 
 
-def _check_cross(q, k, v, kv_lens, like_q, like_k, lse, dtype):
-    """(B, H, Hkv, Nq, Nk, d) after checking every tensor; like_q, like_k: (name, tensor) pairs shaped like q and k."""
-    if q.dim() != 4 or k.dim() != 4:
+def _check_cross(q, k, v, kv_lens, dtype):
+    """(device index, B, H, Hkv, Nq, Nk, d) after checking the inputs."""
+    sq, sk = q.shape, k.shape
+    if len(sq) != 4 or len(sk) != 4:
         raise ValueError("q must be [B, H, Nq, d] and k, v [B, Hkv, Nk, d]")
-    B, H, Nq, d = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    if k.shape != (B, Hkv, Nk, d) or Hkv < 1 or H % Hkv:
+    B, H, Nq, d = sq
+    Hkv, Nk = sk[1], sk[2]
+    if sk[0] != B or sk[3] != d or Hkv < 1 or H % Hkv:
         raise ValueError("k, v must be [B, Hkv, Nk, d] with q's B and d, and Hkv dividing H")
-    device = q.device
-    for pairs, shape in (([("q", q)] + like_q, q.shape), ([("k", k), ("v", v)] + like_k, k.shape)):
-        for name, t in pairs:
-            if t.dtype != dtype or not t.is_cuda or t.device != device or not t.is_contiguous() or t.shape != shape:
-                raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {tuple(shape)}, all on one device")
-    if lse.dtype != torch.float32 or lse.device != device or not lse.is_contiguous() or lse.shape != (B, H, Nq):
-        raise ValueError("lse must be a contiguous float32 [B, H, Nq] tensor on q's device")
+    index = q.get_device()
+    if index < 0:
+        raise ValueError("q must be on a CUDA device")
+    _check_tensor("q", q, dtype, sq, index)
+    _check_tensor("k", k, dtype, sk, index)
+    _check_tensor("v", v, dtype, sk, index)
     if kv_lens is not None:
-        _check_ints("kv_lens", kv_lens, (B,), device)
-    return B, H, Hkv, Nq, Nk, d
-
-
-def _check_workspace(workspace, device):
-    if workspace is None:
-        return 0
-    if workspace.device != device or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {device}")
-    return workspace.numel() * workspace.element_size()
+        _check_tensor("kv_lens", kv_lens, torch.int32, (B,), index)
+    return index, B, H, Hkv, Nq, Nk, d
 
 
 def _raw_cross(fn_name, dtype, q, k, v, kv_lens, out, lse, scale, n_splits, workspace, stream):
-    B, H, Hkv, Nq, Nk, d = _check_cross(q, k, v, kv_lens, [("out", out)], [], lse, dtype)
-    nbytes = _check_workspace(workspace, q.device)
-    with _on(q.device, stream):
-        rc = getattr(lib, fn_name)(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(out), _ptr(lse), B, H, Hkv, Nq, Nk, d,
-                                   float(scale), int(n_splits), _ptr(workspace), nbytes,
-                                   ctypes.c_void_p(_stream_handle(stream)))
+    """``out``, ``lse`` None: allocated; ``n_splits`` None: chosen, with a workspace from torch."""
+    index, B, H, Hkv, Nq, Nk, d = _check_cross(q, k, v, kv_lens, dtype)
+    with _on(index, stream):
+        if out is None:
+            out = torch.empty_like(q)
+            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+            n_splits = fa_cross_num_splits(B, H, Nq, Nk) if n_splits is None else n_splits
+            if n_splits > 1:
+                workspace = torch.empty(fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits), dtype=torch.uint8,
+                                        device=q.device)
+        else:
+            _check_tensor("out", out, dtype, q.shape, index)
+            _check_tensor("lse", lse, torch.float32, (B, H, Nq), index)
+        rc = getattr(lib, fn_name)(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   None if kv_lens is None else kv_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
+                                   Hkv, Nq, Nk, d, scale, int(n_splits),
+                                   None if workspace is None else workspace.data_ptr(), _nbytes(workspace, index),
+                                   _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, fn_name)
+    return out, lse
 
 
 def fa_fwd_cross(q, k, v, kv_lens, out, lse, scale, n_splits=1, workspace=None, stream=None):
@@ -795,31 +826,35 @@ def fa_fwd_cross_fp16(q, k, v, kv_lens, out, lse, scale, n_splits=1, workspace=N
 def attention_cross(q, k, v, kv_lens=None, scale=None, n_splits=None, stream=None):
     """O [B, H, Nq, d] and lse [B, H, Nq] of queries over the keys of another sequence; allocates the outputs and, when
     the keys are split, the workspace."""
-    if q.dtype not in _FP16_SUFFIX:
+    suffix = _FP16_SUFFIX.get(q.dtype)
+    if suffix is None:
         raise ValueError(f"unsupported dtype {q.dtype}")
-    B, H, Nq, d = q.shape
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _on(q.device, stream) if q.is_cuda else contextlib.nullcontext():
-        n_splits = fa_cross_num_splits(B, H, Nq, k.shape[2]) if n_splits is None else n_splits
-        ws = None
-        if n_splits > 1:
-            ws = torch.empty(fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits), dtype=torch.uint8, device=q.device)
-        out = torch.empty_like(q)
-        lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
-    _raw_cross("fa_fwd_cross" + _FP16_SUFFIX[q.dtype], q.dtype, q, k, v, kv_lens, out, lse, scale, n_splits, ws, stream)
-    return out, lse
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    return _raw_cross("fa_fwd_cross" + suffix, q.dtype, q, k, v, kv_lens, None, None, scale, n_splits, None, stream)
 
 
 def _raw_bwd_cross(fn_name, dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream):
-    B, H, Hkv, Nq, Nk, d = _check_cross(q, k, v, kv_lens, [("out", out), ("dout", dout), ("dq", dq)],
-                                        [("dk", dk), ("dv", dv)], lse, dtype)
-    nbytes = _check_workspace(workspace, q.device)
-    with _on(q.device, stream):
-        rc = getattr(lib, fn_name)(_ptr(q), _ptr(k), _ptr(v), _ptr(kv_lens), _ptr(out), _ptr(dout), _ptr(lse), _ptr(dq),
-                                   _ptr(dk), _ptr(dv), B, H, Hkv, Nq, Nk, d, float(scale), _ptr(workspace), nbytes,
-                                   ctypes.c_void_p(_stream_handle(stream)))
+    """``dq``, ``dk``, ``dv`` None: allocated; ``workspace`` None: allocated."""
+    index, B, H, Hkv, Nq, Nk, d = _check_cross(q, k, v, kv_lens, dtype)
+    _check_tensor("out", out, dtype, q.shape, index)
+    _check_tensor("dout", dout, dtype, q.shape, index)
+    _check_tensor("lse", lse, torch.float32, (B, H, Nq), index)
+    with _on(index, stream):
+        if workspace is None:
+            workspace = torch.empty(fa_bwd_workspace_bytes(B, H, Nq, d), dtype=torch.uint8, device=q.device)
+        if dq is None:
+            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        else:
+            _check_tensor("dq", dq, dtype, q.shape, index)
+            _check_tensor("dk", dk, dtype, k.shape, index)
+            _check_tensor("dv", dv, dtype, k.shape, index)
+        rc = getattr(lib, fn_name)(q.data_ptr(), k.data_ptr(), v.data_ptr(),
+                                   None if kv_lens is None else kv_lens.data_ptr(), out.data_ptr(), dout.data_ptr(),
+                                   lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Nq, Nk, d,
+                                   scale, workspace.data_ptr(), _nbytes(workspace, index), _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, fn_name)
+    return dq, dk, dv
 
 
 def fa_bwd_cross(q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream=None):
@@ -837,17 +872,12 @@ def fa_bwd_cross_fp16(q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, works
 def attention_cross_backward(q, k, v, out, dout, lse, kv_lens=None, scale=None, workspace=None, stream=None):
     """(dq, dk, dv) of sum(dout * out) for out, lse from ``attention_cross``; allocates the outputs and, unless given,
     the workspace with torch."""
-    if q.dtype not in _FP16_SUFFIX:
+    suffix = _FP16_SUFFIX.get(q.dtype)
+    if suffix is None:
         raise ValueError(f"unsupported dtype {q.dtype}")
-    B, H, Nq, d = q.shape
-    scale = 1.0 / math.sqrt(d) if scale is None else scale
-    with _on(q.device, stream) if q.is_cuda else contextlib.nullcontext():
-        if workspace is None:
-            workspace = torch.empty(fa_bwd_workspace_bytes(B, H, Nq, d), dtype=torch.uint8, device=q.device)
-        dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    _raw_bwd_cross("fa_bwd_cross" + _FP16_SUFFIX[q.dtype], q.dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale,
-                   workspace, stream)
-    return dq, dk, dv
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    return _raw_bwd_cross("fa_bwd_cross" + suffix, q.dtype, q, k, v, kv_lens, out, dout, lse, None, None, None, scale,
+                          workspace, stream)
 
 
 def fa_get_device_status(stream=None) -> int:
