@@ -477,11 +477,12 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4)) return FA_ERR_ALIGN;
     if (B < 1 || H < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq) return FA_ERR_SHAPE;
     if (max_len < 1 || max_len > static_cast<int64_t>(max_pages) * page) return FA_ERR_SHAPE;
-    if (n_parts < 1 || n_parts > (1 << 20)) return FA_ERR_SHAPE;
+    if (n_parts < 0 || n_parts > (1 << 20)) return FA_ERR_SHAPE;
     if (static_cast<int64_t>(B) * H * Nq > INT32_MAX) return FA_ERR_SHAPE;
     const int rows = H / Hkv * Nq;
     if (fa::kvq8_tiles(B, Hkv, rows, max_len, d) > (1 << 30)) return FA_ERR_SHAPE;
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < fa::kvq8_workspace_bytes(rows, d, n_parts))
+    if (n_parts > 0 &&
+        (!workspace || !aligned(workspace, 256) || workspace_bytes < fa::kvq8_workspace_bytes(rows, d, n_parts)))
         return FA_ERR_WORKSPACE;
     DeviceInfo *di = device_info();
     if (!di) return FA_ERR_LAUNCH;
@@ -889,7 +890,7 @@ int fa_kvq8_num_parts(int B, int H, int Hkv, int Nq, int max_len, int d) {
 }
 
 long long fa_kvq8_workspace_bytes(int H, int Hkv, int Nq, int d, int n_parts) {
-    if (H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || n_parts < 1) return FA_ERR_SHAPE;
+    if (H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || n_parts < 0) return FA_ERR_SHAPE;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     return static_cast<long long>(fa::kvq8_workspace_bytes(H / Hkv * Nq, d, n_parts));
 }

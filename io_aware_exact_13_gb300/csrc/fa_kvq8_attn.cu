@@ -173,7 +173,29 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
     // ---------------------------------------------------------------- this warp's stretch of the line
     // Each warp adds the lengths up for itself: no barrier between the lengths' arrival and the first page's read.
     int cur, end, b = 0, base = 0, len = 0, per;  // base: first tile of sequence b
-    {
+    int start;  // the CTA's first tile
+    if (p.parts == 0) {  // a CTA for each unit, its tiles in quarters; the line begins with the sequence
+        b = blockIdx.x / units;
+        const int unit = blockIdx.x - b * units;
+        bool bad;
+        len = q8_len(p, b, bad);
+        if (bad && threadIdx.x == 0) atomicExch(p.status, kStatusSeqlensQ8);
+        const int n = q8_tiles(len), quarter = (n + kWarps - 1) / kWarps;
+        if (n == 0) {
+            const int kvh = unit / p.row_tiles, row0 = (unit - kvh * p.row_tiles) * RT, rows = min(RT, p.rows - row0);
+            const size_t at = ((size_t)b * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq + row0;
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + at * D);
+            for (int i = threadIdx.x; i < rows * (D / 8); i += kWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = threadIdx.x; i < rows; i += kWarps * 32) p.lse[at + i] = -INFINITY;
+            return;
+        }
+        per = n;
+        start = unit * n;
+        cur = start + min(n, warp * quarter);
+        end = start + min(n, (warp + 1) * quarter);
+        if (lane < 2) seg[2 * warp + lane].unit = -1;
+        __syncwarp();
+    } else {
         int total = 0, first_len = 0, s_bad = 0;  // first_len: the length of this lane's first sequence
 #pragma unroll 4
         for (int s = lane; s < p.B; s += 32) {
@@ -222,8 +244,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
             base += __shfl_sync(0xffffffffu, incl, 31);
         }
         __syncwarp();
+        start = blockIdx.x * per;
     }
-    const int start = blockIdx.x * per;  // of the CTA
     const int warp_start = cur;
 
     while (cur < end) {
@@ -557,7 +579,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
             if (seg[next].unit == uid) z = next;
         const bool all = seg[a].beg == seg[a].first && seg[z].end == seg[z].last;
         const size_t part = 2 * (size_t)blockIdx.x + (seg[a].first <= start ? 0 : 1);
-        if (threadIdx.x == 0 && seg[a].first < start) p.shared[blockIdx.x] = make_int4(uid, seg[a].first, seg[a].last, per);
+        if (threadIdx.x == 0 && !all && seg[a].first < start) p.shared[blockIdx.x] = make_int4(uid, seg[a].first, seg[a].last, per);
         const int ub = uid / units, unit = uid - ub * units;
         const int kvh = unit / p.row_tiles, row0 = (unit - kvh * p.row_tiles) * RT;
         const size_t row_base = ((size_t)ub * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq + row0;
@@ -599,12 +621,11 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
 // The units that several parts share: their summaries merged onto their common maximum (fa_splitkv.cu's rule). A unit
 // that n parts share is merged by the CTAs of its parts but the first, each doing every (n - 1)-th row; where a CTA has
 // few rows, several groups of threads share a row's summaries out.
-constexpr int kCombineThreads = 512;
+constexpr int kCombineThreads = 128;
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(kCombineThreads) fa_kvq8_combine(const Q8Params p) {
     constexpr int LANES = D / 4, SLOTS = kCombineThreads / LANES;  // four columns of a row per thread
     constexpr int AHEAD = 8;                                      // summaries loaded before the first is used
-    static_assert(RT <= SLOTS, "a slot for each row");
     __shared__ float4 sm_a[SLOTS][LANES];
     __shared__ float sm_m[SLOTS], sm_w[SLOTS];
     grid_dependency_wait();
@@ -622,11 +643,12 @@ __global__ void __launch_bounds__(kCombineThreads) fa_kvq8_combine(const Q8Param
     // part p0 may begin in an earlier unit; every later one begins in this one
     const int slot0 = 2 * p0 + (p0 * per >= first ? 0 : 1);
     const int slot = threadIdx.x / LANES, lane = threadIdx.x % LANES, group = slot % groups;
-    const int r = mine + slot / groups * (n - 1);
-    float M = -INFINITY, W = 0.f;
-    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (slot < groups * rows) {
-        for (int s0 = group; s0 < n; s0 += AHEAD * groups) {
+    for (int r0 = slot / groups; r0 - slot / groups < rows; r0 += SLOTS / groups) {  // as often for every thread
+        const bool in = r0 < rows;
+        const int r = mine + (in ? r0 : 0) * (n - 1);
+        float M = -INFINITY, W = 0.f;
+        float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s0 = in ? group : n; s0 < n; s0 += AHEAD * groups) {
             float l[AHEAD];
             float4 v[AHEAD];
 #pragma unroll
@@ -658,34 +680,38 @@ __global__ void __launch_bounds__(kCombineThreads) fa_kvq8_combine(const Q8Param
                 A.w = fmaf(w, v[k].w, A.w);
             }
         }
-        sm_a[slot][lane] = A;
-        if (lane == 0) {
-            sm_m[slot] = M;
-            sm_w[slot] = W;
+        if (groups > 1) {
+            sm_a[slot][lane] = A;
+            if (lane == 0) {
+                sm_m[slot] = M;
+                sm_w[slot] = W;
+            }
+            __syncthreads();
+            if (group == 0) {
+                for (int i = 1; i < groups; ++i) M = fmaxf(M, sm_m[slot + i]);
+                W = 0.f;
+                A = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int i = 0; i < groups && M != -INFINITY; ++i) {
+                    const float f = __expf(sm_m[slot + i] - M);
+                    const float4 v = sm_a[slot + i][lane];
+                    W += f * sm_w[slot + i];
+                    A.x = fmaf(f, v.x, A.x);
+                    A.y = fmaf(f, v.y, A.y);
+                    A.z = fmaf(f, v.z, A.z);
+                    A.w = fmaf(f, v.w, A.w);
+                }
+            }
+            __syncthreads();
+        }
+        if (group == 0 && in) {
+            const float inv = W > 0.f ? 1.0f / W : 0.f;
+            uint2 o;
+            o.x = pack16<T>(A.x * inv, A.y * inv);
+            o.y = pack16<T>(A.z * inv, A.w * inv);
+            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * lane) = o;
+            if (lane == 0) p.lse[row_base + r] = W > 0.f ? M + __logf(W) : -INFINITY;
         }
     }
-    __syncthreads();
-    if (group != 0 || slot >= groups * rows) return;
-    for (int i = 1; i < groups; ++i) M = fmaxf(M, sm_m[slot + i]);
-    W = 0.f;
-    A = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
-        for (int i = 0; i < groups; ++i) {
-            const float f = __expf(sm_m[slot + i] - M);
-            const float4 v = sm_a[slot + i][lane];
-            W += f * sm_w[slot + i];
-            A.x = fmaf(f, v.x, A.x);
-            A.y = fmaf(f, v.y, A.y);
-            A.z = fmaf(f, v.z, A.z);
-            A.w = fmaf(f, v.w, A.w);
-        }
-    }
-    const float inv = W > 0.f ? 1.0f / W : 0.f;
-    uint2 o;
-    o.x = pack16<T>(A.x * inv, A.y * inv);
-    o.y = pack16<T>(A.z * inv, A.w * inv);
-    *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * lane) = o;
-    if (lane == 0) p.lse[row_base + r] = W > 0.f ? M + __logf(W) : -INFINITY;
 }
 
 int page_log2(int page) {
@@ -707,7 +733,9 @@ template <typename T, int D, int FMT, int NT, bool CAUSAL>
 int launch_q8(const Kvq8AttnArgs &a) {
     using C = Q8Cfg<D, NT>;
     auto kern = fa_kvq8_partial<T, D, FMT, NT, CAUSAL>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess) return -5;
+    if (C::SMEM > 48 * 1024 &&
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
+        return -5;
     Q8Params p;
     p.q = a.q;
     p.out = a.out;
@@ -736,9 +764,10 @@ int launch_q8(const Kvq8AttnArgs &a) {
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     // (not as a programmatic dependent: its CTAs would take their places beside those of the kernel ahead, and
     // the one wave that the parts are sized for would become two)
-    kern<<<a.parts, kWarps * 32, C::SMEM, a.stream>>>(p);
+    const int grid = a.parts > 0 ? a.parts : a.B * a.c.Hkv * p.row_tiles;
+    kern<<<grid, kWarps * 32, C::SMEM, a.stream>>>(p);
     if (cudaGetLastError() != cudaSuccess) return -5;
-    if (a.parts == 1) return 0;
+    if (a.parts <= 1) return 0;
     return launch_dependent(fa_kvq8_combine<T, D, C::RT>, dim3(a.parts), dim3(kCombineThreads), 0,
                             a.stream, p) == cudaSuccess
                ? 0
@@ -772,8 +801,12 @@ long long kvq8_tiles(int B, int Hkv, int rows, int max_len, int d) {
     return (long long)B * Hkv * units_per_head(rows, d) * ((max_len + kTileKeys - 1) / kTileKeys);
 }
 
+// Short contexts (up to 512 keys, eight tiles for a warp): a CTA for each unit and no merge kernel, 7.8 us against 12.0
+// of the line for B 16, H 32 / 8, d 128, 300 keys, 15.6 against 20.4 for B 64, d 64, 4 rows; from 1000 keys on the line is
+// ahead (B 1: 8.6 against 15.7 us) or level (B 64: 28.8 against 26.0). Otherwise one part for each CTA that can be
+// resident, and at least one tile for each of a CTA's warps.
 int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int d, int num_sms) {
-    // one part for each CTA that can be resident, and at least one tile for each of a CTA's warps
+    if (max_len <= 512) return 0;
     const int nt = tiles_per_unit(rows, d);
     const long long slots = (long long)q8_ctas(d, nt) * num_sms;
     const long long by_len = (kvq8_tiles(B, Hkv, rows, max_len, d) + kWarps - 1) / kWarps;

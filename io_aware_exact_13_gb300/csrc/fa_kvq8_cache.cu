@@ -106,17 +106,10 @@ __global__ void __launch_bounds__(NT) fa_kvq8_append_kernel(const AppendParams p
     const int n = c1 - c0;
     const int pg = (held >> p.page_shift) + ord;
     if (n == 0 || pg > ((held + n - 1) >> p.page_shift)) return;
-    const int phys = __ldg(p.page_table + (long long)seq * p.max_pages + pg);
-    if (phys < 0 || phys >= p.n_pages) {
-        if (threadIdx.x == 0) atomicExch(p.status, kStatusPage);
-        return;
-    }
+    const int phys = __ldg(p.page_table + (long long)seq * p.max_pages + pg);  // looked at once the values are on their way
     const int t0 = pg << p.page_shift;  // position of the page's first slot
     const int lo = max(held, t0) - t0;  // slots [lo, hi) take new tokens, [0, lo) hold earlier ones
     const int hi = min(held + n - t0, page);
-    const long long unit = (long long)phys * p.Hkv + head;
-    float *scale = p.scale[kv] + unit;
-    const float s_old = lo > 0 ? *scale : 0.0f;
 
     const T *src = static_cast<const T *>(p.src[kv]) + (long long)head * p.head[kv];
     const int vec_shift = p.d_shift - 3;  // 8-value vectors per row
@@ -130,6 +123,13 @@ __global__ void __launch_bounds__(NT) fa_kvq8_append_kernel(const AppendParams p
         if (slot >= lo && slot < hi)
             x[i] = __ldg(reinterpret_cast<const uint4 *>(src + (long long)(c0 + (t0 + slot - held)) * p.token[kv] + chunk * 8));
     }
+    if (phys < 0 || phys >= p.n_pages) {
+        if (threadIdx.x == 0) atomicExch(p.status, kStatusPage);
+        return;
+    }
+    const long long unit = (long long)phys * p.Hkv + head;
+    float *scale = p.scale[kv] + unit;
+    const float s_old = lo > 0 ? *scale : 0.0f;
 #pragma unroll
     for (int i = 0; i < VEC; ++i) {
         const uint32_t a = __vmaxs2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
@@ -207,8 +207,9 @@ struct ReadParams {
     int nseq, total, max_len, groups_per_seq;
 };
 
-constexpr int kReadThreads = 256;
-constexpr int kReadTokens = 64;  // tokens per CTA: K and V of one head
+// Small CTAs again: 64 threads and 16 tokens 80.0 us, 128 and 32 82.9, 256 and 64 86.0 (87000 tokens, 8 heads, d 128).
+constexpr int kReadThreads = 64;
+constexpr int kReadTokens = 16;  // tokens per CTA: K and V of one head
 
 // One CTA reads kReadTokens tokens of one (sequence, head), K and V: a thread's loads (16 codes
 // each) are all issued before the first is used.
@@ -319,12 +320,14 @@ int launch_append_t(const Kvq8AppendArgs &a) {
     const long long grid = 2ll * a.c.Hkv * pages * a.nseq;
     if (grid > INT32_MAX) return -3;
     const unsigned g = static_cast<unsigned>(grid);
-    // threads and vectors so that a CTA's registers hold one page of one head
+    // Eight vectors per thread (a warp at least): small CTAs keep more of them, and of their dependent first reads (lengths,
+    // page), on an SM. With 128 or 256 threads for every page size, pages of 16 tokens took 86 us instead of 72, of 64
+    // tokens 77 instead of 65 (74000 tokens, 8 heads, d 128).
     switch (a.c.page * a.c.d / 8) {
-        case 128: fa_kvq8_append_kernel<T, FMT, 128, 1><<<g, 128, 0, a.stream>>>(p); break;
-        case 256: fa_kvq8_append_kernel<T, FMT, 128, 2><<<g, 128, 0, a.stream>>>(p); break;
-        case 512: fa_kvq8_append_kernel<T, FMT, 128, 4><<<g, 128, 0, a.stream>>>(p); break;
-        case 1024: fa_kvq8_append_kernel<T, FMT, 256, 4><<<g, 256, 0, a.stream>>>(p); break;
+        case 128: fa_kvq8_append_kernel<T, FMT, 32, 4><<<g, 32, 0, a.stream>>>(p); break;
+        case 256: fa_kvq8_append_kernel<T, FMT, 32, 8><<<g, 32, 0, a.stream>>>(p); break;
+        case 512: fa_kvq8_append_kernel<T, FMT, 64, 8><<<g, 64, 0, a.stream>>>(p); break;
+        case 1024: fa_kvq8_append_kernel<T, FMT, 128, 8><<<g, 128, 0, a.stream>>>(p); break;
         case 2048: fa_kvq8_append_kernel<T, FMT, 256, 8><<<g, 256, 0, a.stream>>>(p); break;
         default: return -4;
     }

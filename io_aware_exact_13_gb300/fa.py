@@ -630,11 +630,12 @@ def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, ca
             _check_tensor("lse", lse, torch.float32, shape[:3], index)
         if n_parts is None:
             n_parts = fa_kvq8_num_parts(B, H, Hkv, Nq, max_len, d)
-        if workspace is None:
+        if workspace is None and n_parts > 0:
             workspace = torch.empty(fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts), dtype=torch.uint8, device=q.device)
         rc = getattr(lib, fn_name)(q.data_ptr(), *cache_ptrs, n_pages, max_pages, page, kv_lens.data_ptr(),
                                    out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, max_len, d, fmt, scale, bool(causal),
-                                   n_parts, workspace.data_ptr(), _nbytes(workspace, index),
+                                   n_parts, None if workspace is None else workspace.data_ptr(),
+                                   _nbytes(workspace, index),
                                    _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, fn_name)
