@@ -83,15 +83,15 @@ struct AppendParams {
     int nseq, total, max_new, pages_per_seq;
 };
 
-// One CTA writes the new tokens of one (sequence, page, head, K or V): every value is read once
-// into registers (VEC 16-byte vectors per thread hold the whole page), the page's largest
-// magnitude is reduced over the CTA, and the codes are written as 8-byte vectors.
-template <typename T, int FMT, int NT, int VEC>
-__global__ void __launch_bounds__(NT) fa_kvq8_append_kernel(const AppendParams p) {
+// One CTA writes the new tokens of one (sequence, page, head), K or V, or both (KVS = 2, small pages): every value is
+// read once into registers (VEC 16-byte vectors per thread hold the whole page), the page's largest magnitude is
+// reduced over the CTA, and the codes are written as 8-byte vectors.
+template <typename T, int FMT, int NT, int VEC, int KVS>
+__global__ void __launch_bounds__(NT, KVS == 1 ? 1024 / NT : 1) fa_kvq8_append_kernel(const AppendParams p) {
     __shared__ uint32_t warp_max[NT / 32];
     uint32_t u = blockIdx.x;
-    const int kv = u & 1u;
-    u >>= 1;
+    const int kv0 = KVS == 2 ? 0 : u & 1u;
+    if (KVS == 1) u >>= 1;
     const int head = u % p.Hkv;
     u /= p.Hkv;
     const int ord = u % p.pages_per_seq, seq = u / p.pages_per_seq;
@@ -111,88 +111,97 @@ __global__ void __launch_bounds__(NT) fa_kvq8_append_kernel(const AppendParams p
     const int lo = max(held, t0) - t0;  // slots [lo, hi) take new tokens, [0, lo) hold earlier ones
     const int hi = min(held + n - t0, page);
 
-    const T *src = static_cast<const T *>(p.src[kv]) + (long long)head * p.head[kv];
     const int vec_shift = p.d_shift - 3;  // 8-value vectors per row
-    uint4 x[VEC];
-    uint32_t most = 0;  // the largest magnitude's 15 bits, in either half
+    uint4 xs[KVS][VEC];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const int vec = threadIdx.x + i * NT;
-        const int slot = vec >> vec_shift, chunk = vec & ((1 << vec_shift) - 1);
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (slot >= lo && slot < hi)
-            x[i] = __ldg(reinterpret_cast<const uint4 *>(src + (long long)(c0 + (t0 + slot - held)) * p.token[kv] + chunk * 8));
+    for (int j = 0; j < KVS; ++j) {
+        const T *src = static_cast<const T *>(p.src[kv0 + j]) + (long long)head * p.head[kv0 + j];
+        const long long token = p.token[kv0 + j];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int vec = threadIdx.x + i * NT;
+            const int slot = vec >> vec_shift, chunk = vec & ((1 << vec_shift) - 1);
+            xs[j][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (slot >= lo && slot < hi)
+                xs[j][i] = __ldg(reinterpret_cast<const uint4 *>(src + (long long)(c0 + (t0 + slot - held)) * token + chunk * 8));
+        }
     }
     if (phys < 0 || phys >= p.n_pages) {
         if (threadIdx.x == 0) atomicExch(p.status, kStatusPage);
         return;
     }
     const long long unit = (long long)phys * p.Hkv + head;
-    float *scale = p.scale[kv] + unit;
-    const float s_old = lo > 0 ? *scale : 0.0f;
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const uint32_t a = __vmaxs2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
-        const uint32_t b = __vmaxs2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu);
-        most = __vmaxs2(most, __vmaxs2(a, b));
-    }
-    auto block_max = [&](uint32_t m) {
-        m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
-        if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
-        __syncthreads();
-        m = warp_max[0];
-#pragma unroll
-        for (int w = 1; w < NT / 32; ++w) m = max(m, warp_max[w]);
-        return m;
-    };
-    uint32_t top = block_max(most);
-    if (top >= exponent_mask<T>()) {  // infinities or NaN: no code stands for them; they are written as 0 and reported
-        if (threadIdx.x == 0) atomicExch(p.status, kStatusValue);
-        most = 0;
+    for (int j = 0; j < KVS; ++j) {
+        if (j > 0) __syncthreads();  // warp_max is used again
+        float *scale = p.scale[kv0 + j] + unit;
+        const float s_old = lo > 0 ? *scale : 0.0f;
+        uint4 (&x)[VEC] = xs[j];
+        uint32_t most = 0;  // the largest magnitude's 15 bits, in either half
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            uint32_t *w = reinterpret_cast<uint32_t *>(&x[i]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if ((w[e] & 0x7FFFu) >= exponent_mask<T>()) w[e] &= 0xFFFF0000u;
-                if (((w[e] >> 16) & 0x7FFFu) >= exponent_mask<T>()) w[e] &= 0x0000FFFFu;
-                most = __vmaxs2(most, w[e] & 0x7FFF7FFFu);
-            }
+            const uint32_t a = __vmaxs2(x[i].x & 0x7FFF7FFFu, x[i].y & 0x7FFF7FFFu);
+            const uint32_t b = __vmaxs2(x[i].z & 0x7FFF7FFFu, x[i].w & 0x7FFF7FFFu);
+            most = __vmaxs2(most, __vmaxs2(a, b));
         }
-        __syncthreads();  // every thread has read the first maxima
-        top = block_max(most);
-    }
-    const float s = fmaxf(scale_for<FMT>(unpack2<T>(top).x), s_old);
-    const float inv = s > 0.0f ? 1.0f / s : 0.0f;
-    if (threadIdx.x == 0) *scale = s;  // every thread read the old one before block_max's barrier
-    uint8_t *dst = p.codes[kv] + (unit << (p.page_shift + p.d_shift));
-    const bool grew = lo > 0 && s != s_old;
-    const float ratio = s_old * inv;
+        auto block_max = [&](uint32_t m) {
+            m = __reduce_max_sync(0xffffffffu, max(m & 0xFFFFu, m >> 16));
+            if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = m;
+            __syncthreads();
+            m = warp_max[0];
 #pragma unroll
-    for (int i = 0; i < VEC; ++i) {
-        const int vec = threadIdx.x + i * NT;
-        const int slot = vec >> vec_shift;
-        if (slot >= lo && slot < hi) {
-            const float2 a = unpack2<T>(x[i].x), b = unpack2<T>(x[i].y), c = unpack2<T>(x[i].z), d = unpack2<T>(x[i].w);
-            uint2 o;
-            o.x = encode4<FMT>(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
-            o.y = encode4<FMT>(c.x * inv, c.y * inv, d.x * inv, d.y * inv);
-            *reinterpret_cast<uint2 *>(dst + (long long)vec * 8) = o;
-        } else if (grew && slot < lo) {
-            const uint2 was = *reinterpret_cast<const uint2 *>(dst + (long long)vec * 8);
-            uint2 o;
-            const uint32_t w[2] = {was.x, was.y};
-            uint32_t r[2];
+            for (int w = 1; w < NT / 32; ++w) m = max(m, warp_max[w]);
+            return m;
+        };
+        uint32_t top = block_max(most);
+        if (top >= exponent_mask<T>()) {  // infinities or NaN: no code stands for them; they are written as 0 and reported
+            if (threadIdx.x == 0) atomicExch(p.status, kStatusValue);
+            most = 0;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                uint32_t h0, h1;
-                codes_to_half2<FMT>(w[e], h0, h1);
-                const float2 a = unpack2<__half>(h0), b = unpack2<__half>(h1);
-                r[e] = encode4<FMT>(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+            for (int i = 0; i < VEC; ++i) {
+                uint32_t *w = reinterpret_cast<uint32_t *>(&x[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if ((w[e] & 0x7FFFu) >= exponent_mask<T>()) w[e] &= 0xFFFF0000u;
+                    if (((w[e] >> 16) & 0x7FFFu) >= exponent_mask<T>()) w[e] &= 0x0000FFFFu;
+                    most = __vmaxs2(most, w[e] & 0x7FFF7FFFu);
+                }
             }
-            o.x = r[0];
-            o.y = r[1];
-            *reinterpret_cast<uint2 *>(dst + (long long)vec * 8) = o;
+            __syncthreads();  // every thread has read the first maxima
+            top = block_max(most);
+        }
+        const float s = fmaxf(scale_for<FMT>(unpack2<T>(top).x), s_old);
+        const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+        if (threadIdx.x == 0) *scale = s;  // every thread read the old one before block_max's barrier
+        uint8_t *dst = p.codes[kv0 + j] + (unit << (p.page_shift + p.d_shift));
+        const bool grew = lo > 0 && s != s_old;
+        const float ratio = s_old * inv;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const int vec = threadIdx.x + i * NT;
+            const int slot = vec >> vec_shift;
+            if (slot >= lo && slot < hi) {
+                const float2 a = unpack2<T>(x[i].x), b = unpack2<T>(x[i].y), c = unpack2<T>(x[i].z), d = unpack2<T>(x[i].w);
+                uint2 o;
+                o.x = encode4<FMT>(a.x * inv, a.y * inv, b.x * inv, b.y * inv);
+                o.y = encode4<FMT>(c.x * inv, c.y * inv, d.x * inv, d.y * inv);
+                *reinterpret_cast<uint2 *>(dst + (long long)vec * 8) = o;
+            } else if (grew && slot < lo) {
+                const uint2 was = *reinterpret_cast<const uint2 *>(dst + (long long)vec * 8);
+                uint2 o;
+                const uint32_t w[2] = {was.x, was.y};
+                uint32_t r[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t h0, h1;
+                    codes_to_half2<FMT>(w[e], h0, h1);
+                    const float2 a = unpack2<__half>(h0), b = unpack2<__half>(h1);
+                    r[e] = encode4<FMT>(a.x * ratio, a.y * ratio, b.x * ratio, b.y * ratio);
+                }
+                o.x = r[0];
+                o.y = r[1];
+                *reinterpret_cast<uint2 *>(dst + (long long)vec * 8) = o;
+            }
         }
     }
 }
@@ -317,18 +326,19 @@ int launch_append_t(const Kvq8AppendArgs &a) {
     long long pages = ((long long)a.max_new + a.c.page - 2) / a.c.page + 1;
     if (pages > a.c.max_pages) pages = a.c.max_pages;
     p.pages_per_seq = static_cast<int>(pages);
-    const long long grid = 2ll * a.c.Hkv * pages * a.nseq;
+    const int vecs = a.c.page * a.c.d / 8;
+    const long long grid = (vecs > 128 ? 2ll : 1ll) * a.c.Hkv * pages * a.nseq;
     if (grid > INT32_MAX) return -3;
     const unsigned g = static_cast<unsigned>(grid);
     // Eight vectors per thread (a warp at least): small CTAs keep more of them, and of their dependent first reads (lengths,
     // page), on an SM. With 128 or 256 threads for every page size, pages of 16 tokens took 86 us instead of 72, of 64
-    // tokens 77 instead of 65 (74000 tokens, 8 heads, d 128).
-    switch (a.c.page * a.c.d / 8) {
-        case 128: fa_kvq8_append_kernel<T, FMT, 32, 4><<<g, 32, 0, a.stream>>>(p); break;
-        case 256: fa_kvq8_append_kernel<T, FMT, 32, 8><<<g, 32, 0, a.stream>>>(p); break;
-        case 512: fa_kvq8_append_kernel<T, FMT, 64, 8><<<g, 64, 0, a.stream>>>(p); break;
-        case 1024: fa_kvq8_append_kernel<T, FMT, 128, 8><<<g, 128, 0, a.stream>>>(p); break;
-        case 2048: fa_kvq8_append_kernel<T, FMT, 256, 8><<<g, 256, 0, a.stream>>>(p); break;
+    // tokens 77 instead of 65 (74000 tokens, 8 heads, d 128). At 16 tokens of d 64 a warp takes K and V: 36 us instead of 53.
+    switch (vecs) {
+        case 128: fa_kvq8_append_kernel<T, FMT, 32, 4, 2><<<g, 32, 0, a.stream>>>(p); break;
+        case 256: fa_kvq8_append_kernel<T, FMT, 32, 8, 1><<<g, 32, 0, a.stream>>>(p); break;
+        case 512: fa_kvq8_append_kernel<T, FMT, 64, 8, 1><<<g, 64, 0, a.stream>>>(p); break;
+        case 1024: fa_kvq8_append_kernel<T, FMT, 128, 8, 1><<<g, 128, 0, a.stream>>>(p); break;
+        case 2048: fa_kvq8_append_kernel<T, FMT, 256, 8, 1><<<g, 256, 0, a.stream>>>(p); break;
         default: return -4;
     }
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
