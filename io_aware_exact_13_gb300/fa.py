@@ -476,7 +476,7 @@ def kv_cache_q8(n_pages, Hkv, page, d, dtype=torch.int8, device="cuda") -> KVCac
 def _on(index, stream):
     """Context in which device ``index`` is current and torch allocates for ``stream`` (None: the device's current one)."""
     if stream is None:
-        return _NOTHING if index == torch.cuda.current_device() else torch.cuda.device(index)
+        return _NOTHING if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
     if stream.device.index != index:
@@ -514,6 +514,9 @@ def _nbytes(workspace, index):
     return workspace.numel() * workspace.element_size()
 
 
+_F32, _I32 = torch.float32, torch.int32
+
+
 def _check_kvq8(cache, page_table):
     """(device index, codes' shape, arguments of the cache for the C call) after checking its tensors against each
     other, and the page table's form."""
@@ -525,15 +528,18 @@ def _check_kvq8(cache, page_table):
     index = kc.get_device()
     if index < 0:
         raise ValueError("the cache must be on a CUDA device")
-    _check_tensor("k_codes", kc, kc.dtype, shape, index)
-    _check_tensor("v_codes", vc, kc.dtype, shape, index)
-    scales = shape[:2]
-    _check_tensor("k_scale", ks, torch.float32, scales, index)
-    _check_tensor("v_scale", vs, torch.float32, scales, index)
-    table = page_table.shape
-    if len(table) != 2:
-        raise ValueError("page_table must be int32 [nseq, max_pages]")
-    _check_tensor("page_table", page_table, torch.int32, table, index)
+    table, scales = page_table.shape, shape[:2]
+    if not (vc.dtype is kc.dtype and vc.shape == shape and ks.dtype is _F32 and vs.dtype is _F32 and ks.shape == scales
+            and vs.shape == scales and page_table.dtype is _I32 and len(table) == 2 and vc.get_device() == index
+            and ks.get_device() == index and vs.get_device() == index and page_table.get_device() == index
+            and kc.is_contiguous() and vc.is_contiguous() and ks.is_contiguous() and vs.is_contiguous()
+            and page_table.is_contiguous()):
+        if len(table) != 2:
+            raise ValueError("page_table must be int32 [nseq, max_pages]")
+        for name, t, dtype, want in (("k_codes", kc, kc.dtype, shape), ("v_codes", vc, kc.dtype, shape),
+                                     ("k_scale", ks, _F32, scales), ("v_scale", vs, _F32, scales),
+                                     ("page_table", page_table, _I32, table)):
+            _check_tensor(name, t, dtype, want, index)
     ptrs = (kc.data_ptr(), vc.data_ptr(), ks.data_ptr(), vs.data_ptr(), page_table.data_ptr())
     return index, fmt, shape, table, ptrs
 
@@ -624,14 +630,14 @@ def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, ca
     with _on(index, stream):
         if out is None:
             out = torch.empty_like(q)
-            lse = torch.empty(shape[:3], dtype=torch.float32, device=q.device)
+            lse = cache.k_scale.new_empty((B, H, Nq))
         else:
             _check_tensor("out", out, dtype, shape, index)
             _check_tensor("lse", lse, torch.float32, shape[:3], index)
         if n_parts is None:
             n_parts = fa_kvq8_num_parts(B, H, Hkv, Nq, max_len, d)
         if workspace is None and n_parts > 0:
-            workspace = torch.empty(fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts), dtype=torch.uint8, device=q.device)
+            workspace = kv_lens.new_empty((fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) + 3) // 4)
         rc = getattr(lib, fn_name)(q.data_ptr(), *cache_ptrs, n_pages, max_pages, page, kv_lens.data_ptr(),
                                    out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, max_len, d, fmt, scale, bool(causal),
                                    n_parts, None if workspace is None else workspace.data_ptr(),

@@ -87,7 +87,7 @@ def test_append_and_read_sizes_are_refused(fa):
 
 def test_attention_sizes_and_workspace_are_refused(fa):
     for kw in (dict(B=0), dict(H=0), dict(H=3), dict(Nq=0), dict(Nq=17), dict(max_len=0), dict(max_len=65),
-               dict(n_parts=0), dict(n_parts=(1 << 20) + 1), dict(B=1 << 20, H=1 << 12),
+               dict(n_parts=-1), dict(n_parts=(1 << 20) + 1), dict(B=1 << 20, H=1 << 12),
                dict(B=1 << 18, max_pages=1 << 14, max_len=1 << 18)):
         assert attend(fa, **kw) == fa.FA_ERR_SHAPE, kw
     need = fa.fa_kvq8_workspace_bytes(4, 2, 1, 64, 2)
@@ -100,7 +100,7 @@ def test_attention_sizes_and_workspace_are_refused(fa):
     assert fa.lib.fa_kvq8_workspace_bytes(4, 2, 1, 96, 1) == fa.FA_ERR_UNSUPPORTED
     for B, Hkv, n in ((1, 1, 1), (1, 8, 100000), (300, 8, 5000), (4, 2, 63)):
         s = fa.fa_kvq8_num_parts(B, 4 * Hkv, Hkv, 1, n, 128)
-        assert 1 <= s <= B * Hkv * ((n + 63) // 64)
+        assert (s == 0) == (n <= 512) and s <= B * Hkv * ((n + 63) // 64)
 
 
 def test_binding_refuses(fa):
