@@ -257,12 +257,13 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *ou
  * causal != 0 aligns the last query with the last key: query i sees keys j <= i + kv_lens[b] - Nq.
  * A row that sees no key gets out = 0 and lse = -inf. Codes, scores, sums and accumulators are
  * not rounded below fp32; the softmax weights are rounded to fp16 before they multiply V (bf16
- * queries enter the products exactly down to 2^-24 of their row's largest magnitude). All sequences'
- * keys are cut, as one line, into n_parts equal stretches, whatever the lengths are; the summaries
- * of sequences that more than one part shares go through the workspace (256-byte aligned, at least
- * fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) bytes, contents on entry irrelevant, not shared by
- * overlapping calls). The result does not depend on timing: two calls on the same inputs, with the
- * same n_parts, give the same bits.
+ * queries enter the products exactly down to 2^-24 of their row's largest magnitude). With n_parts
+ * > 0 all sequences' keys are cut, as one line, into n_parts equal stretches, whatever the lengths
+ * are; the summaries of sequences that more than one part shares go through the workspace (256-byte
+ * aligned, at least fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) bytes, contents on entry
+ * irrelevant, not shared by overlapping calls). n_parts = 0 gives each sequence and K/V head a CTA of
+ * its own, in one launch and without a workspace (it may be NULL): for short contexts. The result
+ * does not depend on timing: two calls on the same inputs, with the same n_parts, give the same bits.
  * Other errors as for fa_fwd_splitkv; FA_ERR_UNSUPPORTED for another page or d, FA_ERR_ARG for
  * another format, FA_ERR_SHAPE for strides that are no multiples of 8. */
 enum { FA_KVQ8_INT8 = 0, FA_KVQ8_E4M3 = 1 };
@@ -287,7 +288,8 @@ int fa_kvq8_read_fp16(const void *k_codes, const void *v_codes, const float *k_s
                       const int *first_or_null, int nseq, int total, int max_len, void *k, void *v, int Hkv, int d,
                       int format, void *stream);
 
-/* A part count that fills the GPU once, without parts of less than 64 keys (>= 1), or a negative status. */
+/* A part count for lengths up to max_len: 0 for short contexts, otherwise one that fills the GPU once, without parts of
+ * less than 64 keys; or a negative status. */
 int fa_kvq8_num_parts(int B, int H, int Hkv, int Nq, int max_len, int d);
 /* Workspace bytes fa_fwd_kvq8 needs, or a negative status. */
 long long fa_kvq8_workspace_bytes(int H, int Hkv, int Nq, int d, int n_parts);

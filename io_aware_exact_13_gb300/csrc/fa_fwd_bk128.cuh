@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *lse_out = CROSS && p.n_splits > 1 ? p.lse_part + (part - orow_idx) : p.lse;
             if (row < rows_end)  // lse: [B][H][N], or [H][total] for a packed batch
                 lse_out[VARLEN ? (size_t)(bh % p.H) * p.total + itm.tok0 + row : (size_t)bh * p.N + row] =
-                    (l > 0.0f) ? (m_ref + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
+                    (CROSS ? l != 0.0f : l > 0.0f) ? (m_ref + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
         }
     }
 

@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                 const int r = 8 * t + 2 * c + e;
                 float f = ex2_approx(mw[t][e] - m[t][e]);  // 0 where every weight was (mw = kNone)
                 if (whole) {
-                    f = ls > 0.f ? f / ls : 0.f;
+                    f = ls == 0.f ? 0.f : f / ls;  // (a sum that is NaN, from a NaN query, stays NaN)
                     if (row0 + r < p.rows) {
                         uint32_t w[MT];
 #pragma unroll
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                         T *dst = static_cast<T *>(p.out) + (row_base + row0 + r) * D + C::VB * g;
 #pragma unroll
                         for (int i = 0; i < MT; i += 4) st_global_v4(dst + 2 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
-                        if (g == 0) p.lse[row_base + row0 + r] = ls > 0.f ? (m[t][e] + lg2_approx(ls)) * kLn2 : -INFINITY;
+                        if (g == 0) p.lse[row_base + row0 + r] = ls == 0.f ? -INFINITY : (m[t][e] + lg2_approx(ls)) * kLn2;
                     }
                 } else {
                     float4 *dst = reinterpret_cast<float4 *>(sm_o + (slot * RT + r) * C::PITCH + C::VB * g);
@@ -600,8 +600,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                 A.z = fmaf(f, v.z, A.z);
                 A.w = fmaf(f, v.w, A.w);
             }
-            const float inv = L > 0.f ? 1.0f / L : 0.f;
-            const float lse = L > 0.f ? (M + lg2_approx(L)) * kLn2 : -INFINITY;
+            const float inv = L == 0.f ? 0.f : 1.0f / L;
+            const float lse = L == 0.f ? -INFINITY : (M + lg2_approx(L)) * kLn2;
             if (all) {
                 uint2 w;
                 w.x = pack16<T>(A.x * inv, A.y * inv);
@@ -664,7 +664,7 @@ __global__ void __launch_bounds__(kCombineThreads) fa_kvq8_combine(const Q8Param
             }
             float m = M;
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) m = fmaxf(m, l[k]);
+            for (int k = 0; k < AHEAD; ++k) m = fmaxf(m, isnan(l[k]) ? 0.f : l[k]);  // NaN goes through the weights
             if (m == -INFINITY) continue;  // parts that saw no key
             const float f = __expf(M - m);
             W *= f;
@@ -704,12 +704,12 @@ __global__ void __launch_bounds__(kCombineThreads) fa_kvq8_combine(const Q8Param
             __syncthreads();
         }
         if (group == 0 && in) {
-            const float inv = W > 0.f ? 1.0f / W : 0.f;
+            const float inv = W == 0.f ? 0.f : 1.0f / W;
             uint2 o;
             o.x = pack16<T>(A.x * inv, A.y * inv);
             o.y = pack16<T>(A.z * inv, A.w * inv);
             *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * lane) = o;
-            if (lane == 0) p.lse[row_base + r] = W > 0.f ? M + __logf(W) : -INFINITY;
+            if (lane == 0) p.lse[row_base + r] = W == 0.f ? -INFINITY : M + __logf(W);
         }
     }
 }

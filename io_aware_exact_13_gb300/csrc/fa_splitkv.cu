@@ -390,7 +390,10 @@ __global__ void __launch_bounds__(D) fa_splitkv_combine(const float *__restrict_
     const int row = blockIdx.x;  // (b*h)*Nq + i
     const int e = threadIdx.x;
     float M = -INFINITY;
-    for (int s = 0; s < n_splits; ++s) M = fmaxf(M, lse_part[(size_t)s * rows + row]);
+    for (int s = 0; s < n_splits; ++s) {
+        const float ls = lse_part[(size_t)s * rows + row];
+        M = fmaxf(M, isnan(ls) ? 0.f : ls);  // NaN goes through the weights
+    }
     float W = 0.f, A = 0.f;
     if (M != -INFINITY) {
         for (int s = 0; s < n_splits; ++s) {
@@ -400,8 +403,8 @@ __global__ void __launch_bounds__(D) fa_splitkv_combine(const float *__restrict_
             A = fmaf(w, o_part[((size_t)s * rows + row) * D + e], A);
         }
     }
-    out[(size_t)row * D + e] = Vec<T>::from_f(W > 0.f ? A / W : 0.f);
-    if (e == 0) lse[row] = W > 0.f ? M + __logf(W) : -INFINITY;
+    out[(size_t)row * D + e] = Vec<T>::from_f(W == 0.f ? 0.f : A / W);
+    if (e == 0) lse[row] = W == 0.f ? -INFINITY : M + __logf(W);
 }
 
 template <typename T, int D, int NQ>

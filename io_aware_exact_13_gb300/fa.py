@@ -634,12 +634,11 @@ def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, ca
         else:
             _check_tensor("out", out, dtype, shape, index)
             _check_tensor("lse", lse, torch.float32, shape[:3], index)
-        if n_parts is None:
-            n_parts = fa_kvq8_num_parts(B, H, Hkv, Nq, max_len, d)
+        n_parts = fa_kvq8_num_parts(B, H, Hkv, Nq, max_len, d) if n_parts is None else int(n_parts)
         if workspace is None and n_parts > 0:
             workspace = kv_lens.new_empty((fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) + 3) // 4)
         rc = getattr(lib, fn_name)(q.data_ptr(), *cache_ptrs, n_pages, max_pages, page, kv_lens.data_ptr(),
-                                   out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, max_len, d, fmt, scale, bool(causal),
+                                   out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, max_len, d, fmt, float(scale), bool(causal),
                                    n_parts, None if workspace is None else workspace.data_ptr(),
                                    _nbytes(workspace, index),
                                    _raw_stream(index, stream))
@@ -811,7 +810,7 @@ def _raw_cross(fn_name, dtype, q, k, v, kv_lens, out, lse, scale, n_splits, work
             _check_tensor("lse", lse, torch.float32, (B, H, Nq), index)
         rc = getattr(lib, fn_name)(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                    None if kv_lens is None else kv_lens.data_ptr(), out.data_ptr(), lse.data_ptr(), B, H,
-                                   Hkv, Nq, Nk, d, scale, int(n_splits),
+                                   Hkv, Nq, Nk, d, float(scale), int(n_splits),
                                    None if workspace is None else workspace.data_ptr(), _nbytes(workspace, index),
                                    _raw_stream(index, stream))
     if rc != FA_OK:
@@ -858,7 +857,8 @@ def _raw_bwd_cross(fn_name, dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv,
         rc = getattr(lib, fn_name)(q.data_ptr(), k.data_ptr(), v.data_ptr(),
                                    None if kv_lens is None else kv_lens.data_ptr(), out.data_ptr(), dout.data_ptr(),
                                    lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, H, Hkv, Nq, Nk, d,
-                                   scale, workspace.data_ptr(), _nbytes(workspace, index), _raw_stream(index, stream))
+                                   float(scale), workspace.data_ptr(), _nbytes(workspace, index),
+                                   _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, fn_name)
     return dq, dk, dv

@@ -216,6 +216,19 @@ def test_lengths_out_of_range_count_as_zero(fa):
     status_ok(fa)
 
 
+@pytest.mark.parametrize("n_splits", [1, 3])
+def test_a_nan_query_stays_its_own_row(fa, n_splits):
+    q, k, v, _ = inputs(19, "fp16", 2, 2, 1, 30, 400, 64)
+    want, wl = fa.attention_cross(q, k, v, n_splits=n_splits)
+    q[1, 0, 7, 3] = float("nan")
+    out, lse = fa.attention_cross(q, k, v, n_splits=n_splits)
+    status_ok(fa)
+    assert bool(torch.isnan(out[1, 0, 7]).all()) and bool(torch.isnan(lse[1, 0, 7]))
+    kept = torch.ones(lse.shape, dtype=torch.bool, device=DEV)
+    kept[1, 0, 7] = False
+    assert torch.equal(out[kept], want[kept]) and torch.equal(lse[kept], wl[kept])
+
+
 def test_equal_lengths_are_the_plain_forward_bit_for_bit(fa):
     q, k, v, _ = inputs(13, "bf16", 2, 3, 3, 700, 700, 128)
     out, lse = fa.attention_cross(q, k, v, n_splits=1)

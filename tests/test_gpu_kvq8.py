@@ -331,7 +331,7 @@ def test_attention_page_scales_far_apart(fa, fmt, dtype):
     cache.k_scale[table[0, 4]] = 0.0
     cache.k_scale[table[0, 5], 1] = 0.01337
     q = torch.from_numpy(rng.standard_normal((1, 4, 1, d))).to(DT[dtype]).to(DEV)
-    for n_parts in (1, 4):
+    for n_parts in (0, 1, 4):
         out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([n]), n_parts=n_parts)
         status_ok(fa)
         check_attention(q, cache, table, [n], out, lse, 1 / math.sqrt(d), False)
@@ -345,7 +345,7 @@ def test_attention_pages_of_zeros_before_keys_a_row_does_not_see(fa, fmt):
     cache = filled(fa, rng, fmt, n_pages, 1, 16, 64)
     cache.v_scale[table[0, :3]] = 0.0
     q = torch.from_numpy(rng.standard_normal((1, 2, 16, 64))).half().to(DEV)
-    for n_parts in (1, 2):
+    for n_parts in (0, 1, 2):
         out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([60]), causal=True, n_parts=n_parts)
         status_ok(fa)
         check_attention(q, cache, table, [60], out, lse, 0.125, True)
@@ -392,14 +392,15 @@ def test_attention_ignores_what_lies_behind_the_lengths(fa):
         check_attention(q, clean, table, lens, out, lse, 1 / math.sqrt(d), causal)
 
 
-def test_attention_bad_pages_and_lengths(fa):
+@pytest.mark.parametrize("n_parts", [0, 1, 2])
+def test_attention_bad_pages_and_lengths(fa, n_parts):
     """Keys of a page that is none are left out; a length out of range counts as 0."""
     rng = np.random.default_rng(25)
     page, d = 16, 64
     cache = filled(fa, rng, "int8", 12, 1, page, d)
     table = np.array([[0, 1, 2, 3], [4, 5, 77, 6], [7, 8, 9, 10], [-1, 11, 11, 11]])
     q = torch.from_numpy(rng.standard_normal((4, 2, 1, d))).bfloat16().to(DEV)
-    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([64, 60, 65, 10]), n_parts=2)
+    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints([64, 60, 65, 10]), n_parts=n_parts)
     torch.cuda.synchronize()
     assert fa.fa_get_device_status() in (fa.FA_ERR_PAGE, fa.FA_ERR_SEQLENS)
     check_attention(q[:1], cache, table[:1], [64], out[:1], lse[:1], 1 / 8, False)
@@ -415,12 +416,70 @@ def test_attention_repeats_bit_for_bit_and_part_counts_agree(fa):
     table, n_pages = random_table(rng, lens, page)
     cache = filled(fa, rng, "int8", n_pages, 2, page, d)
     q = torch.from_numpy(rng.standard_normal((2, 8, 1, d))).bfloat16().to(DEV)
-    for n_parts in (1, 2, 5, 47, 3000):
+    for n_parts in (0, 1, 2, 5, 47, 3000):
         got = [fa.attention_kvq8(q, cache, ints(table.tolist()), ints(lens), n_parts=n_parts, max_len=3000)
                for _ in range(2)]
         assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
         check_attention(q, cache, table, lens, *got[0], 1 / math.sqrt(d), False)
     status_ok(fa)
+
+
+@pytest.mark.parametrize("n_parts", [0, 1, 3, 40, 500])
+def test_attention_many_sequences_of_uneven_lengths(fa, n_parts):
+    """Runs of empty sequences, more sequences than a warp looks at in one go, parts that end anywhere."""
+    rng = np.random.default_rng(32)
+    page, d, H, Hkv = 16, 64, 6, 2
+    lens = [int(x) for x in rng.integers(0, 60, 150)]
+    lens[:5] = [0, 0, 33, 0, 1]
+    lens[60:100] = [0] * 40
+    lens[-3:] = [0, 200, 0]
+    table, n_pages = random_table(rng, lens, page)
+    cache = filled(fa, rng, "int8", n_pages, Hkv, page, d)
+    q = torch.from_numpy(rng.standard_normal((len(lens), H, 2, d))).half().to(DEV)
+    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints(lens), causal=True, n_parts=n_parts, max_len=200)
+    status_ok(fa)
+    check_attention(q, cache, table, lens, out, lse, 1 / 8, True)
+
+
+def test_attention_nothing_cached(fa):
+    cache = fa.kv_cache_q8(4, 2, 32, 128, torch.float8_e4m3fn, DEV)
+    q = torch.ones((3, 4, 1, 128), dtype=torch.bfloat16, device=DEV)
+    table = ints([[0, 1], [2, 3], [0, 0]])
+    for n_parts in (0, 1, 7):
+        out, lse = fa.attention_kvq8(q, cache, table, ints([0, 0, 0]), n_parts=n_parts)
+        status_ok(fa)
+        assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+
+
+def test_attention_guard_bands(fa):
+    """Nothing is written outside out, lse and the workspace; a row that is NaN stays its own."""
+    rng = np.random.default_rng(33)
+    lens, page, d = [900, 31], 32, 128
+    table, n_pages = random_table(rng, lens, page)
+    cache = filled(fa, rng, "e4m3", n_pages, 1, page, d)
+    q = torch.from_numpy(rng.standard_normal((2, 3, 5, d))).bfloat16().to(DEV)
+    q[0, 1, 2, 3] = float("nan")
+    n = q.numel()
+    for n_parts in (0, 1, 9):
+        nb = fa.fa_kvq8_workspace_bytes(3, 1, 5, d, n_parts)
+        bo = torch.full((n + 8192,), 3.0, dtype=q.dtype, device=DEV)
+        bl = torch.full((30 + 2048,), 3.0, device=DEV)
+        ws = torch.full((nb + 1024,), 7, dtype=torch.uint8, device=DEV)
+        out, lse = bo[4096 : 4096 + n].view(q.shape), bl[1024 : 1024 + 30].view(2, 3, 5)
+        fa.fa_fwd_kvq8(q, cache, ints(table.tolist()), ints(lens), out, lse, 0.1, False, 900, n_parts, ws[:nb])
+        status_ok(fa)
+        assert bool((bo[:4096] == 3.0).all()) and bool((bo[4096 + n :] == 3.0).all())
+        assert bool((bl[:1024] == 3.0).all()) and bool((bl[1024 + 30 :] == 3.0).all())
+        assert bool((ws[nb:] == 7).all())
+        assert bool(torch.isnan(out[0, 1, 2]).all()) and bool(torch.isnan(lse[0, 1, 2]))
+        clean = q.clone()
+        clean[0, 1, 2] = 0
+        out[0, 1, 2] = 0
+        kept = torch.ones((2, 3, 5), dtype=torch.bool, device=DEV)
+        kept[0, 1, 2] = False
+        want, wl = fa.attention_kvq8(clean, cache, ints(table.tolist()), ints(lens), scale=0.1, max_len=900, n_parts=n_parts)
+        assert torch.equal(out[kept], want[kept]) and torch.equal(lse[kept], wl[kept])
+        check_attention(clean, cache, table, lens, want, wl, 0.1, False)
 
 
 def test_attention_offsets_past_32_bits(fa):
