@@ -666,6 +666,7 @@ int bwd_common(bool fp16, const void *q, const void *k, const void *v, const voi
     if (cross) {
         a.Hkv = Hkv;
         a.Nk = Nk;
+        a.num_sms = di->num_sms;
         a.kv_lens = kv_lens;
         log_call("backward over keys of another length %s d=%d B=%d H=%d Hkv=%d Nq=%d Nk=%d lens=%s", fp16 ? "fp16" : "bf16",
                  d, B, H, Hkv, N, Nk, kv_lens ? "given" : "all");

@@ -107,30 +107,21 @@ struct BwdParams {
 // of every head that shares its keys, head by head, so dK and dV of shared heads are summed in the same accumulators.
 // Iteration it is query block it % n_qblk of head it / n_qblk of the group, and the row statistics of the group's heads
 // follow each other, so theirs is simply block it.
-struct CrossBlock {
-    int len, row;   // keys of the batch index; first key row of the block
-    bool none;      // the block lies past them
-};
-__device__ __forceinline__ CrossBlock cross_block(const BwdParams &p, int bh, int j) {
-    CrossBlock c;
-    c.len = p.Nk;
-    if (p.kv_lens != nullptr) {
-        c.len = __ldg(p.kv_lens + bh / p.Hkv);
-        if (c.len < 0 || c.len > p.Nk) {
-            if (threadIdx.x == 0) atomicExch(p.status, -8);  // FA_ERR_SEQLENS: counts as 0
-            c.len = 0;
-        }
+__device__ __forceinline__ int cross_len(const BwdParams &p, int b) {
+    if (p.kv_lens == nullptr) return p.Nk;
+    const int len = __ldg(p.kv_lens + b);
+    if (len < 0 || len > p.Nk) {
+        if ((threadIdx.x & 31) == 0) atomicExch(p.status, -8);  // FA_ERR_SEQLENS: counts as 0
+        return 0;
     }
-    c.row = j * kBlk;
-    c.none = c.row >= c.len;
-    return c;
+    return len;
 }
 // dK and dV of a key block that no query sees.
-template <typename T, int D>
-__device__ __forceinline__ void zero_block(const BwdParams &p, int bh, int row) {
+template <typename T, int D, int THREADS>
+__device__ __forceinline__ void zero_block(const BwdParams &p, int bh, int row, int thread) {
     const int rows = min(kBlk, p.Nk - row);
     const size_t at = ((size_t)bh * p.Nk + (size_t)row) * D;
-    for (int i = threadIdx.x; i < rows * D / 8; i += kBwdThreads) {
+    for (int i = thread; i < rows * D / 8; i += THREADS) {
         st_global_v4(reinterpret_cast<T *>(p.dk) + at + 8 * i, 0u, 0u, 0u, 0u);
         st_global_v4(reinterpret_cast<T *>(p.dv) + at + 8 * i, 0u, 0u, 0u, 0u);
     }
@@ -276,10 +267,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     grid_launch_dependents();       // fa_bwd_post may be scheduled once every CTA has started
     int n_keys = p.N;               // keys of the sequence
     if constexpr (CROSS) {
-        const CrossBlock cb = cross_block(p, bh, j);
-        n_keys = cb.len;
-        if (cb.none) {  // (fa_bwd_post must not start before fa_bwd_pre is done, so wait for it here too)
-            zero_block<T, D>(p, bh, cb.row);
+        n_keys = cross_len(p, bh / p.Hkv);
+        if (j * kBlk >= n_keys) {  // (fa_bwd_post must not start before fa_bwd_pre is done, so wait for it here too)
+            zero_block<T, D, kBwdThreads>(p, bh, j * kBlk, threadIdx.x);
             grid_dependency_wait();
             return;
         }
@@ -597,7 +587,7 @@ struct BwdCfgH64 {
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
 };
 
-template <typename T, bool CAUSAL, bool CROSS = false>
+template <typename T, bool CAUSAL>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_kernel_h64(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -624,19 +614,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int j = blockIdx.x / p.BH;
     const int n_qblk = p.Npad / kBlk;
     const int i0 = CAUSAL ? j : 0;
-    const int n_it = CROSS ? n_qblk * p.group : n_qblk - i0;  // >= 1
+    const int n_it = n_qblk - i0;  // >= 1
     grid_launch_dependents();      // fa_bwd_post may be scheduled once every CTA has started
-    int n_keys = p.N;              // keys of the sequence
-    if constexpr (CROSS) {
-        const CrossBlock cb = cross_block(p, bh, j);
-        n_keys = cb.len;
-        if (cb.none) {  // (as in fa_bwd_kernel)
-            zero_block<T, 64>(p, bh, cb.row);
-            grid_dependency_wait();
-            return;
-        }
-    }
-    const int qh0 = CROSS ? bh * p.group : bh;  // first query head of the group
 
     if (threadIdx.x == 0) {
         mbar_init(bar_kv, 1);
@@ -678,10 +657,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (!bwd_wait(bar_qd_empty(s), ((it / ST) & 1u) ^ 1u, p)) break;
                 const uint32_t dst = smem_u32(smem + C::SMEM_QD + s * 2 * C::CHUNK);
                 mbar_arrive_expect_tx(bar_qd_full(s), 2 * C::CHUNK);
-                const int row0 = (CROSS ? it % n_qblk : i0 + it) * kBlk;
-                const int qh = CROSS ? qh0 + it / n_qblk : bh;
-                tma_load_3d(dst, &tm_q, bar_qd_full(s), 0, row0, qh, pol);
-                tma_load_3d(dst + C::CHUNK, &tm_do, bar_qd_full(s), 0, row0, qh, pol);
+                const int row0 = (i0 + it) * kBlk;
+                tma_load_3d(dst, &tm_q, bar_qd_full(s), 0, row0, bh, pol);
+                tma_load_3d(dst + C::CHUNK, &tm_do, bar_qd_full(s), 0, row0, bh, pol);
                 issued = it + 1;
             }
             bwd_wait(bar_kv, 0, p);  // every copy into this CTA's shared memory lands before exit
@@ -702,12 +680,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint64_t v_km = smem_desc_sw128(smem_u32(smem + C::SMEM_V), 16, 1024);
         const uint64_t k_mn = smem_desc_sw128(smem_u32(smem + C::SMEM_K), C::CHUNK, 1024);
         bool ok = bwd_wait_warp(bar_kv, 0, p);
-        if (CROSS && ok && (j + 1) * kBlk > n_keys && n_keys < p.Nk) {
-            zero_rows<1, C::CHUNK>(smem_u32(smem + C::SMEM_K), n_keys - j * kBlk, lane);
-            zero_rows<1, C::CHUNK>(smem_u32(smem + C::SMEM_V), n_keys - j * kBlk, lane);
-            fence_proxy_async_smem();
-            __syncwarp();
-        }
         if (warp == 1) {
             // S_h^T = K_j Q_h^T, dP_h^T = V_j dO_h^T of block it (query rows 64h.. of the stage = +8 KB)
             auto issue_s = [&](int it, int h) {
@@ -800,15 +772,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const uint32_t lane_base = (uint32_t)(w * 32) << 16;
         const uint32_t s_col = tmem + lane_base + 128u * g;  // S_g; dP_g at +64
         const int key = j * kBlk + r;
-        const bool key_ok = key < n_keys;
-        const bool ragged_keys = (j + 1) * kBlk > n_keys;
+        const bool key_ok = key < p.N;
+        const bool ragged_keys = (j + 1) * kBlk > p.N;
         const uint32_t ds_row0 = smem_u32(smem + C::SMEM_DS) + g * C::CHUNK + r * 128;  // + (block & 1) * 32 KB
         // dQ of block b is staged in this warp's own 32 rows of b's dS buffer: dK(b) and dQ(b) have read it by
         // the time dQ(b) is read out, and this warp writes those rows again only in the pass of block b + 2
         const uint32_t box0 = smem_u32(smem + C::SMEM_DS) + g * C::CHUNK + w * 4096;  // + (block & 1) * 32 KB
         const uint32_t stats0 = smem_u32(smem + C::SMEM_STATS) + g * 1024;  // + buffer * 512
         // thread r hands over -lse2 (r < 64) or -D (r >= 64) of query row 64g + (r & 63)
-        const float *stat_src = (r < 64 ? p.lse2 : p.dsum) + (size_t)qh0 * p.Npad + 64 * g + (r & 63);
+        const float *stat_src = (r < 64 ? p.lse2 : p.dsum) + (size_t)bh * p.Npad + 64 * g + (r & 63);
         grid_dependency_wait();  // statistics and the zeroed dQ accumulator are written by fa_bwd_pre
         float stat_next = -__ldg(stat_src + i0 * kBlk);
         bool ok = true;
@@ -820,8 +792,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tc_fence_before();
             mbar_arrive(bar_dq_free);
             const uint32_t box = box0 + ((blk - i0) & 1) * 2 * C::CHUNK;
-            stage_and_reduce_dq(&tm_dq, box, qv, p.scale, lane, 32 * g, (CROSS ? blk % n_qblk : blk) * kBlk + w * 32,
-                                CROSS ? qh0 + blk / n_qblk : bh);
+            stage_and_reduce_dq(&tm_dq, box, qv, p.scale, lane, 32 * g, blk * kBlk + w * 32, bh);
             return true;
         };
         for (int it = 0; ok && it < n_it; ++it) {
@@ -873,12 +844,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (ok) {  // the last dq_full covers every dV and dK product
             tc_fence_after();
             const float mul = g == 0 ? 1.0f : p.scale;
-            const int k_rows = CROSS ? p.Nk : p.N;  // rows past the sequence's keys get their zeros
-            const bool store = key < k_rows;
-            T *dst = reinterpret_cast<T *>(g == 0 ? p.dv : p.dk) + ((size_t)bh * k_rows + (size_t)(store ? key : 0)) * 64;
+            T *dst = reinterpret_cast<T *>(g == 0 ? p.dv : p.dk) + ((size_t)bh * p.N + (size_t)(key_ok ? key : 0)) * 64;
             uint32_t a[32], b[32];
             tmem_ld32x2_wait(tmem + lane_base + 320 + 64 * g, a, tmem + lane_base + 320 + 64 * g + 32, b);
-            if (store) {
+            if (key_ok) {
 #pragma unroll
                 for (int c = 0; c < 32; c += 8) {
                     st_global_v4(dst + c, pk2<T>(__uint_as_float(a[c]) * mul, __uint_as_float(a[c + 1]) * mul),
@@ -893,6 +862,407 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
         }
         if (lane == 0) bulk_wait_all();  // the dQ reductions, behind the dV / dK stores
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// d = 64 with keys of another sequence (CROSS). The products, their order and the tensor-memory columns are those of
+// fa_bwd_kernel_h64, but a CTA goes through several key blocks: a decoder has few query blocks (four for 448 rows), and
+// with a CTA per key block its start (tensor memory, barriers, the first copies) and its end (the last dQ, dK and dV)
+// took as long as its products. Here K and V are double-buffered and the next block's copies, S and dP run during the
+// end of the last one; only the first dV/dK product waits until the gradient warps have taken dV and dK out of tensor
+// memory. All phases are those of one running iteration count g: iteration g belongs to the CTA's key block g / n_it.
+// The CTA's blocks are every gridDim.x-th of those that hold keys, batch index by batch index; blocks without keys are
+// set to zero first, by the CTAs in turn.
+template <typename T>
+struct BwdCfgX64 : BwdCfgH64<T> {
+    using B = BwdCfgH64<T>;
+    static constexpr int CHUNK = B::CHUNK, STAGES = B::STAGES;
+    static constexpr int SMEM_KV = 0;                              // 2 x (K_j, V_j)
+    static constexpr int SMEM_QD = 4 * CHUNK;                      // STAGES x (Q_i, dO_i)
+    static constexpr int SMEM_DS = SMEM_QD + STAGES * 2 * CHUNK;   // dS[2]
+    static constexpr int SMEM_STATS = SMEM_DS + 4 * CHUNK;
+    static constexpr int SMEM_BAR = SMEM_STATS + 2 * 2 * 128 * 4;
+    // kv_full[2], kv_free[2], qd_full[ST], qd_empty[ST], sp_full[2], p_full[2], dq_full, dq_free, stats[2], drain,
+    // acc_done[2], acc_free
+    static constexpr int NUM_BARS = 4 + 2 * STAGES + 2 + 2 + 2 + 2 + 1 + 2 + 1;
+    static constexpr int SMEM_USED = SMEM_BAR + NUM_BARS * 8 + 16;
+    static constexpr int SMEM_BYTES = 232448;
+    static constexpr int SLACK = SMEM_BYTES - SMEM_USED;  // to align the base to 1024 bytes
+    static_assert(SLACK >= 256, "shared memory budget");
+};
+
+// The CTA's next key block: block j of K/V head bh, of a batch index with len keys.
+struct CrossCursor {
+    int a, b = 0, base = 0, len, bh = 0, j = 0;
+    __device__ __forceinline__ explicit CrossCursor(const BwdParams &p) : a((int)blockIdx.x - (int)gridDim.x) { len = cross_len(p, 0); }
+    __device__ __forceinline__ bool next(const BwdParams &p) {
+        a += gridDim.x;
+        const int B = p.BH / p.Hkv;
+        for (;;) {
+            const int blocks = (len + kBlk - 1) / kBlk * p.Hkv;
+            if (a < base + blocks) break;
+            base += blocks;
+            if (++b >= B) return false;
+            len = cross_len(p, b);
+        }
+        const int r = a - base;
+        j = r / p.Hkv;
+        bh = b * p.Hkv + (r - j * p.Hkv);
+        return true;
+    }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads, 1)
+    fa_bwd_cross_kernel_h64(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                            const __grid_constant__ CUtensorMap tm_dq, const BwdParams p) {
+    using C = BwdCfgX64<T>;
+    constexpr int ST = C::STAGES;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t pad = (uint32_t)((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    grid_launch_dependents();  // fa_bwd_post may be scheduled once every CTA has started
+    if (pad > (uint32_t)C::SLACK) {  // cannot happen with no static shared memory; never overflow
+        if (threadIdx.x == 0) atomicExch(p.status, kStatusSmemAlign);
+        grid_dependency_wait();
+        return;
+    }
+    uint8_t *smem = smem_raw + pad;
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + C::SMEM_BAR);
+    auto bar_kv_full = [&](int b) { return smem_u32(bars + b); };
+    auto bar_kv_free = [&](int b) { return smem_u32(bars + 2 + b); };  // both issuing warps' last product of the block
+    auto bar_qd_full = [&](int s) { return smem_u32(bars + 4 + s); };
+    auto bar_qd_empty = [&](int s) { return smem_u32(bars + 4 + ST + s); };
+    auto bar_sp_full = [&](int h) { return smem_u32(bars + 4 + 2 * ST + h); };
+    auto bar_p_full = [&](int h) { return smem_u32(bars + 6 + 2 * ST + h); };
+    const uint32_t bar_dq_full = smem_u32(bars + 8 + 2 * ST);
+    const uint32_t bar_dq_free = smem_u32(bars + 9 + 2 * ST);
+    auto bar_stats = [&](int h) { return smem_u32(bars + 10 + 2 * ST + h); };
+    const uint32_t bar_drain = smem_u32(bars + 12 + 2 * ST);
+    auto bar_acc_done = [&](int h) { return smem_u32(bars + 13 + 2 * ST + h); };
+    const uint32_t bar_acc_free = smem_u32(bars + 15 + 2 * ST);  // dV, dK of the block taken out (256 arrivals)
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SMEM_BAR + C::NUM_BARS * 8);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int n_qblk = p.Npad / kBlk;
+    const int n_it = n_qblk * p.group;  // iterations per key block: the query blocks of every head of the group
+
+    if (threadIdx.x == 0) {
+        prefetch_tensormap(&tm_k);
+        prefetch_tensormap(&tm_v);
+        prefetch_tensormap(&tm_q);
+        prefetch_tensormap(&tm_do);
+        prefetch_tensormap(&tm_dq);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(bar_kv_full(b), 1);
+            mbar_init(bar_kv_free(b), 2);
+        }
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(bar_qd_full(s), 1);
+            mbar_init(bar_qd_empty(s), 2);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(bar_sp_full(h), 1);
+            mbar_init(bar_p_full(h), 128);
+            mbar_init(bar_stats(h), 128);
+            mbar_init(bar_acc_done(h), 1);
+        }
+        mbar_init(bar_dq_full, 1);
+        mbar_init(bar_dq_free, kGradThreads);
+        mbar_init(bar_acc_free, kGradThreads);
+        mbar_init(bar_drain, 2);
+        fence_mbar_init();
+        fence_proxy_async_smem();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        // ---------------------------------------------------------------- TMA producer
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_last();
+            CrossCursor x(p);
+            int g = 0, n = 0;
+            bool ok = true;
+            for (; ok && x.next(p); ++n) {
+                const int b = n & 1;
+                ok = bwd_wait(bar_kv_free(b), ((n >> 1) & 1u) ^ 1u, p);
+                if (!ok) break;
+                const uint32_t kv = smem_u32(smem + C::SMEM_KV + b * 2 * C::CHUNK);
+                mbar_arrive_expect_tx(bar_kv_full(b), 2 * C::CHUNK);
+                tma_load_3d(kv, &tm_k, bar_kv_full(b), 0, x.j * kBlk, x.bh, pol);
+                tma_load_3d(kv + C::CHUNK, &tm_v, bar_kv_full(b), 0, x.j * kBlk, x.bh, pol);
+                int row = 0, qh = x.bh * p.group;
+                for (int it = 0; it < n_it; ++it, ++g) {
+                    const int s = g % ST;
+                    ok = bwd_wait(bar_qd_empty(s), ((g / ST) & 1u) ^ 1u, p);
+                    if (!ok) break;
+                    const uint32_t dst = smem_u32(smem + C::SMEM_QD + s * 2 * C::CHUNK);
+                    mbar_arrive_expect_tx(bar_qd_full(s), 2 * C::CHUNK);
+                    tma_load_3d(dst, &tm_q, bar_qd_full(s), 0, row, qh, pol);
+                    tma_load_3d(dst + C::CHUNK, &tm_do, bar_qd_full(s), 0, row, qh, pol);
+                    row += kBlk;
+                    if (row == p.Npad) {
+                        row = 0;
+                        ++qh;
+                    }
+                }
+                if (!ok) {
+                    ++n;
+                    break;
+                }
+            }
+            // every copy into this CTA's shared memory lands before exit
+            for (int m = n - 2 > 0 ? n - 2 : 0; m < n; ++m) bwd_wait(bar_kv_full(m & 1), (m >> 1) & 1u, p);
+            for (int m = g - ST > 0 ? g - ST : 0; m < g; ++m) bwd_wait(bar_qd_full(m % ST), (m / ST) & 1u, p);
+        }
+    } else if (warp == 1 || warp == 2) {
+        // ---------------------------------------------------------------- MMA issuers (as in fa_bwd_kernel_h64)
+        const uint32_t issue = lane == 0 ? 1u : 0u;
+        // K and V of the CTA's n-th block, rows past the sequence's keys set to zero
+        auto take_kv = [&](int n, const CrossCursor &x) -> bool {
+            const int b = n & 1;
+            if (!bwd_wait_warp(bar_kv_full(b), (n >> 1) & 1u, p)) return false;
+            if ((x.j + 1) * kBlk > x.len && x.len < p.Nk) {
+                const uint32_t kv = smem_u32(smem + C::SMEM_KV + b * 2 * C::CHUNK);
+                zero_rows<1, C::CHUNK>(kv, x.len - x.j * kBlk, lane);
+                zero_rows<1, C::CHUNK>(kv + C::CHUNK, x.len - x.j * kBlk, lane);
+                fence_proxy_async_smem();
+                __syncwarp();
+            }
+            return true;
+        };
+        CrossCursor x(p);
+        bool ok = true;
+        if (warp == 1) {
+            // S_h^T = K_j Q_h^T, dP_h^T = V_j dO_h^T of iteration g, of the CTA's n-th block
+            auto issue_s = [&](int g, int n, int h) {
+                const uint32_t kv = smem_u32(smem + C::SMEM_KV + (n & 1) * 2 * C::CHUNK);
+                const uint64_t k_km = smem_desc_sw128(kv, 16, 1024), v_km = smem_desc_sw128(kv + C::CHUNK, 16, 1024);
+                const uint32_t q_s = smem_u32(smem + C::SMEM_QD + (g % ST) * 2 * C::CHUNK);
+                const uint64_t q_km = smem_desc_sw128(q_s, 16, 1024);
+                const uint64_t do_km = smem_desc_sw128(q_s + C::CHUNK, 16, 1024);
+                const uint64_t hoff = (uint64_t)((h * 64 * 128) >> 4);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t off = (uint64_t)((k * 32) >> 4);
+                    mma_ss(tmem + 128 * h, k_km + off, q_km + hoff + off, C::ID_S, k > 0 ? 1u : 0u, issue);
+                    mma_ss(tmem + 128 * h + 64, v_km + off, do_km + hoff + off, C::ID_S, k > 0 ? 1u : 0u, issue);
+                }
+                tc_commit(bar_sp_full(h), issue);
+            };
+            bool more = x.next(p);
+            if (more) {
+                ok = take_kv(0, x) && bwd_wait_warp(bar_qd_full(0), 0, p);
+                if (ok) {
+                    tc_fence_after();
+                    issue_s(0, 0, 0);
+                    issue_s(0, 0, 1);
+                    tc_commit(bar_qd_empty(0), issue);
+                    if (n_it == 1) tc_commit(bar_kv_free(0), issue);
+                }
+            }
+            // after the passes of iteration g have read S and dP, those of iteration g + 1 (block n, its it-th)
+            for (int g = 0, n = 0, it = 0; ok && more; ++g) {
+                const bool crossing = ++it == n_it;
+                if (crossing) {
+                    it = 0;
+                    ++n;
+                    more = x.next(p);
+                }
+                ok = bwd_wait_warp(bar_p_full(0), g & 1u, p);
+                if (ok && more) {
+                    ok = (!crossing || take_kv(n, x)) && bwd_wait_warp(bar_qd_full((g + 1) % ST), ((g + 1) / ST) & 1u, p);
+                    if (ok) {
+                        tc_fence_after();
+                        issue_s(g + 1, n, 0);
+                    }
+                }
+                if (ok) ok = bwd_wait_warp(bar_p_full(1), g & 1u, p);
+                if (ok && more) {
+                    tc_fence_after();
+                    issue_s(g + 1, n, 1);
+                    tc_commit(bar_qd_empty((g + 1) % ST), issue);
+                    if (it == n_it - 1) tc_commit(bar_kv_free(n & 1), issue);
+                }
+            }
+        } else {
+            auto issue_acc = [&](int g, int h, bool first) {
+                const uint32_t q_s = smem_u32(smem + C::SMEM_QD + (g % ST) * 2 * C::CHUNK);
+                const uint64_t q_mn = smem_desc_sw128(q_s, C::CHUNK, 1024);
+                const uint64_t do_mn = smem_desc_sw128(q_s + C::CHUNK, C::CHUNK, 1024);
+                const uint64_t dst_km =
+                    smem_desc_sw128(smem_u32(smem + C::SMEM_DS + (g & 1) * 2 * C::CHUNK + h * C::CHUNK), 16, 1024);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint64_t off = (uint64_t)(((h * 64 + k * 16) * 128) >> 4);
+                    const uint32_t acc = (!first || h > 0 || k > 0) ? 1u : 0u;
+                    mma_ts(tmem + 320, tmem + 256 + 32 * h + 8 * k, do_mn + off, C::ID_ACC, acc, issue);
+                    mma_ss(tmem + 384, dst_km + (uint64_t)((k * 32) >> 4), q_mn + off, C::ID_ACC, acc, issue);
+                }
+                tc_commit(bar_acc_done(h), issue);
+            };
+            int g = 0;
+            for (int n = 0; ok && x.next(p); ++n) {
+                ok = take_kv(n, x);
+                const uint64_t k_mn =
+                    smem_desc_sw128(smem_u32(smem + C::SMEM_KV + (n & 1) * 2 * C::CHUNK), C::CHUNK, 1024);
+                for (int it = 0; ok && it < n_it; ++it, ++g) {
+                    const int s = g % ST;
+                    ok = bwd_wait_warp(bar_p_full(0), g & 1u, p) && bwd_wait_warp(bar_qd_full(s), (g / ST) & 1u, p);
+                    // the last block's dV and dK have been taken out
+                    if (ok && it == 0 && n > 0) ok = bwd_wait_warp(bar_acc_free, (n - 1) & 1u, p);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_acc(g, 0, it == 0);
+                    ok = bwd_wait_warp(bar_p_full(1), g & 1u, p);
+                    if (!ok) break;
+                    tc_fence_after();
+                    issue_acc(g, 1, it == 0);
+                    tc_commit(bar_qd_empty(s), issue);
+                    if (g > 0) ok = bwd_wait_warp(bar_dq_free, (g - 1) & 1u, p);  // the last dQ read out
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t ds_mn =
+                        smem_desc_sw128(smem_u32(smem + C::SMEM_DS + (g & 1) * 2 * C::CHUNK), C::CHUNK, 1024);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const uint64_t off = (uint64_t)((k * 2048) >> 4);
+                        mma_ss(tmem + 448, ds_mn + off, k_mn + off, C::ID_DQ, k > 0 ? 1u : 0u, issue);
+                    }
+                    tc_commit(bar_dq_full, issue);
+                    if (it == n_it - 1) tc_commit(bar_kv_free(n & 1), issue);
+                }
+            }
+        }
+        tc_commit(bar_drain, issue);
+        if (warp == 1) bwd_wait_warp(bar_drain, 0, p);  // both warps' products, before TMEM is freed
+    } else if (warp == 3) {
+        // ---------------------------------------------------------------- key blocks without keys
+        const int blocks = (p.Nk + kBlk - 1) / kBlk;
+        for (long long i = blockIdx.x; i < (long long)p.BH * blocks; i += gridDim.x) {
+            const int bh = (int)(i % p.BH), j = (int)(i / p.BH);
+            const int len = cross_len(p, bh / p.Hkv);
+            if (j * kBlk >= len) zero_block<T, 64, 32>(p, bh, j * kBlk, lane);
+        }
+    } else if (warp >= 4) {
+        // ---------------------------------------------------------------- gradient warps
+        const int gr = (warp - 4) >> 2;  // half of the query block
+        const int w = warp & 3;
+        const int r = w * 32 + lane;     // TMEM lane: key r, later query row r
+        const uint32_t lane_base = (uint32_t)(w * 32) << 16;
+        const uint32_t s_col = tmem + lane_base + 128u * gr;
+        const uint32_t ds_row0 = smem_u32(smem + C::SMEM_DS) + gr * C::CHUNK + r * 128;
+        const uint32_t box0 = smem_u32(smem + C::SMEM_DS) + gr * C::CHUNK + w * 4096;
+        const uint32_t stats0 = smem_u32(smem + C::SMEM_STATS) + gr * 1024;
+        const float *stat_row = (r < 64 ? p.lse2 : p.dsum) + 64 * gr + (r & 63);
+        grid_dependency_wait();  // statistics and the zeroed dQ accumulator are written by fa_bwd_pre
+        CrossCursor x(p);
+        bool ok = true, more = x.next(p);
+        float stat_next = more ? -__ldg(stat_row + (size_t)x.bh * p.group * p.Npad) : 0.f;
+        auto readout = [&](int g, int qh, int row) -> bool {  // dQ of iteration g
+            if (!bwd_wait_warp(bar_dq_full, (uint32_t)g & 1u, p)) return false;
+            tc_fence_after();
+            uint32_t qv[32];
+            tmem_ld32_wait(tmem + lane_base + 448 + 32 * gr, qv);
+            tc_fence_before();
+            mbar_arrive(bar_dq_free);
+            stage_and_reduce_dq(&tm_dq, box0 + (g & 1) * 2 * C::CHUNK, qv, p.scale, lane, 32 * gr, row + w * 32, qh);
+            return true;
+        };
+        for (int g = 0; ok && more;) {
+            const int bh = x.bh, key = x.j * kBlk + r, len = x.len;
+            const bool key_ok = key < len, ragged_keys = (x.j + 1) * kBlk > len;
+            const float *stat_src = stat_row + (size_t)bh * p.group * p.Npad;
+            more = x.next(p);  // the block after this one
+            int qh = bh * p.group, row = 0;
+            for (int it = 0; it < n_it; ++it, ++g) {
+                const uint32_t stats = stats0 + (g & 1) * 512;
+                st_shared_f32(stats + r * 4, stat_next);
+                mbar_arrive(bar_stats(gr));
+                ok = bwd_wait_warp(bar_stats(gr), g & 1u, p) && bwd_wait_warp(bar_sp_full(gr), g & 1u, p);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t ds_row = ds_row0 + (g & 1) * 2 * C::CHUNK;
+                if (lane == 0) bulk_wait_read_all();  // the reduction staged in these rows has read them
+                __syncwarp();
+                if (g > 0 && !bwd_wait_warp(bar_acc_done(gr), (g - 1) & 1u, p)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+#pragma unroll 1
+                for (int c0 = 0; c0 < 64; c0 += 32) {
+                    uint32_t sv[32], dpv[32];
+                    tmem_ld32x2_wait(s_col + c0, sv, s_col + 64 + c0, dpv);
+                    uint32_t pp[16], dsp[16];
+                    if (ragged_keys)
+                        p_ds_chunk<T, false, true>(sv, dpv, stats + c0 * 4, stats + (64 + c0) * 4, p.scale_log2, true,
+                                                   key_ok, key, 0, pp, dsp);
+                    else
+                        p_ds_chunk<T, false, false>(sv, dpv, stats + c0 * 4, stats + (64 + c0) * 4, p.scale_log2, false,
+                                                    key_ok, key, 0, pp, dsp);
+                    tmem_st16(tmem + lane_base + 256u + 32u * gr + c0 / 2, pp);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const uint32_t unit = (uint32_t)((c0 / 8 + u) ^ (r & 7));
+                        st_shared_v4(ds_row + unit * 16, dsp[4 * u], dsp[4 * u + 1], dsp[4 * u + 2], dsp[4 * u + 3]);
+                    }
+                }
+                tmem_wait_st();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                mbar_arrive(bar_p_full(gr));
+                if (it + 1 < n_it) stat_next = -__ldg(stat_src + (it + 1) * kBlk);
+                else if (more) stat_next = -__ldg(stat_row + (size_t)x.bh * p.group * p.Npad);
+                if (it > 0) {  // dQ of the last iteration: the block before this one, or the last of the head before
+                    ok = row > 0 ? readout(g - 1, qh, row - kBlk) : readout(g - 1, qh - 1, p.Npad - kBlk);
+                    if (!ok) break;
+                }
+                row += kBlk;
+                if (row == p.Npad) {
+                    row = 0;
+                    ++qh;
+                }
+            }
+            if (ok) ok = readout(g - 1, bh * p.group + p.group - 1, p.Npad - kBlk);
+            if (!ok) break;
+            // dV_j (half A's group), dK_j (B's): the last dq_full covers every dV and dK product of the block
+            const float mul = gr == 0 ? 1.0f : p.scale;
+            uint32_t a[32], b[32];
+            tmem_ld32x2_wait(tmem + lane_base + 320 + 64 * gr, a, tmem + lane_base + 320 + 64 * gr + 32, b);
+            tc_fence_before();
+            mbar_arrive(bar_acc_free);  // the next block's products may overwrite them
+            if (key < p.Nk) {  // (rows past the sequence's keys get their zeros)
+                T *dst = reinterpret_cast<T *>(gr == 0 ? p.dv : p.dk) + ((size_t)bh * p.Nk + (size_t)key) * 64;
+#pragma unroll
+                for (int c = 0; c < 32; c += 8) {
+                    st_global_v4(dst + c, pk2<T>(__uint_as_float(a[c]) * mul, __uint_as_float(a[c + 1]) * mul),
+                                 pk2<T>(__uint_as_float(a[c + 2]) * mul, __uint_as_float(a[c + 3]) * mul),
+                                 pk2<T>(__uint_as_float(a[c + 4]) * mul, __uint_as_float(a[c + 5]) * mul),
+                                 pk2<T>(__uint_as_float(a[c + 6]) * mul, __uint_as_float(a[c + 7]) * mul));
+                    st_global_v4(dst + 32 + c, pk2<T>(__uint_as_float(b[c]) * mul, __uint_as_float(b[c + 1]) * mul),
+                                 pk2<T>(__uint_as_float(b[c + 2]) * mul, __uint_as_float(b[c + 3]) * mul),
+                                 pk2<T>(__uint_as_float(b[c + 4]) * mul, __uint_as_float(b[c + 5]) * mul),
+                                 pk2<T>(__uint_as_float(b[c + 6]) * mul, __uint_as_float(b[c + 7]) * mul));
+                }
+            }
+        }
+        if (lane == 0) bulk_wait_all();  // the dQ reductions
     }
     __syncwarp();
     tc_fence_before();
@@ -965,10 +1335,11 @@ template <typename T, int D, bool CAUSAL, bool CROSS = false>
 int launch_bwd_variant(const BwdArgs &a) {
     // d = 64 runs the overlapped half-block kernel; d = 128 (tensor memory full) the serial one
     auto kern = [] {
-        if constexpr (D == 64) return fa_bwd_kernel_h64<T, CAUSAL, CROSS>;
+        if constexpr (D == 64 && CROSS) return fa_bwd_cross_kernel_h64<T>;
+        else if constexpr (D == 64) return fa_bwd_kernel_h64<T, CAUSAL>;
         else return fa_bwd_kernel<T, D, CAUSAL, CROSS>;
     }();
-    constexpr int smem_bytes = D == 64 ? BwdCfgH64<T>::SMEM_BYTES : BwdCfg<T, D>::SMEM_BYTES;
+    constexpr int smem_bytes = D == 64 ? (CROSS ? BwdCfgX64<T>::SMEM_BYTES : BwdCfgH64<T>::SMEM_BYTES) : BwdCfg<T, D>::SMEM_BYTES;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes) != cudaSuccess)
         return -5;
     const int BH = a.B * a.H;
@@ -1004,7 +1375,8 @@ int launch_bwd_variant(const BwdArgs &a) {
     p.scale = a.scale;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
-    const int64_t grid = static_cast<int64_t>(BHkv) * (bwd_padded_rows(Nk) / kBlk);
+    int64_t grid = static_cast<int64_t>(BHkv) * (bwd_padded_rows(Nk) / kBlk);
+    if (D == 64 && CROSS && grid > a.num_sms) grid = a.num_sms;  // each CTA takes several key blocks
     // programmatic dependents: the backward's copies of K, V, Q, dO start while fa_bwd_pre drains (its
     // gradient warps wait for the statistics), and fa_bwd_post's launch overlaps the backward's tail
     if (launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), smem_bytes, a.stream, tq, tk,

@@ -21,7 +21,7 @@ struct BwdArgs {
     int *status;
     uint64_t timeout_ns;
     // keys of another sequence (launch_bwd_cross): k, v, dk, dv [B][Hkv][Nk][d], N query rows
-    int Hkv = 0, Nk = 0;
+    int Hkv = 0, Nk = 0, num_sms = 0;
     const int *kv_lens = nullptr;  // [B] keys in use, or nullptr (Nk)
 };
 
