@@ -370,8 +370,9 @@ int fa_bwd_fp16(const void *q, const void *k, const void *v, const void *out, co
  * ceil(Nk / 128); fa_cross_num_splits gives a count that fills the GPU), whose summaries go
  * through the workspace and are merged as in fa_fwd_splitkv: 256-byte aligned, at least
  * fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits) bytes; it may be NULL when n_splits is 1.
- * Backward: out and lse are the forward's; the workspace is fa_bwd_workspace_bytes(B, H, Nq, d)
- * bytes, as for fa_bwd; dq is accumulated in fp32 in an order that varies from call to call.
+ * Backward: out and lse are the forward's; the workspace (256-byte aligned) has at least
+ * fa_bwd_cross_workspace_bytes bytes, asked for with the device current that the call will run on.
+ * dq is accumulated in fp32 in an order that varies from call to call; dk and dv do not vary.
  * Calls that share a workspace must not overlap on the GPU. Errors as for fa_fwd_gqa and fa_bwd. */
 int fa_cross_num_splits(int B, int H, int Nq, int Nk);
 int fa_fwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, void *out, float *lse, int B,
@@ -380,6 +381,7 @@ int fa_fwd_cross(const void *q, const void *k, const void *v, const int *kv_lens
 int fa_fwd_cross_fp16(const void *q, const void *k, const void *v, const int *kv_lens_or_null, void *out, float *lse,
                       int B, int H, int Hkv, int Nq, int Nk, int d, float scale, int n_splits, void *workspace,
                       unsigned long long workspace_bytes, void *stream);
+long long fa_bwd_cross_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d);
 int fa_bwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, const void *out,
                  const void *dout, const float *lse, void *dq, void *dk, void *dv, int B, int H, int Hkv, int Nq, int Nk,
                  int d, float scale, void *workspace, unsigned long long workspace_bytes, void *stream);

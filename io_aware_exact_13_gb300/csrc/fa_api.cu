@@ -54,6 +54,7 @@ __device__ int g_fa_status = 0;
 namespace {
 
 constexpr int kMaxDevices = 64;
+constexpr int kNominalSms = 148;                       // for sizing helpers called without a device
 constexpr uint64_t kDefaultTimeoutNs = 4000000000ull;  // 4 s per pipeline wait
 
 struct DeviceInfo {
@@ -635,8 +636,16 @@ int bwd_common(bool fp16, const void *q, const void *k, const void *v, const voi
     }
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     const size_t need = fa::bwd_workspace_bytes(bh, N, d);
-    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need) return FA_ERR_WORKSPACE;
-    DeviceInfo *di = device_info();
+    DeviceInfo *di = nullptr;
+    size_t need_cross = 0;
+    int parts = 1;
+    if (cross) {  // the part count goes by the device's SMs
+        di = device_info();
+        parts = fa::bwd_cross_parts(static_cast<int64_t>(B) * Hkv, H / Hkv, N, Nk, di ? di->num_sms : kNominalSms);
+        need_cross = fa::bwd_cross_part_bytes(static_cast<int64_t>(B) * Hkv, Nk, d, parts);
+    }
+    if (!workspace || !aligned(workspace, 256) || workspace_bytes < need + need_cross) return FA_ERR_WORKSPACE;
+    if (!cross) di = device_info();
     if (!di || !encoder()) return FA_ERR_LAUNCH;
     fa::BwdArgs a;
     a.q = q;
@@ -668,6 +677,8 @@ int bwd_common(bool fp16, const void *q, const void *k, const void *v, const voi
         a.Nk = Nk;
         a.num_sms = di->num_sms;
         a.kv_lens = kv_lens;
+        a.parts = parts;
+        a.kv_part = parts > 1 ? reinterpret_cast<float *>(ws + need) : nullptr;  // need is a multiple of 256
         log_call("backward over keys of another length %s d=%d B=%d H=%d Hkv=%d Nq=%d Nk=%d lens=%s", fp16 ? "fp16" : "bf16",
                  d, B, H, Hkv, N, Nk, kv_lens ? "given" : "all");
         return fa::launch_bwd_cross(a, fp16);
@@ -796,7 +807,7 @@ int fa_fwd_host_fp16(const void *q_host, const void *k_host, const void *v_host,
 int fa_splitkv_num_splits(int B, int H, int Nq, int Nk, int d) {
     if (B < 1 || H < 1 || Nk < 1 || Nq < 1) return FA_ERR_SHAPE;
     DeviceInfo *di = device_info();
-    const int64_t sms = di ? di->num_sms : 148;
+    const int64_t sms = di ? di->num_sms : kNominalSms;
     const int64_t bh = static_cast<int64_t>(B) * H;
     // Fill the GPU in exactly one wave: as many splits per head as there are
     // resident CTA slots per head (a partly filled second wave would cost
@@ -887,7 +898,7 @@ int fa_kvq8_num_parts(int B, int H, int Hkv, int Nq, int max_len, int d) {
     if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || max_len < 1) return FA_ERR_SHAPE;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     DeviceInfo *di = device_info();
-    return fa::kvq8_num_parts(B, Hkv, H / Hkv * Nq, max_len, d, di ? di->num_sms : 148);
+    return fa::kvq8_num_parts(B, Hkv, H / Hkv * Nq, max_len, d, di ? di->num_sms : kNominalSms);
 }
 
 long long fa_kvq8_workspace_bytes(int H, int Hkv, int Nq, int d, int n_parts) {
@@ -949,7 +960,7 @@ int fa_bwd_fp16(const void *q, const void *k, const void *v, const void *out, co
 int fa_cross_num_splits(int B, int H, int Nq, int Nk) {
     if (B < 1 || H < 1 || Nq < 1 || Nk < 1) return FA_ERR_SHAPE;
     DeviceInfo *di = device_info();
-    return cross_num_splits(B, H, Nq, Nk, di ? di->num_sms : 148);
+    return cross_num_splits(B, H, Nq, Nk, di ? di->num_sms : kNominalSms);
 }
 
 int fa_fwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, void *out, float *lse, int B,
@@ -964,6 +975,16 @@ int fa_fwd_cross_fp16(const void *q, const void *k, const void *v, const int *kv
                       unsigned long long workspace_bytes, void *stream) {
     return cross_common(Type::FP16, q, k, v, kv_lens_or_null, out, lse, B, H, Hkv, Nq, Nk, d, scale, n_splits,
                         workspace, workspace_bytes, stream);
+}
+
+long long fa_bwd_cross_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d) {
+    const long long n = fa_bwd_workspace_bytes(B, H, Nq, d);
+    if (n < 0) return n;
+    if (Hkv < 1 || H % Hkv != 0 || Nk < 1) return FA_ERR_SHAPE;
+    DeviceInfo *di = device_info();
+    const int64_t bh = static_cast<int64_t>(B) * Hkv;
+    const int parts = fa::bwd_cross_parts(bh, H / Hkv, Nq, Nk, di ? di->num_sms : kNominalSms);
+    return n + static_cast<long long>(fa::bwd_cross_part_bytes(bh, Nk, d, parts));
 }
 
 int fa_bwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, const void *out,

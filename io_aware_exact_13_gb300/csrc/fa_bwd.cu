@@ -101,7 +101,29 @@ struct BwdParams {
     // of which batch index b uses the first kv_lens[b] (nullptr: all), and `group` query heads share one
     const int *kv_lens;
     int Nk, Hkv, group;
+    // with few key blocks the iterations of a block are cut into `parts` runs of neighbouring ones, each with its own CTA
+    // and its own fp32 dK, dV in kv_part [parts][2][BH][Nk][d], added up by fa_bwd_cross_post
+    int parts;
+    float *kv_part;
 };
+
+// Iterations [first, first + count) of part `part`.
+struct CrossRunIt {
+    int first, count;
+};
+__device__ __forceinline__ CrossRunIt cross_run_it(const BwdParams &p, int n_it, int part) {
+    CrossRunIt r;
+    r.first = (int)((long long)n_it * part / p.parts);
+    r.count = (int)((long long)n_it * (part + 1) / p.parts) - r.first;
+    return r;
+}
+// 32 columns of a row of dK or dV (already scaled) into a part's fp32 sums.
+__device__ __forceinline__ void store_part(float *dst, const uint32_t (&a)[32], float mul) {
+#pragma unroll
+    for (int c = 0; c < 32; c += 4)
+        st_global_v4(dst + c, __float_as_uint(__uint_as_float(a[c]) * mul), __float_as_uint(__uint_as_float(a[c + 1]) * mul),
+                     __float_as_uint(__uint_as_float(a[c + 2]) * mul), __float_as_uint(__uint_as_float(a[c + 3]) * mul));
+}
 
 // CROSS (keys of another sequence, heads shared by `group` query heads): the CTA of a key block visits the query blocks
 // of every head that shares its keys, head by head, so dK and dV of shared heads are summed in the same accumulators.
@@ -260,16 +282,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     // Block b -> (key block j, head bh); low j first, which in the causal case
     // are the blocks with the most query blocks to visit.
     const int bh = blockIdx.x % p.BH;
-    const int j = blockIdx.x / p.BH;
+    const int part = CROSS ? blockIdx.x / p.BH % p.parts : 0;
+    const int j = CROSS ? blockIdx.x / p.BH / p.parts : blockIdx.x / p.BH;
     const int n_qblk = p.Npad / kBlk;
     const int i0 = CAUSAL ? j : 0;  // first query block that sees key block j
-    const int n_it = CROSS ? n_qblk * p.group : n_qblk - i0;  // >= 1
+    const CrossRunIt run = CROSS ? cross_run_it(p, n_qblk * p.group, part) : CrossRunIt{0, n_qblk - i0};
+    const int n_it = run.count;     // >= 1
     grid_launch_dependents();       // fa_bwd_post may be scheduled once every CTA has started
     int n_keys = p.N;               // keys of the sequence
     if constexpr (CROSS) {
         n_keys = cross_len(p, bh / p.Hkv);
         if (j * kBlk >= n_keys) {  // (fa_bwd_post must not start before fa_bwd_pre is done, so wait for it here too)
-            zero_block<T, D, kBwdThreads>(p, bh, j * kBlk, threadIdx.x);
+            if (p.parts == 1) zero_block<T, D, kBwdThreads>(p, bh, j * kBlk, threadIdx.x);
             grid_dependency_wait();
             return;
         }
@@ -316,8 +340,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int it = 0; it < n_it; ++it) {
                 const int s = it % ST;
                 const uint32_t dst = smem_u32(smem + C::SMEM_QD + s * 2 * C::TILE);
-                const int row0 = (CROSS ? it % n_qblk : i0 + it) * kBlk;
-                const int qh = CROSS ? qh0 + it / n_qblk : bh;
+                const int row0 = (CROSS ? (run.first + it) % n_qblk : i0 + it) * kBlk;
+                const int qh = CROSS ? qh0 + (run.first + it) / n_qblk : bh;
                 if (!bwd_wait(bar_q_empty(s), ((it / ST) & 1u) ^ 1u, p)) break;
                 mbar_arrive_expect_tx(bar_q_full(s), C::TILE);
                 for (int c = 0; c < C::NCH; ++c) tma_load_3d(dst + c * C::CHUNK, &tm_q, bar_q_full(s), c * 64, row0, qh, pol);
@@ -411,15 +435,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // this warp's 4 KB of the dS buffer (its 32 key rows of chunk g), reused to stage dQ tiles
         const uint32_t stage = ds_base + g * C::CHUNK + w * 4096;
         // one statistic per thread: -lse2 (group 0) or -D (group 1) of query row r of the block
-        const float *stat_src = (g == 0 ? p.lse2 : p.dsum) + (size_t)qh0 * p.Npad + r;
+        const float *stat_src = (g == 0 ? p.lse2 : p.dsum) + (size_t)qh0 * p.Npad + (size_t)run.first * kBlk + r;
         grid_dependency_wait();  // statistics and the zeroed dQ accumulator are written by fa_bwd_pre
         float stat_next = -__ldg(stat_src + i0 * kBlk);
         const bool ragged_keys = (j + 1) * kBlk > n_keys;
         bool ok = true;
         for (int it = 0; ok && it < n_it; ++it) {
             const int i = i0 + it;
-            const int row0 = (CROSS ? it % n_qblk : i) * kBlk;
-            const int qh = CROSS ? qh0 + it / n_qblk : bh;
+            const int row0 = (CROSS ? (run.first + it) % n_qblk : i) * kBlk;
+            const int qh = CROSS ? qh0 + (run.first + it) / n_qblk : bh;
             // hand over the block's statistics (their last readers passed p_full of the previous block)
             st_shared_f32(stats + (g * 128 + r) * 4, stat_next);
             mbar_arrive(bar_stats);
@@ -516,7 +540,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int c0 = 0; c0 < D; c0 += 64) {
                 uint32_t a[32], b[32];
                 tmem_ld32x2_wait(tmem + lane_base + src_col + c0, a, tmem + lane_base + src_col + c0 + 32, b);
-                if (store) {
+                if (CROSS && p.parts > 1) {
+                    if (store) {
+                        float *sum = p.kv_part + (((size_t)(2 * part + (g == 0 ? 1 : 0)) * p.BH + bh) * k_rows + key) * D + c0;
+                        store_part(sum, a, mul);
+                        store_part(sum + 32, b, mul);
+                    }
+                } else if (store) {
 #pragma unroll
                     for (int c = 0; c < 32; c += 8) {
                         st_global_v4(dst + c0 + c, pk2<T>(__uint_as_float(a[c]) * mul, __uint_as_float(a[c + 1]) * mul),
@@ -899,23 +929,31 @@ struct BwdCfgX64 : BwdCfgH64<T> {
     static_assert(SLACK >= 256, "shared memory budget");
 };
 
-// The CTA's next key block: block j of K/V head bh, of a batch index with len keys.
+// The CTA's next key block (or part of its iterations): block j of K/V head bh, of a batch index with len keys;
+// `count` iterations from query block `row` / kBlk of head qh on.
 struct CrossCursor {
-    int a, b = 0, base = 0, len, bh = 0, j = 0;
+    int a, b = 0, base = 0, len, bh = 0, j = 0, part = 0, first = 0, count = 0, qh = 0, row = 0;
     __device__ __forceinline__ explicit CrossCursor(const BwdParams &p) : a((int)blockIdx.x - (int)gridDim.x) { len = cross_len(p, 0); }
     __device__ __forceinline__ bool next(const BwdParams &p) {
         a += gridDim.x;
-        const int B = p.BH / p.Hkv;
+        const int B = p.BH / p.Hkv, n_qblk = p.Npad / kBlk;
         for (;;) {
-            const int blocks = (len + kBlk - 1) / kBlk * p.Hkv;
-            if (a < base + blocks) break;
-            base += blocks;
+            const int items = (len + kBlk - 1) / kBlk * p.Hkv * p.parts;
+            if (a < base + items) break;
+            base += items;
             if (++b >= B) return false;
             len = cross_len(p, b);
         }
-        const int r = a - base;
-        j = r / p.Hkv;
-        bh = b * p.Hkv + (r - j * p.Hkv);
+        int r = a - base;
+        j = r / (p.Hkv * p.parts);
+        r -= j * p.Hkv * p.parts;
+        part = r / p.Hkv;
+        bh = b * p.Hkv + (r - part * p.Hkv);
+        const CrossRunIt run = cross_run_it(p, n_qblk * p.group, part);
+        first = run.first;
+        count = run.count;
+        qh = bh * p.group + first / n_qblk;
+        row = first % n_qblk * kBlk;
         return true;
     }
 };
@@ -952,8 +990,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SMEM_BAR + C::NUM_BARS * 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int n_qblk = p.Npad / kBlk;
-    const int n_it = n_qblk * p.group;  // iterations per key block: the query blocks of every head of the group
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tm_k);
@@ -1006,8 +1042,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 mbar_arrive_expect_tx(bar_kv_full(b), 2 * C::CHUNK);
                 tma_load_3d(kv, &tm_k, bar_kv_full(b), 0, x.j * kBlk, x.bh, pol);
                 tma_load_3d(kv + C::CHUNK, &tm_v, bar_kv_full(b), 0, x.j * kBlk, x.bh, pol);
-                int row = 0, qh = x.bh * p.group;
-                for (int it = 0; it < n_it; ++it, ++g) {
+                int row = x.row, qh = x.qh;
+                for (int it = 0; it < x.count; ++it, ++g) {
                     const int s = g % ST;
                     ok = bwd_wait(bar_qd_empty(s), ((g / ST) & 1u) ^ 1u, p);
                     if (!ok) break;
@@ -1073,12 +1109,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     issue_s(0, 0, 0);
                     issue_s(0, 0, 1);
                     tc_commit(bar_qd_empty(0), issue);
-                    if (n_it == 1) tc_commit(bar_kv_free(0), issue);
+                    if (x.count == 1) tc_commit(bar_kv_free(0), issue);
                 }
             }
             // after the passes of iteration g have read S and dP, those of iteration g + 1 (block n, its it-th)
             for (int g = 0, n = 0, it = 0; ok && more; ++g) {
-                const bool crossing = ++it == n_it;
+                const bool crossing = ++it == x.count;
                 if (crossing) {
                     it = 0;
                     ++n;
@@ -1097,7 +1133,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     tc_fence_after();
                     issue_s(g + 1, n, 1);
                     tc_commit(bar_qd_empty((g + 1) % ST), issue);
-                    if (it == n_it - 1) tc_commit(bar_kv_free(n & 1), issue);
+                    if (it == x.count - 1) tc_commit(bar_kv_free(n & 1), issue);
                 }
             }
         } else {
@@ -1121,7 +1157,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 ok = take_kv(n, x);
                 const uint64_t k_mn =
                     smem_desc_sw128(smem_u32(smem + C::SMEM_KV + (n & 1) * 2 * C::CHUNK), C::CHUNK, 1024);
-                for (int it = 0; ok && it < n_it; ++it, ++g) {
+                for (int it = 0; ok && it < x.count; ++it, ++g) {
                     const int s = g % ST;
                     ok = bwd_wait_warp(bar_p_full(0), g & 1u, p) && bwd_wait_warp(bar_qd_full(s), (g / ST) & 1u, p);
                     // the last block's dV and dK have been taken out
@@ -1145,7 +1181,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                         mma_ss(tmem + 448, ds_mn + off, k_mn + off, C::ID_DQ, k > 0 ? 1u : 0u, issue);
                     }
                     tc_commit(bar_dq_full, issue);
-                    if (it == n_it - 1) tc_commit(bar_kv_free(n & 1), issue);
+                    if (it == x.count - 1) tc_commit(bar_kv_free(n & 1), issue);
                 }
             }
         }
@@ -1157,7 +1193,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (long long i = blockIdx.x; i < (long long)p.BH * blocks; i += gridDim.x) {
             const int bh = (int)(i % p.BH), j = (int)(i / p.BH);
             const int len = cross_len(p, bh / p.Hkv);
-            if (j * kBlk >= len) zero_block<T, 64, 32>(p, bh, j * kBlk, lane);
+            if (p.parts == 1 && j * kBlk >= len) zero_block<T, 64, 32>(p, bh, j * kBlk, lane);
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- gradient warps
@@ -1173,7 +1209,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         grid_dependency_wait();  // statistics and the zeroed dQ accumulator are written by fa_bwd_pre
         CrossCursor x(p);
         bool ok = true, more = x.next(p);
-        float stat_next = more ? -__ldg(stat_row + (size_t)x.bh * p.group * p.Npad) : 0.f;
+        auto stats_of = [&](const CrossCursor &c) { return stat_row + (size_t)c.bh * p.group * p.Npad + (size_t)c.first * kBlk; };
+        float stat_next = more ? -__ldg(stats_of(x)) : 0.f;
         auto readout = [&](int g, int qh, int row) -> bool {  // dQ of iteration g
             if (!bwd_wait_warp(bar_dq_full, (uint32_t)g & 1u, p)) return false;
             tc_fence_after();
@@ -1185,12 +1222,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             return true;
         };
         for (int g = 0; ok && more;) {
-            const int bh = x.bh, key = x.j * kBlk + r, len = x.len;
+            const int bh = x.bh, key = x.j * kBlk + r, len = x.len, count = x.count, part = x.part;
             const bool key_ok = key < len, ragged_keys = (x.j + 1) * kBlk > len;
-            const float *stat_src = stat_row + (size_t)bh * p.group * p.Npad;
+            const float *stat_src = stats_of(x);
+            int qh = x.qh, row = x.row;
             more = x.next(p);  // the block after this one
-            int qh = bh * p.group, row = 0;
-            for (int it = 0; it < n_it; ++it, ++g) {
+            for (int it = 0; it < count; ++it, ++g) {
                 const uint32_t stats = stats0 + (g & 1) * 512;
                 st_shared_f32(stats + r * 4, stat_next);
                 mbar_arrive(bar_stats(gr));
@@ -1227,8 +1264,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 fence_proxy_async_smem();
                 tc_fence_before();
                 mbar_arrive(bar_p_full(gr));
-                if (it + 1 < n_it) stat_next = -__ldg(stat_src + (it + 1) * kBlk);
-                else if (more) stat_next = -__ldg(stat_row + (size_t)x.bh * p.group * p.Npad);
+                if (it + 1 < count) stat_next = -__ldg(stat_src + (it + 1) * kBlk);
+                else if (more) stat_next = -__ldg(stats_of(x));
                 if (it > 0) {  // dQ of the last iteration: the block before this one, or the last of the head before
                     ok = row > 0 ? readout(g - 1, qh, row - kBlk) : readout(g - 1, qh - 1, p.Npad - kBlk);
                     if (!ok) break;
@@ -1239,7 +1276,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                     ++qh;
                 }
             }
-            if (ok) ok = readout(g - 1, bh * p.group + p.group - 1, p.Npad - kBlk);
+            if (ok) ok = row > 0 ? readout(g - 1, qh, row - kBlk) : readout(g - 1, qh - 1, p.Npad - kBlk);
             if (!ok) break;
             // dV_j (half A's group), dK_j (B's): the last dq_full covers every dV and dK product of the block
             const float mul = gr == 0 ? 1.0f : p.scale;
@@ -1247,7 +1284,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             tmem_ld32x2_wait(tmem + lane_base + 320 + 64 * gr, a, tmem + lane_base + 320 + 64 * gr + 32, b);
             tc_fence_before();
             mbar_arrive(bar_acc_free);  // the next block's products may overwrite them
-            if (key < p.Nk) {  // (rows past the sequence's keys get their zeros)
+            if (p.parts > 1) {
+                if (key < p.Nk) {
+                    float *sum = p.kv_part + (((size_t)(2 * part + (gr == 0 ? 1 : 0)) * p.BH + bh) * p.Nk + key) * 64;
+                    store_part(sum, a, mul);
+                    store_part(sum + 32, b, mul);
+                }
+            } else if (key < p.Nk) {  // (rows past the sequence's keys get their zeros)
                 T *dst = reinterpret_cast<T *>(gr == 0 ? p.dv : p.dk) + ((size_t)bh * p.Nk + (size_t)key) * 64;
 #pragma unroll
                 for (int c = 0; c < 32; c += 8) {
@@ -1331,6 +1374,31 @@ __global__ void __launch_bounds__(256) fa_bwd_post(const float *__restrict__ dq_
     reinterpret_cast<uint2 *>(dq)[i] = o;
 }
 
+// The parts' fp32 dK, dV added up in order (so the same every time) and converted; 0 past a sequence's keys.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) fa_bwd_cross_post(const BwdParams p) {
+    grid_dependency_wait();
+    const size_t per = (size_t)p.BH * p.Nk * D / 4;  // 4-column units of dK, and of dV
+    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= 2 * per) return;
+    const bool v = i >= per;
+    const size_t u = v ? i - per : i, row = u / (D / 4);
+    const int bh = (int)(row / p.Nk), key = (int)(row - (size_t)bh * p.Nk);
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (key < cross_len(p, bh / p.Hkv)) {
+        const float4 *src = reinterpret_cast<const float4 *>(p.kv_part) + (v ? per : 0) + u;
+#pragma unroll 4
+        for (int k = 0; k < p.parts; ++k) {
+            const float4 x = src[2 * k * per];
+            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
+        }
+    }
+    uint2 o;
+    o.x = pk2<T>(s.x, s.y);
+    o.y = pk2<T>(s.z, s.w);
+    reinterpret_cast<uint2 *>(v ? p.dv : p.dk)[u] = o;
+}
+
 template <typename T, int D, bool CAUSAL, bool CROSS = false>
 int launch_bwd_variant(const BwdArgs &a) {
     // d = 64 runs the overlapped half-block kernel; d = 128 (tensor memory full) the serial one
@@ -1375,13 +1443,21 @@ int launch_bwd_variant(const BwdArgs &a) {
     p.scale = a.scale;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
-    int64_t grid = static_cast<int64_t>(BHkv) * (bwd_padded_rows(Nk) / kBlk);
+    p.parts = CROSS ? a.parts : 1;
+    p.kv_part = CROSS ? a.kv_part : nullptr;
+    int64_t grid = static_cast<int64_t>(BHkv) * (bwd_padded_rows(Nk) / kBlk) * p.parts;
     if (D == 64 && CROSS && grid > a.num_sms) grid = a.num_sms;  // each CTA takes several key blocks
     // programmatic dependents: the backward's copies of K, V, Q, dO start while fa_bwd_pre drains (its
     // gradient warps wait for the statistics), and fa_bwd_post's launch overlaps the backward's tail
     if (launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), smem_bytes, a.stream, tq, tk,
                          tv, tdo, tdq, p) != cudaSuccess)
         return -5;
+    if (CROSS && a.parts > 1) {
+        const size_t units = 2 * static_cast<size_t>(BHkv) * Nk * D / 4;
+        if (launch_dependent(fa_bwd_cross_post<T, D>, dim3(static_cast<unsigned>((units + 255) / 256)), dim3(256), 0, a.stream,
+                             p) != cudaSuccess)
+            return -5;
+    }
     const size_t n4 = static_cast<size_t>(BH) * a.N * D / 4;
     if (launch_dependent(fa_bwd_post<T>, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, a.stream,
                          static_cast<const float *>(a.dq_acc), static_cast<T *>(a.dq), n4) != cudaSuccess)

@@ -23,7 +23,22 @@ struct BwdArgs {
     // keys of another sequence (launch_bwd_cross): k, v, dk, dv [B][Hkv][Nk][d], N query rows
     int Hkv = 0, Nk = 0, num_sms = 0;
     const int *kv_lens = nullptr;  // [B] keys in use, or nullptr (Nk)
+    int parts = 1;                 // CTAs that share the query blocks of a key block
+    float *kv_part = nullptr;      // workspace for parts > 1: fp32 [parts][2][B*Hkv][Nk][d] (dK, dV)
 };
+
+// CTAs per key block for the backward over keys of another length: where there are fewer key blocks than half the
+// SMs, as many as fill the GPU, each with at least one (head, query block).
+inline int bwd_cross_parts(int64_t BHkv, int group, int Nq, int Nk, int num_sms) {
+    const int64_t blocks = BHkv * ((static_cast<int64_t>(Nk) + kBwdRows - 1) / kBwdRows);
+    const int64_t n_it = group * ((static_cast<int64_t>(Nq) + kBwdRows - 1) / kBwdRows);
+    int64_t n = num_sms / blocks;
+    if (n > n_it) n = n_it;
+    return n < 1 ? 1 : static_cast<int>(n);
+}
+inline size_t bwd_cross_part_bytes(int64_t BHkv, int Nk, int d, int parts) {
+    return parts > 1 ? static_cast<size_t>(parts) * 2 * static_cast<size_t>(BHkv) * Nk * d * sizeof(float) : 0;
+}
 
 inline int64_t bwd_padded_rows(int N) { return ((static_cast<int64_t>(N) + kBwdRows - 1) / kBwdRows) * kBwdRows; }
 

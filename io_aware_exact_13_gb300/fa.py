@@ -83,6 +83,7 @@ SIGNATURES = {
                                [ctypes.c_float, ctypes.c_int, ctypes.c_int, _vp]),
     "fa_fwd_varlen": (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _vp]),
     "fa_fwd_varlen_fp16": (ctypes.c_int, [_vp] * 6 + [ctypes.c_int] * 6 + [ctypes.c_float, ctypes.c_int, _vp]),
+    "fa_bwd_cross_workspace_bytes": (ctypes.c_longlong, [ctypes.c_int] * 6),
     "fa_cross_num_splits": (ctypes.c_int, [ctypes.c_int] * 4),
     "fa_kvq8_num_parts": (ctypes.c_int, [ctypes.c_int] * 6),
     "fa_kvq8_workspace_bytes": (ctypes.c_longlong, [ctypes.c_int] * 5),
@@ -839,6 +840,13 @@ def attention_cross(q, k, v, kv_lens=None, scale=None, n_splits=None, stream=Non
     return _raw_cross("fa_fwd_cross" + suffix, q.dtype, q, k, v, kv_lens, None, None, scale, n_splits, None, stream)
 
 
+def fa_bwd_cross_workspace_bytes(B, H, Hkv, Nq, Nk, d) -> int:
+    n = int(lib.fa_bwd_cross_workspace_bytes(int(B), int(H), int(Hkv), int(Nq), int(Nk), int(d)))
+    if n < 0:
+        raise FAError(n, "fa_bwd_cross_workspace_bytes")
+    return n
+
+
 def _raw_bwd_cross(fn_name, dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream):
     """``dq``, ``dk``, ``dv`` None: allocated; ``workspace`` None: allocated."""
     index, B, H, Hkv, Nq, Nk, d = _check_cross(q, k, v, kv_lens, dtype)
@@ -847,7 +855,8 @@ def _raw_bwd_cross(fn_name, dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv,
     _check_tensor("lse", lse, torch.float32, (B, H, Nq), index)
     with _on(index, stream):
         if workspace is None:
-            workspace = torch.empty(fa_bwd_workspace_bytes(B, H, Nq, d), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty(fa_bwd_cross_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8,
+                                    device=q.device)
         if dq is None:
             dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         else:
@@ -866,7 +875,8 @@ def _raw_bwd_cross(fn_name, dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv,
 
 def fa_bwd_cross(q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream=None):
     """bf16 gradients of ``fa_fwd_cross`` into ``dq`` (like q) and ``dk``, ``dv`` (like k, summed over the query heads
-    that share them; 0 past kv_lens); ``workspace`` of ``fa_bwd_workspace_bytes(B, H, Nq, d)`` bytes."""
+    that share them; 0 past kv_lens); ``workspace`` of
+    ``fa_bwd_cross_workspace_bytes(B, H, Hkv, Nq, Nk, d)`` bytes."""
     _raw_bwd_cross("fa_bwd_cross", torch.bfloat16, q, k, v, kv_lens, out, dout, lse, dq, dk, dv, scale, workspace, stream)
 
 

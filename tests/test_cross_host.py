@@ -58,7 +58,11 @@ def test_splits_and_workspaces_are_refused(fa):
     assert fwd(fa, n_splits=3) == fa.FA_ERR_WORKSPACE
     assert fwd(fa, n_splits=3, ws=0x900010, ws_bytes=need) == fa.FA_ERR_WORKSPACE
     assert fwd(fa, n_splits=3, ws=0x900000, ws_bytes=need - 1) == fa.FA_ERR_WORKSPACE
-    need = fa.fa_bwd_workspace_bytes(2, 4, 5, 64)
+    need = fa.fa_bwd_cross_workspace_bytes(2, 4, 2, 5, 300, 64)
+    assert need >= fa.fa_bwd_workspace_bytes(2, 4, 5, 64)
+    for bad in ((0, 4, 2, 5, 300, 64), (2, 4, 3, 5, 300, 64), (2, 4, 2, 5, 0, 64)):
+        assert fa.lib.fa_bwd_cross_workspace_bytes(*bad) == fa.FA_ERR_SHAPE
+    assert fa.lib.fa_bwd_cross_workspace_bytes(2, 4, 2, 5, 300, 96) == fa.FA_ERR_UNSUPPORTED
     assert bwd(fa, ws=0) == fa.FA_ERR_WORKSPACE
     assert bwd(fa, ws_bytes=need - 1) == fa.FA_ERR_WORKSPACE
     assert fa.lib.fa_cross_num_splits(0, 1, 1, 1) == fa.FA_ERR_SHAPE

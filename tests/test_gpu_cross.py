@@ -111,6 +111,10 @@ CASES = [
     ("fp16", 5, 2, 1, 64, 200, 64, [0, 200, 16, 17, 113]),
     ("bf16", 1, 3, 3, 700, 90, 128, [33]),
     ("bf16", 2, 4, 4, 2, 2049, 128, [2049, 1025]),
+    # more key blocks than SMs (one CTA for a block's gradients at d = 128, several blocks for a CTA at d = 64)
+    ("bf16", 4, 8, 8, 130, 700, 64, [700, 641, 0, 130]),
+    ("fp16", 4, 8, 8, 130, 700, 128, [700, 640, 129, 1]),
+    ("fp16", 40, 10, 5, 3, 140, 64, [int(x) for x in np.random.default_rng(5).integers(0, 141, 40)]),
 ]
 
 
@@ -255,7 +259,7 @@ def test_guard_bands(fa):
     bq, dq = guarded(q.shape, q.dtype)
     bk, dk = guarded(k.shape, k.dtype)
     bv, dv = guarded(k.shape, k.dtype)
-    nb2 = fa.fa_bwd_workspace_bytes(B, H, Nq, d)
+    nb2 = fa.fa_bwd_cross_workspace_bytes(B, H, Hkv, Nq, Nk, d)
     ws2 = torch.full((nb2 + 512,), 7, dtype=torch.uint8, device=DEV)
     fa.fa_bwd_cross_fp16(q, k, v, ints(lens), out, do, lse, dq, dk, dv, 0.125, ws2[:nb2])
     status_ok(fa)
