@@ -9,6 +9,9 @@
 // the gradient of sum(dO o O) (D_i = sum_j P_ij dP_ij because the rows of P
 // sum to one).
 //
+// (Keys of another sequence, CROSS: the same plan with the key count of the batch index, heads that share keys, and a
+// kernel of its own at d = 64; see cross_run_it and fa_bwd_cross_kernel_h64.)
+//
 // Two kernels share that plan: fa_bwd_kernel_h64 (d = 64, further below), which
 // overlaps the tensor core with the gradient warps over half blocks, and
 // fa_bwd_kernel (used for d = 128, where the dV and dK accumulators leave no
@@ -907,10 +910,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // fa_bwd_kernel_h64, but a CTA goes through several key blocks: a decoder has few query blocks (four for 448 rows), and
 // with a CTA per key block its start (tensor memory, barriers, the first copies) and its end (the last dQ, dK and dV)
 // took as long as its products. Here K and V are double-buffered and the next block's copies, S and dP run during the
-// end of the last one; only the first dV/dK product waits until the gradient warps have taken dV and dK out of tensor
-// memory. All phases are those of one running iteration count g: iteration g belongs to the CTA's key block g / n_it.
+// end of the last one. The gradient warps take the last block's dQ, dV and dK after the next block's first pass, while
+// the products of that pass's half blocks are due: only the first dV/dK product waits until dV and dK are out of tensor
+// memory. All phases are those of one running iteration count g.
 // The CTA's blocks are every gridDim.x-th of those that hold keys, batch index by batch index; blocks without keys are
-// set to zero first, by the CTAs in turn.
+// set to zero by the CTAs in turn. Measured (B 8, H 16, fp16, 448 queries, up to 1500 keys ragged, the whole backward):
+// 111 us with a CTA per key block, 105 with several per CTA, 99 with the read-out behind the next block's first pass.
 template <typename T>
 struct BwdCfgX64 : BwdCfgH64<T> {
     using B = BwdCfgH64<T>;
@@ -1221,7 +1226,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             stage_and_reduce_dq(&tm_dq, box0 + (g & 1) * 2 * C::CHUNK, qv, p.scale, lane, 32 * gr, row + w * 32, qh);
             return true;
         };
-        for (int g = 0; ok && more;) {
+        // dV_j (half A's group), dK_j (B's) of key `key`: the last dq_full covers every dV and dK product of the block
+        auto take = [&](int bh, int key, int part) {
+            const float mul = gr == 0 ? 1.0f : p.scale;
+            uint32_t a[32], b[32];
+            tmem_ld32x2_wait(tmem + lane_base + 320 + 64 * gr, a, tmem + lane_base + 320 + 64 * gr + 32, b);
+            tc_fence_before();
+            mbar_arrive(bar_acc_free);  // the next block's products may overwrite them
+            if (key >= p.Nk) return;    // (rows past the sequence's keys get their zeros)
+            if (p.parts > 1) {
+                float *sum = p.kv_part + (((size_t)(2 * part + (gr == 0 ? 1 : 0)) * p.BH + bh) * p.Nk + key) * 64;
+                store_part(sum, a, mul);
+                store_part(sum + 32, b, mul);
+                return;
+            }
+            T *dst = reinterpret_cast<T *>(gr == 0 ? p.dv : p.dk) + ((size_t)bh * p.Nk + (size_t)key) * 64;
+#pragma unroll
+            for (int c = 0; c < 32; c += 8) {
+                st_global_v4(dst + c, pk2<T>(__uint_as_float(a[c]) * mul, __uint_as_float(a[c + 1]) * mul),
+                             pk2<T>(__uint_as_float(a[c + 2]) * mul, __uint_as_float(a[c + 3]) * mul),
+                             pk2<T>(__uint_as_float(a[c + 4]) * mul, __uint_as_float(a[c + 5]) * mul),
+                             pk2<T>(__uint_as_float(a[c + 6]) * mul, __uint_as_float(a[c + 7]) * mul));
+                st_global_v4(dst + 32 + c, pk2<T>(__uint_as_float(b[c]) * mul, __uint_as_float(b[c + 1]) * mul),
+                             pk2<T>(__uint_as_float(b[c + 2]) * mul, __uint_as_float(b[c + 3]) * mul),
+                             pk2<T>(__uint_as_float(b[c + 4]) * mul, __uint_as_float(b[c + 5]) * mul),
+                             pk2<T>(__uint_as_float(b[c + 6]) * mul, __uint_as_float(b[c + 7]) * mul));
+            }
+        };
+        int g = 0, last_qh = 0, last_row = 0, last_bh = 0, last_key = 0, last_part = 0;  // of the iteration, block before
+        while (ok && more) {
             const int bh = x.bh, key = x.j * kBlk + r, len = x.len, count = x.count, part = x.part;
             const bool key_ok = key < len, ragged_keys = (x.j + 1) * kBlk > len;
             const float *stat_src = stats_of(x);
@@ -1266,45 +1299,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 mbar_arrive(bar_p_full(gr));
                 if (it + 1 < count) stat_next = -__ldg(stat_src + (it + 1) * kBlk);
                 else if (more) stat_next = -__ldg(stats_of(x));
-                if (it > 0) {  // dQ of the last iteration: the block before this one, or the last of the head before
-                    ok = row > 0 ? readout(g - 1, qh, row - kBlk) : readout(g - 1, qh - 1, p.Npad - kBlk);
+                if (g > 0) {  // dQ of the last iteration and, when it ended a block, that block's dV, dK
+                    ok = readout(g - 1, last_qh, last_row);
                     if (!ok) break;
+                    if (it == 0) take(last_bh, last_key, last_part);
                 }
+                last_qh = qh;
+                last_row = row;
                 row += kBlk;
                 if (row == p.Npad) {
                     row = 0;
                     ++qh;
                 }
             }
-            if (ok) ok = row > 0 ? readout(g - 1, qh, row - kBlk) : readout(g - 1, qh - 1, p.Npad - kBlk);
-            if (!ok) break;
-            // dV_j (half A's group), dK_j (B's): the last dq_full covers every dV and dK product of the block
-            const float mul = gr == 0 ? 1.0f : p.scale;
-            uint32_t a[32], b[32];
-            tmem_ld32x2_wait(tmem + lane_base + 320 + 64 * gr, a, tmem + lane_base + 320 + 64 * gr + 32, b);
-            tc_fence_before();
-            mbar_arrive(bar_acc_free);  // the next block's products may overwrite them
-            if (p.parts > 1) {
-                if (key < p.Nk) {
-                    float *sum = p.kv_part + (((size_t)(2 * part + (gr == 0 ? 1 : 0)) * p.BH + bh) * p.Nk + key) * 64;
-                    store_part(sum, a, mul);
-                    store_part(sum + 32, b, mul);
-                }
-            } else if (key < p.Nk) {  // (rows past the sequence's keys get their zeros)
-                T *dst = reinterpret_cast<T *>(gr == 0 ? p.dv : p.dk) + ((size_t)bh * p.Nk + (size_t)key) * 64;
-#pragma unroll
-                for (int c = 0; c < 32; c += 8) {
-                    st_global_v4(dst + c, pk2<T>(__uint_as_float(a[c]) * mul, __uint_as_float(a[c + 1]) * mul),
-                                 pk2<T>(__uint_as_float(a[c + 2]) * mul, __uint_as_float(a[c + 3]) * mul),
-                                 pk2<T>(__uint_as_float(a[c + 4]) * mul, __uint_as_float(a[c + 5]) * mul),
-                                 pk2<T>(__uint_as_float(a[c + 6]) * mul, __uint_as_float(a[c + 7]) * mul));
-                    st_global_v4(dst + 32 + c, pk2<T>(__uint_as_float(b[c]) * mul, __uint_as_float(b[c + 1]) * mul),
-                                 pk2<T>(__uint_as_float(b[c + 2]) * mul, __uint_as_float(b[c + 3]) * mul),
-                                 pk2<T>(__uint_as_float(b[c + 4]) * mul, __uint_as_float(b[c + 5]) * mul),
-                                 pk2<T>(__uint_as_float(b[c + 6]) * mul, __uint_as_float(b[c + 7]) * mul));
-                }
-            }
+            last_bh = bh;
+            last_key = key;
+            last_part = part;
         }
+        if (ok && g > 0 && readout(g - 1, last_qh, last_row)) take(last_bh, last_key, last_part);
         if (lane == 0) bulk_wait_all();  // the dQ reductions
     }
     __syncwarp();
