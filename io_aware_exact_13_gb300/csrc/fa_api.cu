@@ -616,6 +616,13 @@ int varlen_common(bool fp16, const void *q, const void *k, const void *v, void *
     return fp16 ? fa::launch_fwd_varlen_fp16(a) : fa::launch_fwd_varlen_bf16(a);
 }
 
+// Bytes behind bwd_workspace_bytes for the runs of cut key blocks.
+size_t bwd_cross_part_bytes(int B, int H, int Hkv, int Nq, int Nk, int d, const DeviceInfo *di) {
+    const int sms = di ? di->num_sms : kNominalSms;
+    const int64_t blocks = fa::bwd_cross_blocks(static_cast<int64_t>(B) * Hkv, Nk);
+    return fa::bwd_cross_part_bytes(fa::bwd_cross_slots(blocks, fa::bwd_cross_iters(H / Hkv, Nq), sms), d, sms);
+}
+
 int bwd_common(bool fp16, const void *q, const void *k, const void *v, const void *out, const void *dout,
                const float *lse, void *dq, void *dk, void *dv, int B, int H, int N, int d, float scale, int causal,
                void *workspace, unsigned long long workspace_bytes, void *stream, bool cross = false, int Hkv = 0,
@@ -638,11 +645,9 @@ int bwd_common(bool fp16, const void *q, const void *k, const void *v, const voi
     const size_t need = fa::bwd_workspace_bytes(bh, N, d);
     DeviceInfo *di = nullptr;
     size_t need_cross = 0;
-    int parts = 1;
-    if (cross) {  // the part count goes by the device's SMs
+    if (cross) {  // how blocks are cut goes by the device's SMs
         di = device_info();
-        parts = fa::bwd_cross_parts(static_cast<int64_t>(B) * Hkv, H / Hkv, N, Nk, di ? di->num_sms : kNominalSms);
-        need_cross = fa::bwd_cross_part_bytes(static_cast<int64_t>(B) * Hkv, Nk, d, parts);
+        need_cross = bwd_cross_part_bytes(B, H, Hkv, N, Nk, d, di);
     }
     if (!workspace || !aligned(workspace, 256) || workspace_bytes < need + need_cross) return FA_ERR_WORKSPACE;
     if (!cross) di = device_info();
@@ -677,8 +682,7 @@ int bwd_common(bool fp16, const void *q, const void *k, const void *v, const voi
         a.Nk = Nk;
         a.num_sms = di->num_sms;
         a.kv_lens = kv_lens;
-        a.parts = parts;
-        a.kv_part = parts > 1 ? reinterpret_cast<float *>(ws + need) : nullptr;  // need is a multiple of 256
+        a.kv_part = reinterpret_cast<float *>(ws + need);  // need is a multiple of 256
         log_call("backward over keys of another length %s d=%d B=%d H=%d Hkv=%d Nq=%d Nk=%d lens=%s", fp16 ? "fp16" : "bf16",
                  d, B, H, Hkv, N, Nk, kv_lens ? "given" : "all");
         return fa::launch_bwd_cross(a, fp16);
@@ -982,9 +986,7 @@ long long fa_bwd_cross_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, in
     if (n < 0) return n;
     if (Hkv < 1 || H % Hkv != 0 || Nk < 1) return FA_ERR_SHAPE;
     DeviceInfo *di = device_info();
-    const int64_t bh = static_cast<int64_t>(B) * Hkv;
-    const int parts = fa::bwd_cross_parts(bh, H / Hkv, Nq, Nk, di ? di->num_sms : kNominalSms);
-    return n + static_cast<long long>(fa::bwd_cross_part_bytes(bh, Nk, d, parts));
+    return n + static_cast<long long>(bwd_cross_part_bytes(B, H, Hkv, Nq, Nk, d, di));
 }
 
 int fa_bwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, const void *out,

@@ -10,7 +10,7 @@
 // sum to one).
 //
 // (Keys of another sequence, CROSS: the same plan with the key count of the batch index, heads that share keys, and a
-// kernel of its own at d = 64; see cross_run_it and fa_bwd_cross_kernel_h64.)
+// kernel of its own at d = 64; see BwdCrossPlan and fa_bwd_cross_kernel_h64.)
 //
 // Two kernels share that plan: fa_bwd_kernel_h64 (d = 64, further below), which
 // overlaps the tensor core with the gradient warps over half blocks, and
@@ -55,6 +55,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <algorithm>
 
 #include "fa_bwd.cuh"
 #include "fa_launch.cuh"
@@ -104,20 +106,28 @@ struct BwdParams {
     // of which batch index b uses the first kv_lens[b] (nullptr: all), and `group` query heads share one
     const int *kv_lens;
     int Nk, Hkv, group;
-    // with few key blocks the iterations of a block are cut into `parts` runs of neighbouring ones, each with its own CTA
-    // and its own fp32 dK, dV in kv_part [parts][2][BH][Nk][d], added up by fa_bwd_cross_post
-    int parts;
+    // iterations of the last blocks are cut into runs (BwdCrossPlan) with fp32 dK, dV in kv_part [slot][2][128][d],
+    // added up by fa_bwd_cross_post
+    int sms;
     float *kv_part;
+    int4 *kv_cut;  // [0]: cut blocks, runs of each; [1 + t]: head, block, key count of cut block t
 };
 
-// Iterations [first, first + count) of part `part`.
-struct CrossRunIt {
-    int first, count;
+// Item a of the plan: the rank of its key block in the line of blocks, its iterations [first, first + count) and where a
+// run's fp32 sums go (slot, -1 for a whole block).
+struct CrossItem {
+    int rank, first, count, slot;
 };
-__device__ __forceinline__ CrossRunIt cross_run_it(const BwdParams &p, int n_it, int part) {
-    CrossRunIt r;
-    r.first = (int)((long long)n_it * part / p.parts);
-    r.count = (int)((long long)n_it * (part + 1) / p.parts) - r.first;
+__device__ __forceinline__ CrossItem cross_item(const BwdCrossPlan &plan, int a, int n_it) {
+    CrossItem r = {a, 0, n_it, -1};
+    if (a >= plan.full && plan.parts > 1) {
+        r.slot = a - plan.full;
+        r.rank = plan.full + r.slot / plan.parts;
+        const int part = r.slot - (r.rank - plan.full) * plan.parts;
+        const int each = n_it / plan.parts, more = n_it - each * plan.parts;  // the first `more` runs have one more
+        r.first = part * each + min(part, more);
+        r.count = each + (part < more ? 1 : 0);
+    }
     return r;
 }
 // 32 columns of a row of dK or dV (already scaled) into a part's fp32 sums.
@@ -136,10 +146,48 @@ __device__ __forceinline__ int cross_len(const BwdParams &p, int b) {
     if (p.kv_lens == nullptr) return p.Nk;
     const int len = __ldg(p.kv_lens + b);
     if (len < 0 || len > p.Nk) {
-        if ((threadIdx.x & 31) == 0) atomicExch(p.status, -8);  // FA_ERR_SEQLENS: counts as 0
+        atomicExch(p.status, -8);  // FA_ERR_SEQLENS: counts as 0
         return 0;
     }
     return len;
+}
+// The line of key blocks that hold keys: batch index by batch index, in each block by block, in each block head by head.
+// The two below are a whole warp's: lane i looks at every 32nd batch index.
+__device__ __forceinline__ BwdCrossPlan cross_plan(const BwdParams &p) {
+    const int B = p.BH / p.Hkv;
+    int n = 0;
+    for (int b = threadIdx.x & 31; b < B; b += 32) n += (cross_len(p, b) + kBlk - 1) / kBlk;
+    return bwd_cross_plan((int)__reduce_add_sync(0xffffffffu, n) * p.Hkv, p.group * (p.Npad / kBlk), p.sms);
+}
+// What fa_bwd_cross_post is to add up, by one thread of the first CTA and one of each cut block's first run.
+__device__ __forceinline__ void note_plan(const BwdParams &p, const BwdCrossPlan &plan) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) p.kv_cut[0] = make_int4(plan.parts > 1 ? plan.valid - plan.full : 0, plan.parts, 0, 0);
+}
+__device__ __forceinline__ void note_cut(const BwdParams &p, int parts, int slot, int first, int bh, int j, int len) {
+    if (slot >= 0 && first == 0) p.kv_cut[1 + slot / parts] = make_int4(bh, j, len, 0);
+}
+// Batch index, its key count, block j and head bh of the block of a rank.
+struct CrossBlock {
+    int len, j, bh;
+};
+__device__ __forceinline__ CrossBlock cross_block(const BwdParams &p, int rank) {
+    const int B = p.BH / p.Hkv, lane = threadIdx.x & 31;
+    for (int b0 = 0;; b0 += 32) {
+        const int len = b0 + lane < B ? cross_len(p, b0 + lane) : 0;
+        const int items = (len + kBlk - 1) / kBlk * p.Hkv;
+        int end = items;  // blocks up to and with this lane's batch index
+        for (int off = 1; off < 32; off <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, end, off);
+            if (lane >= off) end += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, end > rank);
+        if (past != 0 || b0 + 32 >= B) {  // (a rank below the plan's `valid` is always found)
+            const int at = past != 0 ? __ffs(past) - 1 : 0;
+            const int r = rank - __shfl_sync(0xffffffffu, end - items, at);
+            return {__shfl_sync(0xffffffffu, len, at), r / p.Hkv, (b0 + at) * p.Hkv + r % p.Hkv};
+        }
+        rank -= __shfl_sync(0xffffffffu, end, 31);
+    }
 }
 // dK and dV of a key block that no query sees.
 template <typename T, int D, int THREADS>
@@ -284,23 +332,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // Block b -> (key block j, head bh); low j first, which in the causal case
     // are the blocks with the most query blocks to visit.
-    const int bh = blockIdx.x % p.BH;
-    const int part = CROSS ? blockIdx.x / p.BH % p.parts : 0;
-    const int j = CROSS ? blockIdx.x / p.BH / p.parts : blockIdx.x / p.BH;
+    int bh = blockIdx.x % p.BH, j = blockIdx.x / p.BH;
     const int n_qblk = p.Npad / kBlk;
     const int i0 = CAUSAL ? j : 0;  // first query block that sees key block j
-    const CrossRunIt run = CROSS ? cross_run_it(p, n_qblk * p.group, part) : CrossRunIt{0, n_qblk - i0};
-    const int n_it = run.count;     // >= 1
+    CrossItem run = {0, 0, n_qblk - i0, -1};
     grid_launch_dependents();       // fa_bwd_post may be scheduled once every CTA has started
     int n_keys = p.N;               // keys of the sequence
+    // CROSS: the key block that this CTA's index would have among all blocks, set to zero if it holds no keys
+    const int zero_bh = bh, zero_row = j * kBlk;
+    bool zero = false;
     if constexpr (CROSS) {
-        n_keys = cross_len(p, bh / p.Hkv);
-        if (j * kBlk >= n_keys) {  // (fa_bwd_post must not start before fa_bwd_pre is done, so wait for it here too)
-            if (p.parts == 1) zero_block<T, D, kBwdThreads>(p, bh, j * kBlk, threadIdx.x);
-            grid_dependency_wait();
+        const BwdCrossPlan plan = cross_plan(p);
+        note_plan(p, plan);
+        zero = zero_row < p.Nk && zero_row >= cross_len(p, bh / p.Hkv);
+        if ((int)blockIdx.x >= plan.items) {
+            if (zero) zero_block<T, D, kBwdThreads>(p, zero_bh, zero_row, threadIdx.x);
+            grid_dependency_wait();  // (fa_bwd_cross_post must not start before fa_bwd_pre is done, so wait for it here too)
             return;
         }
+        run = cross_item(plan, blockIdx.x, n_qblk * p.group);
+        const CrossBlock x = cross_block(p, run.rank);
+        n_keys = x.len;
+        j = x.j;
+        bh = x.bh;
+        if (threadIdx.x == 0) note_cut(p, plan.parts, run.slot, run.first, bh, j, n_keys);
     }
+    const int n_it = run.count;     // >= 1
     const int qh0 = CROSS ? bh * p.group : bh;  // first query head of the group
 
     if (threadIdx.x == 0) {
@@ -425,6 +482,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         // Every MMA of both warps is complete before tensor memory is freed.
         tc_commit(bar_drain, issue);
         if (warp == 1) bwd_wait_warp(bar_drain, 0, p);
+    } else if (CROSS && warp == 3) {
+        if (zero) zero_block<T, D, 32>(p, zero_bh, zero_row, lane);
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- gradient warps
         const int g = (warp - 4) >> 2;             // warpgroup: query columns / head columns half g
@@ -543,9 +602,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             for (int c0 = 0; c0 < D; c0 += 64) {
                 uint32_t a[32], b[32];
                 tmem_ld32x2_wait(tmem + lane_base + src_col + c0, a, tmem + lane_base + src_col + c0 + 32, b);
-                if (CROSS && p.parts > 1) {
-                    if (store) {
-                        float *sum = p.kv_part + (((size_t)(2 * part + (g == 0 ? 1 : 0)) * p.BH + bh) * k_rows + key) * D + c0;
+                if (CROSS && run.slot >= 0) {
+                    if (key_ok) {
+                        float *sum = p.kv_part + (((size_t)(2 * run.slot + (g == 0 ? 1 : 0)) * kBlk + r) * D + c0);
                         store_part(sum, a, mul);
                         store_part(sum + 32, b, mul);
                     }
@@ -915,7 +974,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // memory. All phases are those of one running iteration count g.
 // The CTA's blocks are every gridDim.x-th of those that hold keys, batch index by batch index; blocks without keys are
 // set to zero by the CTAs in turn. Measured (B 8, H 16, fp16, 448 queries, up to 1500 keys ragged, the whole backward):
-// 111 us with a CTA per key block, 105 with several per CTA, 99 with the read-out behind the next block's first pass.
+// 111 us with a CTA per key block, 105 with several per CTA, 99 with the read-out behind the next block's first pass, 95
+// with the blocks of the last wave cut.
 template <typename T>
 struct BwdCfgX64 : BwdCfgH64<T> {
     using B = BwdCfgH64<T>;
@@ -934,29 +994,28 @@ struct BwdCfgX64 : BwdCfgH64<T> {
     static_assert(SLACK >= 256, "shared memory budget");
 };
 
-// The CTA's next key block (or part of its iterations): block j of K/V head bh, of a batch index with len keys;
-// `count` iterations from query block `row` / kBlk of head qh on.
+// The CTA's next item: block j of K/V head bh, of a batch index with len keys; `count` iterations from query block
+// `row` / kBlk of head qh on.
 struct CrossCursor {
-    int a, b = 0, base = 0, len, bh = 0, j = 0, part = 0, first = 0, count = 0, qh = 0, row = 0;
+    int a, b = 0, base = 0, len, bh = 0, j = 0, slot = -1, first = 0, count = 0, qh = 0, row = 0;
     __device__ __forceinline__ explicit CrossCursor(const BwdParams &p) : a((int)blockIdx.x - (int)gridDim.x) { len = cross_len(p, 0); }
-    __device__ __forceinline__ bool next(const BwdParams &p) {
+    __device__ __forceinline__ bool next(const BwdParams &p, const BwdCrossPlan &plan) {
         a += gridDim.x;
-        const int B = p.BH / p.Hkv, n_qblk = p.Npad / kBlk;
-        for (;;) {
-            const int items = (len + kBlk - 1) / kBlk * p.Hkv * p.parts;
-            if (a < base + items) break;
-            base += items;
-            if (++b >= B) return false;
-            len = cross_len(p, b);
+        if (a >= plan.items) return false;
+        const int n_qblk = p.Npad / kBlk;
+        const CrossItem item = cross_item(plan, a, n_qblk * p.group);
+        for (;;) {  // (ends: the item's rank is below the number of blocks)
+            const int blocks = (len + kBlk - 1) / kBlk * p.Hkv;
+            if (item.rank < base + blocks) break;
+            base += blocks;
+            len = cross_len(p, ++b);
         }
-        int r = a - base;
-        j = r / (p.Hkv * p.parts);
-        r -= j * p.Hkv * p.parts;
-        part = r / p.Hkv;
-        bh = b * p.Hkv + (r - part * p.Hkv);
-        const CrossRunIt run = cross_run_it(p, n_qblk * p.group, part);
-        first = run.first;
-        count = run.count;
+        const int r = item.rank - base;
+        j = r / p.Hkv;
+        bh = b * p.Hkv + (r - j * p.Hkv);
+        slot = item.slot;
+        first = item.first;
+        count = item.count;
         qh = bh * p.group + first / n_qblk;
         row = first % n_qblk * kBlk;
         return true;
@@ -995,6 +1054,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SMEM_BAR + C::NUM_BARS * 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const BwdCrossPlan plan = cross_plan(p);
+    note_plan(p, plan);
 
     if (threadIdx.x == 0) {
         prefetch_tensormap(&tm_k);
@@ -1039,8 +1100,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             CrossCursor x(p);
             int g = 0, n = 0;
             bool ok = true;
-            for (; ok && x.next(p); ++n) {
+            for (; ok && x.next(p, plan); ++n) {
                 const int b = n & 1;
+                note_cut(p, plan.parts, x.slot, x.first, x.bh, x.j, x.len);
                 ok = bwd_wait(bar_kv_free(b), ((n >> 1) & 1u) ^ 1u, p);
                 if (!ok) break;
                 const uint32_t kv = smem_u32(smem + C::SMEM_KV + b * 2 * C::CHUNK);
@@ -1106,7 +1168,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 }
                 tc_commit(bar_sp_full(h), issue);
             };
-            bool more = x.next(p);
+            bool more = x.next(p, plan);
             if (more) {
                 ok = take_kv(0, x) && bwd_wait_warp(bar_qd_full(0), 0, p);
                 if (ok) {
@@ -1123,7 +1185,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (crossing) {
                     it = 0;
                     ++n;
-                    more = x.next(p);
+                    more = x.next(p, plan);
                 }
                 ok = bwd_wait_warp(bar_p_full(0), g & 1u, p);
                 if (ok && more) {
@@ -1158,7 +1220,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 tc_commit(bar_acc_done(h), issue);
             };
             int g = 0;
-            for (int n = 0; ok && x.next(p); ++n) {
+            for (int n = 0; ok && x.next(p, plan); ++n) {
                 ok = take_kv(n, x);
                 const uint64_t k_mn =
                     smem_desc_sw128(smem_u32(smem + C::SMEM_KV + (n & 1) * 2 * C::CHUNK), C::CHUNK, 1024);
@@ -1198,7 +1260,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (long long i = blockIdx.x; i < (long long)p.BH * blocks; i += gridDim.x) {
             const int bh = (int)(i % p.BH), j = (int)(i / p.BH);
             const int len = cross_len(p, bh / p.Hkv);
-            if (p.parts == 1 && j * kBlk >= len) zero_block<T, 64, 32>(p, bh, j * kBlk, lane);
+            if (j * kBlk >= len) zero_block<T, 64, 32>(p, bh, j * kBlk, lane);
         }
     } else if (warp >= 4) {
         // ---------------------------------------------------------------- gradient warps
@@ -1213,7 +1275,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const float *stat_row = (r < 64 ? p.lse2 : p.dsum) + 64 * gr + (r & 63);
         grid_dependency_wait();  // statistics and the zeroed dQ accumulator are written by fa_bwd_pre
         CrossCursor x(p);
-        bool ok = true, more = x.next(p);
+        bool ok = true, more = x.next(p, plan);
         auto stats_of = [&](const CrossCursor &c) { return stat_row + (size_t)c.bh * p.group * p.Npad + (size_t)c.first * kBlk; };
         float stat_next = more ? -__ldg(stats_of(x)) : 0.f;
         auto readout = [&](int g, int qh, int row) -> bool {  // dQ of iteration g
@@ -1227,19 +1289,20 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             return true;
         };
         // dV_j (half A's group), dK_j (B's) of key `key`: the last dq_full covers every dV and dK product of the block
-        auto take = [&](int bh, int key, int part) {
+        auto take = [&](int bh, int key, int slot, bool key_ok) {
             const float mul = gr == 0 ? 1.0f : p.scale;
             uint32_t a[32], b[32];
             tmem_ld32x2_wait(tmem + lane_base + 320 + 64 * gr, a, tmem + lane_base + 320 + 64 * gr + 32, b);
             tc_fence_before();
             mbar_arrive(bar_acc_free);  // the next block's products may overwrite them
-            if (key >= p.Nk) return;    // (rows past the sequence's keys get their zeros)
-            if (p.parts > 1) {
-                float *sum = p.kv_part + (((size_t)(2 * part + (gr == 0 ? 1 : 0)) * p.BH + bh) * p.Nk + key) * 64;
+            if (slot >= 0) {
+                if (!key_ok) return;
+                float *sum = p.kv_part + ((size_t)(2 * slot + (gr == 0 ? 1 : 0)) * kBlk + r) * 64;
                 store_part(sum, a, mul);
                 store_part(sum + 32, b, mul);
                 return;
             }
+            if (key >= p.Nk) return;    // (rows past the sequence's keys get their zeros)
             T *dst = reinterpret_cast<T *>(gr == 0 ? p.dv : p.dk) + ((size_t)bh * p.Nk + (size_t)key) * 64;
 #pragma unroll
             for (int c = 0; c < 32; c += 8) {
@@ -1253,13 +1316,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                              pk2<T>(__uint_as_float(b[c + 6]) * mul, __uint_as_float(b[c + 7]) * mul));
             }
         };
-        int g = 0, last_qh = 0, last_row = 0, last_bh = 0, last_key = 0, last_part = 0;  // of the iteration, block before
+        int g = 0, last_qh = 0, last_row = 0, last_bh = 0, last_key = 0, last_slot = 0;  // of the iteration, block before
+        bool last_ok = false;
         while (ok && more) {
-            const int bh = x.bh, key = x.j * kBlk + r, len = x.len, count = x.count, part = x.part;
+            const int bh = x.bh, key = x.j * kBlk + r, len = x.len, count = x.count, slot = x.slot;
             const bool key_ok = key < len, ragged_keys = (x.j + 1) * kBlk > len;
             const float *stat_src = stats_of(x);
             int qh = x.qh, row = x.row;
-            more = x.next(p);  // the block after this one
+            more = x.next(p, plan);  // the block after this one
             for (int it = 0; it < count; ++it, ++g) {
                 const uint32_t stats = stats0 + (g & 1) * 512;
                 st_shared_f32(stats + r * 4, stat_next);
@@ -1302,7 +1366,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 if (g > 0) {  // dQ of the last iteration and, when it ended a block, that block's dV, dK
                     ok = readout(g - 1, last_qh, last_row);
                     if (!ok) break;
-                    if (it == 0) take(last_bh, last_key, last_part);
+                    if (it == 0) take(last_bh, last_key, last_slot, last_ok);
                 }
                 last_qh = qh;
                 last_row = row;
@@ -1314,9 +1378,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             }
             last_bh = bh;
             last_key = key;
-            last_part = part;
+            last_ok = key_ok;
+            last_slot = slot;
         }
-        if (ok && g > 0 && readout(g - 1, last_qh, last_row)) take(last_bh, last_key, last_part);
+        if (ok && g > 0 && readout(g - 1, last_qh, last_row)) take(last_bh, last_key, last_slot, last_ok);
         if (lane == 0) bulk_wait_all();  // the dQ reductions
     }
     __syncwarp();
@@ -1386,29 +1451,40 @@ __global__ void __launch_bounds__(256) fa_bwd_post(const float *__restrict__ dq_
     reinterpret_cast<uint2 *>(dq)[i] = o;
 }
 
-// The parts' fp32 dK, dV added up in order (so the same every time) and converted; 0 past a sequence's keys.
+// fa_bwd_post for keys of another length: the first sum_ctas CTAs add up the runs' fp32 dK, dV of cut key blocks, in order
+// (so the same every time), and convert them, 256 units of 4 columns at a time; they are the first because a sum of many
+// runs takes longest.
 template <typename T, int D>
-__global__ void __launch_bounds__(256) fa_bwd_cross_post(const BwdParams p) {
+__global__ void __launch_bounds__(256) fa_bwd_cross_post(const BwdParams p, T *__restrict__ dq, size_t n4, int sum_ctas) {
     grid_dependency_wait();
-    const size_t per = (size_t)p.BH * p.Nk * D / 4;  // 4-column units of dK, and of dV
-    const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= 2 * per) return;
-    const bool v = i >= per;
-    const size_t u = v ? i - per : i, row = u / (D / 4);
-    const int bh = (int)(row / p.Nk), key = (int)(row - (size_t)bh * p.Nk);
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (key < cross_len(p, bh / p.Hkv)) {
-        const float4 *src = reinterpret_cast<const float4 *>(p.kv_part) + (v ? per : 0) + u;
-#pragma unroll 4
-        for (int k = 0; k < p.parts; ++k) {
-            const float4 x = src[2 * k * per];
-            s.x += x.x, s.y += x.y, s.z += x.z, s.w += x.w;
-        }
+    if ((int)blockIdx.x >= sum_ctas) {
+        const size_t i = (size_t)(blockIdx.x - sum_ctas) * 256 + threadIdx.x;
+        if (i >= n4) return;
+        const float4 v = reinterpret_cast<const float4 *>(p.dq_acc)[i];
+        reinterpret_cast<uint2 *>(dq)[i] = make_uint2(pk2<T>(v.x, v.y), pk2<T>(v.z, v.w));
+        return;
     }
-    uint2 o;
-    o.x = pk2<T>(s.x, s.y);
-    o.y = pk2<T>(s.z, s.w);
-    reinterpret_cast<uint2 *>(v ? p.dv : p.dk)[u] = o;
+    constexpr int kUnits = kBlk * D / 4;          // of dK, and of dV
+    constexpr int kPieces = 2 * kUnits / 256;
+    const int4 plan = p.kv_cut[0];
+    for (int c = blockIdx.x; c < plan.x * kPieces; c += sum_ctas) {
+        const int t = c / kPieces;
+        const int4 at = p.kv_cut[1 + t];
+        const int u = c % kPieces * 256 + (int)threadIdx.x, v = u / kUnits, row = u % kUnits / (D / 4), col = u % (D / 4);
+        const int key = at.y * kBlk + row;
+        if (key >= p.Nk) continue;
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (key < at.z) {  // (0 past the sequence's keys)
+            const float4 *src = reinterpret_cast<const float4 *>(p.kv_part) + (size_t)t * plan.y * 2 * kUnits + u;
+#pragma unroll 8
+            for (int k = 0; k < plan.y; ++k) {
+                const float4 y = src[(size_t)k * 2 * kUnits];
+                s.x += y.x, s.y += y.y, s.z += y.z, s.w += y.w;
+            }
+        }
+        reinterpret_cast<uint2 *>(v ? p.dv : p.dk)[((size_t)at.x * p.Nk + key) * (D / 4) + col] =
+            make_uint2(pk2<T>(s.x, s.y), pk2<T>(s.z, s.w));
+    }
 }
 
 template <typename T, int D, bool CAUSAL, bool CROSS = false>
@@ -1455,22 +1531,39 @@ int launch_bwd_variant(const BwdArgs &a) {
     p.scale = a.scale;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
-    p.parts = CROSS ? a.parts : 1;
-    p.kv_part = CROSS ? a.kv_part : nullptr;
-    int64_t grid = static_cast<int64_t>(BHkv) * (bwd_padded_rows(Nk) / kBlk) * p.parts;
-    if (D == 64 && CROSS && grid > a.num_sms) grid = a.num_sms;  // each CTA takes several key blocks
+    p.sms = a.num_sms;
+    p.kv_cut = reinterpret_cast<int4 *>(a.kv_part);
+    p.kv_part = a.kv_part + bwd_cross_cut_bytes(a.num_sms) / sizeof(float);
+    int64_t grid = static_cast<int64_t>(BHkv) * (bwd_padded_rows(Nk) / kBlk), slots = 0;
+    if (CROSS) {  // every item that key counts may give
+        const int64_t n_it = bwd_cross_iters(p.group, a.N);
+        if (a.kv_lens == nullptr) {
+            const BwdCrossPlan plan = bwd_cross_plan(static_cast<int>(grid), static_cast<int>(n_it), a.num_sms);
+            slots = plan.items - plan.full;
+            grid = plan.items;
+        } else {
+            slots = bwd_cross_slots(grid, n_it, a.num_sms);
+            grid = grid > a.num_sms || slots < grid ? grid + slots : slots;
+        }
+        if (D == 64 && grid > a.num_sms) grid = a.num_sms;  // each CTA takes several items
+        if (grid > INT32_MAX) return -5;
+    }
     // programmatic dependents: the backward's copies of K, V, Q, dO start while fa_bwd_pre drains (its
     // gradient warps wait for the statistics), and fa_bwd_post's launch overlaps the backward's tail
     if (launch_dependent(kern, dim3(static_cast<unsigned>(grid)), dim3(kBwdThreads), smem_bytes, a.stream, tq, tk,
                          tv, tdo, tdq, p) != cudaSuccess)
         return -5;
-    if (CROSS && a.parts > 1) {
-        const size_t units = 2 * static_cast<size_t>(BHkv) * Nk * D / 4;
-        if (launch_dependent(fa_bwd_cross_post<T, D>, dim3(static_cast<unsigned>((units + 255) / 256)), dim3(256), 0, a.stream,
-                             p) != cudaSuccess)
-            return -5;
-    }
     const size_t n4 = static_cast<size_t>(BH) * a.N * D / 4;
+    if constexpr (CROSS) {
+        const int64_t dq_ctas = static_cast<int64_t>((n4 + 255) / 256);
+        const int64_t pieces = std::min<int64_t>(slots, a.num_sms) * (kBlk * D / 512);  // of all blocks that may be cut
+        const int64_t sum_ctas = std::min<int64_t>(pieces, 8 * a.num_sms);              // (eight fit on an SM)
+        if (dq_ctas + sum_ctas > INT32_MAX) return -5;
+        if (launch_dependent(fa_bwd_cross_post<T, D>, dim3(static_cast<unsigned>(dq_ctas + sum_ctas)), dim3(256), 0,
+                             a.stream, p, static_cast<T *>(a.dq), n4, static_cast<int>(sum_ctas)) != cudaSuccess)
+            return -5;
+        return cudaGetLastError() == cudaSuccess ? 0 : -5;
+    }
     if (launch_dependent(fa_bwd_post<T>, dim3(static_cast<unsigned>((n4 + 255) / 256)), dim3(256), 0, a.stream,
                          static_cast<const float *>(a.dq_acc), static_cast<T *>(a.dq), n4) != cudaSuccess)
         return -5;

@@ -187,3 +187,30 @@ def simulate_bwd_cross(counts, stages, seed, acc_free=True, kv_free_count=2, acc
                 del agents[c]
                 waiting[c] = None
     return True
+
+
+def plan(valid, n_it, num_sms):
+    """bwd_cross_plan: (full, parts, items) of `valid` key blocks of n_it iterations each."""
+    tail = valid % num_sms
+    parts, best = 1, n_it + 1
+    for m in (1, 2):
+        if tail:
+            k = min(m * num_sms // tail, n_it)
+            cost = -(-tail * k // num_sms) * (-(-n_it // k) + 2)
+            if k > 1 and cost < best:
+                best, parts = cost, k
+    return valid - tail, parts, valid - tail + tail * parts
+
+
+def slots(blocks, n_it, num_sms):
+    """bwd_cross_slots: workspace slots for any number of blocks up to `blocks`."""
+    return 0 if n_it < 2 else min(min(blocks, num_sms) * n_it, 2 * num_sms)
+
+
+def item(full, parts, a, n_it):
+    """cross_item: (rank of the block, first iteration, iterations, slot) of item a."""
+    if a < full or parts == 1:
+        return a, 0, n_it, -1
+    part = (a - full) % parts
+    each, more = divmod(n_it, parts)
+    return full + (a - full) // parts, part * each + min(part, more), each + (part < more), a - full

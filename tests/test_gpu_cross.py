@@ -14,6 +14,8 @@ import numpy as np
 import pytest
 import torch
 
+from cross_model import plan
+
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
 DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
@@ -138,6 +140,37 @@ def test_gradients(fa, dtype, B, H, Hkv, Nq, Nk, d, lens):
     out, lse = fa.attention_cross(q, k, v, kv_lens)
     got = fa.attention_cross_backward(q, k, v, out, do, lse, kv_lens)
     status_ok(fa)
+    ref = reference(q, k, v, lens, 1 / math.sqrt(d), do)
+    for name, t in zip(("dq", "dk", "dv"), got):
+        check(name, t, ref[name])
+
+
+CUT = [
+    # dtype, B, H, Hkv, Nq, Nk, d, lens: more key blocks than SMs, the last of them cut (8 of 160, 84 of 236, 16 of 168,
+    # on 152 SMs; then 60 blocks, all cut)
+    ("bf16", 4, 8, 4, 300, 1250, 128, [1250, 1250, 1249, 1153]),
+    ("fp16", 4, 8, 4, 300, 1250, 64, None),
+    ("fp16", 5, 8, 4, 1300, 1700, 128, [1700, 1600, 1664, 1281, 1000]),
+    ("bf16", 6, 4, 2, 400, 1700, 64, None),
+    ("fp16", 18, 6, 2, 257, 300, 64, [300, 0, 260, 1, 128, 129] * 3),
+    ("bf16", 18, 6, 2, 257, 300, 128, [300, 0, 260, 1, 128, 129] * 3),
+]
+
+
+@pytest.mark.parametrize("dtype,B,H,Hkv,Nq,Nk,d,lens", CUT)
+def test_gradients_of_cut_key_blocks(fa, dtype, B, H, Hkv, Nq, Nk, d, lens):
+    """Key blocks whose queries are shared out over CTAs; dk and dv are the same bits every time."""
+    valid = sum((n + 127) // 128 for n in ([Nk] * B if lens is None else lens)) * Hkv
+    _, parts, _ = plan(valid, H // Hkv * ((Nq + 127) // 128), fa.fa_num_sms())
+    if fa.fa_num_sms() == 152:
+        assert parts > 1
+    q, k, v, do = inputs(Nq + Nk, dtype, B, H, Hkv, Nq, Nk, d)
+    kv_lens = None if lens is None else ints(lens)
+    out, lse = fa.attention_cross(q, k, v, kv_lens)
+    got = fa.attention_cross_backward(q, k, v, out, do, lse, kv_lens)
+    again = fa.attention_cross_backward(q, k, v, out, do, lse, kv_lens)
+    status_ok(fa)
+    assert torch.equal(got[1], again[1]) and torch.equal(got[2], again[2])
     ref = reference(q, k, v, lens, 1 / math.sqrt(d), do)
     for name, t in zip(("dq", "dk", "dv"), got):
         check(name, t, ref[name])
