@@ -261,8 +261,9 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *ou
  * > 0 all sequences' keys are cut, as one line, into n_parts equal stretches, whatever the lengths
  * are; the summaries of sequences that more than one part shares go through the workspace (256-byte
  * aligned, at least fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) bytes, contents on entry
- * irrelevant, not shared by overlapping calls). n_parts = 0 gives each sequence and K/V head a CTA of
- * its own, in one launch and without a workspace (it may be NULL): for short contexts. The result
+ * irrelevant, not shared by overlapping calls). n_parts = 0 gives each sequence and K/V head CTAs of
+ * its own (up to eight, by the number of sequences and by max_len), in one launch and without a
+ * workspace (it may be NULL): for short contexts, and longer ones of few sequences. The result
  * does not depend on timing: two calls on the same inputs, with the same n_parts, give the same bits.
  * Other errors as for fa_fwd_splitkv; FA_ERR_UNSUPPORTED for another page or d, FA_ERR_ARG for
  * another format, FA_ERR_SHAPE for strides that are no multiples of 8. */
@@ -288,7 +289,7 @@ int fa_kvq8_read_fp16(const void *k_codes, const void *v_codes, const float *k_s
                       const int *first_or_null, int nseq, int total, int max_len, void *k, void *v, int Hkv, int d,
                       int format, void *stream);
 
-/* A part count for lengths up to max_len: 0 for short contexts, otherwise one that fills the GPU once, without parts of
+/* A part count for lengths up to max_len: 0 where that is faster, otherwise one that fills the GPU once, without parts of
  * less than 64 keys; or a negative status. */
 int fa_kvq8_num_parts(int B, int H, int Hkv, int Nq, int max_len, int d);
 /* Workspace bytes fa_fwd_kvq8 needs, or a negative status. */

@@ -500,6 +500,7 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     a.scale = scale;
     a.causal = causal ? 1 : 0;
     a.parts = n_parts;
+    a.num_sms = di->num_sms;
     a.workspace = static_cast<float *>(workspace);
     a.status = di->status;
     a.stream = static_cast<cudaStream_t>(stream);

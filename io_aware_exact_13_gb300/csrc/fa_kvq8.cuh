@@ -51,7 +51,7 @@ struct Kvq8AttnArgs {
     const int *kv_lens;
     int B, H, Nq, max_len;
     float scale;
-    int causal, parts;
+    int causal, parts, num_sms;
     float *workspace;
     int *status;
     cudaStream_t stream;
@@ -88,17 +88,6 @@ template <int FMT>
 __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t &lo, uint32_t &hi) {
     if constexpr (FMT == kKvq8Int8) int8x4_to_half2(w, lo, hi);
     else e4m3x4_to_half2(w, lo, hi);
-}
-
-// Asynchronous copies of 16 or 8 bytes per thread; with src_bytes = 0 nothing is read and zeros are written.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, uint32_t src_bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
 }  // namespace fa

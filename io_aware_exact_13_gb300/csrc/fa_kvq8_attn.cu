@@ -24,9 +24,9 @@
 //     w_j = s_j log2 e + log2 vs(j), keep a running maximum of their own: the fp16 rounding of the
 //     weights is then relative to the largest contribution, whatever the pages' scales are, and
 //     a page of zeros (vs = 0) still counts in the sum. The sum l and all accumulators are fp32.
-// Q is rounded to nothing: fp16 as given, and bf16 rows scaled by a power of two into fp16's
-// range, which is exact down to 2^-24 of the row's largest magnitude. P (the weights) are rounded
-// to fp16, 2^-11 relative.
+// Q is not rounded: fp16 as given, and bf16 rows scaled by a power of two into fp16's range,
+// which is exact down to 2^-24 of the row's largest magnitude. The weights are rounded to fp16,
+// 2^-11 relative (2^-25 of the largest below fp16's normal range).
 //
 // Ragged batches: all sequences' tiles are one line (sequence by sequence, head by head) that the warps of one
 // wave of CTAs cut into equal stretches, whatever the lengths are; each warp finds its place by adding the
@@ -34,9 +34,12 @@
 // case below.) A unit that one warp does alone is written at once; the warps of a CTA merge theirs in shared
 // memory; what several CTAs share goes through the workspace to fa_kvq8_combine.
 //
-// Measured on one GB300 (copy rate 6.80 TB/s): B 64, H 64 / 8, d 128, e4m3, ragged up to 16384 keys 211 us (92 % of
-// the copy rate); B 16, H 32 / 8, d 128, int8, ragged up to 8192 keys 42 us (60 %); time is about bytes / rate + 15 us,
-// of which launch and lengths are 2.3, the merge kernel 5.
+// Short contexts, and longer ones of few sequences, take a CTA or a cluster of CTAs per unit instead, in one launch: the
+// CTAs of a cluster merge through each other's shared memory (see kvq8_num_parts).
+//
+// Measured on one GB300 (copy rate 6.80 TB/s): B 64, H 64 / 8, d 128, e4m3, ragged up to 16384 keys 209 us (93 % of the
+// copy rate); B 16, H 32 / 8, d 128, int8, ragged up to 8192 keys 40 us (64 %); time is about bytes / rate + 14 us, of
+// which launch and lengths are 2.3 and the merge kernel 4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -47,12 +50,12 @@
 #include "fa_kvq8.cuh"
 #include "pdl.cuh"
 #include "ptx.cuh"
-#include "warp_mma.cuh"
 
 namespace fa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kMostCluster = 8;  // CTAs of a unit, all of a portable cluster
 constexpr int kTileKeys = 16;
 constexpr float kTau = 8.0f;  // log2 units by which a reference maximum may be exceeded before it moves
 constexpr float kNone = -1e30f;  // reference maximum of a row that has seen no key
@@ -97,7 +100,7 @@ struct Q8Params {
     int *status;
     int B, H, Hkv, Nq, rows, row_tiles;  // rows = (H / Hkv) Nq query rows share a K/V head, in row_tiles tiles
     int n_pages, max_pages, page_shift;
-    int max_len, parts;
+    int max_len, parts, cluster;  // cluster: CTAs of a unit when parts is 0
     float scale_log2;
 };
 
@@ -115,7 +118,29 @@ __device__ __forceinline__ int q8_len(const Q8Params &p, int b, bool &bad) {
     bad = len < 0 || len > p.max_len;
     return bad ? 0 : len;
 }
-__device__ __forceinline__ int q8_tiles(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+__host__ __device__ __forceinline__ int q8_tiles(int len) { return (len + kTileKeys - 1) / kTileKeys; }
+
+// All threads of the cluster's CTAs: what any wrote to its shared memory before is seen by every one after.
+__device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Shared memory of another CTA of the cluster, at the address that `here` has in this one.
+__device__ __forceinline__ uint32_t cluster_addr(const void *here, int rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(here)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ float ld_cluster_f32(uint32_t a) {
+    float x;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(a) : "memory");
+    return x;
+}
+__device__ __forceinline__ float4 ld_cluster_v4f(uint32_t a) {
+    float4 x;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w) : "r"(a) : "memory");
+    return x;
+}
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     uint32_t y;
@@ -174,26 +199,31 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
     // Each warp adds the lengths up for itself: no barrier between the lengths' arrival and the first page's read.
     int cur, end, b = 0, base = 0, len = 0, per;  // base: first tile of sequence b
     int start;  // the CTA's first tile
-    if (p.parts == 0) {  // a CTA for each unit, its tiles in quarters; the line begins with the sequence
-        b = blockIdx.x / units;
-        const int unit = blockIdx.x - b * units;
+    const int rank = p.parts == 0 ? (int)blockIdx.x % p.cluster : 0;  // of this CTA in its cluster
+    if (p.parts == 0) {  // a cluster for each unit, its tiles shared out evenly over all warps; the line begins with the sequence
+        b = blockIdx.x / p.cluster / units;
+        const int unit = blockIdx.x / p.cluster - b * units;
         bool bad;
         len = q8_len(p, b, bad);
         if (bad && threadIdx.x == 0) atomicExch(p.status, kStatusSeqlensQ8);
-        const int n = q8_tiles(len), quarter = (n + kWarps - 1) / kWarps;
+        const int n = q8_tiles(len), each = (n + kWarps * p.cluster - 1) / (kWarps * p.cluster), w = rank * kWarps + warp;
         if (n == 0) {
             const int kvh = unit / p.row_tiles, row0 = (unit - kvh * p.row_tiles) * RT, rows = min(RT, p.rows - row0);
             const size_t at = ((size_t)b * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq + row0;
             uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + at * D);
-            for (int i = threadIdx.x; i < rows * (D / 8); i += kWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
-            for (int i = threadIdx.x; i < rows; i += kWarps * 32) p.lse[at + i] = -INFINITY;
+            for (int i = w * 32 + lane; i < rows * (D / 8); i += p.cluster * kWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = w * 32 + lane; i < rows; i += p.cluster * kWarps * 32) p.lse[at + i] = -INFINITY;
             return;
         }
         per = n;
         start = unit * n;
-        cur = start + min(n, warp * quarter);
-        end = start + min(n, (warp + 1) * quarter);
+        cur = start + min(n, w * each);
+        end = start + min(n, (w + 1) * each);
         if (lane < 2) seg[2 * warp + lane].unit = -1;
+        for (int r = lane; r < RT; r += 32) {  // what a warp without tiles leaves
+            sm_m[2 * warp * RT + r] = kNone;
+            sm_l[2 * warp * RT + r] = 0.f;
+        }
         __syncwarp();
     } else {
         int total = 0, first_len = 0, s_bad = 0;  // first_len: the length of this lane's first sequence
@@ -564,6 +594,76 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
             }
     }
 
+    // ---------------------------------------------------------------- a unit shared by the CTAs of a cluster
+    // Each CTA merges its warps' summaries (into slot 1, which no warp has used); then the CTAs share out the unit's
+    // rows and columns and merge each other's. One tile is one warp's, which has written the rows.
+    if (p.parts == 0 && p.cluster > 1) {
+        if (per == 1) return;
+        const int unit = blockIdx.x / p.cluster - b * units;
+        const int kvh = unit / p.row_tiles, row0 = (unit - kvh * p.row_tiles) * RT, rows = min(RT, p.rows - row0);
+        const size_t row_base = ((size_t)b * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq + row0;
+        __syncthreads();
+        for (int idx = threadIdx.x; idx < rows * (D / 4); idx += kWarps * 32) {
+            const int r = idx / (D / 4), e4 = idx % (D / 4);
+            float M = kNone, L = 0.f;
+            float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm_m[2 * w * RT + r]);
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                if (seg[2 * w].unit < 0) continue;  // a warp without tiles
+                const float f = ex2_approx(sm_m[2 * w * RT + r] - M);
+                const float4 v = *reinterpret_cast<const float4 *>(sm_o + (2 * w * RT + r) * C::PITCH + 4 * e4);
+                L += f * sm_l[2 * w * RT + r];
+                A.x = fmaf(f, v.x, A.x);
+                A.y = fmaf(f, v.y, A.y);
+                A.z = fmaf(f, v.z, A.z);
+                A.w = fmaf(f, v.w, A.w);
+            }
+            *reinterpret_cast<float4 *>(sm_o + (RT + r) * C::PITCH + 4 * e4) = A;
+            if (e4 == 0) {
+                sm_m[RT + r] = M;
+                sm_l[RT + r] = L;
+            }
+        }
+        cluster_sync();
+        for (int idx = rank * kWarps * 32 + threadIdx.x; idx < rows * (D / 4); idx += p.cluster * kWarps * 32) {
+            const int r = idx / (D / 4), e4 = idx % (D / 4);
+            float m[kMostCluster], l[kMostCluster];
+            float4 v[kMostCluster];
+#pragma unroll
+            for (int q = 0; q < kMostCluster; ++q) {
+                m[q] = kNone, l[q] = 0.f, v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (q < p.cluster) {
+                    m[q] = ld_cluster_f32(cluster_addr(sm_m + RT + r, q));
+                    l[q] = ld_cluster_f32(cluster_addr(sm_l + RT + r, q));
+                    v[q] = ld_cluster_v4f(cluster_addr(sm_o + (RT + r) * C::PITCH + 4 * e4, q));
+                }
+            }
+            float M = m[0], L = 0.f;
+            float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int q = 1; q < kMostCluster; ++q) M = fmaxf(M, m[q]);
+#pragma unroll
+            for (int q = 0; q < kMostCluster; ++q) {
+                const float f = ex2_approx(m[q] - M);
+                L += f * l[q];
+                A.x = fmaf(f, v[q].x, A.x);
+                A.y = fmaf(f, v[q].y, A.y);
+                A.z = fmaf(f, v[q].z, A.z);
+                A.w = fmaf(f, v[q].w, A.w);
+            }
+            const float inv = L == 0.f ? 0.f : 1.0f / L;
+            uint2 w;
+            w.x = pack16<T>(A.x * inv, A.y * inv);
+            w.y = pack16<T>(A.z * inv, A.w * inv);
+            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * e4) = w;
+            if (e4 == 0) p.lse[row_base + r] = L == 0.f ? -INFINITY : (M + lg2_approx(L)) * kLn2;
+        }
+        cluster_sync();  // a CTA's shared memory stays until its neighbours have read it
+        return;
+    }
+
     // ---------------------------------------------------------------- units shared by warps or CTAs
     // Neighbouring stretches of one unit are merged. Where they are all of it the rows are written, otherwise the
     // CTA's summary: slot 0 of the part for the unit that holds the CTA's first tile, slot 1 for its last one.
@@ -729,6 +829,14 @@ int tiles_per_unit(int rows, int d) {
 }
 int units_per_head(int rows, int d) { return (rows + 8 * tiles_per_unit(rows, d) - 1) / (8 * tiles_per_unit(rows, d)); }
 
+// CTAs for each unit when parts is 0: as many as fit in one wave and have a tile for every warp, up to 8. (B 1, H 8, d 64:
+// 500 keys 7.8, 5.9, 4.9, 4.6 us with 1, 2, 4, 8; with two waves instead of one, B 16, H 32 / 8, d 128, 8.8 becomes 14.0.)
+int cluster_size(long long units, int tiles, long long slots) {
+    int c = 1;
+    while (2 * c <= kMostCluster && 2 * c * units <= slots && tiles > kWarps * c) c *= 2;
+    return c;
+}
+
 template <typename T, int D, int FMT, int NT, bool CAUSAL>
 int launch_q8(const Kvq8AttnArgs &a) {
     using C = Q8Cfg<D, NT>;
@@ -764,8 +872,20 @@ int launch_q8(const Kvq8AttnArgs &a) {
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     // (not as a programmatic dependent: its CTAs would take their places beside those of the kernel ahead, and
     // the one wave that the parts are sized for would become two)
-    const int grid = a.parts > 0 ? a.parts : a.B * a.c.Hkv * p.row_tiles;
-    kern<<<grid, kWarps * 32, C::SMEM, a.stream>>>(p);
+    p.cluster = a.parts > 0 ? 1 : cluster_size((long long)a.B * a.c.Hkv * p.row_tiles, q8_tiles(a.max_len),
+                                               (long long)C::CTAS * a.num_sms);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.parts > 0 ? a.parts : a.B * a.c.Hkv * p.row_tiles * p.cluster);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = p.cluster;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return -5;
     if (cudaGetLastError() != cudaSuccess) return -5;
     if (a.parts <= 1) return 0;
     return launch_dependent(fa_kvq8_combine<T, D, C::RT>, dim3(a.parts), dim3(kCombineThreads), 0,
@@ -801,14 +921,18 @@ long long kvq8_tiles(int B, int Hkv, int rows, int max_len, int d) {
     return (long long)B * Hkv * units_per_head(rows, d) * ((max_len + kTileKeys - 1) / kTileKeys);
 }
 
-// Short contexts (up to 512 keys, eight tiles for a warp): a CTA for each unit and no merge kernel, 7.8 us against 12.0
-// of the line for B 16, H 32 / 8, d 128, 300 keys, 15.6 against 20.4 for B 64, d 64, 4 rows; from 1000 keys on the line is
-// ahead (B 1: 8.6 against 15.7 us) or level (B 64: 28.8 against 26.0). Otherwise one part for each CTA that can be
-// resident, and at least one tile for each of a CTA's warps.
+// Parts 0, a cluster of CTAs for each unit and no merge kernel, while no warp has many tiles: 8, or more where the clusters
+// fill most of a wave, since the line then has little to spread (16; 12 with one CTA for a unit). Measured, cluster against
+// line: B 1, H 8, d 64: 500 keys 4.6 against 7.6 us, 4000 8.0 / 8.8, 8000 11.8 / 9.6. B 4, H 32 / 8, d 128: 1000 keys 7.5 /
+// 10.1, 4000 15.6 / 16.5, 8000 24.7 / 21.5. B 16, H 32 / 8, d 128: 500 keys 8.8 / 12.2, 2000 18.6 / 22.8, 4000 30.7 / 33.9,
+// ragged 27.1 / 27.4. B 32: 2000 30.8 / 33.9, ragged 27.0 / 26.4. B 64, one CTA: 600 21.0 / 25.1, 1000 ragged 26.4 / 26.6.
+// Otherwise one part for each CTA that can be resident, and at least one tile for each of a CTA's warps.
 int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int d, int num_sms) {
-    if (max_len <= 512) return 0;
-    const int nt = tiles_per_unit(rows, d);
-    const long long slots = (long long)q8_ctas(d, nt) * num_sms;
+    const int nt = tiles_per_unit(rows, d), tiles = q8_tiles(max_len);
+    const long long slots = (long long)q8_ctas(d, nt) * num_sms, units = (long long)B * Hkv * units_per_head(rows, d);
+    const int c = cluster_size(units, tiles, slots), each = (tiles + kWarps * c - 1) / (kWarps * c);
+    const bool full = 2 * c * units > slots && c * units <= slots;
+    if (each <= (!full ? 8 : c > 1 ? 16 : 12)) return 0;
     const long long by_len = (kvq8_tiles(B, Hkv, rows, max_len, d) + kWarps - 1) / kWarps;
     return (int)(by_len < slots ? by_len : slots);
 }

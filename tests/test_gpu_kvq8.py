@@ -441,6 +441,37 @@ def test_attention_many_sequences_of_uneven_lengths(fa, n_parts):
     check_attention(q, cache, table, lens, out, lse, 1 / 8, True)
 
 
+@pytest.mark.parametrize("fmt,dtype,page,H,Hkv,Nq,d,n_seq,longest,causal", [
+    ("int8", "bf16", 16, 8, 8, 1, 64, 6, 1500, False),     # eight CTAs for a unit, warps without tiles
+    ("e4m3", "fp16", 64, 12, 2, 7, 128, 7, 2100, True),    # several row tiles
+    ("int8", "fp16", 32, 40, 5, 4, 64, 5, 700, True),
+    ("e4m3", "bf16", 128, 32, 8, 1, 128, 15, 400, False),  # four
+    ("int8", "bf16", 16, 16, 8, 2, 64, 26, 300, True),     # two
+    ("e4m3", "fp16", 16, 8, 8, 1, 64, 60, 120, True),      # one
+])
+def test_attention_with_several_ctas_for_a_unit(fa, fmt, dtype, page, H, Hkv, Nq, d, n_seq, longest, causal):
+    """One launch, the CTAs of a unit merging through each other's shared memory: lengths of nothing, one token, one tile,
+    as many tiles as warps, one more, and any; the same bits every time."""
+    rng = np.random.default_rng(H * n_seq + d)
+    lens = [longest, 0, 1, 16, 17][:n_seq] + [int(x) for x in rng.integers(0, longest + 1, max(0, n_seq - 5))]
+    lens[-1] = min(longest, 512 if n_seq % 2 else 513)
+    table, n_pages = random_table(rng, lens, page)
+    cache = filled(fa, rng, fmt, n_pages, Hkv, page, d)
+    q = torch.from_numpy(rng.standard_normal((n_seq, H, Nq, d))).to(DT[dtype]).to(DEV)
+    got = [fa.attention_kvq8(q, cache, ints(table.tolist()), ints(lens), causal=causal, n_parts=0, max_len=longest)
+           for _ in range(2)]
+    status_ok(fa)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    check_attention(q, cache, table, lens, *got[0], 1 / math.sqrt(d), causal)
+    q[0, H - 1, Nq - 1, 3] = float("nan")  # a NaN query gives NaN, and only its own row
+    out, lse = fa.attention_kvq8(q, cache, ints(table.tolist()), ints(lens), causal=causal, n_parts=0, max_len=longest)
+    status_ok(fa)
+    assert bool(out[0, H - 1, Nq - 1].isnan().all()) and bool(lse[0, H - 1, Nq - 1].isnan())
+    keep = torch.ones(n_seq, H, Nq, dtype=torch.bool, device=DEV)
+    keep[0, H - 1, Nq - 1] = False
+    assert torch.equal(out[keep], got[0][0][keep]) and torch.equal(lse[keep], got[0][1][keep])
+
+
 def test_attention_nothing_cached(fa):
     cache = fa.kv_cache_q8(4, 2, 32, 128, torch.float8_e4m3fn, DEV)
     q = torch.ones((3, 4, 1, 128), dtype=torch.bfloat16, device=DEV)
