@@ -27,6 +27,7 @@ import os
 from typing import NamedTuple
 
 import torch
+from torch._C._dynamo.guards import _empty_strided_cuda
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
 if not os.path.exists(_LIB_PATH):
@@ -502,6 +503,20 @@ def _raw_stream(index, stream):
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
+# Contiguous tensors on the current device, past torch's dispatcher: 2 us beside a launch where torch.empty takes 4 and
+# Tensor.new_empty 6.
+def _empty4(a, b, c, d, dtype):
+    return _empty_strided_cuda((a, b, c, d), (b * c * d, c * d, d, 1), dtype)
+
+
+def _empty3(a, b, c, dtype):
+    return _empty_strided_cuda((a, b, c), (b * c, c, 1), dtype)
+
+
+def _empty_bytes(n):
+    return _empty_strided_cuda((n,), (1,), torch.uint8)
+
+
 def _check_tensor(name, t, dtype, shape, index):
     if t.dtype is not dtype or t.get_device() != index or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{index}")
@@ -587,10 +602,10 @@ def kvq8_read(cache, page_table, cu_seqlens, total, max_len, first=None, dtype=t
     if suffix is None:
         raise ValueError(f"unsupported dtype {dtype}")
     name = "fa_kvq8_read" + suffix
-    shape, device = (int(total), Hkv, d), cache.k_codes.device
+    shape = (int(total), Hkv, d)
     with _on(index, stream):
-        k = torch.empty(shape, dtype=dtype, device=device) if k is None else k
-        v = torch.empty(shape, dtype=dtype, device=device) if v is None else v
+        k = _empty3(*shape, dtype) if k is None else k
+        v = _empty3(*shape, dtype) if v is None else v
         _check_tensor("k", k, dtype, shape, index)
         _check_tensor("v", v, dtype, shape, index)
         rc = getattr(lib, name)(*cache_ptrs, n_pages, max_pages, page, cu_seqlens.data_ptr(),
@@ -630,14 +645,14 @@ def _raw_kvq8(fn_name, dtype, q, cache, page_table, kv_lens, out, lse, scale, ca
     max_len = max_pages * page if max_len is None else int(max_len)
     with _on(index, stream):
         if out is None:
-            out = torch.empty_like(q)
-            lse = cache.k_scale.new_empty((B, H, Nq))
+            out = _empty4(B, H, Nq, d, dtype)
+            lse = _empty3(B, H, Nq, _F32)
         else:
             _check_tensor("out", out, dtype, shape, index)
             _check_tensor("lse", lse, torch.float32, shape[:3], index)
         n_parts = fa_kvq8_num_parts(B, H, Hkv, Nq, max_len, d) if n_parts is None else int(n_parts)
         if workspace is None and n_parts > 0:
-            workspace = kv_lens.new_empty((fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) + 3) // 4)
+            workspace = _empty_bytes(fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts))
         rc = getattr(lib, fn_name)(q.data_ptr(), *cache_ptrs, n_pages, max_pages, page, kv_lens.data_ptr(),
                                    out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, max_len, d, fmt, float(scale), bool(causal),
                                    n_parts, None if workspace is None else workspace.data_ptr(),
@@ -800,12 +815,11 @@ def _raw_cross(fn_name, dtype, q, k, v, kv_lens, out, lse, scale, n_splits, work
     index, B, H, Hkv, Nq, Nk, d = _check_cross(q, k, v, kv_lens, dtype)
     with _on(index, stream):
         if out is None:
-            out = torch.empty_like(q)
-            lse = torch.empty((B, H, Nq), dtype=torch.float32, device=q.device)
+            out = _empty4(B, H, Nq, d, dtype)
+            lse = _empty3(B, H, Nq, _F32)
             n_splits = fa_cross_num_splits(B, H, Nq, Nk) if n_splits is None else n_splits
             if n_splits > 1:
-                workspace = torch.empty(fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits), dtype=torch.uint8,
-                                        device=q.device)
+                workspace = _empty_bytes(fa_splitkv_workspace_bytes(B, H, Nq, d, n_splits))
         else:
             _check_tensor("out", out, dtype, q.shape, index)
             _check_tensor("lse", lse, torch.float32, (B, H, Nq), index)
@@ -855,10 +869,10 @@ def _raw_bwd_cross(fn_name, dtype, q, k, v, kv_lens, out, dout, lse, dq, dk, dv,
     _check_tensor("lse", lse, torch.float32, (B, H, Nq), index)
     with _on(index, stream):
         if workspace is None:
-            workspace = torch.empty(fa_bwd_cross_workspace_bytes(B, H, Hkv, Nq, Nk, d), dtype=torch.uint8,
-                                    device=q.device)
+            workspace = _empty_bytes(fa_bwd_cross_workspace_bytes(B, H, Hkv, Nq, Nk, d))
         if dq is None:
-            dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+            dq = _empty4(B, H, Nq, d, dtype)
+            dk, dv = _empty4(B, Hkv, Nk, d, dtype), _empty4(B, Hkv, Nk, d, dtype)
         else:
             _check_tensor("dq", dq, dtype, q.shape, index)
             _check_tensor("dk", dk, dtype, k.shape, index)
