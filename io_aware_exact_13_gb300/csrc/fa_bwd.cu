@@ -152,12 +152,22 @@ __device__ __forceinline__ int cross_len(const BwdParams &p, int b) {
     return len;
 }
 // The line of key blocks that hold keys: batch index by batch index, in each block by block, in each block head by head.
-// The two below are a whole warp's: lane i looks at every 32nd batch index.
-__device__ __forceinline__ BwdCrossPlan cross_plan(const BwdParams &p) {
-    const int B = p.BH / p.Hkv;
+// cross_plan and cross_block are a whole warp's: lane i counts the i-th of 32 runs of neighbouring batch indices, and
+// `before` is how many blocks lie before its run.
+__device__ __forceinline__ BwdCrossPlan cross_plan(const BwdParams &p, int &before) {
+    const int B = p.BH / p.Hkv, lane = threadIdx.x & 31, run = (B + 31) / 32;
     int n = 0;
-    for (int b = threadIdx.x & 31; b < B; b += 32) n += (cross_len(p, b) + kBlk - 1) / kBlk;
-    return bwd_cross_plan((int)__reduce_add_sync(0xffffffffu, n) * p.Hkv, p.group * (p.Npad / kBlk), p.sms);
+#pragma unroll 4
+    for (int b = lane * run; b < min(B, (lane + 1) * run); ++b) n += (cross_len(p, b) + kBlk - 1) / kBlk;
+    n *= p.Hkv;
+    int end = n;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, end, off);
+        if (lane >= off) end += x;
+    }
+    before = end - n;
+    return bwd_cross_plan(__shfl_sync(0xffffffffu, end, 31), p.group * (p.Npad / kBlk), p.sms);
 }
 // What fa_bwd_cross_post is to add up, by one thread of the first CTA and one of each cut block's first run.
 __device__ __forceinline__ void note_plan(const BwdParams &p, const BwdCrossPlan &plan) {
@@ -170,12 +180,15 @@ __device__ __forceinline__ void note_cut(const BwdParams &p, int parts, int slot
 struct CrossBlock {
     int len, j, bh;
 };
-__device__ __forceinline__ CrossBlock cross_block(const BwdParams &p, int rank) {
-    const int B = p.BH / p.Hkv, lane = threadIdx.x & 31;
-    for (int b0 = 0;; b0 += 32) {
+__device__ __forceinline__ CrossBlock cross_block(const BwdParams &p, int rank, int before) {
+    const int B = p.BH / p.Hkv, lane = threadIdx.x & 31, run = (B + 31) / 32;
+    const int at_run = 31 - __clz(__ballot_sync(0xffffffffu, before <= rank));  // (lane 0's is 0)
+    rank -= __shfl_sync(0xffffffffu, before, at_run);
+    for (int b0 = at_run * run;; b0 += 32) {
         const int len = b0 + lane < B ? cross_len(p, b0 + lane) : 0;
         const int items = (len + kBlk - 1) / kBlk * p.Hkv;
         int end = items;  // blocks up to and with this lane's batch index
+#pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, end, off);
             if (lane >= off) end += x;
@@ -342,7 +355,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int zero_bh = bh, zero_row = j * kBlk;
     bool zero = false;
     if constexpr (CROSS) {
-        const BwdCrossPlan plan = cross_plan(p);
+        int before;
+        const BwdCrossPlan plan = cross_plan(p, before);
         note_plan(p, plan);
         zero = zero_row < p.Nk && zero_row >= cross_len(p, bh / p.Hkv);
         if ((int)blockIdx.x >= plan.items) {
@@ -351,7 +365,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             return;
         }
         run = cross_item(plan, blockIdx.x, n_qblk * p.group);
-        const CrossBlock x = cross_block(p, run.rank);
+        const CrossBlock x = cross_block(p, run.rank, before);
         n_keys = x.len;
         j = x.j;
         bh = x.bh;
@@ -1054,7 +1068,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SMEM_BAR + C::NUM_BARS * 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const BwdCrossPlan plan = cross_plan(p);
+    int before;
+    const BwdCrossPlan plan = cross_plan(p, before);
     note_plan(p, plan);
 
     if (threadIdx.x == 0) {
