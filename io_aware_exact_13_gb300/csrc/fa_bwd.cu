@@ -152,7 +152,14 @@ __device__ __forceinline__ int cross_len(const BwdParams &p, int b) {
     return len;
 }
 // The line of key blocks that hold keys: batch index by batch index, in each block by block, in each block head by head.
-// cross_plan and cross_block are a whole warp's: lane i counts the i-th of 32 runs of neighbouring batch indices, and
+// The next three are a whole warp's. Here lane i looks at every 32nd batch index.
+__device__ __forceinline__ BwdCrossPlan cross_plan(const BwdParams &p) {
+    const int B = p.BH / p.Hkv;
+    int n = 0;
+    for (int b = threadIdx.x & 31; b < B; b += 32) n += (cross_len(p, b) + kBlk - 1) / kBlk;
+    return bwd_cross_plan((int)__reduce_add_sync(0xffffffffu, n) * p.Hkv, p.group * (p.Npad / kBlk), p.sms);
+}
+// For cross_block: lane i counts the i-th of 32 runs of neighbouring batch indices, and
 // `before` is how many blocks lie before its run.
 __device__ __forceinline__ BwdCrossPlan cross_plan(const BwdParams &p, int &before) {
     const int B = p.BH / p.Hkv, lane = threadIdx.x & 31, run = (B + 31) / 32;
@@ -1068,8 +1075,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + C::SMEM_BAR + C::NUM_BARS * 8);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int before;
-    const BwdCrossPlan plan = cross_plan(p, before);
+    const BwdCrossPlan plan = cross_plan(p);
     note_plan(p, plan);
 
     if (threadIdx.x == 0) {
