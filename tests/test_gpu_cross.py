@@ -117,6 +117,7 @@ CASES = [
     ("bf16", 4, 8, 8, 130, 700, 64, [700, 641, 0, 130]),
     ("fp16", 4, 8, 8, 130, 700, 128, [700, 640, 129, 1]),
     ("fp16", 40, 10, 5, 3, 140, 64, [int(x) for x in np.random.default_rng(5).integers(0, 141, 40)]),
+    ("bf16", 70, 4, 2, 130, 200, 64, [0] * 40 + [int(x) for x in np.random.default_rng(9).integers(0, 201, 30)]),
 ]
 
 
@@ -154,6 +155,7 @@ CUT = [
     ("bf16", 6, 4, 2, 400, 1700, 64, None),
     ("fp16", 18, 6, 2, 257, 300, 64, [300, 0, 260, 1, 128, 129] * 3),
     ("bf16", 18, 6, 2, 257, 300, 128, [300, 0, 260, 1, 128, 129] * 3),
+    ("fp16", 70, 4, 2, 130, 200, 128, [int(x) for x in np.random.default_rng(8).integers(0, 201, 70)]),  # many sequences
 ]
 
 
