@@ -43,6 +43,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include <type_traits>
@@ -58,7 +59,9 @@ constexpr int kWarps = 4;
 constexpr int kMostCluster = 8;  // CTAs of a unit, all of a portable cluster
 constexpr int kTileKeys = 16;
 constexpr float kTau = 8.0f;  // log2 units by which a reference maximum may be exceeded before it moves
-constexpr float kNone = -1e30f;  // reference maximum of a row that has seen no key
+// Reference maximum of a row that has seen no key: below every finite score, and finite itself, so that the differences
+// with it that empty rows and stretches form are numbers.
+constexpr float kNone = -FLT_MAX;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Resident CTAs per SM that the kernel is compiled for: 128, 168 or 255 registers per thread.
@@ -527,8 +530,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
             for (int t = 0; t < NT; ++t) {
                 float f[2], w[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)  // (the limit: a row that saw only pages of zeros has m - mw = 1e30, and w = 0 here)
-                    f[e] = ex2_approx(fminf(lv + (m[t][e] - mw[t][e]), 120.0f));
+                for (int e = 0; e < 2; ++e)  // (a row that saw only pages of zeros has mw = kNone, and m - mw may be infinite)
+                    f[e] = lv == -INFINITY ? 0.f : ex2_approx(fminf(lv + (m[t][e] - mw[t][e]), 120.0f));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[t][e] - m[t][e & 1]);
                 l[t][0] += w[0] + w[2];

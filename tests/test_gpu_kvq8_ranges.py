@@ -1,0 +1,62 @@
+"""GPU tests of the 8-bit key/value cache at the edges of its ranges, against the definitions in 64 bits (kvq8_ref):
+scores and page scales of any size, queries of uneven magnitude, scales that no append wrote, and each status by itself."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kvq8_ref as ref
+from test_gpu_kvq8 import CODE, DEV, DT, as_ref, check_attention, check_cache, filled, ints, numbers, random_table, status_ok
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def fa():
+    assert torch.cuda.is_available(), "GPU tests need a CUDA device"
+    from io_aware_exact_13_gb300 import build
+
+    build.build()
+    from io_aware_exact_13_gb300 import fa as mod
+
+    mod.fa_get_device_status()
+    return mod
+
+
+# ---------------------------------------------------------------- scores far below zero
+@pytest.mark.parametrize("n_parts", [0, 1, 3])
+@pytest.mark.parametrize("fmt,d,Nq", [("int8", 64, 1), ("e4m3", 128, 1), ("int8", 128, 5), ("e4m3", 64, 12)])
+def test_attention_rows_of_very_low_scores(fa, fmt, d, Nq, n_parts):
+    """Scores of -1e32 and +1e32: a row whose scores are all far below zero still has a largest one, whose value it gets.
+
+    Scores are single products here and every row's largest stands alone, 2^-3 of itself above the next, so the weights are
+    1 and 0 and out is one value, rounded once: half a step. lse is one product's roundings, of scale log2 e,
+    of the page scale times it, of the score, of ln 2 and the last one: 5 2^-24 of itself, below 2^-21."""
+    rng = np.random.default_rng(41)
+    lens, page, H = [1, 37, 700, 0], 16, 2
+    table, n_pages = random_table(rng, lens, page)
+    cache = filled(fa, rng, fmt, n_pages, 1, page, d)
+    k = np.zeros((n_pages, 1, page, d))
+    k[..., 0] = 96.0
+    for s, n in enumerate(lens):
+        if n:
+            k[table[s, 0], 0, 0, 0] = 64.0            # the key that the rows of low scores are left with
+            if n > 1:
+                k[table[s, 1], 0, 3, 0] = 112.0       # and the one of the high rows
+    cache.k_codes.copy_(torch.from_numpy(k).to(CODE[fmt]).to(DEV))
+    cache.k_scale.fill_(1.0)
+    q = torch.zeros((4, H, Nq, d), dtype=torch.bfloat16)
+    q[..., 0] = -1e30
+    q[:, 1, Nq // 2 :, 0] = 1e30
+    out, lse = fa.attention_kvq8(q.to(DEV), cache, ints(table.tolist()), ints(lens), scale=1.0, causal=True,
+                                 n_parts=n_parts, max_len=700)
+    status_ok(fa)
+    kc, ks, vc, vs = as_ref(cache)
+    o, l = out.cpu().double().numpy(), lse.cpu().double().numpy()
+    for b, n in enumerate(lens):
+        want, wl, *_ = ref.attend(q[b].double().numpy(), ref.gather(kc, ks, table[b], n), ref.gather(vc, vs, table[b], n), 1.0, True)
+        seen = np.isfinite(wl)
+        assert np.array_equal(np.isneginf(l[b]), ~seen) and np.all(o[b][~seen] == 0.0)
+        assert np.all(np.abs(o[b] - want) <= 2.0 ** -8 * np.abs(want))
+        assert np.all(np.abs(l[b][seen] - wl[seen]) <= 2.0 ** -21 * np.abs(wl[seen]))
