@@ -524,19 +524,24 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                         }
                     }
             }
-            // weights w = p 2^(lv + m - mw) as B fragments: keys 2c, 2c + 1 (+ 8) of row g
+            // weights w = 2^(x + lv - mw) as B fragments: keys 2c, 2c + 1 (+ 8) of row g. One exponential for the whole
+            // exponent: 2^(x - m) and 2^(lv + m - mw) may each leave fp32's range where their product does not.
             uint32_t pb[NT][2];
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                float f[2], w[4];
+                float f[2], s[4], w[4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e)  // (a row that saw only pages of zeros has mw = kNone, and m - mw may be infinite)
-                    f[e] = lv == -INFINITY ? 0.f : ex2_approx(fminf(lv + (m[t][e] - mw[t][e]), 120.0f));
+                    f[e] = lv == -INFINITY ? -INFINITY : fminf(lv + (m[t][e] - mw[t][e]), FLT_MAX);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) w[e] = ex2_approx(x[t][e] - m[t][e & 1]);
-                l[t][0] += w[0] + w[2];
-                l[t][1] += w[1] + w[3];
-                const __half2 h0 = __floats2half2_rn(w[0] * f[0], w[1] * f[1]), h1 = __floats2half2_rn(w[2] * f[0], w[3] * f[1]);
+                for (int e = 0; e < 4; ++e) {
+                    const float a = x[t][e] - m[t][e & 1];
+                    s[e] = ex2_approx(a);
+                    w[e] = ex2_approx(a + f[e & 1]);
+                }
+                l[t][0] += s[0] + s[2];
+                l[t][1] += s[1] + s[3];
+                const __half2 h0 = __floats2half2_rn(w[0], w[1]), h1 = __floats2half2_rn(w[2], w[3]);
                 pb[t][0] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h0));
                 pb[t][1] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h1));
             }

@@ -60,3 +60,40 @@ def test_attention_rows_of_very_low_scores(fa, fmt, d, Nq, n_parts):
         assert np.array_equal(np.isneginf(l[b]), ~seen) and np.all(o[b][~seen] == 0.0)
         assert np.all(np.abs(o[b] - want) <= 2.0 ** -8 * np.abs(want))
         assert np.all(np.abs(l[b][seen] - wl[seen]) <= 2.0 ** -21 * np.abs(wl[seen]))
+
+
+# ---------------------------------------------------------------- V scales far apart
+@pytest.mark.parametrize("n_parts", [0, 1, 2])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("first", ["low", "high"])
+def test_attention_small_weights_of_large_values(fa, fmt, first, n_parts):
+    """A page of scores 0 and values near 2^-110, and one of scores -87 (weights near 2^-126) and values near 2^20, which
+    make the result: neither a weight nor the quotient of the scales may leave its range on the way.
+
+    Bound: as in check_attention, but the scores are single products of up to 126 in log2 units, each with roundings of
+    4 2^-24 of itself: 126 2^-22 ln 2 < 2^-15 relative, inside its 2^-12; no weight is below fp16's normal range against
+    the largest contribution but those of the page that is 2^-5 of it, so its second term stays."""
+    rng = np.random.default_rng(42)
+    page, n, d = 32, 150, 64
+    table, n_pages = random_table(rng, [n], page)
+    cache = filled(fa, rng, fmt, n_pages, 1, page, d)
+    high = np.array([i % 2 == (first == "low") for i in range(table.shape[1])])  # by page: values of 2^20
+    k = np.zeros((n_pages, 1, page, d))
+    k[table[0][high], ..., 0] = -64.0
+    cache.k_codes.copy_(torch.from_numpy(k).to(CODE[fmt]).to(DEV))
+    cache.k_scale.fill_(87.0 / 64)
+    e = np.zeros(n_pages)
+    e[table[0]] = np.where(high, 20.0, -110.0)
+    cache.v_scale.copy_(torch.from_numpy(2.0 ** e)[:, None].float().to(DEV))
+    q = torch.zeros((1, 2, 3, d), dtype=torch.bfloat16)
+    q[..., 0] = 1.0
+    out, lse = fa.attention_kvq8(q.to(DEV), cache, ints(table.tolist()), ints([n]), scale=1.0, causal=True, n_parts=n_parts)
+    status_ok(fa)
+    kc, ks, vc, vs = as_ref(cache)
+    v = ref.gather(vc, vs, table[0], n)
+    want, wl, mag, _, tot = ref.attend(q[0].double().numpy(), ref.gather(kc, ks, table[0], n), v, 1.0, True)
+    o, l = out[0].cpu().double().numpy(), lse[0].cpu().double().numpy()
+    big = np.exp(-87.0) * np.abs(v).max()  # the largest contribution's size
+    tol = (2.0 ** -11 + 2.0 ** -12) * mag + 2.0 ** -25 * n * big / tot[..., None] + 2.0 ** -8 * np.abs(want)
+    assert np.all(np.abs(o - want) <= tol), float((np.abs(o - want) / tol).max())
+    assert np.all(np.abs(l - wl) <= 2.0 ** -13 + 2.0 ** -22 * np.abs(wl))
