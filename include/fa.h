@@ -256,8 +256,9 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *ou
  * kv_lens[b] positions, 0 <= kv_lens[b] <= max_len <= max_pages * page (max_len: host-side bound).
  * causal != 0 aligns the last query with the last key: query i sees keys j <= i + kv_lens[b] - Nq.
  * A row that sees no key gets out = 0 and lse = -inf. Codes, scores, sums and accumulators are
- * not rounded below fp32; the softmax weights are rounded to fp16 before they multiply V (bf16
- * queries enter the products exactly down to 2^-24 of their row's largest magnitude). With n_parts
+ * not rounded below fp32; the softmax weights are rounded to fp16 before they multiply V. bf16
+ * queries enter the products as fp16 under a power of two for each row: exactly for elements down
+ * to 2^-32 of their row's largest magnitude, and off by at most 2^-40 of it below. With n_parts
  * > 0 all sequences' keys are cut, as one line, into n_parts equal stretches, whatever the lengths
  * are; the summaries of sequences that more than one part shares go through the workspace (256-byte
  * aligned, at least fa_kvq8_workspace_bytes(H, Hkv, Nq, d, n_parts) bytes, contents on entry

@@ -97,3 +97,30 @@ def test_attention_small_weights_of_large_values(fa, fmt, first, n_parts):
     tol = (2.0 ** -11 + 2.0 ** -12) * mag + 2.0 ** -25 * n * big / tot[..., None] + 2.0 ** -8 * np.abs(want)
     assert np.all(np.abs(o - want) <= tol), float((np.abs(o - want) / tol).max())
     assert np.all(np.abs(l - wl) <= 2.0 ** -13 + 2.0 ** -22 * np.abs(wl))
+
+
+# ---------------------------------------------------------------- queries of uneven magnitude
+@pytest.mark.parametrize("apart,base", [(10, 0), (18, 0), (22, 0), (27, 0), (32, 0), (32, 95), (32, -118), (5, -118), (1, -112),
+                                        (0, -110), (20, 60)])
+@pytest.mark.parametrize("fmt,d,Nq", [("int8", 64, 1), ("e4m3", 128, 3)])
+def test_attention_small_elements_beside_an_outlier(fa, fmt, d, Nq, apart, base):
+    """bf16 rows with one element up to 2^32 times the rest, over keys whose code there is 0, anywhere in the type's range:
+    the scores are made of the small elements alone, which enter the products exactly (check_attention's bound has no term
+    for Q)."""
+    rng = np.random.default_rng(43 + apart + abs(base))
+    lens, page, H = [200, 17], 16, 4
+    table, n_pages = random_table(rng, lens, page)
+    cache = filled(fa, rng, fmt, n_pages, 2, page, d)
+    x = rng.choice([-1, 1], (2, H, Nq, d)) * (1 + rng.integers(0, 128, (2, H, Nq, d)) / 128)  # all 8 bits in use, in [1, 2)
+    dim = rng.integers(0, d, (2, H, Nq))
+    np.put_along_axis(x, dim[..., None], 2.0 ** apart, -1)
+    x *= 2.0 ** base
+    codes = cache.k_codes.view(torch.uint8)
+    codes[..., torch.from_numpy(np.unique(dim)).to(DEV)] = 0
+    q = torch.from_numpy(x).bfloat16()
+    assert np.array_equal(q.double().numpy(), x)
+    for n_parts in (0, 2):
+        out, lse = fa.attention_kvq8(q.to(DEV), cache, ints(table.tolist()), ints(lens), n_parts=n_parts,
+                                     scale=2.0 ** -base / math.sqrt(d))
+        status_ok(fa)
+        check_attention(q, cache, table, lens, out, lse, 2.0 ** -base / math.sqrt(d), False)
