@@ -66,6 +66,26 @@ long long kvq8_tiles(int B, int Hkv, int rows, int max_len, int d);
 int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int d, int num_sms);
 size_t kvq8_workspace_bytes(int rows, int d, int parts);
 
+// Scales that are no powers of two (append writes none, but a cache may come from elsewhere): a product or quotient with
+// one is rounded to fp32 before it is rounded to a code or to 16 bits, and twice is not once: what fp32 rounds to the
+// middle between two results need not lie there. So fp32's rounding is made one to odd: an inexact result takes the
+// neighbour whose last bit is 1, and the second rounding is then that of the exact value.
+__device__ __forceinline__ bool power_of_two(float s) { return (__float_as_uint(s) & 0x7FFFFFu) == 0u; }  // or 0
+// q = fl(exact), not 0 or far from the second rounding's middles; rest has the sign of exact - q.
+__device__ __forceinline__ float to_odd(float q, float rest) {
+    const int b = __float_as_int(q);
+    if (rest == 0.0f || (b & 1) || q == 0.0f) return q;
+    return __int_as_float((b ^ __float_as_int(rest)) >= 0 ? b + 1 : b - 1);
+}
+__device__ __forceinline__ float product_odd(float a, float b) {
+    const float q = a * b;
+    return to_odd(q, fmaf(a, b, -q));
+}
+__device__ __forceinline__ float quotient_odd(float a, float s) {  // s > 0
+    const float q = __fdiv_rn(a, s);
+    return to_odd(q, fmaf(-q, s, a));
+}
+
 // Four int8 codes -> two pairs of fp16, exact: code + 128 under the exponent of 1024 is the
 // fp16 number 1152 + code.
 __device__ __forceinline__ void int8x4_to_half2(uint32_t w, uint32_t &lo, uint32_t &hi) {

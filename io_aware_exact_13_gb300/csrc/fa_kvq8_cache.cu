@@ -6,6 +6,7 @@
 // a code is x / s rounded to nearest even. A page that held tokens before the call keeps its
 // scale or, when the new tokens need a larger one, takes that and has its codes rounded to it:
 //     s = max(s_old, s_new),   c' = rne(c s_old / s),   c = rne(x / s).
+// (A page whose scale came from elsewhere keeps it while it is large enough; its codes are rounded once as well.)
 // Why powers of two: x / s and c s_old / s are then exact, so a code depends on the values alone
 // and not on how a division rounds; and a scale that grows at least doubles, so a code's
 // roundings in all of its page's growths add up to less than one step (1/2 + 1/4 + ...). With
@@ -176,6 +177,45 @@ __global__ void __launch_bounds__(NT, KVS == 1 ? 1024 / NT : 1) fa_kvq8_append_k
         uint8_t *dst = p.codes[kv0 + j] + (unit << (p.page_shift + p.d_shift));
         const bool grew = lo > 0 && s != s_old;
         const float ratio = s_old * inv;
+        if (!power_of_two(s) || (grew && !power_of_two(s_old))) {  // a scale from elsewhere: a rare, slower way
+            const T *src = static_cast<const T *>(p.src[kv0 + j]) + (long long)head * p.head[kv0 + j];
+            const float up = s < 0x1p-60f ? 0x1p60f : 1.0f;  // (keeps the quotient's remainder in range; exact)
+#pragma unroll 1
+            for (int vec = threadIdx.x; vec < NT * VEC; vec += NT) {
+                const int slot = vec >> vec_shift, chunk = vec & ((1 << vec_shift) - 1);
+                float f[8];
+                if (slot >= lo && slot < hi) {
+                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(
+                        src + (long long)(c0 + (t0 + slot - held)) * p.token[kv0 + j] + chunk * 8));
+                    const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 a = unpack2<T>(w[e]);
+                        f[2 * e] = isfinite(a.x) ? quotient_odd(a.x * up, s * up) : 0.0f;
+                        f[2 * e + 1] = isfinite(a.y) ? quotient_odd(a.y * up, s * up) : 0.0f;
+                    }
+                } else if (grew && slot < lo) {
+                    const uint2 was = *reinterpret_cast<const uint2 *>(dst + (long long)vec * 8);
+                    const uint32_t w[2] = {was.x, was.y};
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        uint32_t h[2];
+                        codes_to_half2<FMT>(w[e], h[0], h[1]);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const float2 a = unpack2<__half>(h[i]);
+                            f[4 * e + 2 * i] = product_odd(a.x, ratio);
+                            f[4 * e + 2 * i + 1] = product_odd(a.y, ratio);
+                        }
+                    }
+                } else {
+                    continue;
+                }
+                *reinterpret_cast<uint2 *>(dst + (long long)vec * 8) =
+                    make_uint2(encode4<FMT>(f[0], f[1], f[2], f[3]), encode4<FMT>(f[4], f[5], f[6], f[7]));
+            }
+            continue;
+        }
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const int vec = threadIdx.x + i * NT;

@@ -124,3 +124,68 @@ def test_attention_small_elements_beside_an_outlier(fa, fmt, d, Nq, apart, base)
                                      scale=2.0 ** -base / math.sqrt(d))
         status_ok(fa)
         check_attention(q, cache, table, lens, out, lse, 2.0 ** -base / math.sqrt(d), False)
+
+
+# ---------------------------------------------------------------- scales that are no powers of two
+def halfway(rng, fmt, dtype, scales, shape):
+    """16-bit values at or next to the middle between two codes under `scales` (broadcast), of at most half the largest."""
+    codes = np.arange(-64.0, 65.0)
+    if fmt == "e4m3":
+        codes = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+        codes = np.unique(codes[np.abs(codes) <= 224])
+    return torch.from_numpy(rng.choice((codes[1:] + codes[:-1]) / 2, shape) * scales).to(DT[dtype])
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_append_to_pages_of_any_scale(fa, fmt, dtype):
+    """Pages that hold tokens under scales that are no powers of two: they keep them while these are large enough, and
+    codes are x / s rounded once. A scale that is a small odd number times a power of two puts many values exactly in the
+    middle, where the even code is due."""
+    rng = np.random.default_rng(44)
+    page, Hkv, d, n_seq = 16, 2, 64, 100
+    held = [int(x) for x in rng.integers(1, page, n_seq)]
+    cache = filled(fa, rng, fmt, n_seq, Hkv, page, d)
+    s = rng.integers(3, 128, (n_seq, Hkv)) * 2.0 ** -12  # by sequence
+    s[::5] = rng.uniform(0.01, 0.02, s[::5].shape).astype(np.float32)
+    table = rng.permutation(n_seq)[:, None]
+    for scale in (cache.k_scale, cache.v_scale):
+        scale[torch.from_numpy(table[:, 0])] = torch.from_numpy(s).float().to(DEV)
+    want = as_ref(cache)
+    new = [page - h for h in held]
+    cu = [0] + [int(c) for c in np.cumsum(new)]
+    k, v = (halfway(rng, fmt, dtype, np.repeat(s, new, axis=0)[:, :, None], (cu[-1], Hkv, d)) for _ in range(2))
+    fa.kvq8_append(cache, k.to(DEV), v.to(DEV), ints(table.tolist()), ints(cu), ints(held), page)
+    for i, x in ((0, k), (2, v)):
+        ref.append(want[i], want[i + 1], fmt, x.double().numpy(), table, cu, held)
+    assert np.array_equal(want[1][table[:, 0]], s.astype(np.float32))  # none grew
+    status_ok(fa)
+    check_cache(cache, want)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_append_that_grows_a_scale_of_any_value(fa, fmt):
+    """Earlier codes are rounded once to the power of two that a larger new token asks for, whatever their scale was: every
+    c s_old / s here is off the middle between two codes by less than fp32 resolves."""
+    rng = np.random.default_rng(45)
+    page, d, n = 32, 64, 2000
+    c0 = np.array([3.0, 5.0, 7.0, 11.0, 13.0, 15.0]) if fmt == "e4m3" else np.arange(3.0, 127.0, 2.0)
+    codes = rng.choice(c0, n)
+    if fmt == "int8":
+        mid = rng.integers(0, codes.astype(int)) + 0.5
+    else:
+        mid = 2.0 ** rng.integers(-3, 1, n) * (rng.integers(8, 16, n) + 0.5) / 8
+    s_old = (mid / codes).astype(np.float32)
+    assert np.all((s_old > 0) & (s_old < 1))
+    cache = fa.kv_cache_q8(n, 1, page, d, CODE[fmt], DEV)
+    for t, s in ((cache.k_codes, cache.k_scale), (cache.v_codes, cache.v_scale)):
+        t.copy_(torch.from_numpy(np.broadcast_to(codes[:, None, None, None], t.shape).copy()).to(CODE[fmt]).to(DEV))
+        s.copy_(torch.from_numpy(s_old).float()[:, None].to(DEV))
+    want = as_ref(cache)
+    big = torch.full((n, 1, d), ref.QMAX[fmt], dtype=torch.bfloat16)  # scale 1
+    table, cu, held = np.arange(n)[:, None], list(range(n + 1)), [5] * n
+    fa.kvq8_append(cache, big.to(DEV), big.to(DEV), ints(table.tolist()), ints(cu), ints(held), 1)
+    for i in (0, 2):
+        ref.append(want[i], want[i + 1], fmt, big.double().numpy(), table, cu, held)
+    status_ok(fa)
+    check_cache(cache, want)
