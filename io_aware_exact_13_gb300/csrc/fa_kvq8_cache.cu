@@ -321,8 +321,13 @@ __global__ void __launch_bounds__(kReadThreads) fa_kvq8_read_kernel(const ReadPa
                 uint32_t h0, h1;
                 codes_to_half2<FMT>(w[e], h0, h1);
                 const float2 a = unpack2<__half>(h0), b = unpack2<__half>(h1);
-                o[2 * e] = pack2h<T>(a.x * s[kv][i], a.y * s[kv][i]);
-                o[2 * e + 1] = pack2h<T>(b.x * s[kv][i], b.y * s[kv][i]);
+                if (power_of_two(s[kv][i])) {
+                    o[2 * e] = pack2h<T>(a.x * s[kv][i], a.y * s[kv][i]);
+                    o[2 * e + 1] = pack2h<T>(b.x * s[kv][i], b.y * s[kv][i]);
+                } else {
+                    o[2 * e] = pack2h<T>(product_odd(a.x, s[kv][i]), product_odd(a.y, s[kv][i]));
+                    o[2 * e + 1] = pack2h<T>(product_odd(b.x, s[kv][i]), product_odd(b.y, s[kv][i]));
+                }
             }
             uint4 *dst = reinterpret_cast<uint4 *>(static_cast<T *>(p.dst[kv]) + row);
             dst[0] = make_uint4(o[0], o[1], o[2], o[3]);

@@ -189,3 +189,26 @@ def test_append_that_grows_a_scale_of_any_value(fa, fmt):
         ref.append(want[i], want[i + 1], fmt, big.double().numpy(), table, cu, held)
     status_ok(fa)
     check_cache(cache, want)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_read_under_scales_of_any_value(fa, fmt, dtype):
+    """code * scale rounded once to the 16-bit type, next to the middle between two of its numbers."""
+    rng = np.random.default_rng(46)
+    page, d, n = 16, 64, 4000
+    bits = 8 if dtype == "bf16" else 11
+    c0 = np.array([9.0, 11.0, 13.0, 15.0]) if fmt == "e4m3" else np.arange(3.0, 128.0, 2.0)
+    codes = rng.choice(c0, n)
+    mid = (rng.integers(2 ** (bits - 1), 2 ** bits, n) + 0.5) * 2.0 ** -bits
+    s = (mid / codes).astype(np.float32)
+    cache = fa.kv_cache_q8(n, 1, page, d, CODE[fmt], DEV)
+    for t, sc in ((cache.k_codes, cache.k_scale), (cache.v_codes, cache.v_scale)):
+        t.copy_(torch.from_numpy(np.broadcast_to(codes[:, None, None, None], t.shape).copy()).to(CODE[fmt]).to(DEV))
+        sc.copy_(torch.from_numpy(s)[:, None].to(DEV))
+    k, v = fa.kvq8_read(cache, ints(np.arange(n)[None].tolist()), ints([0, n * page]), n * page, n * page, dtype=DT[dtype])
+    status_ok(fa)
+    m, e = np.frexp(codes * s.astype(np.float64))  # the product in 64 bits is exact, and rounded once (torch's conversion
+    want = np.ldexp(np.rint(m * 2.0 ** bits), e - bits)  # from 64 bits may go by way of 32)
+    want = torch.from_numpy(np.repeat(want, page)).to(DT[dtype])[:, None, None].expand(-1, 1, d)
+    assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want)
