@@ -376,6 +376,15 @@ int splitkv_common(bool fp16, const void *q, const void *k, const void *v, void 
     return fa::launch_splitkv(a, fp16);
 }
 
+// What the 8-bit cache's calls take, and their sizing helpers with them: positions and tiles stay below 2^31 with room to
+// add, and B * H * Nq rows fit an int.
+constexpr int kKvq8MaxLen = 1 << 30, kKvq8MaxTiles = 1 << 30, kKvq8MaxParts = 1 << 20;
+bool kvq8_rows_ok(int B, int H, int Hkv, int Nq) {
+    if (H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq) return false;
+    const int64_t bh = static_cast<int64_t>(B) * H;
+    return bh <= INT32_MAX && bh * Nq <= INT32_MAX;
+}
+
 int check_kvq8_cache(const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,
                      const int *page_table, int n_pages, int max_pages, int page, int Hkv, int d, int format) {
     if (!k_codes || !v_codes || !k_scale || !v_scale || !page_table) return FA_ERR_NULL;
@@ -386,7 +395,7 @@ int check_kvq8_cache(const void *k_codes, const void *v_codes, const float *k_sc
     if (page != 16 && page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     if (format != FA_KVQ8_INT8 && format != FA_KVQ8_E4M3) return FA_ERR_ARG;
-    if (static_cast<int64_t>(max_pages) * page > (1 << 30)) return FA_ERR_SHAPE;  // positions stay below 2^31
+    if (static_cast<int64_t>(max_pages) * page > kKvq8MaxLen) return FA_ERR_SHAPE;
     return FA_OK;
 }
 
@@ -448,7 +457,7 @@ int kvq8_read_common(bool fp16, const void *k_codes, const void *v_codes, const 
     if (rc != FA_OK) return rc;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_seqlens, 4) || (first && !aligned(first, 4)))
         return FA_ERR_ALIGN;
-    if (nseq < 1 || total < 1 || max_len < 1 || max_len > (1 << 30)) return FA_ERR_SHAPE;
+    if (nseq < 1 || total < 1 || max_len < 1 || max_len > kKvq8MaxLen) return FA_ERR_SHAPE;
     DeviceInfo *di = device_info();
     if (!di) return FA_ERR_LAUNCH;
     fa::Kvq8ReadArgs a;
@@ -476,12 +485,11 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     int rc = check_kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
     if (rc != FA_OK) return rc;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4)) return FA_ERR_ALIGN;
-    if (B < 1 || H < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq) return FA_ERR_SHAPE;
+    if (B < 1 || !kvq8_rows_ok(B, H, Hkv, Nq)) return FA_ERR_SHAPE;
     if (max_len < 1 || max_len > static_cast<int64_t>(max_pages) * page) return FA_ERR_SHAPE;
-    if (n_parts < 0 || n_parts > (1 << 20)) return FA_ERR_SHAPE;
-    if (static_cast<int64_t>(B) * H * Nq > INT32_MAX) return FA_ERR_SHAPE;
+    if (n_parts < 0 || n_parts > kKvq8MaxParts) return FA_ERR_SHAPE;
     const int rows = H / Hkv * Nq;
-    if (fa::kvq8_tiles(B, Hkv, rows, max_len, d) > (1 << 30)) return FA_ERR_SHAPE;
+    if (fa::kvq8_tiles(B, Hkv, rows, max_len, d) > kKvq8MaxTiles) return FA_ERR_SHAPE;
     if (n_parts > 0 &&
         (!workspace || !aligned(workspace, 256) || workspace_bytes < fa::kvq8_workspace_bytes(rows, d, n_parts)))
         return FA_ERR_WORKSPACE;
@@ -520,14 +528,21 @@ int cross_num_splits(int B, int H, int Nq, int Nk, int num_sms) {
     return n < 1 ? 1 : static_cast<int>(n);
 }
 
+// Sizes of B, H, Hkv, Nq, Nk that the calls for keys of another length take, and their sizing helpers with them: as for the
+// other forwards, and an int of key blocks.
+bool cross_sizes_ok(int B, int H, int Hkv, int Nq, int Nk) {
+    if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nk < 1) return false;
+    const int64_t bh = static_cast<int64_t>(B) * H;
+    if (bh > INT32_MAX || bh * ((static_cast<int64_t>(Nq) + 255) / 256) > INT32_MAX) return false;
+    return static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Nk) + 127) / 128) <= INT32_MAX;
+}
+
 int check_cross(const void *q, const void *k, const void *v, const int *kv_lens, const void *out, const float *lse,
                 int B, int H, int Hkv, int Nq, int Nk, int d) {
     int rc = check_args(Type::BF16, q, k, v, nullptr, out, lse, B, H, Nq, d);
     if (rc != FA_OK) return rc;
     if (kv_lens && !aligned(kv_lens, 4)) return FA_ERR_ALIGN;
-    if (Hkv < 1 || H % Hkv != 0 || Nk < 1) return FA_ERR_SHAPE;
-    if (static_cast<int64_t>(B) * Hkv * ((static_cast<int64_t>(Nk) + 127) / 128) > INT32_MAX) return FA_ERR_SHAPE;
-    return FA_OK;
+    return cross_sizes_ok(B, H, Hkv, Nq, Nk) ? FA_OK : FA_ERR_SHAPE;
 }
 
 int cross_common(Type ty, const void *q, const void *k, const void *v, const int *kv_lens, void *out, float *lse,
@@ -900,14 +915,15 @@ int fa_kvq8_read_fp16(FA_READ_ARGS) {
 #undef FA_READ_ARGS
 
 int fa_kvq8_num_parts(int B, int H, int Hkv, int Nq, int max_len, int d) {
-    if (B < 1 || H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || max_len < 1) return FA_ERR_SHAPE;
+    if (B < 1 || !kvq8_rows_ok(B, H, Hkv, Nq) || max_len < 1 || max_len > kKvq8MaxLen) return FA_ERR_SHAPE;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (fa::kvq8_tiles(B, Hkv, H / Hkv * Nq, max_len, d) > kKvq8MaxTiles) return FA_ERR_SHAPE;
     DeviceInfo *di = device_info();
     return fa::kvq8_num_parts(B, Hkv, H / Hkv * Nq, max_len, d, di ? di->num_sms : kNominalSms);
 }
 
 long long fa_kvq8_workspace_bytes(int H, int Hkv, int Nq, int d, int n_parts) {
-    if (H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq || n_parts < 0) return FA_ERR_SHAPE;
+    if (!kvq8_rows_ok(1, H, Hkv, Nq) || n_parts < 0 || n_parts > kKvq8MaxParts) return FA_ERR_SHAPE;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     return static_cast<long long>(fa::kvq8_workspace_bytes(H / Hkv * Nq, d, n_parts));
 }
@@ -963,7 +979,7 @@ int fa_bwd_fp16(const void *q, const void *k, const void *v, const void *out, co
 }
 
 int fa_cross_num_splits(int B, int H, int Nq, int Nk) {
-    if (B < 1 || H < 1 || Nq < 1 || Nk < 1) return FA_ERR_SHAPE;
+    if (!cross_sizes_ok(B, H, 1, Nq, 1) || Nk < 1) return FA_ERR_SHAPE;
     DeviceInfo *di = device_info();
     return cross_num_splits(B, H, Nq, Nk, di ? di->num_sms : kNominalSms);
 }
@@ -985,7 +1001,7 @@ int fa_fwd_cross_fp16(const void *q, const void *k, const void *v, const int *kv
 long long fa_bwd_cross_workspace_bytes(int B, int H, int Hkv, int Nq, int Nk, int d) {
     const long long n = fa_bwd_workspace_bytes(B, H, Nq, d);
     if (n < 0) return n;
-    if (Hkv < 1 || H % Hkv != 0 || Nk < 1) return FA_ERR_SHAPE;
+    if (!cross_sizes_ok(B, H, Hkv, Nq, Nk)) return FA_ERR_SHAPE;
     DeviceInfo *di = device_info();
     return n + static_cast<long long>(bwd_cross_part_bytes(B, H, Hkv, Nq, Nk, d, di));
 }
