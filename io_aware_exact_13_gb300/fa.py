@@ -27,7 +27,15 @@ import os
 from typing import NamedTuple
 
 import torch
-from torch._C._dynamo.guards import _empty_strided_cuda
+
+# Private names of torch that save host time on the calls beside kernels of a few microseconds, where this torch has them
+# (None: the public way is taken).
+try:
+    from torch._C._dynamo.guards import _empty_strided_cuda
+except ImportError:
+    _empty_strided_cuda = None
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libfa.so")
 if not os.path.exists(_LIB_PATH):
@@ -478,7 +486,8 @@ def kv_cache_q8(n_pages, Hkv, page, d, dtype=torch.int8, device="cuda") -> KVCac
 def _on(index, stream):
     """Context in which device ``index`` is current and torch allocates for ``stream`` (None: the device's current one)."""
     if stream is None:
-        return _NOTHING if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
+        current = _get_device() if _get_device is not None else torch.cuda.current_device()
+        return _NOTHING if index == current else torch.cuda.device(index)
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=torch.device("cuda", index))
     if stream.device.index != index:
@@ -499,22 +508,29 @@ _NOTHING = _Nothing()
 
 def _raw_stream(index, stream):
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(index)
+        return _get_raw_stream(index) if _get_raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
-# Contiguous tensors on the current device, past torch's dispatcher: 2 us beside a launch where torch.empty takes 4 and
-# Tensor.new_empty 6.
+# Contiguous tensors on the current device, past torch's dispatcher where that is possible: 2 us beside a launch where
+# torch.empty takes 4 and Tensor.new_empty 6. Dispatch modes do not see them. Under deterministic algorithms torch fills
+# what it hands out with NaN; its public function does so here too.
+def _empty(shape, strides, dtype):
+    if _empty_strided_cuda is None or torch.are_deterministic_algorithms_enabled():
+        return torch.empty_strided(shape, strides, dtype=dtype, device="cuda")
+    return _empty_strided_cuda(shape, strides, dtype)
+
+
 def _empty4(a, b, c, d, dtype):
-    return _empty_strided_cuda((a, b, c, d), (b * c * d, c * d, d, 1), dtype)
+    return _empty((a, b, c, d), (b * c * d, c * d, d, 1), dtype)
 
 
 def _empty3(a, b, c, dtype):
-    return _empty_strided_cuda((a, b, c), (b * c, c, 1), dtype)
+    return _empty((a, b, c), (b * c, c, 1), dtype)
 
 
 def _empty_bytes(n):
-    return _empty_strided_cuda((n,), (1,), torch.uint8)
+    return _empty((n,), (1,), torch.uint8)
 
 
 def _check_tensor(name, t, dtype, shape, index):
