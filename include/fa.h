@@ -24,7 +24,8 @@
  *                  attention", section "Tile order and on-chip capacity").
  *                  Causal and mask combine additively when both are given.
  *   scale        : multiplies Q K^T (typically 1/sqrt(d)).
- * A query row whose every key is excluded gets out = 0 and lse = -inf.
+ * A query row whose every key is excluded gets out = 0 and lse = -inf. A row with a NaN score (a
+ * NaN in its query, or in a key that it sees) gets NaN, out and lse.
  *
  * Ownership: every pointer is caller-owned device memory. The library allocates
  * no device memory, keeps no per-call state and may be called from several

@@ -691,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_warp(sy.pv_done(t, (g - 1) & 1u), ((g - 1) >> 1) & 1u, abort_flag, p);
             if (!ok) break;
             tc_fence_after();
-            float inv = (l > 0.0f) ? 1.0f / l : 0.0f;
+            float inv = (l != 0.0f) ? 1.0f / l : 0.0f;  // (a sum that is NaN, from a NaN query, stays NaN)
             if constexpr (DROP) inv *= p.drop_scale;  // kept probabilities are scaled by 1 / q
             const size_t orow_idx = VARLEN ? ((size_t)(itm.tok0 + row) * p.H + (size_t)(bh % p.H))
                                            : ((size_t)bh * p.N + (size_t)row);
@@ -724,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             float *lse_out = CROSS && p.n_splits > 1 ? p.lse_part + (part - orow_idx) : p.lse;
             if (row < rows_end)  // lse: [B][H][N], or [H][total] for a packed batch
                 lse_out[VARLEN ? (size_t)(bh % p.H) * p.total + itm.tok0 + row : (size_t)bh * p.N + row] =
-                    (CROSS ? l != 0.0f : l > 0.0f) ? (m_ref + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
+                    (l != 0.0f) ? (m_ref + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
         }
     }
 

@@ -107,10 +107,11 @@ __global__ void __launch_bounds__(kThreadsF32) fa_fwd_fp32_kernel(const float *_
         float mb = x[0];
 #pragma unroll
         for (int j = 1; j < kKeys; ++j) mb = fmaxf(mb, x[j]);
-        const float m_new = fmaxf(m_run, mb);
-        if (m_new == -INFINITY) continue;  // nothing visible yet for this row
-        const float alpha = ex2_approx(m_run - m_new);  // 0 when m_run = -inf
-        m_run = m_new;
+        const float m_old = m_run;
+        m_run = fmaxf(m_run, mb);
+        // 0 in place of -inf while nothing is visible, or all that is is NaN: the weights are then 0, or NaN
+        const float m_new = m_run == -INFINITY ? 0.0f : m_run;
+        const float alpha = ex2_approx(m_old - m_new);  // 0 when m_old = -inf
         l *= alpha;
 #pragma unroll
         for (int c = 0; c < C4; ++c) {
@@ -134,12 +135,12 @@ __global__ void __launch_bounds__(kThreadsF32) fa_fwd_fp32_kernel(const float *_
         }
     }
     if (!row_ok) return;
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
+    const float inv = l != 0.f ? 1.0f / l : 0.f;
     float4 *orow = reinterpret_cast<float4 *>(out + head + (size_t)row * D);
 #pragma unroll
     for (int c = 0; c < C4; ++c)
         orow[4 * c + quad] = make_float4(o[c].x * inv, o[c].y * inv, o[c].z * inv, o[c].w * inv);
-    if (quad == 0) lse[(size_t)bh * N + row] = l > 0.f ? (m_run + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
+    if (quad == 0) lse[(size_t)bh * N + row] = l != 0.f ? (m_run + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
 }
 
 template <int D, bool CAUSAL, bool MASK>

@@ -878,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = wait_warp(sy.pv_done(t, gl & 1u), (gl >> 1) & 1u, abort_flag, p);
             if (!ok) break;
             tc_fence_after();
-            const float inv = (l > 0.0f) ? 1.0f / l : 0.0f;
+            const float inv = (l != 0.0f) ? 1.0f / l : 0.0f;  // (a sum that is NaN, from a NaN query, stays NaN)
             // [B][H][N][d] rows, or token-major [total][H][d] rows of a packed batch
             const size_t orow_idx = VARLEN ? ((size_t)(itm.tok0 + row) * p.H + (size_t)(bh % p.H))
                                            : ((size_t)bh * p.N + (size_t)row);
@@ -899,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (row < n)  // lse: [B][H][N], or [H][total] for a packed batch
                 p.lse[VARLEN ? (size_t)(bh % p.H) * p.total + itm.tok0 + row : (size_t)bh * p.N + row] =
-                    (l > 0.0f) ? (m_ref + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
+                    (l != 0.0f) ? (m_ref + lg2_approx(l)) * 0.6931471805599453f : -INFINITY;
         }
         if constexpr (HAS_MASK) {  // a mask copy still in flight (after a timeout) lands before the CTA exits
             if (mpending) {

@@ -135,6 +135,7 @@ __global__ void __launch_bounds__(kWarpsSK * 32) fa_splitkv_partial(const T *__r
             for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
                 for (int u = 0; u < kUnroll; ++u) s[u] += __shfl_xor_sync(0xffffffffu, s[u], off);
+            const float m_old = m[i];
             float mb = -INFINITY;
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
@@ -143,10 +144,10 @@ __global__ void __launch_bounds__(kWarpsSK * 32) fa_splitkv_partial(const T *__r
                 s[u] = ok ? s[u] * scale_log2 : -INFINITY;
                 mb = fmaxf(mb, s[u]);
             }
-            const float m_new = fmaxf(m[i], mb);
-            if (m_new == -INFINITY) continue;  // nothing visible yet for this row
-            const float corr = ex2_approx(m[i] - m_new);  // 0 when m was -inf
-            m[i] = m_new;
+            m[i] = fmaxf(m[i], mb);
+            // 0 in place of -inf while nothing is visible, or all that is is NaN: the weights are then 0, or NaN
+            const float m_new = m[i] == -INFINITY ? 0.f : m[i];
+            const float corr = ex2_approx(m_old - m_new);  // 0 when m was -inf
             l[i] *= corr;
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[i][e] *= corr;
@@ -177,18 +178,17 @@ __global__ void __launch_bounds__(kWarpsSK * 32) fa_splitkv_partial(const T *__r
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarpsSK; ++w) M = fmaxf(M, sm_m[w][i]);
+        if (M == -INFINITY) M = 0.f;  // nothing visible, or all that is is NaN: the sums say which
         float L = 0.f, A = 0.f;
-        if (M != -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < kWarpsSK; ++w) {
-                const float f = ex2_approx(sm_m[w][i] - M);  // 0 for an empty warp
-                L += f * sm_l[w][i];
-                A += f * sm_a[w][i][e];
-            }
+        for (int w = 0; w < kWarpsSK; ++w) {
+            const float f = ex2_approx(sm_m[w][i] - M);  // 0 for an empty warp
+            L += f * sm_l[w][i];
+            A += f * sm_a[w][i][e];
         }
         const size_t row = ((size_t)split * BH + bh) * Nq + i;
-        o_part[row * D + e] = L > 0.f ? A / L : 0.f;
-        if (e == 0) lse_part[row] = L > 0.f ? (M + lg2_approx(L)) * 0.6931471805599453f : -INFINITY;
+        o_part[row * D + e] = L == 0.f ? 0.f : A / L;
+        if (e == 0) lse_part[row] = L == 0.f ? -INFINITY : (M + lg2_approx(L)) * 0.6931471805599453f;
     }
 }
 
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kWarpsSK * 32) fa_splitkv_partial_mma(
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float mr = m[e >> 1];
-                pv[t][e] = mr == -INFINITY ? 0.f : ex2_approx(x[t][e] - mr);
+                pv[t][e] = ex2_approx(x[t][e] - (mr == -INFINITY ? 0.f : mr));  // 0 for a key that is not visible
             }
         l[0] += (pv[0][0] + pv[0][1]) + (pv[1][0] + pv[1][1]);
         l[1] += (pv[0][2] + pv[0][3]) + (pv[1][2] + pv[1][3]);
@@ -364,18 +364,17 @@ __global__ void __launch_bounds__(kWarpsSK * 32) fa_splitkv_partial_mma(
         float M = -INFINITY;
 #pragma unroll
         for (int w = 0; w < kWarpsSK; ++w) M = fmaxf(M, sm_m[w * 16 + i]);
+        if (M == -INFINITY) M = 0.f;  // nothing visible, or all that is is NaN: the sums say which
         float Lsum = 0.f, A = 0.f;
-        if (M != -INFINITY) {
 #pragma unroll
-            for (int w = 0; w < kWarpsSK; ++w) {
-                const float f = ex2_approx(sm_m[w * 16 + i] - M);  // 0 for a warp that saw nothing
-                Lsum += f * sm_l[w * 16 + i];
-                A += f * sm_o[((size_t)w * 16 + i) * D + e];
-            }
+        for (int w = 0; w < kWarpsSK; ++w) {
+            const float f = ex2_approx(sm_m[w * 16 + i] - M);  // 0 for a warp that saw nothing
+            Lsum += f * sm_l[w * 16 + i];
+            A += f * sm_o[((size_t)w * 16 + i) * D + e];
         }
         const size_t row = ((size_t)split * BH + bh) * Nq + i;
-        o_part[row * D + e] = Lsum > 0.f ? A / Lsum : 0.f;
-        if (e == 0) lse_part[row] = Lsum > 0.f ? (M + lg2_approx(Lsum)) * 0.6931471805599453f : -INFINITY;
+        o_part[row * D + e] = Lsum == 0.f ? 0.f : A / Lsum;
+        if (e == 0) lse_part[row] = Lsum == 0.f ? -INFINITY : (M + lg2_approx(Lsum)) * 0.6931471805599453f;
     }
 }
 
