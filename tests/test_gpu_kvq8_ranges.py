@@ -212,3 +212,54 @@ def test_read_under_scales_of_any_value(fa, fmt, dtype):
     want = np.ldexp(np.rint(m * 2.0 ** bits), e - bits)  # from 64 bits may go by way of 32)
     want = torch.from_numpy(np.repeat(want, page)).to(DT[dtype])[:, None, None].expand(-1, 1, d)
     assert torch.equal(k.cpu(), want) and torch.equal(v.cpu(), want)
+
+
+# ---------------------------------------------------------------- each status by itself
+BAD_PAGE = [([[0, 1], [2, 99]], [20, 20]), ([[0, 1], [-1, 3]], [20, 20])]
+BAD_LEN = [([[0, 1], [2, 3]], [20, 33]), ([[0, 1], [2, 3]], [20, -1])]
+
+
+@pytest.mark.parametrize("table,held,want", [
+    ([[0, 1], [2, 99]], [19, 19], "FA_ERR_PAGE"),
+    ([[0, 1], [-1, 3]], [19, 5], "FA_ERR_PAGE"),
+    ([[0, 1], [2, 3]], [19, 32], "FA_ERR_SEQLENS"),
+    ([[0, 1], [2, 3]], [-1, 19], "FA_ERR_SEQLENS"),
+    ([[0, 1], [99, 3]], [19, 19], "FA_OK"),  # an entry that the new token does not need
+])
+def test_append_reports_what_was_wrong(fa, table, held, want):
+    cache = fa.kv_cache_q8(4, 1, 16, 64, torch.int8, DEV)
+    x = torch.ones((2, 1, 64), dtype=torch.bfloat16, device=DEV)
+    fa.kvq8_append(cache, x, x, ints(table), ints([0, 1, 2]), ints(held), 1)
+    torch.cuda.synchronize()
+    assert fa.fa_get_device_status() == getattr(fa, want)
+    status_ok(fa)
+
+
+@pytest.mark.parametrize("table,lens", BAD_PAGE + BAD_LEN[:1])
+def test_read_reports_what_was_wrong(fa, table, lens):
+    cache = fa.kv_cache_q8(4, 1, 16, 64, torch.int8, DEV)
+    cu = [0, lens[0], lens[0] + lens[1]]
+    fa.kvq8_read(cache, ints(table), ints(cu), cu[-1], 40)
+    torch.cuda.synchronize()
+    want = fa.FA_ERR_PAGE if table in [t for t, _ in BAD_PAGE] else fa.FA_ERR_SEQLENS
+    assert fa.fa_get_device_status() == want
+    # more tokens than max_len, and a first position below 0
+    for first, most in ((None, 19), ([0, -1], 20)):
+        fa.kvq8_read(cache, ints([[0, 1], [2, 3]]), ints([0, 20, 40]), 40, most, None if first is None else ints(first))
+        torch.cuda.synchronize()
+        assert fa.fa_get_device_status() == fa.FA_ERR_SEQLENS
+    status_ok(fa)
+
+
+@pytest.mark.parametrize("n_parts", [0, 1, 2, 5])
+@pytest.mark.parametrize("table,lens", BAD_PAGE + BAD_LEN)
+def test_attention_reports_what_was_wrong(fa, table, lens, n_parts):
+    cache = fa.kv_cache_q8(4, 1, 16, 64, torch.int8, DEV)
+    q = torch.ones((2, 2, 1, 64), dtype=torch.bfloat16, device=DEV)
+    for H in (1, 2):
+        fa.attention_kvq8(q[:, :H].contiguous(), cache, ints(table), ints(lens), n_parts=n_parts)
+        torch.cuda.synchronize()
+        want = fa.FA_ERR_PAGE if table in [t for t, _ in BAD_PAGE] else fa.FA_ERR_SEQLENS
+        assert fa.fa_get_device_status() == want
+    fa.attention_kvq8(q, cache, ints([[0, 1], [2, 3]]), ints([20, 32]), n_parts=n_parts)
+    status_ok(fa)
