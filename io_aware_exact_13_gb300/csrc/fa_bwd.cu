@@ -1552,9 +1552,9 @@ int launch_bwd_variant(const BwdArgs &a) {
     p.scale = a.scale;
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     p.timeout_ns = a.timeout_ns;
-    p.sms = a.num_sms;
-    p.kv_cut = reinterpret_cast<int4 *>(a.kv_part);
-    p.kv_part = a.kv_part + bwd_cross_cut_bytes(a.num_sms) / sizeof(float);
+    p.sms = CROSS ? a.num_sms : 0;
+    p.kv_cut = CROSS ? reinterpret_cast<int4 *>(a.kv_part) : nullptr;
+    p.kv_part = CROSS ? a.kv_part + bwd_cross_cut_bytes(a.num_sms) / sizeof(float) : nullptr;
     int64_t grid = static_cast<int64_t>(BHkv) * (bwd_padded_rows(Nk) / kBlk), slots = 0;
     if (CROSS) {  // every item that key counts may give
         const int64_t n_it = bwd_cross_iters(p.group, a.N);
