@@ -223,7 +223,7 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *ou
 /* ---- 8-bit key/value cache ---------------------------------------------------
  * A paged cache of K and V in 8 bits with one scale for each page and head:
  *   k_codes, v_codes : [n_pages][Hkv][page][d] bytes (int8, or e4m3 as in torch.float8_e4m3fn)
- *   k_scale, v_scale : float [n_pages][Hkv], >= 0 and finite
+ *   k_scale, v_scale : float [n_pages][Hkv], >= 0 and finite (fa_kvq8_append writes powers of two; any is read)
  *   page_table       : int32 [nseq][max_pages]
  * Position t of sequence s is slot t % page of page page_table[s][t / page]; its values are
  * code * scale. page is 16, 32, 64 or 128, d 64 or 128, format FA_KVQ8_INT8 or FA_KVQ8_E4M3.
@@ -242,7 +242,9 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *ou
  * With QMAX = 127 (int8) or 448 (e4m3), a page's scale is the smallest power of two s in
  * [2^-110, 2^120] with |x| <= QMAX s for all its tokens, 0 while all are 0, and codes are x / s
  * rounded to nearest even, saturated. A page that held tokens before keeps its scale or, where
- * the new tokens need a larger one, takes that; then its earlier codes are rounded to it. A page
+ * the new tokens need a larger one, takes that; then its earlier codes are rounded to it. (Under powers
+ * of two all these roundings of a code come to less than one step; a page that came with another
+ * scale may lose up to half a step more when it first grows.) A page
  * that starts empty needs no initial scale. Slots past the last token are not touched. Infinite
  * and NaN values are written as 0 and record FA_ERR_VALUE. A page that takes tokens must belong
  * to one sequence only: a page shared by two that both append to it in one call (the same page
@@ -250,11 +252,14 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *ou
  *
  * fa_kvq8_read gives tokens back: positions first[s] .. first[s] + n - 1 (first NULL: 0), with
  * n = cu_seqlens[s+1] - cu_seqlens[s] <= max_len, as rows cu_seqlens[s] .. of k, v
- * [total][Hkv][d], code * scale rounded to the 16-bit type. Other rows are not touched.
+ * [total][Hkv][d], code * scale rounded once to the 16-bit type. Other rows are not touched. (These are
+ * rows as fa_fwd_varlen takes them, which has one cu_seqlens for queries and keys: it serves them
+ * together with the queries of all their tokens. More than 16 query rows over a cached prefix alone
+ * go through fa_fwd_kvq8 in pieces, the cache read once for each.)
  *
  * fa_fwd_kvq8 is the decoding forward over the cache: q, out [B][H][Nq][d], lse float [B][H][Nq],
  * 1 <= Nq <= 16, Hkv dividing H (heads shared as in fa_fwd_gqa). Sequence b attends to its first
- * kv_lens[b] positions, 0 <= kv_lens[b] <= max_len <= max_pages * page (max_len: host-side bound).
+ * kv_lens[b] positions, 0 <= kv_lens[b] <= max_len, 1 <= max_len <= max_pages * page (host-side bound).
  * causal != 0 aligns the last query with the last key: query i sees keys j <= i + kv_lens[b] - Nq.
  * A row that sees no key gets out = 0 and lse = -inf. Codes, scores, sums and accumulators are
  * not rounded below fp32; the softmax weights are rounded to fp16 before they multiply V. bf16
@@ -376,7 +381,10 @@ int fa_bwd_fp16(const void *q, const void *k, const void *v, const void *out, co
  * Backward: out and lse are the forward's; the workspace (256-byte aligned) has at least
  * fa_bwd_cross_workspace_bytes bytes, asked for with the device current that the call will run on.
  * dq is accumulated in fp32 in an order that varies from call to call; dk and dv do not vary.
- * Calls that share a workspace must not overlap on the GPU. Errors as for fa_fwd_gqa and fa_bwd. */
+ * Calls that share a workspace must not overlap on the GPU. Errors as for fa_fwd_gqa and fa_bwd.
+ * Scores, sums, accumulators and the summaries of runs are fp32. As in fa_fwd and fa_bwd the softmax
+ * weights P are rounded to the input type before P V and P^T dO, dS before dS K and dS^T Q, and every
+ * output once. */
 int fa_cross_num_splits(int B, int H, int Nq, int Nk);
 int fa_fwd_cross(const void *q, const void *k, const void *v, const int *kv_lens_or_null, void *out, float *lse, int B,
                  int H, int Hkv, int Nq, int Nk, int d, float scale, int n_splits, void *workspace,

@@ -37,8 +37,8 @@
 // Short contexts, and longer ones of few sequences, take a CTA or a cluster of CTAs per unit instead, in one launch: the
 // CTAs of a cluster merge through each other's shared memory (see kvq8_num_parts).
 //
-// Measured on one GB300 (copy rate 6.80 TB/s): B 64, H 64 / 8, d 128, e4m3, ragged up to 16384 keys 209 us (93 % of the
-// copy rate); B 16, H 32 / 8, d 128, int8, ragged up to 8192 keys 40 us (64 %); time is about bytes / rate + 14 us, of
+// Measured on one GB300 (copy rate 6.80 TB/s): B 64, H 64 / 8, d 128, e4m3, ragged up to 16384 keys 210 us (92 % of the
+// copy rate); B 16, H 32 / 8, d 128, int8, ragged up to 8192 keys 40 us (63 %); time is about bytes / rate + 14 us, of
 // which launch and lengths are 2.3 and the merge kernel 4.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -64,7 +64,9 @@ constexpr float kTau = 8.0f;  // log2 units by which a reference maximum may be 
 constexpr float kNone = -FLT_MAX;
 constexpr float kLn2 = 0.6931471805599453f;
 
-// Resident CTAs per SM that the kernel is compiled for: 128, 168 or 255 registers per thread.
+// Resident CTAs per SM that the kernel is compiled for: 128, 168 or 255 registers per thread. At d = 128 with one tile the
+// four CTAs' 128 registers leave 20 to 52 bytes spilled; three CTAs, without spills, are slower (B 64, H 64 / 8, up to 16384
+// keys 230 us against 210, B 16, H 32 / 8, up to 8192 keys 43.4 against 40.3).
 __host__ __device__ constexpr int q8_ctas(int D, int NT) { return NT == 1 ? 4 : NT == 2 && D == 64 ? 3 : 2; }
 
 template <int D, int NT>

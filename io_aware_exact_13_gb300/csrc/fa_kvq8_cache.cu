@@ -6,7 +6,8 @@
 // a code is x / s rounded to nearest even. A page that held tokens before the call keeps its
 // scale or, when the new tokens need a larger one, takes that and has its codes rounded to it:
 //     s = max(s_old, s_new),   c' = rne(c s_old / s),   c = rne(x / s).
-// (A page whose scale came from elsewhere keeps it while it is large enough; its codes are rounded once as well.)
+// (A page whose scale came from elsewhere keeps it while it is large enough; its codes are rounded once as well, and once
+// more when it first grows, by a factor that need not be two.)
 // Why powers of two: x / s and c s_old / s are then exact, so a code depends on the values alone
 // and not on how a division rounds; and a scale that grows at least doubles, so a code's
 // roundings in all of its page's growths add up to less than one step (1/2 + 1/4 + ...). With
@@ -257,6 +258,8 @@ struct ReadParams {
 };
 
 // Small CTAs again: 64 threads and 16 tokens 80.0 us, 128 and 32 82.9, 256 and 64 86.0 (87000 tokens, 8 heads, d 128).
+// (The first is 76.3 since scales that are no powers of two have a branch of their own; one sequence of 700 tokens is 2.03
+// instead of 1.93.)
 constexpr int kReadThreads = 64;
 constexpr int kReadTokens = 16;  // tokens per CTA: K and V of one head
 
