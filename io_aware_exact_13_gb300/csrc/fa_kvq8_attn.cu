@@ -536,7 +536,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
             for (int t = 0; t < NT; ++t) {
                 float f[2], s[4], w[4];
 #pragma unroll
-                for (int e = 0; e < 2; ++e)  // (a row that saw only pages of zeros has mw = kNone, and m - mw may be infinite)
+                for (int e = 0; e < 2; ++e)  // (a row that saw only pages of zeros has mw = kNone; m - mw may be infinite)
                     f[e] = lv == -INFINITY ? -INFINITY : fminf(lv + (m[t][e] - mw[t][e]), FLT_MAX);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -936,9 +936,10 @@ long long kvq8_tiles(int B, int Hkv, int rows, int max_len, int d) {
 
 // Parts 0, a cluster of CTAs for each unit and no merge kernel, while no warp has many tiles: 8, or more where the clusters
 // fill most of a wave, since the line then has little to spread (16; 12 with one CTA for a unit). Measured, cluster against
-// line: B 1, H 8, d 64: 500 keys 4.6 against 7.6 us, 4000 8.0 / 8.8, 8000 11.8 / 9.6. B 4, H 32 / 8, d 128: 1000 keys 7.5 /
-// 10.1, 4000 15.6 / 16.5, 8000 24.7 / 21.5. B 16, H 32 / 8, d 128: 500 keys 8.8 / 12.2, 2000 18.6 / 22.8, 4000 30.7 / 33.9,
-// ragged 27.1 / 27.4. B 32: 2000 30.8 / 33.9, ragged 27.0 / 26.4. B 64, one CTA: 600 21.0 / 25.1, 1000 ragged 26.4 / 26.6.
+// line, each case alone in its process (the first is 4.85 us among other work): B 1, H 8, d 64: 500 keys 4.6 against 7.6 us,
+// 4000 8.0 / 8.8, 8000 11.8 / 9.6. B 4, H 32 / 8, d 128: 1000 keys 7.5 / 10.1, 4000 15.6 / 16.5, 8000 24.7 / 21.5. B 16,
+// H 32 / 8, d 128: 500 keys 8.8 / 12.2, 2000 18.6 / 22.8, 4000 30.7 / 33.9, ragged 27.1 / 27.4. B 32: 2000 30.8 / 33.9,
+// ragged 27.0 / 26.4. B 64, one CTA: 600 21.0 / 25.1, 1000 ragged 26.4 / 26.6.
 // Otherwise one part for each CTA that can be resident, and at least one tile for each of a CTA's warps.
 int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int d, int num_sms) {
     const int nt = tiles_per_unit(rows, d), tiles = q8_tiles(max_len);
