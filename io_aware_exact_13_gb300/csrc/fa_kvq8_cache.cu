@@ -89,7 +89,7 @@ struct AppendParams {
 // read once into registers (VEC 16-byte vectors per thread hold the whole page), the page's largest magnitude is
 // reduced over the CTA, and the codes are written as 8-byte vectors.
 template <typename T, int FMT, int NT, int VEC, int KVS>
-__global__ void __launch_bounds__(NT, KVS == 1 ? 1024 / NT : 1) fa_kvq8_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(NT, KVS == 1 ? 1024 / NT : 28) fa_kvq8_append_kernel(const AppendParams p) {
     __shared__ uint32_t warp_max[NT / 32];
     uint32_t u = blockIdx.x;
     const int kv0 = KVS == 2 ? 0 : u & 1u;
@@ -380,7 +380,8 @@ int launch_append_t(const Kvq8AppendArgs &a) {
     const unsigned g = static_cast<unsigned>(grid);
     // Eight vectors per thread (a warp at least): small CTAs keep more of them, and of their dependent first reads (lengths,
     // page), on an SM. With 128 or 256 threads for every page size, pages of 16 tokens took 86 us instead of 72, of 64
-    // tokens 77 instead of 65 (74000 tokens, 8 heads, d 128). At 16 tokens of d 64 a warp takes K and V: 36 us instead of 53.
+    // tokens 77 instead of 65 (74000 tokens, 8 heads, d 128). At 16 tokens of d 64 a warp takes K and V: 36 us instead of 53
+    // (e4m3; 35.0 with 28 CTAs an SM asked for, 38.3 at the 77 registers that the branch for other scales would take).
     switch (vecs) {
         case 128: fa_kvq8_append_kernel<T, FMT, 32, 4, 2><<<g, 32, 0, a.stream>>>(p); break;
         case 256: fa_kvq8_append_kernel<T, FMT, 32, 8, 1><<<g, 32, 0, a.stream>>>(p); break;
