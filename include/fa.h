@@ -242,9 +242,10 @@ int fa_fwd_splitkv_noalloc(const void *q, const void *k, const void *v, void *ou
  * With QMAX = 127 (int8) or 448 (e4m3), a page's scale is the smallest power of two s in
  * [2^-110, 2^120] with |x| <= QMAX s for all its tokens, 0 while all are 0, and codes are x / s
  * rounded to nearest even, saturated. A page that held tokens before keeps its scale or, where
- * the new tokens need a larger one, takes that; then its earlier codes are rounded to it. (Under powers
- * of two all these roundings of a code come to less than one step; a page that came with another
- * scale may lose up to half a step more when it first grows.) A page
+ * the new tokens need a larger one, takes that; then its earlier codes are rounded to it. (All the
+ * roundings of an int8 code come to less than one step. An e4m3 code loses only below its smallest
+ * normal number when its scale grows by a power of two, and up to half a step more when the page came
+ * with a scale that is none.) A page
  * that starts empty needs no initial scale. Slots past the last token are not touched. Infinite
  * and NaN values are written as 0 and record FA_ERR_VALUE. A page that takes tokens must belong
  * to one sequence only: a page shared by two that both append to it in one call (the same page

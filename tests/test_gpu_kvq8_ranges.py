@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import kvq8_ref as ref
-from test_gpu_kvq8 import CODE, DEV, DT, as_ref, check_attention, check_cache, filled, ints, numbers, random_table, status_ok
+from test_gpu_kvq8 import CODE, DEV, DT, as_ref, check_attention, check_cache, filled, ints, random_table, status_ok
 
 pytestmark = pytest.mark.gpu
 
