@@ -313,6 +313,62 @@ int fa_fwd_kvq8_fp16(const void *q, const void *k_codes, const void *v_codes, co
                      int format, float scale, int causal, int n_parts, void *workspace,
                      unsigned long long workspace_bytes, void *stream);
 
+/* ---- weights and eviction of the 8-bit cache -------------------------------------
+ * Under a memory budget the keys that a model has paid least attention to are given up.
+ *
+ * fa_kvq8_weights adds to weight[b][h][j], float [B][Hkv][max_pages * page] in DEVICE memory, 16-byte aligned, the
+ * softmax weight that key j of sequence b received from the query rows that share K/V head h:
+ *   sum over those rows i that see key j of exp(scale q_i . k_j - lse_i)
+ * with q [B][H][Nq][d] and lse [B][H][Nq] as fa_fwd_kvq8 takes and left them, and the same kv_lens, max_len and causal.
+ * Rows with lse = -inf add nothing. (lse may be over more keys than these, as that of fa_fwd_kvq8_prefix.) Weights
+ * of positions that a sequence does not hold are not touched, nor those on bad pages. Sums are fp32 and do not
+ * depend on timing. v_codes and v_scale are not needed.
+ *
+ * fa_kvq8_evict cuts every sequence of n = kv_lens[s] > keep tokens down to keep. Each K/V head keeps the last `recent`
+ * positions (0 <= recent <= keep) and, of those before, the keep - recent of the greatest weight; of equal weights the
+ * lower position, and NaN counts as the greatest. The kept tokens move, in order, to positions 0 .. keep - 1 of the
+ * sequence's pages, in place. A page whose tokens all stay where they are is not touched; any other page gets the scale that
+ * fa_kvq8_append of its tokens would give an empty page, and codes rounded to it once. Slots past the last token are
+ * not touched. Sequences of at most keep tokens stay as they are. Written besides:
+ *   lens_out   int32 [nseq]: the new lengths, min(n, keep)
+ *   kept       int32 [nseq][Hkv][keep]: the old position of each token kept, then -1
+ *   weight_out float like weight: the weights of the tokens kept, then 0 up to the row's end
+ * weight and kv_lens are not changed; none of the outputs may overlap an input (FA_ERR_ARG). A length out of range counts as 0
+ * (FA_ERR_SEQLENS). Tokens from a bad page become zeros, those for a bad page are lost (FA_ERR_PAGE). Pages must belong
+ * to one sequence only where it is cut down: a page that another sequence holds as well, or a table holds
+ * twice, gets undefined contents. Other errors as for fa_kvq8_append; FA_ERR_ARG for keep < 1 or recent out of range. */
+int fa_kvq8_weights(const void *q, const void *k_codes, const float *k_scale, const int *page_table, int n_pages,
+                    int max_pages, int page, const int *kv_lens, const float *lse, float *weight, int B, int H, int Hkv,
+                    int Nq, int max_len, int d, int format, float scale, int causal, void *stream);
+int fa_kvq8_weights_fp16(const void *q, const void *k_codes, const float *k_scale, const int *page_table, int n_pages,
+                         int max_pages, int page, const int *kv_lens, const float *lse, float *weight, int B, int H,
+                         int Hkv, int Nq, int max_len, int d, int format, float scale, int causal, void *stream);
+int fa_kvq8_evict(void *k_codes, void *v_codes, float *k_scale, float *v_scale, const int *page_table, int n_pages,
+                  int max_pages, int page, const int *kv_lens, const float *weight, int keep, int recent, int *lens_out,
+                  int *kept, float *weight_out, int nseq, int Hkv, int d, int format, void *stream);
+
+/* ---- rotary positions of several axes ----------------------------------------------
+ * Queries and keys turned by angles that go by each token's position along its axes (one axis for text; time, height and
+ * width for images and video), before any of the forwards or fa_kvq8_append; inverse != 0 turns back, which is the
+ * gradient. For pair i of a row, dims i and pairs + i, with a = positions[axis[i]][b][n] * inv_freq[i]:
+ *   y_i = x_i cos a - x_{pairs+i} sin a,   y_{pairs+i} = x_i sin a + x_{pairs+i} cos a;
+ * dims from 2 pairs on pass through. pairs is a multiple of 8, at most d / 2.
+ *   q, q_out : [B][Hq][N][d], k, k_out : [B][Hk][N][d] by q_strides, k_strides: HOST arrays of six element strides, those
+ *              of b, n and h of the input, then of the output, multiples of 8; a row's d values are contiguous.
+ *              (Packed tokens [total][H][d] are B = 1, N = total.) Hk = 0: no k. An output may be its input, with the
+ *              same strides, and must not overlap any tensor otherwise.
+ *   positions: int32 [n_axes][B][N] in DEVICE memory, of either sign, 1 <= n_axes <= 8
+ *   inv_freq, axis: HOST arrays of `pairs` frequencies (finite) and axes (0 <= axis < n_axes), read during the call
+ * Angles are formed modulo a turn in 64-bit integers (off by less than 2^-23 turns at any position for frequencies up to
+ * 1, by no more than fp32's rounding at positions below 2^20); products and sums are fp32, results rounded once. Errors as for fa_fwd; FA_ERR_SHAPE for strides or pairs, FA_ERR_ARG for
+ * axes and frequencies. */
+int fa_rotary(const void *q, void *q_out, const long long *q_strides, int Hq, const void *k, void *k_out,
+              const long long *k_strides, int Hk, const int *positions, int n_axes, const double *inv_freq,
+              const int *axis, int pairs, int B, int N, int d, int inverse, void *stream);
+int fa_rotary_fp16(const void *q, void *q_out, const long long *q_strides, int Hq, const void *k, void *k_out,
+                   const long long *k_strides, int Hk, const int *positions, int n_axes, const double *inv_freq,
+                   const int *axis, int pairs, int B, int N, int d, int inverse, void *stream);
+
 /* ---- packed variable-length batch ------------------------------------------
  * The same attention for nseq independent sequences packed back to back
  * ("IO-aware exact attention", section "Tile order and on-chip capacity":

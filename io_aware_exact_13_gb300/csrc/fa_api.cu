@@ -16,6 +16,7 @@
 #include "fa_launch.cuh"
 #include "fa_bwd.cuh"
 #include "fa_kvq8.cuh"
+#include "fa_rotary.cuh"
 #include "fa_splitkv.cuh"
 
 namespace fa {
@@ -517,6 +518,86 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     return fa::launch_kvq8_attention(a, fp16);
 }
 
+int kvq8_weights_common(bool fp16, const void *q, const void *k_codes, const float *k_scale, const int *page_table,
+                        int n_pages, int max_pages, int page, const int *kv_lens, const float *lse, float *weight, int B,
+                        int H, int Hkv, int Nq, int max_len, int d, int format, float scale, int causal, void *stream) {
+    if (!q || !kv_lens || !lse || !weight) return FA_ERR_NULL;
+    int rc = check_kvq8_cache(k_codes, k_codes, k_scale, k_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    if (rc != FA_OK) return rc;
+    if (!aligned(q, 16) || !aligned(kv_lens, 4) || !aligned(lse, 4) || !aligned(weight, 16)) return FA_ERR_ALIGN;
+    if (B < 1 || !kvq8_rows_ok(B, H, Hkv, Nq)) return FA_ERR_SHAPE;
+    if (max_len < 1 || max_len > static_cast<int64_t>(max_pages) * page) return FA_ERR_SHAPE;
+    if (fa::kvq8_tiles(B, Hkv, H / Hkv * Nq, max_len, d) > kKvq8MaxTiles) return FA_ERR_SHAPE;
+    DeviceInfo *di = device_info();
+    if (!di) return FA_ERR_LAUNCH;
+    fa::Kvq8WeightsArgs a;
+    a.c = kvq8_cache(k_codes, nullptr, k_scale, nullptr, page_table, n_pages, max_pages, page, Hkv, d, format);
+    a.q = q;
+    a.lse = lse;
+    a.weight = weight;
+    a.kv_lens = kv_lens;
+    a.B = B;
+    a.H = H;
+    a.Nq = Nq;
+    a.max_len = max_len;
+    a.scale = scale;
+    a.causal = causal ? 1 : 0;
+    a.status = di->status;
+    a.stream = static_cast<cudaStream_t>(stream);
+    log_call("8-bit cache weights %s format=%d page=%d d=%d causal=%d B=%d H=%d Hkv=%d Nq=%d max_len=%d",
+             fp16 ? "fp16" : "bf16", format, page, d, a.causal, B, H, Hkv, Nq, max_len);
+    return fa::launch_kvq8_weights(a, fp16);
+}
+
+bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
+// Strides of one tensor of fa_rotary: input b, n, h, output b, n, h, in elements; whole 16-byte rows.
+bool rotary_tensor(const void *in, void *out, const long long *s, int heads, fa::RotaryTensor *t) {
+    for (int i = 0; i < 6; ++i)
+        if (s[i] % 8) return false;
+    *t = {in, out, s[0], s[1], s[2], s[3], s[4], s[5], heads};
+    return true;
+}
+
+int rotary_common(bool fp16, const void *q, void *q_out, const long long *q_strides, int Hq, const void *k, void *k_out,
+                  const long long *k_strides, int Hk, const int *positions, int n_axes, const double *inv_freq,
+                  const int *axis, int pairs, int B, int N, int d, int inverse, void *stream) {
+    if (!q || !q_out || !q_strides || !positions || !inv_freq || !axis) return FA_ERR_NULL;
+    if (Hk != 0 && (!k || !k_out || !k_strides)) return FA_ERR_NULL;
+    if (!aligned(q, 16) || !aligned(q_out, 16) || !aligned(positions, 4)) return FA_ERR_ALIGN;
+    if (Hk != 0 && (!aligned(k, 16) || !aligned(k_out, 16))) return FA_ERR_ALIGN;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    if (B < 1 || N < 1 || Hq < 1 || Hk < 0 || static_cast<int64_t>(B) * N > INT32_MAX || Hq > (1 << 20) || Hk > (1 << 20))
+        return FA_ERR_SHAPE;
+    if (pairs < 8 || pairs > d / 2 || pairs % 8 != 0) return FA_ERR_SHAPE;
+    if (n_axes < 1 || n_axes > fa::kRotaryMaxAxes) return FA_ERR_ARG;
+    fa::RotaryArgs a;
+    a.x[1] = {nullptr, nullptr, 0, 0, 0, 0, 0, 0, 0};
+    if (!rotary_tensor(q, q_out, q_strides, Hq, &a.x[0]) || (Hk != 0 && !rotary_tensor(k, k_out, k_strides, Hk, &a.x[1])))
+        return FA_ERR_SHAPE;
+    for (int i = 0; i < pairs; ++i) {
+        if (!std::isfinite(inv_freq[i]) || axis[i] < 0 || axis[i] >= n_axes) return FA_ERR_ARG;
+        // the fraction of a turn in 2^-64; a negative frequency is the complement of its magnitude's
+        const double f = std::fmod(std::fabs(inv_freq[i]) / 6.283185307179586476925286766559, 1.0);
+        const uint64_t t = static_cast<uint64_t>(std::ldexp(f, 64));  // f < 1
+        a.turns[i] = inv_freq[i] < 0 ? 0 - t : t;
+        a.axis[i] = static_cast<uint8_t>(axis[i]);
+    }
+    a.positions = positions;
+    a.pairs = pairs;
+    a.B = B;
+    a.N = N;
+    a.d = d;
+    a.inverse = inverse ? 1 : 0;
+    a.stream = static_cast<cudaStream_t>(stream);
+    log_call("rotary %s d=%d pairs=%d axes=%d inverse=%d B=%d N=%d Hq=%d Hk=%d", fp16 ? "fp16" : "bf16", d, pairs, n_axes,
+             a.inverse, B, N, Hq, Hk);
+    return fa::launch_rotary(a, fp16);
+}
+
 // Splits of each work unit's keys for the forward over keys of another length: with fewer units (256 query rows of a
 // head) than half the SMs, as many as fill the GPU once, each of at least two 128-key blocks (a split costs a launch and
 // about 3 us of start and merge, a block 0.5 us).
@@ -944,6 +1025,69 @@ int fa_fwd_kvq8_fp16(FA_KVQ8_ARGS) {
                             workspace_bytes, stream);
 }
 #undef FA_KVQ8_ARGS
+
+#define FA_WEIGHTS_ARGS                                                                                                \
+    const void *q, const void *k_codes, const float *k_scale, const int *page_table, int n_pages, int max_pages,       \
+        int page, const int *kv_lens, const float *lse, float *weight, int B, int H, int Hkv, int Nq, int max_len,     \
+        int d, int format, float scale, int causal, void *stream
+int fa_kvq8_weights(FA_WEIGHTS_ARGS) {
+    return kvq8_weights_common(false, q, k_codes, k_scale, page_table, n_pages, max_pages, page, kv_lens, lse, weight, B,
+                               H, Hkv, Nq, max_len, d, format, scale, causal, stream);
+}
+int fa_kvq8_weights_fp16(FA_WEIGHTS_ARGS) {
+    return kvq8_weights_common(true, q, k_codes, k_scale, page_table, n_pages, max_pages, page, kv_lens, lse, weight, B,
+                               H, Hkv, Nq, max_len, d, format, scale, causal, stream);
+}
+#undef FA_WEIGHTS_ARGS
+
+int fa_kvq8_evict(void *k_codes, void *v_codes, float *k_scale, float *v_scale, const int *page_table, int n_pages,
+                  int max_pages, int page, const int *kv_lens, const float *weight, int keep, int recent, int *lens_out,
+                  int *kept, float *weight_out, int nseq, int Hkv, int d, int format, void *stream) {
+    if (!kv_lens || !weight || !lens_out || !kept || !weight_out) return FA_ERR_NULL;
+    int rc = check_kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    if (rc != FA_OK) return rc;
+    if (!aligned(kv_lens, 4) || !aligned(weight, 16) || !aligned(lens_out, 4) || !aligned(kept, 4) ||
+        !aligned(weight_out, 16))
+        return FA_ERR_ALIGN;
+    if (nseq < 1 || static_cast<int64_t>(nseq) * Hkv > INT32_MAX / 2) return FA_ERR_SHAPE;
+    if (keep < 1 || keep > kKvq8MaxLen || recent < 0 || recent > keep) return FA_ERR_ARG;
+    const uint64_t heads = static_cast<uint64_t>(nseq) * Hkv, weights = heads * max_pages * page * 4;
+    if (overlap(weight, weights, weight_out, weights) || overlap(weight, weights, kept, heads * keep * 4) ||
+        overlap(weight_out, weights, kept, heads * keep * 4) || overlap(kv_lens, nseq * 4ull, lens_out, nseq * 4ull))
+        return FA_ERR_ARG;
+    DeviceInfo *di = device_info();
+    if (!di) return FA_ERR_LAUNCH;
+    fa::Kvq8EvictArgs a;
+    a.c = kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    a.kv_lens = kv_lens;
+    a.weight = weight;
+    a.weight_out = weight_out;
+    a.lens_out = lens_out;
+    a.kept = kept;
+    a.nseq = nseq;
+    a.keep = keep;
+    a.recent = recent;
+    a.num_sms = di->num_sms;
+    a.status = di->status;
+    a.stream = static_cast<cudaStream_t>(stream);
+    log_call("8-bit cache eviction format=%d page=%d d=%d nseq=%d Hkv=%d keep=%d recent=%d", format, page, d, nseq, Hkv,
+             keep, recent);
+    return fa::launch_kvq8_evict(a);
+}
+
+#define FA_ROTARY_ARGS                                                                                                 \
+    const void *q, void *q_out, const long long *q_strides, int Hq, const void *k, void *k_out,                        \
+        const long long *k_strides, int Hk, const int *positions, int n_axes, const double *inv_freq, const int *axis, \
+        int pairs, int B, int N, int d, int inverse, void *stream
+int fa_rotary(FA_ROTARY_ARGS) {
+    return rotary_common(false, q, q_out, q_strides, Hq, k, k_out, k_strides, Hk, positions, n_axes, inv_freq, axis,
+                         pairs, B, N, d, inverse, stream);
+}
+int fa_rotary_fp16(FA_ROTARY_ARGS) {
+    return rotary_common(true, q, q_out, q_strides, Hq, k, k_out, k_strides, Hk, positions, n_axes, inv_freq, axis,
+                         pairs, B, N, d, inverse, stream);
+}
+#undef FA_ROTARY_ARGS
 
 int fa_fwd_varlen(const void *q, const void *k, const void *v, void *out, float *lse, const int *cu_seqlens,
                   int nseq, int total, int max_seqlen, int H, int Hkv, int d, float scale, int causal, void *stream) {

@@ -1,11 +1,12 @@
 // fa_kvq8.cuh -- the 8-bit key/value cache: its layout, host-side arguments, and the
-// device helpers its three kernels (append, read, attention) share.
+// device helpers its kernels (append, read, attention, weights, eviction) share.
 //
 // A cache is n_pages pages of `page` tokens (16, 32, 64 or 128). Codes are
 // [n_pages][Hkv][page][d] bytes, scales [n_pages][Hkv] floats, K and V apart; a value is
 // code * scale. Sequence s keeps position t in page page_table[s][t / page], slot t % page.
 #pragma once
 #include <cuda_fp16.h>
+#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -57,14 +58,46 @@ struct Kvq8AttnArgs {
     cudaStream_t stream;
 };
 
+struct Kvq8WeightsArgs {
+    Kvq8Cache c;
+    const void *q;
+    const float *lse;
+    float *weight;  // [B][Hkv][max_pages * page]
+    const int *kv_lens;
+    int B, H, Nq, max_len;
+    float scale;
+    int causal;
+    int *status;
+    cudaStream_t stream;
+};
+
+struct Kvq8EvictArgs {
+    Kvq8Cache c;
+    const int *kv_lens;
+    const float *weight;  // [nseq][Hkv][max_pages * page]
+    float *weight_out;    // the same shape
+    int *lens_out, *kept;  // [nseq], [nseq][Hkv][keep]
+    int nseq, keep, recent, num_sms;
+    int *status;
+    cudaStream_t stream;
+};
+
 int launch_kvq8_append(const Kvq8AppendArgs &a, bool fp16);
 int launch_kvq8_read(const Kvq8ReadArgs &a, bool fp16);
 int launch_kvq8_attention(const Kvq8AttnArgs &a, bool fp16);
+int launch_kvq8_weights(const Kvq8WeightsArgs &a, bool fp16);
+int launch_kvq8_evict(const Kvq8EvictArgs &a);
 // 16-key tiles of B sequences of max_len keys, over K/V heads and tiles of the `rows` = (H / Hkv) * Nq query rows
 // that share one; a part count for them, and the workspace that it takes.
 long long kvq8_tiles(int B, int Hkv, int rows, int max_len, int d);
 int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int d, int num_sms);
 size_t kvq8_workspace_bytes(int rows, int d, int parts);
+
+inline int kvq8_page_shift(int page) {
+    int s = 0;
+    while ((1 << s) < page) ++s;
+    return s;
+}
 
 // Scales that are no powers of two (append writes none, but a cache may come from elsewhere): a product or quotient with
 // one is rounded to fp32 before it is rounded to a code or to 16 bits, and twice is not once: what fp32 rounds to the
@@ -108,6 +141,32 @@ template <int FMT>
 __device__ __forceinline__ void codes_to_half2(uint32_t w, uint32_t &lo, uint32_t &hi) {
     if constexpr (FMT == kKvq8Int8) int8x4_to_half2(w, lo, hi);
     else e4m3x4_to_half2(w, lo, hi);
+}
+
+// Four values already divided by the scale -> four codes, rounded to nearest even and saturated.
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+    if constexpr (FMT == kKvq8Int8) {
+        // adding 1.5 * 2^23 leaves the rounded integer in the low bits
+        auto code = [](float x) { return __float_as_uint(fminf(fmaxf(x, -127.0f), 127.0f) + 12582912.0f); };
+        return __byte_perm(__byte_perm(code(a), code(b), 0x0040), __byte_perm(code(c), code(d), 0x0040), 0x5410);
+    } else {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    }
+}
+
+// Smallest power of two s with a <= QMAX s, from the bits of a > 0 (QMAX = 1.984375 * 2^6 or
+// 1.75 * 2^8: one more when a's mantissa is above QMAX's); 0 for a = 0.
+template <int FMT>
+__device__ __forceinline__ float scale_for(float a) {
+    if (a == 0.0f) return 0.0f;
+    const uint32_t bits = __float_as_uint(a);
+    const uint32_t over = (bits & 0x7FFFFFu) > (FMT == kKvq8Int8 ? 0x7E0000u : 0x600000u) ? 1u : 0u;
+    int e = (int)(bits >> 23) - 127 + (int)over - (FMT == kKvq8Int8 ? 6 : 8);
+    e = min(max(e, -110), 120);
+    return __uint_as_float((uint32_t)(e + 127) << 23);
 }
 
 }  // namespace fa

@@ -19,7 +19,6 @@
 // Both are bound by HBM: 2 bytes + 1 byte per value.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -47,32 +46,6 @@ __device__ __forceinline__ uint32_t pack2h(float lo, float hi) {
 }
 template <typename T>
 constexpr uint32_t exponent_mask() { return std::is_same<T, __nv_bfloat16>::value ? 0x7F80u : 0x7C00u; }
-
-// Four values already divided by the scale -> four codes, rounded to nearest even and saturated.
-template <int FMT>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
-    if constexpr (FMT == kKvq8Int8) {
-        // adding 1.5 * 2^23 leaves the rounded integer in the low bits
-        auto code = [](float x) { return __float_as_uint(fminf(fmaxf(x, -127.0f), 127.0f) + 12582912.0f); };
-        return __byte_perm(__byte_perm(code(a), code(b), 0x0040), __byte_perm(code(c), code(d), 0x0040), 0x5410);
-    } else {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-        return lo | (hi << 16);
-    }
-}
-
-// Smallest power of two s with a <= QMAX s, from the bits of a > 0 (QMAX = 1.984375 * 2^6 or
-// 1.75 * 2^8: one more when a's mantissa is above QMAX's); 0 for a = 0.
-template <int FMT>
-__device__ __forceinline__ float scale_for(float a) {
-    if (a == 0.0f) return 0.0f;
-    const uint32_t bits = __float_as_uint(a);
-    const uint32_t over = (bits & 0x7FFFFFu) > (FMT == kKvq8Int8 ? 0x7E0000u : 0x600000u) ? 1u : 0u;
-    int e = (int)(bits >> 23) - 127 + (int)over - (FMT == kKvq8Int8 ? 6 : 8);
-    e = min(max(e, -110), 120);
-    return __uint_as_float((uint32_t)(e + 127) << 23);
-}
 
 struct AppendParams {
     const void *src[2];

@@ -118,6 +118,12 @@ for _suffix in ("", "_fp16"):
                                             [ctypes.c_float, ctypes.c_int, _vp, ctypes.c_ulonglong, _vp])
     SIGNATURES["fa_bwd_cross" + _suffix] = (ctypes.c_int, [_vp] * 10 + [ctypes.c_int] * 6 +
                                             [ctypes.c_float, _vp, ctypes.c_ulonglong, _vp])
+    SIGNATURES["fa_kvq8_weights" + _suffix] = (ctypes.c_int, [_vp] * 4 + [ctypes.c_int] * 3 + [_vp] * 3 + [ctypes.c_int] * 7 +
+                                               [ctypes.c_float, ctypes.c_int, _vp])
+    SIGNATURES["fa_rotary" + _suffix] = (ctypes.c_int, [_vp] * 3 + [ctypes.c_int] + [_vp] * 3 + [ctypes.c_int, _vp, ctypes.c_int] +
+                                         [_vp] * 2 + [ctypes.c_int] * 5 + [_vp])
+SIGNATURES["fa_kvq8_evict"] = (ctypes.c_int, [_vp] * 5 + [ctypes.c_int] * 3 + [_vp] * 2 + [ctypes.c_int] * 2 + [_vp] * 3 +
+                               [ctypes.c_int] * 4 + [_vp])
 for _name, (_res, _args) in SIGNATURES.items():
     _f = getattr(lib, _name)
     _f.restype = _res
@@ -701,6 +707,158 @@ def attention_kvq8(q, cache, page_table, kv_lens, scale=None, causal=False, max_
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
     return _raw_kvq8("fa_fwd_kvq8" + suffix, q.dtype, q, cache, page_table, kv_lens, None, None, scale, causal, max_len,
                      n_parts, None, stream)
+
+
+# ---------------------------------------------------------------- weights and eviction of the 8-bit cache
+def kvq8_weights(q, cache, page_table, kv_lens, lse, weight, scale=None, causal=False, max_len=None, stream=None):
+    """Add to ``weight`` [B, Hkv, max_pages * page] (float32, in place) the softmax weight that each cached key received
+    from the query rows ``q`` [B, H, Nq, d] that share its head; ``lse`` [B, H, Nq] as the attention gave it."""
+    index, fmt, (n_pages, Hkv, page, d), (nseq, max_pages), ptrs = _check_kvq8(cache, page_table)
+    shape, dtype = q.shape, q.dtype
+    suffix = _FP16_SUFFIX.get(dtype)
+    if suffix is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if len(shape) != 4:
+        raise ValueError("q must be [B, H, Nq, d]")
+    B, H, Nq, dq = shape
+    if dq != d or H % Hkv or nseq != B:
+        raise ValueError("q: [B, H, Nq, d] with the cache's d, its Hkv dividing H and one page table row per b")
+    _check_tensor("q", q, dtype, shape, index)
+    _check_tensor("kv_lens", kv_lens, _I32, (B,), index)
+    _check_tensor("lse", lse, _F32, (B, H, Nq), index)
+    _check_tensor("weight", weight, _F32, (B, Hkv, max_pages * page), index)
+    scale = 1.0 / math.sqrt(d) if scale is None else scale
+    max_len = max_pages * page if max_len is None else int(max_len)
+    name = "fa_kvq8_weights" + suffix
+    with _on(index, stream):
+        rc = getattr(lib, name)(q.data_ptr(), ptrs[0], ptrs[2], ptrs[4], n_pages, max_pages, page, kv_lens.data_ptr(),
+                                lse.data_ptr(), weight.data_ptr(), B, H, Hkv, Nq, max_len, d, fmt, float(scale),
+                                bool(causal), _raw_stream(index, stream))
+    if rc != FA_OK:
+        raise FAError(rc, name)
+
+
+def kvq8_evict(cache, page_table, kv_lens, weight, keep, recent, lens_out=None, kept=None, weight_out=None, stream=None):
+    """Cut sequences of more than ``keep`` cached tokens down to ``keep``: each head's last ``recent`` and those of the
+    greatest ``weight`` [nseq, Hkv, max_pages * page] move to the front of the sequence's pages, in place. Returns
+    (new lengths [nseq], old positions of the tokens kept [nseq, Hkv, keep] then -1, their weights [like weight] then 0),
+    allocated unless given; ``weight`` and ``kv_lens`` are left as they are."""
+    index, fmt, (n_pages, Hkv, page, d), (nseq, max_pages), ptrs = _check_kvq8(cache, page_table)
+    keep, recent = int(keep), int(recent)
+    wide = (nseq, Hkv, max_pages * page)
+    _check_tensor("kv_lens", kv_lens, _I32, (nseq,), index)
+    _check_tensor("weight", weight, _F32, wide, index)
+    if keep < 1 or not 0 <= recent <= keep:
+        raise FAError(FA_ERR_ARG, "fa_kvq8_evict")
+    with _on(index, stream):
+        lens_out = _empty((nseq,), (1,), _I32) if lens_out is None else lens_out
+        kept = _empty3(nseq, Hkv, keep, _I32) if kept is None else kept
+        weight_out = _empty3(*wide, _F32) if weight_out is None else weight_out
+        _check_tensor("lens_out", lens_out, _I32, (nseq,), index)
+        _check_tensor("kept", kept, _I32, (nseq, Hkv, keep), index)
+        _check_tensor("weight_out", weight_out, _F32, wide, index)
+        rc = lib.fa_kvq8_evict(*ptrs, n_pages, max_pages, page, kv_lens.data_ptr(), weight.data_ptr(), keep, recent,
+                               lens_out.data_ptr(), kept.data_ptr(), weight_out.data_ptr(), nseq, Hkv, d, fmt,
+                               _raw_stream(index, stream))
+    if rc != FA_OK:
+        raise FAError(rc, "fa_kvq8_evict")
+    return lens_out, kept, weight_out
+
+
+# ---------------------------------------------------------------- rotary positions of several axes
+def rotary_frequencies(pairs, sections=None, theta=10000.0, interleaved=False):
+    """(inv_freq, axis) for ``rotary``: CPU tensors of ``pairs`` frequencies theta^(-i / pairs) and of the axis that each
+    pair's angle goes by. ``sections`` counts the pairs of each axis (they add up to ``pairs``; None: one axis); with
+    ``interleaved`` the axes take pairs in turn while they have any left, otherwise one axis after the other."""
+    sections = [pairs] if sections is None else [int(n) for n in sections]
+    if pairs < 1 or min(sections) < 0 or sum(sections) != pairs:
+        raise ValueError(f"sections must count {pairs} pairs")
+    inv = torch.tensor([float(theta) ** (-i / pairs) for i in range(pairs)], dtype=torch.float64)
+    if interleaved:
+        axis = [a for turn in range(max(sections)) for a, n in enumerate(sections) if turn < n]
+    else:
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    return inv, torch.tensor(axis, dtype=torch.int32)
+
+
+_SixStrides = ctypes.c_longlong * 6
+
+
+def _rotary_strides(name, t, index, dtype, packed):
+    """(B, H, N, element strides of b, n, h) of a [total, H, d] or [B, H, N, d] tensor."""
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != index or len(shape) != (3 if packed else 4):
+        raise ValueError(f"{name} must be a {dtype} tensor {'[total, H, d]' if packed else '[B, H, N, d]'} on cuda:{index}")
+    st = t.stride()
+    if st[-1] != 1:
+        raise ValueError(f"{name}: the head dimension must be contiguous")
+    if packed:
+        (N, H, _), B, sb, sn, sh = shape, 1, 0, st[0], st[1]
+    else:
+        (B, H, N, _), (sb, sh, sn, _) = shape, st
+    return B, H, N, (sb if B > 1 else 0, sn if N > 1 else 0, sh if H > 1 else 0)
+
+
+def _rotary(q, k, positions, inv_freq, axis, inverse, inplace, stream):
+    packed, index, dtype = q.dim() == 3, q.get_device(), q.dtype
+    suffix = _FP16_SUFFIX.get(dtype)
+    if suffix is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    if index < 0:
+        raise ValueError("q must be on a CUDA device")
+    B, Hq, N, q_in = _rotary_strides("q", q, index, dtype, packed)
+    d, pairs = q.shape[-1], inv_freq.numel()
+    tokens = (N,) if packed else (B, N)
+    if positions.dim() != len(tokens) + 1:
+        raise ValueError("positions must be [n_axes, total], or [n_axes, B, N] for q of four dimensions")
+    _check_tensor("positions", positions, _I32, (positions.shape[0], *tokens), index)
+    for name, t, want in (("inv_freq", inv_freq, torch.float64), ("axis", axis, _I32)):
+        if t.dtype is not want or t.is_cuda or t.dim() != 1 or t.numel() != pairs or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {want} tensor [pairs] on the CPU")
+    tensors = [(q, q_in)]
+    Hk = 0
+    if k is not None:
+        Bk, Hk, Nk, k_in = _rotary_strides("k", k, index, dtype, packed)
+        if Bk != B or Nk != N or k.shape[-1] != d:
+            raise ValueError("k must have q's tokens and d")
+        tensors.append((k, k_in))
+    name = "fa_rotary" + suffix
+    args, outs = [], []
+    with _on(index, stream):
+        for t, strides in tensors:
+            if inplace:
+                out, to = t, strides
+                if any(s == 0 for s, n in zip(t.stride(), t.shape) if n > 1):
+                    raise ValueError("a tensor that repeats its rows cannot be turned in place")
+            elif packed:
+                out = _empty3(N, t.shape[1], d, dtype)
+                to = (0, t.shape[1] * d, d)
+            else:
+                out = _empty4(B, t.shape[1], N, d, dtype)
+                to = (t.shape[1] * N * d, d, N * d)
+            outs.append(out)
+            args += [t.data_ptr(), out.data_ptr(), _SixStrides(*strides, *to), t.shape[1]]
+        if len(tensors) == 1:
+            outs.append(None)
+            args += [None, None, None, 0]
+        rc = getattr(lib, name)(*args, positions.data_ptr(), positions.shape[0], inv_freq.data_ptr(),
+                                axis.data_ptr(), pairs, B, N, d, bool(inverse), _raw_stream(index, stream))
+    if rc != FA_OK:
+        raise FAError(rc, name)
+    return outs[0], outs[1]
+
+
+def rotary(q, k, positions, inv_freq, axis, inplace=False, stream=None):
+    """``q`` and ``k`` (or None) turned by rotary positions: packed [total, H, d] with ``positions`` [n_axes, total], or
+    [B, H, N, d] with [n_axes, B, N] (int32 on the GPU), any strides that are multiples of 8 with contiguous rows. Pair i,
+    dims i and pairs + i, is turned by positions[axis[i]] * inv_freq[i]; ``inv_freq`` (float64) and ``axis`` (int32) are
+    CPU tensors [pairs], as ``rotary_frequencies`` makes them. Returns (q, k), contiguous, or written in place."""
+    return _rotary(q, k, positions, inv_freq, axis, False, inplace, stream)
+
+
+def rotary_backward(dq, dk, positions, inv_freq, axis, inplace=False, stream=None):
+    """The gradients of ``rotary``'s inputs from those of its outputs: the same angles, turned back."""
+    return _rotary(dq, dk, positions, inv_freq, axis, True, inplace, stream)
 
 
 # ---------------------------------------------------------------- packed variable-length batch
