@@ -313,6 +313,35 @@ int fa_fwd_kvq8_fp16(const void *q, const void *k_codes, const void *v_codes, co
                      int format, float scale, int causal, int n_parts, void *workspace,
                      unsigned long long workspace_bytes, void *stream);
 
+/* ---- a prefix that all sequences share ----------------------------------------------
+ * fa_fwd_kvq8 for a batch whose sequences all begin with the same tokens (a system prompt, a document), held once in the
+ * cache: the prefix's positions are those of prefix_table (int32 [prefix_pages]), of which there are prefix_len[0]
+ * (int32 [1] in DEVICE memory, at most max_prefix, 1 <= max_prefix <= prefix_pages * page, a host-side bound); each
+ * sequence's own kv_lens[b] positions, in page_table as before, come behind them and start in pages of their own. Any
+ * of the lengths may be 0. Results are those of fa_fwd_kvq8 over the whole: causal counts positions over both parts,
+ * so query i sees the first prefix_len[0] + kv_lens[b] - Nq + i + 1 of them.
+ * With n_splits = 0 the prefix is read with every sequence's own keys, and n_parts and the workspace are those of
+ * fa_fwd_kvq8. With n_splits > 0 (at most ceil(max_prefix / 128)) it is read once for the rows of all sequences, in
+ * n_splits runs of keys, and n_parts is for the sequences' own keys; the summaries (fp32) go through the workspace and are merged
+ * as in fa_fwd_splitkv. fa_kvq8_prefix_plan chooses both. The workspace has at least
+ * fa_kvq8_prefix_workspace_bytes bytes (256-byte aligned; it may be NULL where they are 0).
+ * Accuracy, errors and the device status as for fa_fwd_kvq8; a prefix length out of range counts as 0 and records
+ * FA_ERR_SEQLENS. The result does not depend on timing. */
+int fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int *n_splits, int *n_parts);
+long long fa_kvq8_prefix_workspace_bytes(int B, int H, int Hkv, int Nq, int max_prefix, int d, int n_splits, int n_parts);
+int fa_fwd_kvq8_prefix(const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
+                       const float *v_scale, const int *prefix_table, int prefix_pages, const int *prefix_len,
+                       const int *page_table, int n_pages, int max_pages, int page, const int *kv_lens, void *out,
+                       float *lse, int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int format,
+                       float scale, int causal, int n_splits, int n_parts, void *workspace,
+                       unsigned long long workspace_bytes, void *stream);
+int fa_fwd_kvq8_prefix_fp16(const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
+                            const float *v_scale, const int *prefix_table, int prefix_pages, const int *prefix_len,
+                            const int *page_table, int n_pages, int max_pages, int page, const int *kv_lens, void *out,
+                            float *lse, int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int format,
+                            float scale, int causal, int n_splits, int n_parts, void *workspace,
+                            unsigned long long workspace_bytes, void *stream);
+
 /* ---- weights and eviction of the 8-bit cache -------------------------------------
  * Under a memory budget the keys that a model has paid least attention to are given up.
  *

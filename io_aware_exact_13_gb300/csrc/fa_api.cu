@@ -518,6 +518,70 @@ int kvq8_attn_common(bool fp16, const void *q, const void *k_codes, const void *
     return fa::launch_kvq8_attention(a, fp16);
 }
 
+// Positions of a prefix and of a sequence's own, as the line of 16-key tiles counts them.
+int64_t kvq8_line(int max_prefix, int max_len) {
+    return (static_cast<int64_t>(max_prefix) + 15) / 16 * 16 + (static_cast<int64_t>(max_len) + 15) / 16 * 16;
+}
+
+int check_kvq8_prefix(int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d) {
+    if (B < 1 || !kvq8_rows_ok(B, H, Hkv, Nq)) return FA_ERR_SHAPE;
+    if (max_prefix < 1 || max_len < 1 || kvq8_line(max_prefix, max_len) > kKvq8MaxLen) return FA_ERR_SHAPE;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    const int rows = H / Hkv * Nq;
+    if (fa::kvq8_tiles(B, Hkv, rows, static_cast<int>(kvq8_line(max_prefix, max_len)), d) > kKvq8MaxTiles) return FA_ERR_SHAPE;
+    return FA_OK;
+}
+
+int kvq8_prefix_common(bool fp16, const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
+                       const float *v_scale, const int *prefix_table, int prefix_pages, const int *prefix_len,
+                       const int *page_table, int n_pages, int max_pages, int page, const int *kv_lens, void *out,
+                       float *lse, int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int format,
+                       float scale, int causal, int n_splits, int n_parts, void *workspace,
+                       unsigned long long workspace_bytes, void *stream) {
+    if (!q || !prefix_table || !prefix_len || !kv_lens || !out || !lse) return FA_ERR_NULL;
+    int rc = check_kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    if (rc != FA_OK) return rc;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(kv_lens, 4) || !aligned(prefix_table, 4) ||
+        !aligned(prefix_len, 4))
+        return FA_ERR_ALIGN;
+    rc = check_kvq8_prefix(B, H, Hkv, Nq, max_prefix, max_len, d);
+    if (rc != FA_OK) return rc;
+    if (prefix_pages < 1 || max_prefix > static_cast<int64_t>(prefix_pages) * page) return FA_ERR_SHAPE;
+    if (max_len > static_cast<int64_t>(max_pages) * page) return FA_ERR_SHAPE;
+    const long long need = fa_kvq8_prefix_workspace_bytes(B, H, Hkv, Nq, max_prefix, d, n_splits, n_parts);
+    if (need < 0) return static_cast<int>(need);
+    if (need > 0 && (!workspace || !aligned(workspace, 256) || workspace_bytes < static_cast<unsigned long long>(need)))
+        return FA_ERR_WORKSPACE;
+    DeviceInfo *di = device_info();
+    if (!di) return FA_ERR_LAUNCH;
+    fa::Kvq8AttnArgs a;
+    a.c = kvq8_cache(k_codes, v_codes, k_scale, v_scale, page_table, n_pages, max_pages, page, Hkv, d, format);
+    a.q = q;
+    a.out = out;
+    a.lse = lse;
+    a.kv_lens = kv_lens;
+    a.B = B;
+    a.H = H;
+    a.Nq = Nq;
+    a.max_len = max_len;
+    a.scale = scale;
+    a.causal = causal ? 1 : 0;
+    a.parts = n_parts;
+    a.num_sms = di->num_sms;
+    a.workspace = static_cast<float *>(workspace);
+    a.status = di->status;
+    a.stream = static_cast<cudaStream_t>(stream);
+    a.prefix_table = prefix_table;
+    a.prefix_len = prefix_len;
+    a.max_prefix = max_prefix;
+    a.splits = n_splits;
+    a.timeout_ns = kDefaultTimeoutNs;
+    log_call("8-bit cache attention behind a prefix %s format=%d page=%d d=%d causal=%d B=%d H=%d Hkv=%d Nq=%d "
+             "max_prefix=%d max_len=%d splits=%d parts=%d",
+             fp16 ? "fp16" : "bf16", format, page, d, a.causal, B, H, Hkv, Nq, max_prefix, max_len, n_splits, n_parts);
+    return fa::launch_kvq8_prefix(a, fp16);
+}
+
 int kvq8_weights_common(bool fp16, const void *q, const void *k_codes, const float *k_scale, const int *page_table,
                         int n_pages, int max_pages, int page, const int *kv_lens, const float *lse, float *weight, int B,
                         int H, int Hkv, int Nq, int max_len, int d, int format, float scale, int causal, void *stream) {
@@ -1025,6 +1089,43 @@ int fa_fwd_kvq8_fp16(FA_KVQ8_ARGS) {
                             workspace_bytes, stream);
 }
 #undef FA_KVQ8_ARGS
+
+int fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int *n_splits, int *n_parts) {
+    if (!n_splits || !n_parts) return FA_ERR_NULL;
+    const int rc = check_kvq8_prefix(B, H, Hkv, Nq, max_prefix, max_len, d);
+    if (rc != FA_OK) return rc;
+    DeviceInfo *di = device_info();
+    const int sms = di ? di->num_sms : kNominalSms, rows = H / Hkv * Nq;
+    *n_splits = fa::kvq8_prefix_splits(B, Hkv, rows, max_prefix, max_len, d, sms);
+    *n_parts = fa::kvq8_num_parts(B, Hkv, rows, *n_splits > 0 ? max_len : static_cast<int>(kvq8_line(max_prefix, max_len)), d, sms);
+    return FA_OK;
+}
+
+long long fa_kvq8_prefix_workspace_bytes(int B, int H, int Hkv, int Nq, int max_prefix, int d, int n_splits, int n_parts) {
+    if (B < 1 || !kvq8_rows_ok(B, H, Hkv, Nq) || max_prefix < 1 || n_parts < 0 || n_parts > kKvq8MaxParts || n_splits < 0 ||
+        n_splits > (static_cast<int64_t>(max_prefix) + 127) / 128)
+        return FA_ERR_SHAPE;
+    if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
+    return static_cast<long long>(fa::kvq8_prefix_workspace_bytes(B, Hkv, H / Hkv * Nq, d, n_splits, n_parts));
+}
+
+#define FA_KVQ8_PREFIX_ARGS                                                                                            \
+    const void *q, const void *k_codes, const void *v_codes, const float *k_scale, const float *v_scale,               \
+        const int *prefix_table, int prefix_pages, const int *prefix_len, const int *page_table, int n_pages,          \
+        int max_pages, int page, const int *kv_lens, void *out, float *lse, int B, int H, int Hkv, int Nq,             \
+        int max_prefix, int max_len, int d, int format, float scale, int causal, int n_splits, int n_parts,            \
+        void *workspace, unsigned long long workspace_bytes, void *stream
+int fa_fwd_kvq8_prefix(FA_KVQ8_PREFIX_ARGS) {
+    return kvq8_prefix_common(false, q, k_codes, v_codes, k_scale, v_scale, prefix_table, prefix_pages, prefix_len,
+                              page_table, n_pages, max_pages, page, kv_lens, out, lse, B, H, Hkv, Nq, max_prefix, max_len,
+                              d, format, scale, causal, n_splits, n_parts, workspace, workspace_bytes, stream);
+}
+int fa_fwd_kvq8_prefix_fp16(FA_KVQ8_PREFIX_ARGS) {
+    return kvq8_prefix_common(true, q, k_codes, v_codes, k_scale, v_scale, prefix_table, prefix_pages, prefix_len,
+                              page_table, n_pages, max_pages, page, kv_lens, out, lse, B, H, Hkv, Nq, max_prefix, max_len,
+                              d, format, scale, causal, n_splits, n_parts, workspace, workspace_bytes, stream);
+}
+#undef FA_KVQ8_PREFIX_ARGS
 
 #define FA_WEIGHTS_ARGS                                                                                                \
     const void *q, const void *k_codes, const float *k_scale, const int *page_table, int n_pages, int max_pages,       \

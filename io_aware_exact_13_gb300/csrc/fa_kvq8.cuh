@@ -56,6 +56,9 @@ struct Kvq8AttnArgs {
     float *workspace;
     int *status;
     cudaStream_t stream;
+    const int *prefix_table = nullptr, *prefix_len = nullptr;  // of the prefix that all sequences share
+    int max_prefix = 0, splits = 0;
+    unsigned long long timeout_ns = 0;
 };
 
 struct Kvq8WeightsArgs {
@@ -85,6 +88,10 @@ struct Kvq8EvictArgs {
 int launch_kvq8_append(const Kvq8AppendArgs &a, bool fp16);
 int launch_kvq8_read(const Kvq8ReadArgs &a, bool fp16);
 int launch_kvq8_attention(const Kvq8AttnArgs &a, bool fp16);
+int launch_kvq8_prefix(const Kvq8AttnArgs &a, bool fp16);
+// Runs of keys that a shared prefix is cut into (0: it is read with each sequence's own keys), and the workspace.
+int kvq8_prefix_splits(int B, int Hkv, int rows, int max_prefix, int max_len, int d, int num_sms);
+size_t kvq8_prefix_workspace_bytes(int B, int Hkv, int rows, int d, int splits, int parts);
 int launch_kvq8_weights(const Kvq8WeightsArgs &a, bool fp16);
 int launch_kvq8_evict(const Kvq8EvictArgs &a);
 // 16-key tiles of B sequences of max_len keys, over K/V heads and tiles of the `rows` = (H / Hkv) * Nq query rows

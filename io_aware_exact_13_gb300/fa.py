@@ -118,10 +118,15 @@ for _suffix in ("", "_fp16"):
                                             [ctypes.c_float, ctypes.c_int, _vp, ctypes.c_ulonglong, _vp])
     SIGNATURES["fa_bwd_cross" + _suffix] = (ctypes.c_int, [_vp] * 10 + [ctypes.c_int] * 6 +
                                             [ctypes.c_float, _vp, ctypes.c_ulonglong, _vp])
+    SIGNATURES["fa_fwd_kvq8_prefix" + _suffix] = (
+        ctypes.c_int, [_vp] * 6 + [ctypes.c_int] + [_vp] * 2 + [ctypes.c_int] * 3 + [_vp] * 3 + [ctypes.c_int] * 8 +
+        [ctypes.c_float] + [ctypes.c_int] * 3 + [_vp, ctypes.c_ulonglong, _vp])
     SIGNATURES["fa_kvq8_weights" + _suffix] = (ctypes.c_int, [_vp] * 4 + [ctypes.c_int] * 3 + [_vp] * 3 + [ctypes.c_int] * 7 +
                                                [ctypes.c_float, ctypes.c_int, _vp])
     SIGNATURES["fa_rotary" + _suffix] = (ctypes.c_int, [_vp] * 3 + [ctypes.c_int] + [_vp] * 3 + [ctypes.c_int, _vp, ctypes.c_int] +
                                          [_vp] * 2 + [ctypes.c_int] * 5 + [_vp])
+SIGNATURES["fa_kvq8_prefix_plan"] = (ctypes.c_int, [ctypes.c_int] * 7 + [ctypes.POINTER(ctypes.c_int)] * 2)
+SIGNATURES["fa_kvq8_prefix_workspace_bytes"] = (ctypes.c_longlong, [ctypes.c_int] * 8)
 SIGNATURES["fa_kvq8_evict"] = (ctypes.c_int, [_vp] * 5 + [ctypes.c_int] * 3 + [_vp] * 2 + [ctypes.c_int] * 2 + [_vp] * 3 +
                                [ctypes.c_int] * 4 + [_vp])
 for _name, (_res, _args) in SIGNATURES.items():
@@ -707,6 +712,95 @@ def attention_kvq8(q, cache, page_table, kv_lens, scale=None, causal=False, max_
     scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
     return _raw_kvq8("fa_fwd_kvq8" + suffix, q.dtype, q, cache, page_table, kv_lens, None, None, scale, causal, max_len,
                      n_parts, None, stream)
+
+
+# ---------------------------------------------------------------- a prefix that all sequences share
+def fa_kvq8_prefix_plan(B, H, Hkv, Nq, max_prefix, max_len, d):
+    """(n_splits, n_parts) for ``fa_fwd_kvq8_prefix``."""
+    splits, parts = ctypes.c_int(), ctypes.c_int()
+    rc = lib.fa_kvq8_prefix_plan(int(B), int(H), int(Hkv), int(Nq), int(max_prefix), int(max_len), int(d), splits, parts)
+    if rc != FA_OK:
+        raise FAError(rc, "fa_kvq8_prefix_plan")
+    return splits.value, parts.value
+
+
+def fa_kvq8_prefix_workspace_bytes(B, H, Hkv, Nq, max_prefix, d, n_splits, n_parts) -> int:
+    n = int(lib.fa_kvq8_prefix_workspace_bytes(int(B), int(H), int(Hkv), int(Nq), int(max_prefix), int(d), int(n_splits),
+                                               int(n_parts)))
+    if n < 0:
+        raise FAError(n, "fa_kvq8_prefix_workspace_bytes")
+    return n
+
+
+def _raw_kvq8_prefix(fn_name, dtype, q, cache, prefix_table, prefix_len, page_table, kv_lens, out, lse, scale, causal,
+                     max_prefix, max_len, n_splits, n_parts, workspace, stream):
+    """``out``, ``lse`` None: allocated; the bounds, ``n_splits`` with ``n_parts`` and ``workspace`` None: chosen and
+    allocated."""
+    index, fmt, (n_pages, Hkv, page, d), (nseq, max_pages), ptrs = _check_kvq8(cache, page_table)
+    shape = q.shape
+    if len(shape) != 4:
+        raise ValueError("q must be [B, H, Nq, d]")
+    B, H, Nq, dq = shape
+    if dq != d or H % Hkv or nseq != B:
+        raise ValueError("q: [B, H, Nq, d] with the cache's d, its Hkv dividing H and one page table row per b")
+    if prefix_table.dim() != 1:
+        raise ValueError("prefix_table must be int32 [prefix_pages]")
+    if (n_splits is None) != (n_parts is None):
+        raise ValueError("n_splits and n_parts are given together or not at all")
+    _check_tensor("q", q, dtype, shape, index)
+    _check_tensor("kv_lens", kv_lens, _I32, (B,), index)
+    _check_tensor("prefix_table", prefix_table, _I32, prefix_table.shape, index)
+    _check_tensor("prefix_len", prefix_len, _I32, (1,), index)
+    max_len = max_pages * page if max_len is None else int(max_len)
+    max_prefix = prefix_table.shape[0] * page if max_prefix is None else int(max_prefix)
+    with _on(index, stream):
+        if out is None:
+            out = _empty4(B, H, Nq, d, dtype)
+            lse = _empty3(B, H, Nq, _F32)
+        else:
+            _check_tensor("out", out, dtype, shape, index)
+            _check_tensor("lse", lse, _F32, shape[:3], index)
+        if n_splits is None:
+            n_splits, n_parts = fa_kvq8_prefix_plan(B, H, Hkv, Nq, max_prefix, max_len, d)
+        if workspace is None:
+            need = fa_kvq8_prefix_workspace_bytes(B, H, Hkv, Nq, max_prefix, d, n_splits, n_parts)
+            workspace = _empty_bytes(need) if need else None
+        rc = getattr(lib, fn_name)(q.data_ptr(), *ptrs[:4], prefix_table.data_ptr(), prefix_table.shape[0],
+                                   prefix_len.data_ptr(), ptrs[4], n_pages, max_pages, page, kv_lens.data_ptr(),
+                                   out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, max_prefix, max_len, d, fmt, float(scale),
+                                   bool(causal), int(n_splits), int(n_parts),
+                                   None if workspace is None else workspace.data_ptr(), _nbytes(workspace, index),
+                                   _raw_stream(index, stream))
+    if rc != FA_OK:
+        raise FAError(rc, fn_name)
+    return out, lse
+
+
+def fa_fwd_kvq8_prefix(q, cache, prefix_table, prefix_len, page_table, kv_lens, out, lse, scale, causal, max_prefix, max_len,
+                       n_splits, n_parts, workspace, stream=None):
+    """bf16 forward of 1 to 16 query rows per sequence over a shared prefix and their own cached tokens."""
+    _raw_kvq8_prefix("fa_fwd_kvq8_prefix", torch.bfloat16, q, cache, prefix_table, prefix_len, page_table, kv_lens, out, lse,
+                     scale, causal, max_prefix, max_len, n_splits, n_parts, workspace, stream)
+
+
+def fa_fwd_kvq8_prefix_fp16(q, cache, prefix_table, prefix_len, page_table, kv_lens, out, lse, scale, causal, max_prefix,
+                            max_len, n_splits, n_parts, workspace, stream=None):
+    """fp16 forward behind a shared prefix (see ``fa_fwd_kvq8_prefix``)."""
+    _raw_kvq8_prefix("fa_fwd_kvq8_prefix_fp16", torch.float16, q, cache, prefix_table, prefix_len, page_table, kv_lens, out,
+                     lse, scale, causal, max_prefix, max_len, n_splits, n_parts, workspace, stream)
+
+
+def attention_kvq8_prefix(q, cache, prefix_table, prefix_len, page_table, kv_lens, scale=None, causal=False, max_prefix=None,
+                          max_len=None, n_splits=None, n_parts=None, stream=None):
+    """O [B, H, Nq, d] and lse [B, H, Nq] of 1 to 16 query rows per sequence over the prefix_len[0] tokens that all
+    sequences share (pages ``prefix_table``) and each one's own kv_lens[b] behind them. ``max_prefix`` and ``max_len``
+    bound the lengths (the tables' reach unless given); the workspace is a torch allocation."""
+    suffix = _FP16_SUFFIX.get(q.dtype)
+    if suffix is None:
+        raise ValueError(f"unsupported dtype {q.dtype}")
+    scale = 1.0 / math.sqrt(q.shape[-1]) if scale is None else scale
+    return _raw_kvq8_prefix("fa_fwd_kvq8_prefix" + suffix, q.dtype, q, cache, prefix_table, prefix_len, page_table, kv_lens,
+                            None, None, scale, causal, max_prefix, max_len, n_splits, n_parts, None, stream)
 
 
 # ---------------------------------------------------------------- weights and eviction of the 8-bit cache
