@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["fa_api.cu", "fa_fwd_bf16.cu", "fa_fwd_fp16.cu", "fa_fwd_mask_bf16.cu", "fa_fwd_mask_fp16.cu",
            "fa_mask_pack.cu", "fa_fwd_drop_bf16.cu", "fa_fwd_drop_fp16.cu", "fa_fwd_fp32.cu", "fa_splitkv.cu", "fa_splitkv_noalloc.cu", "fa_bwd.cu",
            "fa_fwd_varlen_bf16.cu", "fa_fwd_varlen_fp16.cu", "fa_kvq8_cache.cu", "fa_kvq8_attn.cu",
-           "fa_kvq8_prefix.cu", "fa_kvq8_weights.cu", "fa_kvq8_evict.cu", "fa_rotary.cu",
+           "fa_kvq8_prefix.cu", "fa_kvq8_prefix_own.cu", "fa_kvq8_prefix_tc.cu", "fa_kvq8_weights.cu", "fa_kvq8_evict.cu", "fa_rotary.cu",
            "fa_fwd_cross_bf16.cu", "fa_fwd_cross_fp16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
@@ -69,7 +69,7 @@ def check_ptxas_log(log: str) -> tuple[list[str], list[str]]:
         if m and kernel and (int(m.group(1)) or int(m.group(2))):
             warnings.append(f"{kernel}: spills ({m.group(0)})")
         m = re.search(r"Used (\d+) registers", line)
-        if m and kernel and re.search(r"fa_fwd_(bk128_)?kernel", kernel) and int(m.group(1)) != 128:
+        if m and kernel and re.search(r"fa_fwd_(bk128_)?kernel|fa_kvq8_prefix_kernel", kernel) and int(m.group(1)) != 128:
             problems.append(f"{kernel}: uses {m.group(1)} registers, expected 128")
     return problems, warnings
 

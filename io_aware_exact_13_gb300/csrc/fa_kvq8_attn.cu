@@ -29,7 +29,7 @@ size_t kvq8_workspace_bytes(int rows, int d, int parts) {
 }
 
 int launch_kvq8_attention(const Kvq8AttnArgs &a, bool fp16) {
-    return fp16 ? launch_q8_t<__half, false>(a) : launch_q8_t<__nv_bfloat16, false>(a);
+    return fp16 ? launch_q8_t<__half, kQ8Plain>(a) : launch_q8_t<__nv_bfloat16, kQ8Plain>(a);
 }
 
 }  // namespace fa

@@ -43,7 +43,8 @@
 //
 // PREFIX: the keys of every sequence begin with those of a prefix that all share (a page table and a length of its own),
 // whose tiles come before the sequence's own in its part of the line. (The prefix is then read once for each
-// sequence, after the first time from L2: for few rows. See fa_kvq8_prefix.cu.)
+// sequence, after the first time from L2: for few rows. See fa_kvq8_prefix.cu.) SUMMARY: out and lse are a part of
+// what the rows see, in fp32, to be merged with others.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -59,6 +60,8 @@
 
 namespace fa {
 namespace {
+
+enum Q8Mode { kQ8Plain, kQ8Prefix, kQ8Summary };
 
 constexpr int kWarps = 4;
 constexpr int kMostCluster = 8;  // CTAs of a unit, all of a portable cluster
@@ -187,16 +190,22 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi) {
         return *reinterpret_cast<const uint32_t *>(&h);
     }
 }
+// Four values times f, rounded to the type of `dst`.
 template <typename T>
-__device__ __forceinline__ T from_float(float x) {
-    if constexpr (std::is_same<T, __nv_bfloat16>::value) return __float2bfloat16_rn(x);
-    else return __float2half_rn(x);
+__device__ __forceinline__ void store4(T *dst, float4 a, float f) {
+    if constexpr (std::is_same<T, float>::value)
+        *reinterpret_cast<float4 *>(dst) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+    else
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(pack16<T>(a.x * f, a.y * f), pack16<T>(a.z * f, a.w * f));
 }
 
-template <typename T, int D, int FMT, int NT, bool CAUSAL, bool PREFIX>
+template <typename T, int D, int FMT, int NT, bool CAUSAL, int MODE>
 __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_partial(const Q8Params p) {
     using C = Q8Cfg<D, NT>;
+    using OT = typename std::conditional<MODE == kQ8Summary, float, T>::type;
+    constexpr bool PREFIX = MODE == kQ8Prefix;
     constexpr int KS = C::KS, MT = C::MT, RT = C::RT;
+    constexpr int OUT_VEC = D * (int)sizeof(OT) / 16;  // 16-byte vectors of an output row
     extern __shared__ __align__(128) uint8_t sm[];
     float *sm_o = reinterpret_cast<float *>(sm + C::SM_O), *sm_m = reinterpret_cast<float *>(sm + C::SM_ML);
     float *sm_l = sm_m + 2 * kWarps * RT;
@@ -232,8 +241,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
         if (n == 0) {
             const int kvh = unit / p.row_tiles, row0 = (unit - kvh * p.row_tiles) * RT, rows = min(RT, p.rows - row0);
             const size_t at = ((size_t)b * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq + row0;
-            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + at * D);
-            for (int i = w * 32 + lane; i < rows * (D / 8); i += p.cluster * kWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<OT *>(p.out) + at * D);
+            for (int i = w * 32 + lane; i < rows * OUT_VEC; i += p.cluster * kWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
             for (int i = w * 32 + lane; i < rows; i += p.cluster * kWarps * 32) p.lse[at + i] = -INFINITY;
             return;
         }
@@ -265,8 +274,8 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
             bool bad;
             if (tiles_of(q8_len(p, s, bad)) != 0) continue;
             const size_t rows = (size_t)p.H * p.Nq;
-            uint4 *o = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) + s * rows * D);
-            for (size_t i = threadIdx.x; i < rows * (D / 8); i += kWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+            uint4 *o = reinterpret_cast<uint4 *>(static_cast<OT *>(p.out) + s * rows * D);
+            for (size_t i = threadIdx.x; i < rows * OUT_VEC; i += kWarps * 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
             for (size_t i = threadIdx.x; i < rows; i += kWarps * 32) p.lse[s * rows + i] = -INFINITY;
         }
         if (threadIdx.x == 0) p.shared[blockIdx.x] = make_int4(-1, 0, 0, 0);
@@ -620,12 +629,19 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                 if (whole) {
                     f = ls == 0.f ? 0.f : f / ls;  // (a sum that is NaN, from a NaN query, stays NaN)
                     if (row0 + r < p.rows) {
-                        uint32_t w[MT];
+                        OT *dst = static_cast<OT *>(p.out) + (row_base + row0 + r) * D + C::VB * g;
+                        if constexpr (MODE == kQ8Summary) {
 #pragma unroll
-                        for (int i = 0; i < MT; ++i) w[i] = pack16<T>(o[t][i][e] * f, o[t][i][e + 2] * f);
-                        T *dst = static_cast<T *>(p.out) + (row_base + row0 + r) * D + C::VB * g;
+                            for (int i = 0; i < MT; i += 2)
+                                *reinterpret_cast<float4 *>(dst + 2 * i) = make_float4(o[t][i][e] * f, o[t][i][e + 2] * f,
+                                                                                       o[t][i + 1][e] * f, o[t][i + 1][e + 2] * f);
+                        } else {
+                            uint32_t w[MT];
 #pragma unroll
-                        for (int i = 0; i < MT; i += 4) st_global_v4(dst + 2 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
+                            for (int i = 0; i < MT; ++i) w[i] = pack16<T>(o[t][i][e] * f, o[t][i][e + 2] * f);
+#pragma unroll
+                            for (int i = 0; i < MT; i += 4) st_global_v4(dst + 2 * i, w[i], w[i + 1], w[i + 2], w[i + 3]);
+                        }
                         if (g == 0) p.lse[row_base + row0 + r] = ls == 0.f ? -INFINITY : (m[t][e] + lg2_approx(ls)) * kLn2;
                     }
                 } else {
@@ -701,10 +717,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
                 A.w = fmaf(f, v[q].w, A.w);
             }
             const float inv = L == 0.f ? 0.f : 1.0f / L;
-            uint2 w;
-            w.x = pack16<T>(A.x * inv, A.y * inv);
-            w.y = pack16<T>(A.z * inv, A.w * inv);
-            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * e4) = w;
+            store4(static_cast<OT *>(p.out) + (row_base + r) * D + 4 * e4, A, inv);
             if (e4 == 0) p.lse[row_base + r] = L == 0.f ? -INFINITY : (M + lg2_approx(L)) * kLn2;
         }
         cluster_sync();  // a CTA's shared memory stays until its neighbours have read it
@@ -750,10 +763,7 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
             const float inv = L == 0.f ? 0.f : 1.0f / L;
             const float lse = L == 0.f ? -INFINITY : (M + lg2_approx(L)) * kLn2;
             if (all) {
-                uint2 w;
-                w.x = pack16<T>(A.x * inv, A.y * inv);
-                w.y = pack16<T>(A.z * inv, A.w * inv);
-                *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * e4) = w;
+                store4(static_cast<OT *>(p.out) + (row_base + r) * D + 4 * e4, A, inv);
                 if (e4 == 0) p.lse[row_base + r] = lse;
             } else {
                 *reinterpret_cast<float4 *>(p.o_part + (part * RT + r) * D + 4 * e4) =
@@ -852,10 +862,7 @@ __global__ void __launch_bounds__(kCombineThreads) fa_kvq8_combine(const Q8Param
         }
         if (group == 0 && in) {
             const float inv = W == 0.f ? 0.f : 1.0f / W;
-            uint2 o;
-            o.x = pack16<T>(A.x * inv, A.y * inv);
-            o.y = pack16<T>(A.z * inv, A.w * inv);
-            *reinterpret_cast<uint2 *>(static_cast<T *>(p.out) + (row_base + r) * D + 4 * lane) = o;
+            store4(static_cast<T *>(p.out) + (row_base + r) * D + 4 * lane, A, inv);
             if (lane == 0) p.lse[row_base + r] = W == 0.f ? -INFINITY : M + __logf(W);
         }
     }
@@ -878,10 +885,10 @@ int cluster_size(long long units, int tiles, long long slots) {
     return c;
 }
 
-template <typename T, int D, int FMT, int NT, bool CAUSAL, bool PREFIX>
+template <typename T, int D, int FMT, int NT, bool CAUSAL, int MODE>
 int launch_q8(const Kvq8AttnArgs &a) {
     using C = Q8Cfg<D, NT>;
-    auto kern = fa_kvq8_partial<T, D, FMT, NT, CAUSAL, PREFIX>;
+    auto kern = fa_kvq8_partial<T, D, FMT, NT, CAUSAL, MODE>;
     if (C::SMEM > 48 * 1024 &&
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
         return -5;
@@ -932,32 +939,32 @@ int launch_q8(const Kvq8AttnArgs &a) {
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return -5;
     if (cudaGetLastError() != cudaSuccess) return -5;
     if (a.parts <= 1) return 0;
-    return launch_dependent(fa_kvq8_combine<T, D, C::RT>, dim3(a.parts), dim3(kCombineThreads), 0,
+    return launch_dependent(fa_kvq8_combine<typename std::conditional<MODE == kQ8Summary, float, T>::type, D, C::RT>, dim3(a.parts), dim3(kCombineThreads), 0,
                             a.stream, p) == cudaSuccess
                ? 0
                : -5;
 }
 
-template <typename T, int D, int FMT, int NT, bool PREFIX>
+template <typename T, int D, int FMT, int NT, int MODE>
 int launch_q8_causal(const Kvq8AttnArgs &a) {
-    return a.causal ? launch_q8<T, D, FMT, NT, true, PREFIX>(a) : launch_q8<T, D, FMT, NT, false, PREFIX>(a);
+    return a.causal ? launch_q8<T, D, FMT, NT, true, MODE>(a) : launch_q8<T, D, FMT, NT, false, MODE>(a);
 }
-template <typename T, int D, int FMT, bool PREFIX>
+template <typename T, int D, int FMT, int MODE>
 int launch_q8_rows(const Kvq8AttnArgs &a) {
     const int nt = tiles_per_unit(a.H / a.c.Hkv * a.Nq, D);
-    if (nt == 1) return launch_q8_causal<T, D, FMT, 1, PREFIX>(a);
-    if (nt == 2) return launch_q8_causal<T, D, FMT, 2, PREFIX>(a);
+    if (nt == 1) return launch_q8_causal<T, D, FMT, 1, MODE>(a);
+    if (nt == 2) return launch_q8_causal<T, D, FMT, 2, MODE>(a);
     if constexpr (D == 64)
-        return nt == 3 ? launch_q8_causal<T, D, FMT, 3, PREFIX>(a) : launch_q8_causal<T, D, FMT, 4, PREFIX>(a);
+        return nt == 3 ? launch_q8_causal<T, D, FMT, 3, MODE>(a) : launch_q8_causal<T, D, FMT, 4, MODE>(a);
     return -4;
 }
 
-template <typename T, bool PREFIX>
+template <typename T, int MODE>
 int launch_q8_t(const Kvq8AttnArgs &a) {
     const bool i8 = a.c.format == kKvq8Int8;
     if (a.c.d == 128)
-        return i8 ? launch_q8_rows<T, 128, kKvq8Int8, PREFIX>(a) : launch_q8_rows<T, 128, kKvq8E4m3, PREFIX>(a);
-    if (a.c.d == 64) return i8 ? launch_q8_rows<T, 64, kKvq8Int8, PREFIX>(a) : launch_q8_rows<T, 64, kKvq8E4m3, PREFIX>(a);
+        return i8 ? launch_q8_rows<T, 128, kKvq8Int8, MODE>(a) : launch_q8_rows<T, 128, kKvq8E4m3, MODE>(a);
+    if (a.c.d == 64) return i8 ? launch_q8_rows<T, 64, kKvq8Int8, MODE>(a) : launch_q8_rows<T, 64, kKvq8E4m3, MODE>(a);
     return -4;
 }
 

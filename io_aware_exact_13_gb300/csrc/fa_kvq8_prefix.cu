@@ -1,14 +1,111 @@
-// fa_kvq8_prefix.cu -- attention over the 8-bit cache for a batch whose sequences share a prefix.
+// fa_kvq8_prefix.cu -- attention over the 8-bit cache for a batch whose sequences share a prefix: the choice between
+// reading the prefix with each sequence's own keys (fa_kvq8_attn.cuh) and once for the rows of all (fa_kvq8_prefix_tc.cu),
+// and the merge of the latter's summaries with those of the own keys.
 #include "fa_kvq8_attn.cuh"
+#include "fa_kvq8_prefix.cuh"
 
 namespace fa {
+namespace {
 
-int kvq8_prefix_splits(int, int, int, int, int, int, int) { return 0; }
+constexpr int kMergeThreads = 128;
 
-size_t kvq8_prefix_workspace_bytes(int, int, int rows, int d, int, int parts) { return kvq8_workspace_bytes(rows, d, parts); }
+// out = sum_s w_s o_s / sum_s w_s with w_s = exp(lse_s - max lse), over the own keys' summary and those of the prefix's
+// runs (fa_splitkv.cu's rule). Four columns of a row for each thread; the lanes of a row share the weights out.
+template <typename T, int D>
+__global__ void __launch_bounds__(kMergeThreads)
+    fa_kvq8_prefix_merge(const float *own_o, const float *own_lse, const float *o_part, const float *lse_part, T *out,
+                         float *lse, int rows, int splits) {
+    constexpr int LANES = D / 4;
+    grid_dependency_wait();
+    const long long id = (long long)blockIdx.x * kMergeThreads + threadIdx.x;
+    const long long row = id / LANES;
+    const int lane = (int)(id % LANES);
+    const uint32_t mask = LANES == 32 ? 0xffffffffu : 0xffffu << (threadIdx.x & 16);
+    if (row >= rows) return;
+    float M = -INFINITY;  // NaN goes through the weights
+    for (int s = lane; s <= splits; s += LANES) M = fmaxf(M, s == 0 ? own_lse[row] : lse_part[(long long)(s - 1) * rows + row]);
+#pragma unroll
+    for (int d = LANES / 2; d > 0; d /= 2) M = fmaxf(M, __shfl_xor_sync(mask, M, d, LANES));
+    const float ref = M == -INFINITY ? 0.f : M;
+    float W = 0.f;
+    float4 A = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 <= splits; s0 += LANES) {
+        float w = 0.f;
+        if (s0 + lane <= splits) w = __expf((s0 + lane == 0 ? own_lse[row] : lse_part[(long long)(s0 + lane - 1) * rows + row]) - ref);
+        const int n = min(LANES, splits + 1 - s0);
+#pragma unroll 8
+        for (int i = 0; i < n; ++i) {
+            const float f = __shfl_sync(mask, w, i, LANES);
+            if (f == 0.f) continue;  // a summary without keys holds nothing
+            const int s = s0 + i;
+            const float4 v = *reinterpret_cast<const float4 *>((s == 0 ? own_o : o_part + (long long)(s - 1) * rows * D) + row * D + 4 * lane);
+            W += f;
+            A.x = fmaf(f, v.x, A.x);
+            A.y = fmaf(f, v.y, A.y);
+            A.z = fmaf(f, v.z, A.z);
+            A.w = fmaf(f, v.w, A.w);
+        }
+    }
+    store4(out + row * D + 4 * lane, A, W == 0.f ? 0.f : 1.0f / W);
+    if (lane == 0) lse[row] = W == 0.f ? -INFINITY : M + __logf(W);
+}
+
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <typename T, int D>
+int launch_merge(const Kvq8AttnArgs &a, const float *own_o, const float *own_lse, const float *o_part, const float *lse_part) {
+    const int rows = a.B * a.H * a.Nq;
+    const long long grid = ((long long)rows * (D / 4) + kMergeThreads - 1) / kMergeThreads;
+    if (grid > INT32_MAX) return -3;
+    return launch_dependent(fa_kvq8_prefix_merge<T, D>, dim3((unsigned)grid), dim3(kMergeThreads), 0, a.stream, own_o, own_lse,
+                            o_part, lse_part, static_cast<T *>(a.out), a.lse, rows, a.splits) == cudaSuccess
+               ? 0
+               : -5;
+}
+
+}  // namespace
+
+int kvq8_prefix_splits(int B, int Hkv, int rows, int max_prefix, int max_len, int d, int num_sms) {
+    const long long all = (long long)B * rows;
+    if (all < 24 || max_prefix < 512) return 0;
+    const long long units = Hkv * ((all + 255) / 256);
+    const int blocks = (max_prefix + 127) / 128;
+    const long long most = num_sms / units;
+    return (int)(most < 1 ? 1 : most < blocks ? most : blocks);
+}
+
+// Own summary, the runs' summaries, and what the own keys' parts take.
+size_t kvq8_prefix_workspace_bytes(int B, int Hkv, int rows, int d, int splits, int parts) {
+    const size_t own = kvq8_workspace_bytes(rows, d, parts);
+    if (splits == 0) return own;
+    const size_t n = (size_t)B * Hkv * rows;
+    return align256(n * d * 4) + align256(n * 4) + align256(splits * n * d * 4) + align256(splits * n * 4) + own;
+}
 
 int launch_kvq8_prefix(const Kvq8AttnArgs &a, bool fp16) {
-    return fp16 ? launch_q8_t<__half, true>(a) : launch_q8_t<__nv_bfloat16, true>(a);
+    if (a.splits == 0) return fp16 ? launch_q8_t<__half, kQ8Prefix>(a) : launch_q8_t<__nv_bfloat16, kQ8Prefix>(a);
+    const size_t n = (size_t)a.B * a.H * a.Nq, d = a.c.d;
+    char *at = reinterpret_cast<char *>(a.workspace);
+    auto take = [&](size_t bytes) {
+        float *x = reinterpret_cast<float *>(at);
+        at += align256(bytes);
+        return x;
+    };
+    float *own_o = take(n * d * 4), *own_lse = take(n * 4), *o_part = take(a.splits * n * d * 4), *lse_part = take(a.splits * n * 4);
+    int rc = launch_kvq8_prefix_tc(a, fp16, o_part, lse_part);
+    if (rc != 0) return rc;
+    Kvq8AttnArgs own = a;
+    own.out = own_o;
+    own.lse = own_lse;
+    own.workspace = reinterpret_cast<float *>(at);
+    own.max_prefix = 0;
+    rc = launch_kvq8_prefix_own(own, fp16);
+    if (rc != 0) return rc;
+    if (a.c.d == 128)
+        return fp16 ? launch_merge<__half, 128>(a, own_o, own_lse, o_part, lse_part)
+                    : launch_merge<__nv_bfloat16, 128>(a, own_o, own_lse, o_part, lse_part);
+    return fp16 ? launch_merge<__half, 64>(a, own_o, own_lse, o_part, lse_part)
+                : launch_merge<__nv_bfloat16, 64>(a, own_o, own_lse, o_part, lse_part);
 }
 
 }  // namespace fa

@@ -11,7 +11,7 @@ import kvq8_ref as ref
 from test_gpu_kvq8 import CODE, DEV, DT, as_ref, filled, ints, random_table, status_ok
 
 pytestmark = pytest.mark.gpu
-SPLITS = [(0, 0), (0, 1), (0, 7)]
+SPLITS = [(0, 0), (0, 1), (0, 7), (1, 0), (2, 3), (5, 0)]  # (n_splits, n_parts)
 
 
 @pytest.fixture(scope="module")

@@ -43,7 +43,7 @@ def test_arguments_are_refused(fa, name):
 
 
 def test_workspace_is_refused(fa):
-    for splits, parts in ((0, 1), (0, 3)):
+    for splits, parts in ((0, 1), (0, 3), (1, 0), (1, 2)):
         need = fa.fa_kvq8_prefix_workspace_bytes(2, 4, 2, 1, 70, 64, splits, parts)
         kw = dict(n_splits=splits, n_parts=parts)
         assert need > 0
