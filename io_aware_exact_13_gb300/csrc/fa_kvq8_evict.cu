@@ -2,8 +2,9 @@
 //
 // Selection. Of a sequence's n > keep positions each K/V head keeps the last `recent` and, of the earlier ones, the
 // keep - recent of the greatest weight (ties: the lower position; NaN counts as the greatest). The weights are mapped to
-// integers of the same order, and the smallest weight kept is found bit by bit from the top: T is the largest integer that
-// at least that many reach. All above T stay and, in order of position, as many equal to T as are missing. So the result
+// integers of the same order, and T, the smallest that is kept, is found by counting how many reach a trial value, which is
+// placed by turns where an even spread would have it and in the middle of what is left (about 10 counts for
+// weights of a smooth distribution, 32 each way at most). All above T stay and, in order of position, as many equal to T as are missing. So the result
 // does not depend on timing.
 //
 // Moving. The kept tokens go, in their order, to positions 0 .. keep - 1 of the same pages, in place. A page whose tokens
@@ -71,6 +72,7 @@ struct BlockSum {
 __global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const EvictParams p) {
     __shared__ int sums[2][kSelThreads / 32];
     __shared__ int offs[kSelThreads / 32];
+    __shared__ uint32_t ends[2][kSelThreads / 32];
     grid_launch_dependents();
     const int b = blockIdx.x / p.Hkv, head = blockIdx.x - b * p.Hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -101,34 +103,65 @@ __global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const Evict
     }
     if (need == 0) return;
 
-    float v[kSelEach];
-    auto load = [&](int c0) {  // positions past `old` are left out by their index
+    uint32_t v[kSelEach];
+    auto load = [&](int c0) {  // 0, below every weight, for positions past `old`
         const int at = c0 + threadIdx.x * kSelEach;
 #pragma unroll
         for (int i = 0; i < kSelEach; i += 4) {
             float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
             if (at + i < old) x = *reinterpret_cast<const float4 *>(w + at + i);  // cap is a multiple of 16
-            v[i] = x.x, v[i + 1] = x.y, v[i + 2] = x.z, v[i + 3] = x.w;
+            v[i] = at + i < old ? order_of(x.x) : 0u;
+            v[i + 1] = at + i + 1 < old ? order_of(x.y) : 0u;
+            v[i + 2] = at + i + 2 < old ? order_of(x.z) : 0u;
+            v[i + 3] = at + i + 3 < old ? order_of(x.w) : 0u;
         }
     };
     const bool once = old <= kSelChunk;
-    if (once) load(0);
     BlockSum sum{sums, 0};
-    uint32_t T = 0;
-    int above = 0;  // how many lie above T
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t t = T | (1u << bit);
+    // T lies in [lo, hi]: n_lo >= need reach lo, above < need exceed hi
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    for (int c0 = 0; c0 < old; c0 += kSelChunk) {
+        load(c0);
+#pragma unroll
+        for (int i = 0; i < kSelEach; ++i) {
+            hi = max(hi, v[i]);
+            if (v[i] != 0u) lo = min(lo, v[i]);
+        }
+    }
+    lo = ~__reduce_max_sync(0xffffffffu, ~lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (lane == 0) {
+        ends[0][warp] = lo;
+        ends[1][warp] = hi;
+    }
+    __syncthreads();
+    lo = __reduce_min_sync(0xffffffffu, ends[0][lane]);
+    hi = __reduce_max_sync(0xffffffffu, ends[1][lane]);
+    int n_lo = old, above = 0;
+    for (bool halve = false; lo < hi; halve = !halve) {
+        // by turns where the count would be reached if it fell evenly, and the middle
+        const uint32_t gap = hi - lo;
+        uint32_t t = lo + gap / 2 + 1;
+        if (!halve) {
+            const float share = (float)(n_lo - need) / (float)(n_lo - above);
+            t = lo + 1 + min((uint32_t)(share * (float)gap), gap - 1);
+        }
         int count = 0;
         for (int c0 = 0; c0 < old; c0 += kSelChunk) {
             if (!once) load(c0);
-            const int at = c0 + threadIdx.x * kSelEach;
 #pragma unroll
-            for (int i = 0; i < kSelEach; ++i) count += at + i < old && order_of(v[i]) >= t;
+            for (int i = 0; i < kSelEach; ++i) count += v[i] >= t;
         }
         count = sum(count);
-        if (count >= need) T = t;
-        else above = count;  // the last test that failed is the smallest one above T
+        if (count >= need) lo = t, n_lo = count;
+        else hi = t - 1, above = count;
+        if (count == need) {  // exactly those that reach t
+            lo = t - 1;
+            above = need;
+            break;
+        }
     }
+    const uint32_t T = lo;
     // in order of position
     int taken = 0, equal_left = need - above;
     for (int c0 = 0; c0 < old; c0 += kSelChunk) {
@@ -137,8 +170,7 @@ __global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const Evict
         int mine = 0;  // above T, and equal to it << 16
 #pragma unroll
         for (int i = 0; i < kSelEach; ++i) {
-            const uint32_t o = order_of(v[i]);
-            if (at + i < old) mine += (o > T) + ((o == T) << 16);
+            mine += (v[i] > T) + ((v[i] == T) << 16);
         }
         int incl = mine;
 #pragma unroll
@@ -160,15 +192,13 @@ __global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const Evict
         int gt = before & 0xFFFF, eq = before >> 16;  // each at most kSelChunk = 2^14
 #pragma unroll
         for (int i = 0; i < kSelEach; ++i) {
-            const uint32_t o = order_of(v[i]);
-            if (at + i >= old) break;
-            if (o > T || (o == T && eq < equal_left)) {
+            if (v[i] > T || (v[i] == T && eq < equal_left)) {
                 const int r = taken + gt + min(eq, equal_left);
                 kept[r] = at + i;
-                w_out[r] = v[i];
+                w_out[r] = w[at + i];
             }
-            gt += o > T;
-            eq += o == T;
+            gt += v[i] > T;
+            eq += v[i] == T;
         }
         taken += (total & 0xFFFF) + min(total >> 16, equal_left);
         equal_left -= min(total >> 16, equal_left);
@@ -209,31 +239,57 @@ __global__ void __launch_bounds__(kMoveThreads) fa_kvq8_move_kernel(const EvictP
     const int *kept = p.kept + ((size_t)b * p.Hkv + head) * p.keep;
     const int *table = p.page_table + (size_t)b * p.max_pages;
     const int page = 1 << p.page_shift, per_page = page / 16;  // groups of a page
-    int turn = 0;
-    for (int r0 = 0; r0 < p.keep; r0 += kMoveTokens * p.cluster, turn ^= 1) {
-        const int last = min(r0 + kMoveTokens * p.cluster, p.keep) - 1;
-        if (kept[last] == last) continue;  // nothing of this round moves
-        const int g0 = r0 + rank * kMoveTokens + warp * 16;  // this warp's tokens of the new order
-        uint4 x[VEC];
-        float s[VEC];
-        float most = 0.f;
+    const int round = kMoveTokens * p.cluster, rounds = (p.keep + round - 1) / round;
+    // The first round with a token that moves (all behind it move too), and the last one.
+    int first_round = 0;
+    for (int end = rounds; first_round < end;) {
+        const int mid = (first_round + end) / 2, last = min((mid + 1) * round, p.keep) - 1;
+        if (kept[last] == last) first_round = mid + 1;
+        else end = mid;
+    }
+    // A round's codes and scales are requested while the round before is under way, its positions one round earlier.
+    int pos[VEC];
+    uint4 x[VEC], ahead[VEC];
+    float s[VEC], s_ahead[VEC];
+    auto load_pos = [&](int i_round) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            const int r = g0 + i * PER + lane / LANES;
-            x[i] = make_uint4(0u, 0u, 0u, 0u);
-            s[i] = 0.f;
-            if (r < p.keep) {
-                const int pos = kept[r];
-                const int phys = __ldg(table + (pos >> p.page_shift));
-                if (phys >= 0 && phys < p.n_pages) {
-                    const size_t unit = (size_t)phys * p.Hkv + head;
-                    s[i] = p.scale[kv][unit];
-                    x[i] = *reinterpret_cast<const uint4 *>(p.codes[kv] + ((unit << p.page_shift) + (pos & (page - 1))) * D + (lane % LANES) * 16);
-                } else {
-                    atomicExch(p.status, kStatusPage);  // such a token becomes zeros
-                }
+            const int r = i_round * round + rank * kMoveTokens + warp * 16 + i * PER + lane / LANES;
+            pos[i] = r < p.keep && i_round < rounds ? kept[r] : -1;
+        }
+    };
+    auto load_codes = [&]() {
+        int phys[VEC];
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) phys[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            ahead[i] = make_uint4(0u, 0u, 0u, 0u);
+            s_ahead[i] = 0.f;
+            if (phys[i] >= 0 && phys[i] < p.n_pages) {
+                const size_t unit = (size_t)phys[i] * p.Hkv + head;
+                s_ahead[i] = p.scale[kv][unit];
+                ahead[i] = *reinterpret_cast<const uint4 *>(p.codes[kv] + ((unit << p.page_shift) + (pos[i] & (page - 1))) * D + (lane % LANES) * 16);
+            } else if (pos[i] >= 0) {
+                atomicExch(p.status, kStatusPage);  // such a token becomes zeros
             }
         }
+    };
+    load_pos(first_round);
+    load_codes();
+    load_pos(first_round + 1);
+    int turn = 0;
+    for (int i_round = first_round; i_round < rounds; ++i_round, turn ^= 1) {
+        const int g0 = i_round * round + rank * kMoveTokens + warp * 16;  // this warp's tokens of the new order
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            x[i] = ahead[i];
+            s[i] = s_ahead[i];
+        }
+        // (no round writes what a later one reads, so these may run ahead of this round's writes)
+        load_codes();
+        load_pos(i_round + 2);
+        float most = 0.f;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
@@ -293,13 +349,25 @@ __global__ void __launch_bounds__(kMoveThreads) fa_kvq8_move_kernel(const EvictP
 
 template <int D, int FMT>
 int launch_move(const Kvq8EvictArgs &a, EvictParams p) {
+    // A cluster for each head's K or V while there are fewer CTAs than the GPU holds at once, with a round for each CTA.
     const long long units = 2ll * a.nseq * a.c.Hkv;
     p.cluster = 1;
+    while (2 * p.cluster <= kMostCluster && 2 * p.cluster * units <= 4ll * a.num_sms && p.cluster * kMoveTokens < a.keep) p.cluster *= 2;
     const long long grid = units * p.cluster;
     if (grid > INT32_MAX) return -3;
-    return launch_dependent(fa_kvq8_move_kernel<D, FMT>, dim3((unsigned)grid), dim3(kMoveThreads), 0, a.stream, p) == cudaSuccess
-               ? 0
-               : -5;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = a.stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, fa_kvq8_move_kernel<D, FMT>, p) == cudaSuccess ? 0 : -5;
 }
 
 }  // namespace

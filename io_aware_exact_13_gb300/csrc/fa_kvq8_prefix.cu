@@ -15,7 +15,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads)
     fa_kvq8_prefix_merge(const float *own_o, const float *own_lse, const float *o_part, const float *lse_part, T *out,
                          float *lse, int rows, int splits) {
-    constexpr int LANES = D / 4;
+    constexpr int LANES = D / 4, AHEAD = 8;
     grid_dependency_wait();
     const long long id = (long long)blockIdx.x * kMergeThreads + threadIdx.x;
     const long long row = id / LANES;
@@ -33,17 +33,26 @@ __global__ void __launch_bounds__(kMergeThreads)
         float w = 0.f;
         if (s0 + lane <= splits) w = __expf((s0 + lane == 0 ? own_lse[row] : lse_part[(long long)(s0 + lane - 1) * rows + row]) - ref);
         const int n = min(LANES, splits + 1 - s0);
-#pragma unroll 8
-        for (int i = 0; i < n; ++i) {
-            const float f = __shfl_sync(mask, w, i, LANES);
-            if (f == 0.f) continue;  // a summary without keys holds nothing
-            const int s = s0 + i;
-            const float4 v = *reinterpret_cast<const float4 *>((s == 0 ? own_o : o_part + (long long)(s - 1) * rows * D) + row * D + 4 * lane);
-            W += f;
-            A.x = fmaf(f, v.x, A.x);
-            A.y = fmaf(f, v.y, A.y);
-            A.z = fmaf(f, v.z, A.z);
-            A.w = fmaf(f, v.w, A.w);
+        for (int i0 = 0; i0 < n; i0 += AHEAD) {
+            float f[AHEAD];
+            float4 v[AHEAD];
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                f[k] = __shfl_sync(mask, w, (i0 + k) % LANES, LANES);
+                if (i0 + k >= n) f[k] = 0.f;
+                const int s = s0 + i0 + k;
+                v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (f[k] != 0.f)  // a summary without keys holds nothing
+                    v[k] = *reinterpret_cast<const float4 *>((s == 0 ? own_o : o_part + (long long)(s - 1) * rows * D) + row * D + 4 * lane);
+            }
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                W += f[k];
+                A.x = fmaf(f[k], v[k].x, A.x);
+                A.y = fmaf(f[k], v[k].y, A.y);
+                A.z = fmaf(f[k], v[k].z, A.z);
+                A.w = fmaf(f[k], v[k].w, A.w);
+            }
         }
     }
     store4(out + row * D + 4 * lane, A, W == 0.f ? 0.f : 1.0f / W);

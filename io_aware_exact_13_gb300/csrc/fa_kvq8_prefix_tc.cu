@@ -98,6 +98,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(addr) : "memory");
+    return w;
+}
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
     const __half2 h = __floats2half2_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
@@ -384,7 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
             const bool regular = scan[4] == 0;
             const float up_k = __uint_as_float((uint32_t)(254 + 5 - scan[0]) << 23);  // 32 / ks_max where regular
             const float up_v = scan[2] == 0 ? 0.f : __uint_as_float((uint32_t)(254 + 5 - scan[2]) << 23);
-            constexpr int LANES = D / 16, STEP = kConv / LANES;  // 16-byte vectors of a key, keys of one pass
+            constexpr int LANES = D / 16, STEP = kConv / LANES, N = kBK128 / STEP;  // vectors of a key, keys of a pass, passes
             const int c = tid % LANES;
             uint32_t pos = 0;
             bool ok = true;
@@ -396,24 +401,25 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
                 const uint32_t src = smem_u32(smem + S::SMEM_RAW) + s * S::RAW_TILE + tid * 16;
                 const uint32_t dst = smem_u32(smem + (v ? S::SMEM_V : S::SMEM_K)) + slot * C::KV_TILE + (c / 4) * C::KV_CHUNK;
                 const int in_tile = key_end - (key_first + j * kBK128);  // keys of this block
-                const float up = regular ? (v ? up_v : up_k) : 1.0f;
+                const float up = v ? up_v : up_k;
+                // every load ahead of the first store
+                uint4 w[N];
+                float scale[N];
 #pragma unroll
-                for (int i = 0; i < kBK128 / STEP; ++i) {
+                for (int i = 0; i < N; ++i) w[i] = ld_shared_v4(src + i * kConv * 16);
+#pragma unroll
+                for (int i = 0; i < N; ++i) scale[i] = meta[s * 8 + (i * STEP + tid / LANES) / 16];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
                     const int key = i * STEP + tid / LANES;
-                    const float scale = meta[s * 8 + key / 16];
-                    const float m = regular ? scale * up : 1.0f;
-                    uint4 w;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
-                                 : "r"(src + i * kConv * 16)
-                                 : "memory");
+                    const float m = regular ? scale[i] * up : 1.0f;
                     uint32_t h[8];
                     const uint32_t mul = half2_bits(m, m), bias = half2_bits(-1152.0f * m, -1152.0f * m);
-                    codes_scaled<FMT>(w.x, mul, bias, h[0], h[1]);
-                    codes_scaled<FMT>(w.y, mul, bias, h[2], h[3]);
-                    codes_scaled<FMT>(w.z, mul, bias, h[4], h[5]);
-                    codes_scaled<FMT>(w.w, mul, bias, h[6], h[7]);
-                    if (key >= in_tile || scale < 0.f) {  // nothing there: zeros, whatever the codes were
+                    codes_scaled<FMT>(w[i].x, mul, bias, h[0], h[1]);
+                    codes_scaled<FMT>(w[i].y, mul, bias, h[2], h[3]);
+                    codes_scaled<FMT>(w[i].z, mul, bias, h[4], h[5]);
+                    codes_scaled<FMT>(w[i].w, mul, bias, h[6], h[7]);
+                    if (key >= in_tile || scale[i] < 0.f) {  // nothing there: zeros, whatever the codes were
 #pragma unroll
                         for (int e = 0; e < 8; ++e) h[e] = 0u;
                     }
@@ -422,13 +428,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
                     const uint32_t line = dst + key * 128, u0 = (uint32_t)(2 * (c % 4)), x = (uint32_t)(key & 7);
                     const bool swap = D == 128 && c >= 4;
                     const uint32_t first = ((u0 + (swap ? 1u : 0u)) ^ x) * 16, second = ((u0 + (swap ? 0u : 1u)) ^ x) * 16;
-                    if (swap) {
-                        st_shared_v4(line + first, h[4], h[5], h[6], h[7]);
-                        st_shared_v4(line + second, h[0], h[1], h[2], h[3]);
-                    } else {
-                        st_shared_v4(line + first, h[0], h[1], h[2], h[3]);
-                        st_shared_v4(line + second, h[4], h[5], h[6], h[7]);
-                    }
+                    st_shared_v4(line + first, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
+                    st_shared_v4(line + second, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
                 }
                 mbar_arrive(raw_empty(s));
                 fence_proxy_async_smem();

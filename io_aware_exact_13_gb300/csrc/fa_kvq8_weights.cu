@@ -8,7 +8,7 @@
 //
 // Bound: HBM, the K codes once and eight bytes of weight for each key and head. As in the attention (fa_kvq8_attn.cu) the
 // codes are the 16-row operand of 16x8x16 MMAs, cut from a lane's own 16-byte loads, and up to 32 query rows are the
-// columns; further rows go over the chunk again. bf16 queries enter in fp16 under a power of two for each row.
+// columns; further rows use the codes in the registers again. bf16 queries enter in fp16 under a power of two for each row.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -24,8 +24,9 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTileKeys = 16;
-constexpr int kTiles = 4;                                    // 16-key tiles of a warp
-constexpr int kChunk = kWarps * kTiles * kTileKeys;          // keys of a CTA
+// 16-key tiles of a warp, all in registers, and keys of a CTA.
+__host__ __device__ constexpr int w_tiles(int D, int NT) { return D == 128 || NT == 4 ? 2 : 4; }
+__host__ __device__ constexpr int w_chunk(int D, int NT) { return kWarps * w_tiles(D, NT) * kTileKeys; }
 
 struct WeightParams {
     const void *q;
@@ -46,10 +47,10 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// One CTA: kChunk keys of one (sequence, K/V head); warp w takes tiles w, w + kWarps, ...
+// One CTA: a chunk of keys of one (sequence, K/V head); warp w takes tiles w, w + kWarps, ...
 template <typename T, int D, int FMT, int NT, bool CAUSAL>
-__global__ void __launch_bounds__(kWarps * 32) fa_kvq8_weights_kernel(const WeightParams p) {
-    constexpr int KB = D / 64, KS = D / 16;
+__global__ void __launch_bounds__(kWarps * 32, NT == 4 ? 3 : 4) fa_kvq8_weights_kernel(const WeightParams p) {
+    constexpr int KB = D / 64, KS = D / 16, kTiles = w_tiles(D, NT), kChunk = w_chunk(D, NT);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     int u = blockIdx.x;
     const int chunk = u % p.chunks;
@@ -86,9 +87,24 @@ __global__ void __launch_bounds__(kWarps * 32) fa_kvq8_weights_kernel(const Weig
             }
         }
     }
-    float sum[kTiles][2];
+    uint32_t kw[kTiles][2][KB][4];  // rows g and g + 8 of each tile
+    float sum[kTiles][2], before[kTiles];
+    float *weight = p.weight + (((size_t)b * p.Hkv + kvh) * p.max_pages << p.page_shift) + k0 + g + 8 * c;
 #pragma unroll
-    for (int t = 0; t < kTiles; ++t) sum[t][0] = sum[t][1] = 0.f;
+    for (int t = 0; t < kTiles; ++t) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < KB; ++j) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (g + 8 * r < n_keys[t]) v = __ldcs(reinterpret_cast<const uint4 *>(src[t] + 8 * r * D + j * 64));
+                kw[t][r][j][0] = v.x, kw[t][r][j][1] = v.y, kw[t][r][j][2] = v.z, kw[t][r][j][3] = v.w;
+            }
+        sum[t][0] = sum[t][1] = 0.f;
+    }
+#pragma unroll
+    for (int t = 0; t < kTiles; ++t)  // lanes c = 0, 1 look after keys g and g + 8
+        before[t] = c < 2 && g + 8 * c < n_keys[t] ? weight[t * kWarps * kTileKeys] : 0.f;
 
     const size_t row_base = ((size_t)b * p.H + (size_t)kvh * (p.H / p.Hkv)) * p.Nq;
     for (int row0 = 0; row0 < p.rows; row0 += 8 * NT) {
@@ -145,16 +161,6 @@ __global__ void __launch_bounds__(kWarps * 32) fa_kvq8_weights_kernel(const Weig
         }
 #pragma unroll
         for (int i = 0; i < kTiles; ++i) {
-            if (n_keys[i] == 0) continue;
-            uint32_t kw[2][KB][4];
-#pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int j = 0; j < KB; ++j) {
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (g + 8 * r < n_keys[i]) v = __ldg(reinterpret_cast<const uint4 *>(src[i] + 8 * r * D + j * 64));
-                    kw[r][j][0] = v.x, kw[r][j][1] = v.y, kw[r][j][2] = v.z, kw[r][j][3] = v.w;
-                }
             float x[NT][4];
 #pragma unroll
             for (int t = 0; t < NT; ++t) x[t][0] = x[t][1] = x[t][2] = x[t][3] = 0.f;
@@ -163,8 +169,8 @@ __global__ void __launch_bounds__(kWarps * 32) fa_kvq8_weights_kernel(const Weig
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     uint32_t a[4];
-                    codes_to_half2<FMT>(kw[0][j][e], a[0], a[2]);
-                    codes_to_half2<FMT>(kw[1][j][e], a[1], a[3]);
+                    codes_to_half2<FMT>(kw[i][0][j][e], a[0], a[2]);
+                    codes_to_half2<FMT>(kw[i][1][j][e], a[1], a[3]);
 #pragma unroll
                     for (int t = 0; t < NT; ++t) mma_f16(x[t], a, qb[t][4 * j + e][0], qb[t][4 * j + e][1]);
                 }
@@ -190,16 +196,13 @@ __global__ void __launch_bounds__(kWarps * 32) fa_kvq8_weights_kernel(const Weig
             sum[i][r] += __shfl_xor_sync(0xffffffffu, sum[i][r], 1);
             sum[i][r] += __shfl_xor_sync(0xffffffffu, sum[i][r], 2);
         }
-        const int key = g + 8 * c;  // lanes c = 0, 1 write keys g and g + 8
-        if (c < 2 && key < n_keys[i]) {
-            float *at = p.weight + (((size_t)b * p.Hkv + kvh) * p.max_pages << p.page_shift) + k0 + i * kWarps * kTileKeys + key;
-            *at += sum[i][c];
-        }
+        if (c < 2 && g + 8 * c < n_keys[i]) weight[i * kWarps * kTileKeys] = before[i] + (c == 0 ? sum[i][0] : sum[i][1]);
     }
 }
 
 template <typename T, int D, int FMT, int NT>
 int launch_nt(const Kvq8WeightsArgs &a, WeightParams &p) {
+    p.chunks = (a.max_len + w_chunk(D, NT) - 1) / w_chunk(D, NT);
     const long long grid = (long long)p.chunks * p.Hkv * a.B;
     if (grid > INT32_MAX) return -3;
     if (a.causal)
@@ -224,7 +227,6 @@ int launch_t(const Kvq8WeightsArgs &a) {
     p.Hkv = a.c.Hkv;
     p.Nq = a.Nq;
     p.rows = a.H / a.c.Hkv * a.Nq;
-    p.chunks = (a.max_len + kChunk - 1) / kChunk;
     p.n_pages = a.c.n_pages;
     p.max_pages = a.c.max_pages;
     p.page_shift = kvq8_page_shift(a.c.page);

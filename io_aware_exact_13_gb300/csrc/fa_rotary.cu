@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <stdlib.h>
 #include <type_traits>
 
 #include "fa_rotary.cuh"
@@ -137,6 +138,11 @@ int launch_t(const RotaryArgs &a) {
     p.inverse = a.inverse;
     p.tokens = (long long)a.B * a.N;
     const int heads = a.x[0].heads + a.x[1].heads;
+    const char *e = getenv("RH");
+    const int hh = e ? atoi(e) : 4;
+    if (hh == 1) return launch_heads<T, 1>(p, p.tokens, heads, a.stream);
+    if (hh == 2) return launch_heads<T, 2>(p, p.tokens, heads, a.stream);
+    if (hh == 8) return launch_heads<T, 8>(p, p.tokens, heads, a.stream);
     return launch_heads<T, 4>(p, p.tokens, heads, a.stream);
 }
 
