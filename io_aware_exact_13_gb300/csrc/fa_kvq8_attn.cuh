@@ -200,7 +200,7 @@ __device__ __forceinline__ void store4(T *dst, float4 a, float f) {
 }
 
 template <typename T, int D, int FMT, int NT, bool CAUSAL, int MODE>
-__global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_partial(const Q8Params p) {
+__device__ __forceinline__ void q8_partial(const Q8Params &p) {
     using C = Q8Cfg<D, NT>;
     using OT = typename std::conditional<MODE == kQ8Summary, float, T>::type;
     constexpr bool PREFIX = MODE == kQ8Prefix;
@@ -775,6 +775,13 @@ __global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_parti
     }
 }
 
+template <typename T, int D, int FMT, int NT, bool CAUSAL, int MODE>
+__global__ void __launch_bounds__(kWarps * 32, Q8Cfg<D, NT>::CTAS) fa_kvq8_partial(const Q8Params p) {
+    q8_partial<T, D, FMT, NT, CAUSAL, MODE>(p);
+    // A summary's kernel starts beside the prefix's, of which it needs nothing; it ends behind it, for the merge.
+    if constexpr (MODE == kQ8Summary) grid_dependency_wait();
+}
+
 // The units that several parts share: their summaries merged onto their common maximum (fa_splitkv.cu's rule). A unit
 // that n parts share is merged by the CTAs of its parts but the first, each doing every (n - 1)-th row; where a CTA has
 // few rows, several groups of threads share a row's summaries out.
@@ -785,6 +792,7 @@ __global__ void __launch_bounds__(kCombineThreads) fa_kvq8_combine(const Q8Param
     constexpr int AHEAD = 8;                                      // summaries loaded before the first is used
     __shared__ float4 sm_a[SLOTS][LANES];
     __shared__ float sm_m[SLOTS], sm_w[SLOTS];
+    if constexpr (std::is_same<T, float>::value) grid_launch_dependents();  // a summary: the merge behind it
     grid_dependency_wait();
     const int4 d = p.shared[blockIdx.x];
     if (d.x < 0) return;
@@ -930,12 +938,21 @@ int launch_q8(const Kvq8AttnArgs &a) {
     cfg.blockDim = dim3(kWarps * 32);
     cfg.dynamicSmemBytes = C::SMEM;
     cfg.stream = a.stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = p.cluster;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchAttribute attr[2];
+    int attrs = 0;
+    if (p.cluster > 1) {
+        attr[attrs].id = cudaLaunchAttributeClusterDimension;
+        attr[attrs].val.clusterDim.x = p.cluster;
+        attr[attrs].val.clusterDim.y = attr[attrs].val.clusterDim.z = 1;
+        ++attrs;
+    }
+    if (MODE == kQ8Summary) {
+        attr[attrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[attrs].val.programmaticStreamSerializationAllowed = 1;
+        ++attrs;
+    }
     cfg.attrs = attr;
-    cfg.numAttrs = p.cluster > 1 ? 1 : 0;
+    cfg.numAttrs = attrs;
     if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return -5;
     if (cudaGetLastError() != cudaSuccess) return -5;
     if (a.parts <= 1) return 0;

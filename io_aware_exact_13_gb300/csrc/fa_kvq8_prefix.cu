@@ -8,6 +8,7 @@ namespace fa {
 namespace {
 
 constexpr int kMergeThreads = 128;
+constexpr int kRunBlocks = 5;  // blocks of 128 keys of a run, at least
 
 // out = sum_s w_s o_s / sum_s w_s with w_s = exp(lse_s - max lse), over the own keys' summary and those of the prefix's
 // runs (fa_splitkv.cu's rule). Four columns of a row for each thread; the lanes of a row share the weights out.
@@ -15,7 +16,7 @@ template <typename T, int D>
 __global__ void __launch_bounds__(kMergeThreads)
     fa_kvq8_prefix_merge(const float *own_o, const float *own_lse, const float *o_part, const float *lse_part, T *out,
                          float *lse, int rows, int splits) {
-    constexpr int LANES = D / 4, AHEAD = 8;
+    constexpr int LANES = D / 4, AHEAD = 16;
     grid_dependency_wait();
     const long long id = (long long)blockIdx.x * kMergeThreads + threadIdx.x;
     const long long row = id / LANES;
@@ -78,9 +79,8 @@ int kvq8_prefix_splits(int B, int Hkv, int rows, int max_prefix, int max_len, in
     const long long all = (long long)B * rows;
     if (all < 24 || max_prefix < 512) return 0;
     const long long units = Hkv * ((all + 255) / 256);
-    const int blocks = (max_prefix + 127) / 128;
-    const long long most = num_sms / units;
-    return (int)(most < 1 ? 1 : most < blocks ? most : blocks);
+    const int most = (int)(num_sms / units), by_len = (max_prefix + 128 * kRunBlocks - 1) / (128 * kRunBlocks);
+    return most < 1 ? 1 : most < by_len ? most : by_len;
 }
 
 // Own summary, the runs' summaries, and what the own keys' parts take.
@@ -101,14 +101,13 @@ int launch_kvq8_prefix(const Kvq8AttnArgs &a, bool fp16) {
         return x;
     };
     float *own_o = take(n * d * 4), *own_lse = take(n * 4), *o_part = take(a.splits * n * d * 4), *lse_part = take(a.splits * n * 4);
-    int rc = launch_kvq8_prefix_tc(a, fp16, o_part, lse_part);
-    if (rc != 0) return rc;
     Kvq8AttnArgs own = a;
     own.out = own_o;
     own.lse = own_lse;
     own.workspace = reinterpret_cast<float *>(at);
     own.max_prefix = 0;
-    rc = launch_kvq8_prefix_own(own, fp16);
+    int rc = launch_kvq8_prefix_tc(a, fp16, o_part, lse_part);
+    if (rc == 0) rc = launch_kvq8_prefix_own(own, fp16);
     if (rc != 0) return rc;
     if (a.c.d == 128)
         return fp16 ? launch_merge<__half, 128>(a, own_o, own_lse, o_part, lse_part)

@@ -20,7 +20,9 @@
 //   warps 0-7    softmax and epilogue of the two tiles; each thread first brings its own row of Q
 //   warp  8      loader: whole pages by bulk copies into a ring of raw codes, with the pages' scales
 //   warp  9      S issuer,  warps 10-11 P V issuers
-//   warps 12-15  converters: raw codes -> fp16 in the 128-byte swizzled K and V tiles
+//   warps 12-19  converters: raw codes -> fp16 in the 128-byte swizzled K and V tiles
+// The own keys' kernel behind it is a programmatic dependent that needs nothing of it: it fills the SMs that this one leaves
+// free, and ends after it, so that the merge behind may rely on both.
 #include <float.h>
 
 #include "fa_fwd_bk128.cuh"
@@ -29,7 +31,8 @@
 namespace fa {
 namespace {
 
-constexpr int kConv = 128;          // converter threads
+constexpr int kConv = 256;          // converter threads
+constexpr int kPrefixThreads = 384 + kConv;
 
 constexpr int kSpread = 20;         // log2 of the scales' range that stays exact
 constexpr float kNone = -FLT_MAX;   // a running maximum that has seen no key
@@ -38,18 +41,18 @@ template <int D>
 struct PrefixCfg {
     using C = Cfg128<__half, D>;
     static constexpr int RK = 2, RV = 2;
-    static constexpr int RAW = D == 128 ? 2 : 4;  // tiles of raw codes in flight
+    static constexpr int RAW = D == 128 ? 2 : 4;  // tiles of raw codes in flight, and two more where there is no second Q tile
     static constexpr int RAW_TILE = kBK128 * D;
     static constexpr int SMEM_Q = 0;
     static constexpr int SMEM_K = 2 * C::Q_TILE;
     static constexpr int SMEM_V = SMEM_K + RK * C::KV_TILE;
     static constexpr int SMEM_RAW = SMEM_V + RV * C::KV_TILE;
-    static constexpr int SMEM_META = SMEM_RAW + RAW * RAW_TILE;  // float[RAW][8]: the scales of a raw tile, -1: no page
-    static constexpr int SMEM_SCAN = SMEM_META + RAW * 32;       // int[8]
+    static constexpr int SMEM_META = SMEM_RAW + RAW * RAW_TILE;  // float[RAW + 2][8]: the scales of a raw tile, -1: no page
+    static constexpr int SMEM_SCAN = SMEM_META + (RAW + 2) * 32;  // int[8]
     static constexpr int SMEM_BAR = SMEM_SCAN + 32;
-    // raw_full, raw_empty [RAW]; k_full, k_empty [RK]; v_full, v_empty [RV]; q_full[2] s_full[2] s_free p_full[2]
+    // raw_full, raw_empty [RAW + 2]; k_full, k_empty [RK]; v_full, v_empty [RV]; q_full[2] s_full[2] s_free p_full[2]
     // pv_done[2][2] drain s_issued[2][2] scan
-    static constexpr int B_K = 2 * RAW, B_V = B_K + 2 * RK, B_Q = B_V + 2 * RV, NUM_BARS = B_Q + 2 + 2 + 1 + 2 + 4 + 1 + 4 + 1;
+    static constexpr int B_K = 2 * (RAW + 2), B_V = B_K + 2 * RK, B_Q = B_V + 2 * RV, NUM_BARS = B_Q + 2 + 2 + 1 + 2 + 4 + 1 + 4 + 1;
     static constexpr int SMEM_TMEM_SLOT = SMEM_BAR + NUM_BARS * 8;
     static constexpr int SMEM_ABORT = SMEM_TMEM_SLOT + 8;
     static constexpr int SMEM_USED = SMEM_ABORT + 8;
@@ -98,9 +101,9 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
-    uint4 w;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(addr) : "memory");
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+    uint2 w;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "r"(addr) : "memory");
     return w;
 }
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
@@ -130,16 +133,16 @@ __device__ __forceinline__ void codes_scaled(uint32_t w, uint32_t mul, uint32_t 
 }
 
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const PrefixParams p) {
+__global__ void __launch_bounds__(kPrefixThreads, 1) fa_kvq8_prefix_kernel(const PrefixParams p) {
     using S = PrefixCfg<D>;
     using C = typename S::C;
-    constexpr int RK = S::RK, RV = S::RV, RAW = S::RAW;
+    constexpr int RK = S::RK, RV = S::RV;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t pad = (uint32_t)((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
     uint8_t *smem = smem_raw + pad;
     const uint32_t bars = smem_u32(smem + S::SMEM_BAR);
     auto raw_full = [&](int s) { return bars + 8 * s; };
-    auto raw_empty = [&](int s) { return bars + 8 * (RAW + s); };
+    auto raw_empty = [&](int s) { return bars + 8 * (S::RAW + 2 + s); };
     auto k_full = [&](int s) { return bars + 8 * (S::B_K + s); };
     auto k_empty = [&](int s) { return bars + 8 * (S::B_K + RK + s); };
     auto v_full = [&](int s) { return bars + 8 * (S::B_V + s); };
@@ -163,9 +166,12 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
     const int split = blockIdx.x / p.row_tiles % p.splits;
     const int kvh = blockIdx.x / p.row_tiles / p.splits;
     const int tiles = p.rows - rt * 2 * kBQ > kBQ ? 2 : 1;
+    const uint32_t raw_slots = tiles == 1 ? S::RAW + 2 : S::RAW;
+    auto raw_tile = [&](int s) {
+        return smem_u32(smem) + (s < S::RAW ? S::SMEM_RAW + s * S::RAW_TILE : S::SMEM_Q + C::Q_TILE + (s - S::RAW) * S::RAW_TILE);
+    };
 
     grid_launch_dependents();
-    grid_dependency_wait();
     int len = __ldg(p.prefix_len);
     if (len < 0 || len > p.max_prefix) {
         if (blockIdx.x == 0 && threadIdx.x == 0) atomicExch(p.status, kStatusSeqlensQ8);
@@ -189,8 +195,60 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
         return;
     }
 
+    // What the roles read first is requested before the set-up: the row of Q, the first pages, the scales of the run's pages.
+    const int page = 1 << p.page_shift;
+    uint32_t qw[D / 2];  // softmax warps
+    struct Group {       // loader: page and scales of a 16-key group
+        int phys;
+        float ks, vs;
+    };
+    auto entry = [&](int j) {
+        const int key = key_first + j * kBK128 + lane * 16;
+        return j < nb && lane < 8 && key < key_end ? __ldg(p.prefix_table + (key >> p.page_shift)) : -1;
+    };
+    auto scales = [&](int phys) {
+        Group g = {-1, -1.f, -1.f};
+        if (phys >= 0 && phys < p.n_pages) {
+            const size_t at = (size_t)phys * p.Hkv + kvh;
+            g = {phys, __ldg(p.k_scale + at), __ldg(p.v_scale + at)};
+        }
+        return g;
+    };
+    Group next = {-1, -1.f, -1.f};
+    int ahead = -1;
+    int most_k = 0, least_k = 255, most_v = 0, least_v = 255, odd = 0;  // converters: exponents of the scales
+    if (warp < 8) {
+        const T *src = static_cast<const T *>(p.q) + out_row * D;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+            qw[4 * i] = x.x, qw[4 * i + 1] = x.y, qw[4 * i + 2] = x.z, qw[4 * i + 3] = x.w;
+        }
+    } else if (warp == 8) {
+        ahead = entry(1);
+        next = scales(entry(0));
+    } else if (warp >= 12) {
+        const int last = (key_end - 1) >> p.page_shift;
+        for (int i = (key_first >> p.page_shift) + (int)threadIdx.x - 12 * 32; i <= last; i += kConv) {
+            const int phys = __ldg(p.prefix_table + i);
+            if (phys < 0 || phys >= p.n_pages) {
+                atomicExch(p.status, kStatusPage);
+                odd = 1;
+                continue;
+            }
+            const size_t at = (size_t)phys * p.Hkv + kvh;
+            const uint32_t k = __float_as_uint(__ldg(p.k_scale + at)), v = __float_as_uint(__ldg(p.v_scale + at));
+            odd |= (k & 0x807FFFFFu) != 0 || (v & 0x807FFFFFu) != 0;
+            const int ek = (int)(k >> 23), ev = (int)(v >> 23);
+            most_k = max(most_k, ek);
+            most_v = max(most_v, ev);
+            if (k) least_k = min(least_k, ek);
+            if (v) least_v = min(least_v, ev);
+        }
+    }
+
     if (threadIdx.x == 0) {
-        for (int s = 0; s < RAW; ++s) {
+        for (int s = 0; s < S::RAW + 2; ++s) {
             mbar_init(raw_full(s), 1);
             mbar_init(raw_empty(s), kConv);
         }
@@ -231,32 +289,15 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
 
     if (warp >= 8) {
-        setmaxnreg_dec<72>();
+        setmaxnreg_dec<48>();
         if (warp == 8) {
             // ---------------------------------------------------------- loader: K_0, then K_{j+1}, V_j
             // Lane i < 8 looks after the 16-key group i of a block; pages and scales are read a block ahead.
-            const int page = 1 << p.page_shift;
-            auto entry = [&](int j) {
-                const int key = key_first + j * kBK128 + lane * 16;
-                return j < nb && lane < 8 && key < key_end ? __ldg(p.prefix_table + (key >> p.page_shift)) : -1;
-            };
-            struct Group {
-                int phys;
-                float ks, vs;
-            };
-            auto scales = [&](int phys) {
-                Group g = {-1, -1.f, -1.f};
-                if (phys >= 0 && phys < p.n_pages) {
-                    const size_t at = (size_t)phys * p.Hkv + kvh;
-                    g = {phys, __ldg(p.k_scale + at), __ldg(p.v_scale + at)};
-                }
-                return g;
-            };
             uint32_t pos = 0;
             bool ok = true;
             auto load = [&](const Group &g, bool v) {
-                const int s = pos % RAW;
-                ok = wait_all(raw_empty(s), ((pos / RAW) & 1u) ^ 1u, abort_flag, p);
+                const int s = pos % raw_slots;
+                ok = wait_all(raw_empty(s), ((pos / raw_slots) & 1u) ^ 1u, abort_flag, p);
                 if (!ok) return;
                 if (lane < 8) meta[s * 8 + lane] = g.phys < 0 ? -1.f : v ? g.vs : g.ks;
                 const bool issue = g.phys >= 0 && ((lane * 16) & (page - 1)) == 0;  // a page's first group
@@ -266,13 +307,12 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
                 if (lane == 0) mbar_arrive_expect_tx(raw_full(s), bytes * n);
                 __syncwarp();
                 if (issue)
-                    bulk_load(smem_u32(smem + S::SMEM_RAW) + s * S::RAW_TILE + lane * 16 * D,
+                    bulk_load(raw_tile(s) + lane * 16 * D,
                               (v ? p.v_codes : p.k_codes) + (((size_t)g.phys * p.Hkv + kvh) << p.page_shift) * D, bytes,
                               raw_full(s));
                 ++pos;
             };
-            Group cur = {-1, 0.f, 0.f}, next = scales(entry(0));
-            int ahead = entry(1);
+            Group cur = {-1, 0.f, 0.f};
             for (int j = -1; ok && j < nb; ++j) {
                 const Group after = scales(ahead);  // of block j + 2
                 ahead = entry(j + 3);
@@ -283,8 +323,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
             }
             if (!ok && lane == 0) {  // let the copies in flight land before the CTA can exit
                 const uint64_t t0 = global_timer_ns();
-                for (uint32_t i = pos > (uint32_t)RAW ? pos - RAW : 0; i < pos; ++i)
-                    while (!mbar_try_wait(raw_full(i % RAW), (i / RAW) & 1u) && global_timer_ns() - t0 < p.timeout_ns) {
+                for (uint32_t i = pos > raw_slots ? pos - raw_slots : 0; i < pos; ++i)
+                    while (!mbar_try_wait(raw_full(i % raw_slots), (i / raw_slots) & 1u) && global_timer_ns() - t0 < p.timeout_ns) {
                     }
             }
         } else if (warp == 9) {
@@ -346,24 +386,6 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
             // ---------------------------------------------------------- converters
             const int tid = threadIdx.x - 12 * 32;
             {  // the scales of the run's pages
-                const int first = key_first >> p.page_shift, last = (key_end - 1) >> p.page_shift;
-                int most_k = 0, least_k = 255, most_v = 0, least_v = 255, odd = 0;
-                for (int i = first + tid; i <= last; i += kConv) {
-                    const int phys = __ldg(p.prefix_table + i);
-                    if (phys < 0 || phys >= p.n_pages) {
-                        atomicExch(p.status, kStatusPage);
-                        odd = 1;
-                        continue;
-                    }
-                    const size_t at = (size_t)phys * p.Hkv + kvh;
-                    const uint32_t k = __float_as_uint(__ldg(p.k_scale + at)), v = __float_as_uint(__ldg(p.v_scale + at));
-                    odd |= (k & 0x807FFFFFu) != 0 || (v & 0x807FFFFFu) != 0;
-                    const int ek = (int)(k >> 23), ev = (int)(v >> 23);
-                    most_k = max(most_k, ek);
-                    most_v = max(most_v, ev);
-                    if (k) least_k = min(least_k, ek);
-                    if (v) least_v = min(least_v, ev);
-                }
                 most_k = __reduce_max_sync(0xffffffffu, most_k);
                 most_v = __reduce_max_sync(0xffffffffu, most_v);
                 least_k = __reduce_min_sync(0xffffffffu, least_k);
@@ -390,46 +412,54 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
             const float up_k = __uint_as_float((uint32_t)(254 + 5 - scan[0]) << 23);  // 32 / ks_max where regular
             const float up_v = scan[2] == 0 ? 0.f : __uint_as_float((uint32_t)(254 + 5 - scan[2]) << 23);
             constexpr int LANES = D / 16, STEP = kConv / LANES, N = kBK128 / STEP;  // vectors of a key, keys of a pass, passes
-            const int c = tid % LANES;
+            const int c = tid % LANES, swap = D == 128 && c >= 4 ? 1 : 0;
+            // the lane's two units in its keys' rows (a pass is a multiple of 8 keys: the swizzle is the same in each)
+            const uint32_t unit0 = (uint32_t)((2 * (c % 4) + swap) ^ (tid / LANES & 7)) * 16;
+            const uint32_t unit1 = (uint32_t)((2 * (c % 4) + 1 - swap) ^ (tid / LANES & 7)) * 16;
             uint32_t pos = 0;
             bool ok = true;
             auto convert = [&](int j, bool v) {
-                const int s = pos % RAW, slot = j % 2;
-                ok = wait_all(raw_full(s), (pos / RAW) & 1u, abort_flag, p);
+                const int s = pos % raw_slots, slot = j % 2;
+                ok = wait_all(raw_full(s), (pos / raw_slots) & 1u, abort_flag, p);
                 if (ok) ok = wait_all(v ? v_empty(slot) : k_empty(slot), ((uint32_t)(j / 2) & 1u) ^ 1u, abort_flag, p);
                 if (!ok) return;
-                const uint32_t src = smem_u32(smem + S::SMEM_RAW) + s * S::RAW_TILE + tid * 16;
-                const uint32_t dst = smem_u32(smem + (v ? S::SMEM_V : S::SMEM_K)) + slot * C::KV_TILE + (c / 4) * C::KV_CHUNK;
+                const uint32_t src = raw_tile(s) + tid * 16;
+                const uint32_t dst = smem_u32(smem + (v ? S::SMEM_V : S::SMEM_K)) + slot * C::KV_TILE + (c / 4) * C::KV_CHUNK +
+                                     (tid / LANES) * 128;
+                const uint32_t dst0 = dst + unit0, dst1 = dst + unit1;
                 const int in_tile = key_end - (key_first + j * kBK128);  // keys of this block
                 const float up = v ? up_v : up_k;
-                // every load ahead of the first store
-                uint4 w[N];
-                float scale[N];
-#pragma unroll
-                for (int i = 0; i < N; ++i) w[i] = ld_shared_v4(src + i * kConv * 16);
-#pragma unroll
-                for (int i = 0; i < N; ++i) scale[i] = meta[s * 8 + (i * STEP + tid / LANES) / 16];
+                // A key's 16 dims are two 16-byte units of its 128-byte row. At d = 128 the upper lanes take theirs the
+                // other way round, so that eight lanes meet all banks. Every load goes ahead of the first store.
+                uint2 w[2][N];
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const int key = i * STEP + tid / LANES;
-                    const float m = regular ? scale[i] * up : 1.0f;
-                    uint32_t h[8];
-                    const uint32_t mul = half2_bits(m, m), bias = half2_bits(-1152.0f * m, -1152.0f * m);
-                    codes_scaled<FMT>(w[i].x, mul, bias, h[0], h[1]);
-                    codes_scaled<FMT>(w[i].y, mul, bias, h[2], h[3]);
-                    codes_scaled<FMT>(w[i].z, mul, bias, h[4], h[5]);
-                    codes_scaled<FMT>(w[i].w, mul, bias, h[6], h[7]);
-                    if (key >= in_tile || scale[i] < 0.f) {  // nothing there: zeros, whatever the codes were
+                    w[0][i] = ld_shared_v2(src + i * kConv * 16 + 8 * swap);
+                    w[1][i] = ld_shared_v2(src + i * kConv * 16 + 8 - 8 * swap);
+                }
+                const float scale = meta[s * 8 + (lane & 7)];  // lane e: of the 16-key group e
+                const float m = regular ? scale * up : 1.0f;
+                const uint32_t mul_of = half2_bits(m, m);
+                const bool whole = in_tile >= kBK128 && __all_sync(0xffffffffu, scale >= 0.f);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) h[e] = 0u;
+                for (int i = 0; i < N; ++i) {
+                    const int key = i * STEP + tid / LANES, group = key / 16;  // (of the whole warp)
+                    const uint32_t mul = __shfl_sync(0xffffffffu, mul_of, group);
+                    const uint32_t bias = FMT == kKvq8Int8 ? hmul2_bits(mul, 0xE480E480u) : 0u;  // -1152
+                    uint32_t h[8];
+                    codes_scaled<FMT>(w[0][i].x, mul, bias, h[0], h[1]);
+                    codes_scaled<FMT>(w[0][i].y, mul, bias, h[2], h[3]);
+                    codes_scaled<FMT>(w[1][i].x, mul, bias, h[4], h[5]);
+                    codes_scaled<FMT>(w[1][i].y, mul, bias, h[6], h[7]);
+                    if (!whole) {  // keys that are none are zeros, whatever the codes were
+                        const float there = __shfl_sync(0xffffffffu, scale, group);
+                        if (key >= in_tile || there < 0.f) {
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) h[e] = 0u;
+                        }
                     }
-                    // 16 dims are two 16-byte units of the key's 128-byte row; the upper lanes store theirs the other way
-                    // round, so that eight lanes meet all banks
-                    const uint32_t line = dst + key * 128, u0 = (uint32_t)(2 * (c % 4)), x = (uint32_t)(key & 7);
-                    const bool swap = D == 128 && c >= 4;
-                    const uint32_t first = ((u0 + (swap ? 1u : 0u)) ^ x) * 16, second = ((u0 + (swap ? 0u : 1u)) ^ x) * 16;
-                    st_shared_v4(line + first, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
-                    st_shared_v4(line + second, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+                    st_shared_v4(dst0 + i * STEP * 128, h[0], h[1], h[2], h[3]);
+                    st_shared_v4(dst1 + i * STEP * 128, h[4], h[5], h[6], h[7]);
                 }
                 mbar_arrive(raw_empty(s));
                 fence_proxy_async_smem();
@@ -442,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
             }
         }
     } else {
-        setmaxnreg_inc<184>();
+        setmaxnreg_inc<168>();
         if (t < tiles) {
             // ---------------------------------------------------------- softmax and epilogue of tile t
             const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
@@ -453,14 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
             // Q: this thread's row, in fp16
             float qmul = 1.0f;  // what the row was divided by
             {
-                const T *src = static_cast<const T *>(p.q) + out_row * D;
                 const uint32_t line = smem_u32(smem + S::SMEM_Q) + t * C::Q_TILE + r * 128;
-                uint32_t w[D / 2];
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const uint4 x = live ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
-                    w[4 * i] = x.x, w[4 * i + 1] = x.y, w[4 * i + 2] = x.z, w[4 * i + 3] = x.w;
-                }
+                uint32_t (&w)[D / 2] = qw;
                 if constexpr (std::is_same<T, __nv_bfloat16>::value) {
                     uint32_t most = 0;
 #pragma unroll
@@ -545,11 +569,11 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
                     const float2 sl2v = make_float2(mul, mul), negv = make_float2(neg, neg);
                     float2 ls[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t pv[32];
+                    for (int h = 0; h < 4; ++h) {
+                        uint32_t pv[16];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) {
-                            const float2 a = ffma2(make_float2(x[64 * h + 2 * i], x[64 * h + 2 * i + 1]), sl2v, negv);
+                        for (int i = 0; i < 16; ++i) {
+                            const float2 a = ffma2(make_float2(x[32 * h + 2 * i], x[32 * h + 2 * i + 1]), sl2v, negv);
                             const float2 e = make_float2(ex2_approx(a.x), ex2_approx(a.y));
                             ls[i & 3] = fadd2(ls[i & 3], e);
                             pv[i] = half2_bits(e.x, e.y);
@@ -559,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, 1) fa_kvq8_prefix_kernel(const Prefi
                             if (!ok) break;
                             tc_fence_after();
                         }
-                        tmem_st32(p_addr + 32 * h, pv);
+                        tmem_st16(p_addr + 16 * h, pv);
                     }
                     if (!ok) break;
                     l += ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y)) + ((ls[2].x + ls[2].y) + (ls[3].x + ls[3].y));
@@ -674,7 +698,7 @@ int launch_tc(const PrefixParams &p, cudaStream_t stream) {
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES) != cudaSuccess) return -5;
     const long long grid = (long long)p.Hkv * p.row_tiles * p.splits;
     if (grid > INT32_MAX) return -3;
-    kern<<<(unsigned)grid, kThreads, S::SMEM_BYTES, stream>>>(p);
+    kern<<<(unsigned)grid, kPrefixThreads, S::SMEM_BYTES, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 
