@@ -606,6 +606,7 @@ int kvq8_weights_common(bool fp16, const void *q, const void *k_codes, const flo
     a.max_len = max_len;
     a.scale = scale;
     a.causal = causal ? 1 : 0;
+    a.num_sms = di->num_sms;
     a.status = di->status;
     a.stream = static_cast<cudaStream_t>(stream);
     log_call("8-bit cache weights %s format=%d page=%d d=%d causal=%d B=%d H=%d Hkv=%d Nq=%d max_len=%d",

@@ -69,7 +69,7 @@ struct Kvq8WeightsArgs {
     const int *kv_lens;
     int B, H, Nq, max_len;
     float scale;
-    int causal;
+    int causal, num_sms;
     int *status;
     cudaStream_t stream;
 };

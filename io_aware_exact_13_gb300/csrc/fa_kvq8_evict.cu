@@ -2,9 +2,8 @@
 //
 // Selection. Of a sequence's n > keep positions each K/V head keeps the last `recent` and, of the earlier ones, the
 // keep - recent of the greatest weight (ties: the lower position; NaN counts as the greatest). The weights are mapped to
-// integers of the same order, and T, the smallest that is kept, is found by counting how many reach a trial value, which is
-// placed by turns where an even spread would have it and in the middle of what is left (about 10 counts for
-// weights of a smooth distribution, 32 each way at most). All above T stay and, in order of position, as many equal to T as are missing. So the result
+// integers of the same order, and T, the smallest that is kept, is found by histograms of 2048 bins between the least
+// and the greatest, then within the bin that the count is reached in, three at most. All above T stay and, in order of position, as many equal to T as are missing. So the result
 // does not depend on timing.
 //
 // Moving. The kept tokens go, in their order, to positions 0 .. keep - 1 of the same pages, in place. A page whose tokens
@@ -34,7 +33,7 @@ struct EvictParams {
     const float *weight;
     float *weight_out;
     int *lens_out, *kept, *status;
-    int n_pages, max_pages, page_shift, Hkv, keep, recent, cluster;
+    int nseq, n_pages, max_pages, page_shift, Hkv, keep, recent, cluster;
 };
 
 __device__ __forceinline__ int evict_len(const EvictParams &p, int b, bool &bad) {
@@ -43,38 +42,54 @@ __device__ __forceinline__ int evict_len(const EvictParams &p, int b, bool &bad)
     return bad ? 0 : len;
 }
 
+// Sequences in the order of the CTAs that work on them: those that are cut down first, then the others, so that every SM gets
+// as many of the former. All lanes of a warp call.
+__device__ __forceinline__ int nth_sequence(const EvictParams &p, int nth, bool &cut) {
+    const int lane = threadIdx.x & 31;
+    int b = -1, before = 0;
+    cut = true;
+    for (;;) {
+        for (int s0 = 0; s0 < p.nseq && b < 0; s0 += 32) {
+            bool bad;
+            const bool in = s0 + lane < p.nseq;
+            uint32_t mine = __ballot_sync(0xffffffffu, in && (evict_len(p, s0 + lane, bad) > p.keep) == cut);
+            const int here = __popc(mine);
+            if (nth < before + here) {
+                for (int i = before; i < nth; ++i) mine &= mine - 1u;
+                b = s0 + __ffs(mine) - 1;
+            }
+            before += here;
+        }
+        if (b >= 0 || !cut) return b;
+        cut = false;
+    }
+}
+
 // Integers of the weights' order; NaN above all, -0 with 0.
 __device__ __forceinline__ uint32_t order_of(float w) {
     const uint32_t u = __float_as_uint(w + 0.0f);
     return isnan(w) ? 0xFFFFFFFFu : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
+// And back; all NaN are one.
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelEach = 16;  // consecutive positions of a thread
-constexpr int kSelChunk = kSelThreads * kSelEach;
+__device__ __forceinline__ float weight_of(uint32_t v) { return __uint_as_float(v & 0x80000000u ? v ^ 0x80000000u : ~v); }
 
-// Sum over the CTA; every thread gets it. Two buffers in turn, so one barrier a call.
-struct BlockSum {
-    int (*buf)[kSelThreads / 32];
-    int turn;
-    __device__ __forceinline__ int operator()(int x) {
-        x = __reduce_add_sync(0xffffffffu, x);
-        int *s = buf[turn];
-        turn ^= 1;
-        if ((threadIdx.x & 31) == 0) s[threadIdx.x >> 5] = x;
-        __syncthreads();
-        return __reduce_add_sync(0xffffffffu, s[threadIdx.x & 31]);
-    }
-};
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelMost = 24576;  // positions whose weights are kept in shared memory (two CTAs on an SM)
+constexpr int kBins = 2048, kBinBits = 11;
 
-// One CTA for each (sequence, head): the kept positions in order, the weights that go with them, the new length. Up to
-// kSelChunk positions stay in registers; longer sequences are read again for every bit.
-__global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const EvictParams p) {
-    __shared__ int sums[2][kSelThreads / 32];
-    __shared__ int offs[kSelThreads / 32];
-    __shared__ uint32_t ends[2][kSelThreads / 32];
-    grid_launch_dependents();
-    const int b = blockIdx.x / p.Hkv, head = blockIdx.x - b * p.Hkv;
+// One CTA for each (sequence, head): the kept positions in order, the weights that go with them, the new length. Weights
+// past the first `held` positions are read again for every count.
+__global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const EvictParams p, int held) {
+    extern __shared__ uint4 order_sm[];  // [held / 4] integers of the weights' order
+    __shared__ int bins[kBins];  // from the top down
+    __shared__ int sums[kSelWarps];
+    __shared__ int2 found[kSelWarps];
+    __shared__ int hit[3];
+    __shared__ uint32_t ends[2][kSelWarps];
+    // (The moving kernel's CTAs are not let in before these have left: beside them they would be spread unevenly.)
+    bool cut;
+    const int b = nth_sequence(p, blockIdx.x / p.Hkv, cut), head = blockIdx.x % p.Hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     bool bad;
     const int n = evict_len(p, b, bad);
@@ -83,10 +98,27 @@ __global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const Evict
         p.lens_out[b] = min(n, p.keep);
     }
     const size_t cap = (size_t)p.max_pages << p.page_shift;
-    const float *w = p.weight + (size_t)blockIdx.x * cap;
-    float *w_out = p.weight_out + (size_t)blockIdx.x * cap;
-    int *kept = p.kept + (size_t)blockIdx.x * p.keep;
+    const float *w = p.weight + ((size_t)b * p.Hkv + head) * cap;
+    float *w_out = p.weight_out + ((size_t)b * p.Hkv + head) * cap;
+    int *kept = p.kept + ((size_t)b * p.Hkv + head) * p.keep;
     const int stay = min(n, p.keep);
+    const int old = n - p.recent, need = p.keep - p.recent;  // 0 <= need < old where n > keep
+    // the integers' ends: T lies in [lo, hi]
+    uint32_t lo = 0xFFFFFFFFu, hi = 0;
+    if (n > p.keep && need > 0) {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < (old + 3) / 4; i += kSelThreads) {
+            const float4 x = __ldg(reinterpret_cast<const float4 *>(w) + i);  // cap is a multiple of 16
+            uint32_t v[4] = {order_of(x.x), order_of(x.y), order_of(x.z), order_of(x.w)};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (4 * i + e >= old) v[e] = 0u;  // below every weight
+                else lo = min(lo, v[e]);
+                hi = max(hi, v[e]);
+            }
+            if (4 * i < held) order_sm[i] = make_uint4(v[0], v[1], v[2], v[3]);
+        }
+    }
     for (size_t i = (size_t)stay + threadIdx.x; i < cap; i += kSelThreads) w_out[i] = 0.f;
     for (int i = stay + threadIdx.x; i < p.keep; i += kSelThreads) kept[i] = -1;
     if (n <= p.keep) {
@@ -96,255 +128,327 @@ __global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const Evict
         }
         return;
     }
-    const int old = n - p.recent, need = p.keep - p.recent;  // 0 <= need < old
     for (int i = threadIdx.x; i < p.recent; i += kSelThreads) {
         w_out[need + i] = w[old + i];
         kept[need + i] = old + i;
     }
     if (need == 0) return;
-
-    uint32_t v[kSelEach];
-    auto load = [&](int c0) {  // 0, below every weight, for positions past `old`
-        const int at = c0 + threadIdx.x * kSelEach;
-#pragma unroll
-        for (int i = 0; i < kSelEach; i += 4) {
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (at + i < old) x = *reinterpret_cast<const float4 *>(w + at + i);  // cap is a multiple of 16
-            v[i] = at + i < old ? order_of(x.x) : 0u;
-            v[i + 1] = at + i + 1 < old ? order_of(x.y) : 0u;
-            v[i + 2] = at + i + 2 < old ? order_of(x.z) : 0u;
-            v[i + 3] = at + i + 3 < old ? order_of(x.w) : 0u;
-        }
-    };
-    const bool once = old <= kSelChunk;
-    BlockSum sum{sums, 0};
-    // T lies in [lo, hi]: n_lo >= need reach lo, above < need exceed hi
-    uint32_t lo = 0xFFFFFFFFu, hi = 0;
-    for (int c0 = 0; c0 < old; c0 += kSelChunk) {
-        load(c0);
-#pragma unroll
-        for (int i = 0; i < kSelEach; ++i) {
-            hi = max(hi, v[i]);
-            if (v[i] != 0u) lo = min(lo, v[i]);
-        }
-    }
-    lo = ~__reduce_max_sync(0xffffffffu, ~lo);
+    lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     if (lane == 0) {
         ends[0][warp] = lo;
         ends[1][warp] = hi;
     }
     __syncthreads();
-    lo = __reduce_min_sync(0xffffffffu, ends[0][lane]);
-    hi = __reduce_max_sync(0xffffffffu, ends[1][lane]);
-    int n_lo = old, above = 0;
-    for (bool halve = false; lo < hi; halve = !halve) {
-        // by turns where the count would be reached if it fell evenly, and the middle
-        const uint32_t gap = hi - lo;
-        uint32_t t = lo + gap / 2 + 1;
-        if (!halve) {
-            const float share = (float)(n_lo - need) / (float)(n_lo - above);
-            t = lo + 1 + min((uint32_t)(share * (float)gap), gap - 1);
+    lo = __reduce_min_sync(0xffffffffu, ends[0][lane & (kSelWarps - 1)]);
+    hi = __reduce_max_sync(0xffffffffu, ends[1][lane & (kSelWarps - 1)]);
+
+    // Four positions' integers, 0 past `old`.
+    auto four = [&](int i4) {
+        if (4 * i4 < held) return order_sm[i4];
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(w) + i4);
+        const int i = 4 * i4;
+        return make_uint4(i < old ? order_of(x.x) : 0u, i + 1 < old ? order_of(x.y) : 0u, i + 2 < old ? order_of(x.z) : 0u,
+                          i + 3 < old ? order_of(x.w) : 0u);
+    };
+    const int fours = (old + 3) / 4;
+    int above = 0;  // how many exceed hi: fewer than need
+    uint32_t T = lo;
+    while (lo < hi) {
+        const int shift = max(0, 32 - __clz(hi - lo) - kBinBits);
+        const int top_bin = (int)((hi - lo) >> shift);
+        for (int i = threadIdx.x; i < kBins; i += kSelThreads) bins[i] = 0;
+        __syncthreads();
+        auto count = [&](uint32_t v) {
+            if (v >= lo && v <= hi) atomicAdd(bins + (top_bin - (int)((v - lo) >> shift)), 1);
+        };
+#pragma unroll 2
+        for (int i = threadIdx.x; i < fours; i += kSelThreads) {
+            const uint4 v = four(i);
+            count(v.x);
+            count(v.y);
+            count(v.z);
+            count(v.w);
         }
-        int count = 0;
-        for (int c0 = 0; c0 < old; c0 += kSelChunk) {
-            if (!once) load(c0);
-#pragma unroll
-            for (int i = 0; i < kSelEach; ++i) count += v[i] >= t;
-        }
-        count = sum(count);
-        if (count >= need) lo = t, n_lo = count;
-        else hi = t - 1, above = count;
-        if (count == need) {  // exactly those that reach t
-            lo = t - 1;
-            above = need;
-            break;
-        }
-    }
-    const uint32_t T = lo;
-    // in order of position
-    int taken = 0, equal_left = need - above;
-    for (int c0 = 0; c0 < old; c0 += kSelChunk) {
-        if (!once) load(c0);
-        const int at = c0 + threadIdx.x * kSelEach;
-        int mine = 0;  // above T, and equal to it << 16
-#pragma unroll
-        for (int i = 0; i < kSelEach; ++i) {
-            mine += (v[i] > T) + ((v[i] == T) << 16);
-        }
+        __syncthreads();
+        const int4 c = reinterpret_cast<const int4 *>(bins)[threadIdx.x];
+        const int mine = c.x + c.y + c.z + c.w;
         int incl = mine;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) {
             const int x = __shfl_up_sync(0xffffffffu, incl, d);
             if (lane >= d) incl += x;
         }
+        if (lane == 31) sums[warp] = incl;
         __syncthreads();
-        if (lane == 31) offs[warp] = incl;
-        __syncthreads();
-        int part = offs[lane], scan = part;
-#pragma unroll
-        for (int d = 1; d < 32; d *= 2) {
-            const int x = __shfl_up_sync(0xffffffffu, scan, d);
-            if (lane >= d) scan += x;
+        int before = above + incl - mine;
+        for (int i = 0; i < warp; ++i) before += sums[i];
+        if (before < need && need <= before + mine) {  // one thread: the bin that the count is reached in
+            const int each[4] = {c.x, c.y, c.z, c.w};
+            int k = 0;
+            while (before + each[k] < need) before += each[k++];
+            hit[0] = 4 * threadIdx.x + k;
+            hit[1] = before;
+            hit[2] = each[k];
         }
-        const int total = __shfl_sync(0xffffffffu, scan, 31);
-        const int before = __shfl_sync(0xffffffffu, scan - part, warp) + incl - mine;
-        int gt = before & 0xFFFF, eq = before >> 16;  // each at most kSelChunk = 2^14
+        __syncthreads();
+        lo += (uint32_t)(top_bin - hit[0]) << shift;
+        hi = min(hi, lo + ((1u << shift) - 1u));
+        above = hit[1];
+        T = lo;
+        if (above + hit[2] == need) {  // all that reach lo
+            above = need;
+            T = lo - 1;
+            break;
+        }
+    }
+    // In order of position: a warp takes a run of 128-position groups, first counting its weights above and equal to T.
+    const int groups = (fours + 31) / 32, g0 = (int)((long long)warp * groups / kSelWarps);
+    const int g1 = (int)((long long)(warp + 1) * groups / kSelWarps);
+    auto group = [&](int g) { return 32 * g + lane < fours ? four(32 * g + lane) : make_uint4(0u, 0u, 0u, 0u); };
+    int gt = 0, eq = 0;
+    for (int g = g0; g < g1; ++g) {
+        const uint4 v = group(g);
+        gt += (v.x > T) + (v.y > T) + (v.z > T) + (v.w > T);
+        eq += (v.x == T) + (v.y == T) + (v.z == T) + (v.w == T);
+    }
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (lane == 0) found[warp] = make_int2(gt, eq);
+    __syncthreads();
+    gt = eq = 0;
+    for (int i = 0; i < warp; ++i) gt += found[i].x, eq += found[i].y;
+    const int equal = need - above;  // how many of those equal to T stay
+    const uint32_t below = (1u << lane) - 1u;
+    for (int g = g0; g < g1; ++g) {
+        const uint4 q = group(g);
+        const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+        int my_gt = gt, my_eq = eq;  // before this lane's first
 #pragma unroll
-        for (int i = 0; i < kSelEach; ++i) {
-            if (v[i] > T || (v[i] == T && eq < equal_left)) {
-                const int r = taken + gt + min(eq, equal_left);
-                kept[r] = at + i;
-                w_out[r] = w[at + i];
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t is_gt = __ballot_sync(0xffffffffu, v[e] > T), is_eq = __ballot_sync(0xffffffffu, v[e] == T);
+            my_gt += __popc(is_gt & below);
+            my_eq += __popc(is_eq & below);
+            gt += __popc(is_gt);
+            eq += __popc(is_eq);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (v[e] > T || (v[e] == T && my_eq < equal)) {
+                const int r = my_gt + min(my_eq, equal);
+                kept[r] = 4 * (32 * g + lane) + e;
+                w_out[r] = weight_of(v[e]);
             }
-            gt += v[i] > T;
-            eq += v[i] == T;
+            my_gt += v[e] > T;
+            my_eq += v[e] == T;
         }
-        taken += (total & 0xFFFF) + min(total >> 16, equal_left);
-        equal_left -= min(total >> 16, equal_left);
     }
 }
 
 constexpr int kMoveThreads = 256;
 constexpr int kMoveTokens = 128;  // tokens of a CTA's round: one page at least
+constexpr int kStages = 4;
 constexpr int kMostCluster = 8;
 
-__device__ __forceinline__ void cluster_barrier() {
+__device__ __forceinline__ void cluster_arrive() {
     __syncwarp();
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-__device__ __forceinline__ float2 half2_at(uint32_t h) { return __half22float2(*reinterpret_cast<const __half2 *>(&h)); }
+// As cp_async16 (ptx.cuh), four bytes.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t src_bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
+__device__ __forceinline__ __half2 half2_of(uint32_t h) { return *reinterpret_cast<const __half2 *>(&h); }
+// Four codes (as fp16) times the power of two r, rounded to codes once, where no product is past the largest code.
+// int8: code r + 1536 in one rounding is an integer whose low byte is the code's. e4m3: code r is exact in fp16, or below
+// 2^-20, where it becomes 0 either way.
+template <int FMT>
+__device__ __forceinline__ uint32_t rescaled4(__half2 a, __half2 b, __half2 r) {
+    if constexpr (FMT == kKvq8Int8) {
+        const __half2 magic = __half2half2(__ushort_as_half(0x6600));
+        const __half2 x = __hfma2(a, r, magic), y = __hfma2(b, r, magic);
+        return __byte_perm(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y), 0x6420);
+    } else {
+        const uint32_t lo = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hmul2(a, r)), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(__hmul2(b, r)), __NV_SATFINITE, __NV_E4M3);
+        return lo | (hi << 16);
+    }
+}
 
 // One CTA, or a cluster of them, for each (sequence, head, K or V): the kept tokens in rounds of kMoveTokens for each
-// CTA. A warp holds 16 tokens in registers, so a page of 16 has its largest value in one warp.
+// CTA, whose codes and scales are copied into a ring in shared memory kStages - 1 rounds ahead. (No round writes what a later
+// one reads, so the copies may run ahead of the writes.) A warp has 16 tokens of a round, so a page of 16 has its largest
+// value in one warp; every thread works on what it copied itself.
 template <int D, int FMT>
-__global__ void __launch_bounds__(kMoveThreads) fa_kvq8_move_kernel(const EvictParams p) {
-    constexpr int LANES = D / 16;                                   // 16-byte vectors of a token
-    constexpr int PER = 32 / LANES;                                 // tokens of a warp's load
-    constexpr int VEC = 16 / PER;                                   // loads of a warp
-    constexpr int GROUPS = kMoveTokens / 16;                        // of 16 tokens, one for each warp
+__global__ void __launch_bounds__(kMoveThreads, 3) fa_kvq8_move_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int LANES = D / 16;             // 16-byte vectors of a token
+    constexpr int PER = 32 / LANES;           // tokens of a warp's load
+    constexpr int VEC = 16 / PER;             // loads of a warp
+    constexpr int GROUPS = kMoveTokens / 16;  // of 16 tokens, one for each warp
     static_assert(GROUPS == kMoveThreads / 32, "a group of 16 tokens for each warp");
+    extern __shared__ uint4 ring_sm[];  // uint8_t[kStages][kMoveTokens][D]
+    __shared__ float ring_scale[kStages][kMoveTokens];
     __shared__ float top[2][GROUPS];  // largest magnitudes, by turns
     const int rank = blockIdx.x % p.cluster;
     int u = blockIdx.x / p.cluster;
     const int kv = u & 1;
     u >>= 1;
-    const int head = u % p.Hkv, b = u / p.Hkv;
+    const int head = u % p.Hkv, nth = u / p.Hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    bool bad;
-    const int n = evict_len(p, b, bad);
-    if (n <= p.keep) return;  // the same in the whole cluster
+    bool cut;
+    const int b = nth_sequence(p, nth, cut);
+    if (!cut) return;  // the same in the whole cluster
     grid_dependency_wait();
     const int *kept = p.kept + ((size_t)b * p.Hkv + head) * p.keep;
     const int *table = p.page_table + (size_t)b * p.max_pages;
     const int page = 1 << p.page_shift, per_page = page / 16;  // groups of a page
     const int round = kMoveTokens * p.cluster, rounds = (p.keep + round - 1) / round;
-    // The first round with a token that moves (all behind it move too), and the last one.
+    // The first round with a token that moves (all behind it move too).
     int first_round = 0;
     for (int end = rounds; first_round < end;) {
         const int mid = (first_round + end) / 2, last = min((mid + 1) * round, p.keep) - 1;
         if (kept[last] == last) first_round = mid + 1;
         else end = mid;
     }
-    // A round's codes and scales are requested while the round before is under way, its positions one round earlier.
-    int pos[VEC];
-    uint4 x[VEC], ahead[VEC];
-    float s[VEC], s_ahead[VEC];
+    // Every global read is used an iteration after it is requested: positions five rounds ahead, their pages four, codes
+    // and scales three; where this warp's tokens go to, and whether they move, one. Lane t < 16 looks after token t.
+    int pos = -1, pos_of = -1, phys = -1;  // a position, and the one that the page belongs to
     auto load_pos = [&](int i_round) {
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const int r = i_round * round + rank * kMoveTokens + warp * 16 + i * PER + lane / LANES;
-            pos[i] = r < p.keep && i_round < rounds ? kept[r] : -1;
-        }
+        const int r = i_round * round + rank * kMoveTokens + warp * 16 + lane;
+        pos = lane < 16 && i_round < rounds && r < p.keep ? kept[r] : -1;
     };
-    auto load_codes = [&]() {
-        int phys[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) phys[i] = pos[i] < 0 ? -1 : __ldg(table + (pos[i] >> p.page_shift));
+    auto load_pages = [&]() {
+        pos_of = pos;
+        phys = pos < 0 ? -1 : __ldg(table + (pos >> p.page_shift));
+    };
+    const uint8_t *codes = p.codes[kv] + (lane % LANES) * 16;
+    const float *scale = p.scale[kv];
+    const uint32_t ring_at = smem_u32(ring_sm) + (warp * 16 + lane / LANES) * D + (lane % LANES) * 16;
+    auto copy = [&](int stage) {
+        const bool there = phys >= 0 && phys < p.n_pages;
+        if (!there && pos_of >= 0) atomicExch(p.status, kStatusPage);  // such a token becomes zeros
+        const size_t unit = there ? (size_t)phys * p.Hkv + head : 0;
+        const size_t row = there ? (unit << p.page_shift) + (pos_of & (page - 1)) : ~(size_t)0;
+        if (lane < 16) cp_async4(smem_u32(&ring_scale[stage][warp * 16 + lane]), scale + unit, there ? 4u : 0u);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            ahead[i] = make_uint4(0u, 0u, 0u, 0u);
-            s_ahead[i] = 0.f;
-            if (phys[i] >= 0 && phys[i] < p.n_pages) {
-                const size_t unit = (size_t)phys[i] * p.Hkv + head;
-                s_ahead[i] = p.scale[kv][unit];
-                ahead[i] = *reinterpret_cast<const uint4 *>(p.codes[kv] + ((unit << p.page_shift) + (pos[i] & (page - 1))) * D + (lane % LANES) * 16);
-            } else if (pos[i] >= 0) {
-                atomicExch(p.status, kStatusPage);  // such a token becomes zeros
-            }
+            const size_t from = __shfl_sync(0xffffffffu, row, i * PER + lane / LANES);
+            cp_async16(ring_at + stage * (kMoveTokens * D) + i * PER * D, codes + (from == ~(size_t)0 ? 0 : from) * D,
+                       from == ~(size_t)0 ? 0u : 16u);
+        }
+        cp_async_commit();
+    };
+    int to_phys = -1, to_last = 0;
+    auto load_to = [&](int i_round) {  // the page that this warp's tokens go to, the old position of its last token
+        const int first = (i_round * round + rank * kMoveTokens + warp * 16) & ~(page - 1);
+        to_phys = -1, to_last = 0;
+        if (i_round < rounds && first < p.keep) {
+            to_phys = __ldg(table + (first >> p.page_shift));
+            to_last = kept[min(first + page, p.keep) - 1];
         }
     };
     load_pos(first_round);
-    load_codes();
+    load_pages();
     load_pos(first_round + 1);
-    int turn = 0;
-    for (int i_round = first_round; i_round < rounds; ++i_round, turn ^= 1) {
+#pragma unroll
+    for (int s = 0; s < kStages - 1; ++s) {
+        copy(s);
+        load_pages();
+        load_pos(first_round + s + 2);
+    }
+    load_to(first_round);
+    cp_async_wait<kStages - 2>();  // the first round's copies
+    if (p.cluster > 1) cluster_arrive();
+    int turn = 0, stage = 0;
+    for (int i_round = first_round; i_round < rounds; ++i_round, turn ^= 1, stage = stage + 1 == kStages ? 0 : stage + 1) {
         const int g0 = i_round * round + rank * kMoveTokens + warp * 16;  // this warp's tokens of the new order
+        const int dst_phys = to_phys, dst_last = to_last;
+        copy(stage == 0 ? kStages - 1 : stage - 1);
+        load_pages();
+        load_pos(i_round + kStages + 1);
+        load_to(i_round + 1);
+        __syncwarp();  // the scales were copied by other lanes
+        uint32_t x[VEC][8];  // this thread's codes as pairs of fp16
+        float s[VEC], top_code[VEC], most = 0.f;
+        bool odd = false;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
-            x[i] = ahead[i];
-            s[i] = s_ahead[i];
-        }
-        // (no round writes what a later one reads, so these may run ahead of this round's writes)
-        load_codes();
-        load_pos(i_round + 2);
-        float most = 0.f;
+            const int t = warp * 16 + i * PER + lane / LANES;
+            const uint4 w = ring_sm[(stage * kMoveTokens + t) * LANES + lane % LANES];
+            s[i] = ring_scale[stage][t];
+            odd |= !power_of_two(s[i]);
+            codes_to_half2<FMT>(w.x, x[i][0], x[i][1]);
+            codes_to_half2<FMT>(w.y, x[i][2], x[i][3]);
+            codes_to_half2<FMT>(w.z, x[i][4], x[i][5]);
+            codes_to_half2<FMT>(w.w, x[i][6], x[i][7]);
+            __half2 m = __habs2(half2_of(x[i][0]));
 #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            __half2 m = __half2half2(__ushort_as_half(0));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                uint32_t lo, hi;
-                codes_to_half2<FMT>(w[e], lo, hi);
-                m = __hmax2(m, __hmax2(__habs2(*reinterpret_cast<__half2 *>(&lo)), __habs2(*reinterpret_cast<__half2 *>(&hi))));
-            }
+            for (int e = 1; e < 8; ++e) m = __hmax2(m, __habs2(half2_of(x[i][e])));
             const float code = fmaxf(__low2float(m), __high2float(m));
-            most = fmaxf(most, code * s[i] > FLT_MAX ? FLT_MAX : product_odd(code, s[i]));
+            most = fmaxf(most, code * s[i]);
+            top_code[i] = code;
+        }
+        odd = __any_sync(0xffffffffu, odd);
+        if (odd) {
+            most = 0.f;
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) most = fmaxf(most, top_code[i] * s[i] > FLT_MAX ? FLT_MAX : product_odd(top_code[i], s[i]));
         }
         const float group_most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(most)));
         if (lane == 0) top[turn][warp] = group_most;
-        // every read of the round before its first write
-        if (p.cluster > 1) cluster_barrier();
+        // Every read of the round before its first write: the cluster's CTAs said so an iteration ago, and say it now of the
+        // next round.
+        cp_async_wait<kStages - 2>();
         __syncthreads();
+        if (p.cluster > 1) {
+            cluster_wait();
+            cluster_arrive();
+        }
         const int g_page = warp / per_page * per_page;  // the page's first group in this CTA
         float page_most = 0.f;
         for (int i = 0; i < per_page; ++i) page_most = fmaxf(page_most, top[turn][g_page + i]);
         const int first = g0 & ~(page - 1), page_last = min(first + page, p.keep) - 1;
-        if (g0 >= p.keep || kept[page_last] == page_last) continue;  // (warp-uniform) no token of the page moves
-        const int phys = __ldg(table + (first >> p.page_shift));
-        if (phys < 0 || phys >= p.n_pages) {
+        if (g0 >= p.keep || dst_last == page_last) continue;  // (warp-uniform) no token of the page moves
+        if (dst_phys < 0 || dst_phys >= p.n_pages) {
             if (lane == 0) atomicExch(p.status, kStatusPage);
             continue;
         }
-        const size_t unit = (size_t)phys * p.Hkv + head;
+        const size_t unit = (size_t)dst_phys * p.Hkv + head;
         const float now = scale_for<FMT>(page_most);
         const float inv = now > 0.f ? 1.0f / now : 0.f;
         if (warp == g_page && lane == 0) p.scale[kv][unit] = now;
-        uint8_t *dst = p.codes[kv] + ((unit << p.page_shift) + (g0 & (page - 1))) * D;
+        uint8_t *dst = p.codes[kv] + ((unit << p.page_shift) + (g0 & (page - 1))) * D + (lane % LANES) * 16;
+        // Scales that no append wrote, or values past the largest scale: codes are rounded from fp32.
+        const bool slow = odd || page_most > (FMT == kKvq8Int8 ? 127.0f : 448.0f) * 0x1p120f;
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const int t = i * PER + lane / LANES;
-            if (g0 + t >= p.keep) continue;
-            uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            if (s[i] != now || now == 0.f) {
-                // (a token of zeros may have come under a scale far above the page's)
-                const float ratio = fminf(s[i] * inv, 512.0f);
-                const bool exact = power_of_two(s[i]);
+            // (a token of zeros may have come under a scale far above the page's)
+            const float ratio = fminf(s[i] * inv, 512.0f);
+            uint32_t w[4];
+            if (!slow) {
+                const __half2 r = __float2half2_rn(ratio);  // a power of two, or so small that every code becomes 0
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e] = rescaled4<FMT>(half2_of(x[i][2 * e]), half2_of(x[i][2 * e + 1]), r);
+            } else {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    uint32_t lo, hi;
-                    codes_to_half2<FMT>(w[e], lo, hi);
-                    const float2 a = half2_at(lo), c = half2_at(hi);
-                    w[e] = exact ? encode4<FMT>(a.x * ratio, a.y * ratio, c.x * ratio, c.y * ratio)
-                                 : encode4<FMT>(product_odd(a.x, ratio), product_odd(a.y, ratio), product_odd(c.x, ratio),
-                                                product_odd(c.y, ratio));
+                    const float2 a = __half22float2(half2_of(x[i][2 * e])), c = __half22float2(half2_of(x[i][2 * e + 1]));
+                    w[e] = encode4<FMT>(product_odd(a.x, ratio), product_odd(a.y, ratio), product_odd(c.x, ratio),
+                                        product_odd(c.y, ratio));
                 }
             }
-            *reinterpret_cast<uint4 *>(dst + t * D + (lane % LANES) * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (g0 + t < p.keep) *reinterpret_cast<uint4 *>(dst + t * D) = make_uint4(w[0], w[1], w[2], w[3]);
         }
     }
+    cp_async_wait<0>();
+    if (p.cluster > 1) cluster_wait();
 }
 
 template <int D, int FMT>
@@ -355,9 +459,13 @@ int launch_move(const Kvq8EvictArgs &a, EvictParams p) {
     while (2 * p.cluster <= kMostCluster && 2 * p.cluster * units <= 4ll * a.num_sms && p.cluster * kMoveTokens < a.keep) p.cluster *= 2;
     const long long grid = units * p.cluster;
     if (grid > INT32_MAX) return -3;
+    if (kStages * kMoveTokens * D > 48 * 1024 &&
+        cudaFuncSetAttribute(fa_kvq8_move_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kMoveTokens * D) != cudaSuccess)
+        return -5;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = kStages * kMoveTokens * D;
     cfg.stream = a.stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -388,13 +496,19 @@ int launch_kvq8_evict(const Kvq8EvictArgs &a) {
     p.n_pages = a.c.n_pages;
     p.max_pages = a.c.max_pages;
     p.page_shift = kvq8_page_shift(a.c.page);
+    p.nseq = a.nseq;
     p.Hkv = a.c.Hkv;
     p.keep = a.keep;
     p.recent = a.recent;
     p.cluster = 1;
     const long long grid = (long long)a.nseq * a.c.Hkv;
     if (grid > INT32_MAX) return -3;
-    fa_kvq8_select_kernel<<<(unsigned)grid, kSelThreads, 0, a.stream>>>(p);
+    const long long cap = (long long)a.c.max_pages * a.c.page;
+    const int held = (int)(cap < kSelMost ? cap : kSelMost);
+    if (held * 4 > 32 * 1024 && cudaFuncSetAttribute(fa_kvq8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                     kSelMost * 4) != cudaSuccess)
+        return -5;
+    fa_kvq8_select_kernel<<<(unsigned)grid, kSelThreads, held * 4, a.stream>>>(p, held);
     if (cudaGetLastError() != cudaSuccess) return -5;
     const bool i8 = a.c.format == kKvq8Int8;
     if (a.c.d == 128) return i8 ? launch_move<128, kKvq8Int8>(a, p) : launch_move<128, kKvq8E4m3>(a, p);

@@ -845,12 +845,18 @@ def kvq8_evict(cache, page_table, kv_lens, weight, keep, recent, lens_out=None, 
     if keep < 1 or not 0 <= recent <= keep:
         raise FAError(FA_ERR_ARG, "fa_kvq8_evict")
     with _on(index, stream):
-        lens_out = _empty((nseq,), (1,), _I32) if lens_out is None else lens_out
-        kept = _empty3(nseq, Hkv, keep, _I32) if kept is None else kept
-        weight_out = _empty3(*wide, _F32) if weight_out is None else weight_out
-        _check_tensor("lens_out", lens_out, _I32, (nseq,), index)
-        _check_tensor("kept", kept, _I32, (nseq, Hkv, keep), index)
-        _check_tensor("weight_out", weight_out, _F32, wide, index)
+        if lens_out is None:
+            lens_out = _empty((nseq,), (1,), _I32)
+        else:
+            _check_tensor("lens_out", lens_out, _I32, (nseq,), index)
+        if kept is None:
+            kept = _empty3(nseq, Hkv, keep, _I32)
+        else:
+            _check_tensor("kept", kept, _I32, (nseq, Hkv, keep), index)
+        if weight_out is None:
+            weight_out = _empty3(*wide, _F32)
+        else:
+            _check_tensor("weight_out", weight_out, _F32, wide, index)
         rc = lib.fa_kvq8_evict(*ptrs, n_pages, max_pages, page, kv_lens.data_ptr(), weight.data_ptr(), keep, recent,
                                lens_out.data_ptr(), kept.data_ptr(), weight_out.data_ptr(), nseq, Hkv, d, fmt,
                                _raw_stream(index, stream))

@@ -182,7 +182,7 @@ def test_evict_scales_far_apart(fa, fmt):
     check_cache(cache, want)
 
 
-@pytest.mark.parametrize("n,keep,recent", [(16384, 9000, 5), (16390, 16385, 0), (40000, 100, 99), (40000, 33333, 1)])
+@pytest.mark.parametrize("n,keep,recent", [(8200, 4000, 100), (10000, 9999, 3), (12000, 5000, 500), (12288, 1, 0), (16384, 9000, 5), (16390, 16385, 0), (40000, 100, 99), (40000, 33333, 1), (24577, 24500, 7)])
 @pytest.mark.parametrize("kind", ["spread", "ties"])
 def test_evict_long_sequences(fa, n, keep, recent, kind):
     rng = np.random.default_rng(n + keep)
