@@ -1098,7 +1098,7 @@ int fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_l
     DeviceInfo *di = device_info();
     const int sms = di ? di->num_sms : kNominalSms, rows = H / Hkv * Nq;
     *n_splits = fa::kvq8_prefix_splits(B, Hkv, rows, max_prefix, max_len, d, sms);
-    *n_parts = fa::kvq8_num_parts(B, Hkv, rows, *n_splits > 0 ? max_len : static_cast<int>(kvq8_line(max_prefix, max_len)), d, sms);
+    *n_parts = fa::kvq8_prefix_parts(B, Hkv, rows, max_prefix, max_len, d, *n_splits, sms);
     return FA_OK;
 }
 

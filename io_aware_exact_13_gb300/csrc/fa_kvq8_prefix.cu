@@ -8,7 +8,6 @@ namespace fa {
 namespace {
 
 constexpr int kMergeThreads = 128;
-constexpr int kRunBlocks = 5;  // blocks of 128 keys of a run, at least
 
 // out = sum_s w_s o_s / sum_s w_s with w_s = exp(lse_s - max lse), over the own keys' summary and those of the prefix's
 // runs (fa_splitkv.cu's rule). Four columns of a row for each thread; the lanes of a row share the weights out.
@@ -73,14 +72,57 @@ int launch_merge(const Kvq8AttnArgs &a, const float *own_o, const float *own_lse
                : -5;
 }
 
+// The SMs that the own keys' kernel is sized for: those that the prefix's leaves free, where they are enough to be of use.
+int own_sms(long long prefix_ctas, int num_sms) {
+    const long long left = num_sms - prefix_ctas;
+    return left >= num_sms / 8 ? (int)left : num_sms;
+}
+
 }  // namespace
 
+// How the prefix is done, by estimates of each way's time in us. They go by max_prefix and max_len, and were fitted to
+// measured times (below); what they decide is never more than speed.
+//   with every sequence's own keys: a start, the merge of parts, and all keys at the rate of L2, or at that of the products where
+//   many rows share a head;
+//   once for all, in s runs for each 256 rows: a start, the run's blocks, and the merge of summaries; the own keys beside it on
+//   the SMs that are left (a start, and their bytes at the rate that an SM gets, less for short sequences), or after it on all.
+// Measured (us; with every sequence's own keys against once for all), int8, 8 K/V heads. 4 heads share one, d 128: prefix 2048, B 1 to
+// 32: 12.4 / 16.6, 12.9 / 16.6, 14.0 / 16.5, 16.6 / 16.6, 20.7 / 18.6, 30.4 / 20.6; prefix 8192: 16.7 / 22.4, 18.6 / 21.5,
+// 22.8 / 22.3, 30.9 / 22.6, 46.2 / 22.7, 80.0 / 28.1. 8 share one, 32768: 25.0 / 39.1, 33.6 / 39.1, 49.3 / 40.6, 85.9 / 41.9, 152 /
+// 45.3, 289 / 57.5. d 64, not shared, prefix 1000: 8.4 / 14.5 up to 4, 10.4 / 14.5, 10.7 / 14.5, 14.5 / 14.5. With own keys beside:
+// B 16, 8192 + up to 1024: 13 runs 33.0 (own keys after), 11 24.9, 9 24.7; B 64, 8 share one, 32768 + up to 2048: 9 runs 118.8
+// (after), 7 and parts for 40 SMs 107, 6 and 56 SMs 104.
 int kvq8_prefix_splits(int B, int Hkv, int rows, int max_prefix, int max_len, int d, int num_sms) {
     const long long all = (long long)B * rows;
-    if (all < 24 || max_prefix < 512) return 0;
-    const long long units = Hkv * ((all + 255) / 256);
-    const int most = (int)(num_sms / units), by_len = (max_prefix + 128 * kRunBlocks - 1) / (128 * kRunBlocks);
-    return most < 1 ? 1 : most < by_len ? most : by_len;
+    const double units = (double)Hkv * (double)((all + 255) / 256), blocks = (max_prefix + 127) / 128;
+    const double key = 2.0 * d * Hkv, own_bytes = 0.65 * B * max_len * key;  // (ragged lengths: two thirds of the bound)
+    const int nt = tiles_per_unit(rows, d), line_len = q8_tiles(max_prefix) * kTileKeys + max_len;
+    const double per_key = units_per_head(rows, d) * (nt == 1 ? 1.0 : nt == 2 ? 1.5 : nt == 3 ? 3.5 : 4.5);
+    const double line = 10.0 + (kvq8_num_parts(B, Hkv, rows, line_len, d, num_sms) > 0 ? 4.0 : 0.0) + max_prefix / 6000.0 +
+                        per_key * (B * (double)max_prefix * key + own_bytes) / 8.3e6;
+    const double block = (all > 128 ? 2.0 : 1.15) * (d == 64 ? 0.65 : 1.0);
+    const double own_all = 8.0 + own_bytes / 6.2e6;
+    double best = line;
+    int best_splits = 0;
+    const int most = (int)(units <= num_sms ? num_sms / units : 1);
+    for (int s = 1; s <= most && s <= blocks; ++s) {
+        const double prefix = (d == 64 ? 9.0 : 11.0) + block * ((int)((blocks + s - 1) / s)) * (units > num_sms ? units / num_sms : 1.0);
+        const int left = own_sms((long long)units * s, num_sms);
+        const double own = 6.0 + own_bytes / (60e3 * max_len / (max_len + 1000.0)) / left;
+        const double time = left < num_sms ? (prefix > own ? prefix : own) : prefix + own_all - 4.0;
+        const double merge = 4.0 + 0.25 * s;
+        if (time + merge < best) {
+            best = time + merge;
+            best_splits = s;
+        }
+    }
+    return best_splits;
+}
+
+int kvq8_prefix_parts(int B, int Hkv, int rows, int max_prefix, int max_len, int d, int splits, int num_sms) {
+    if (splits == 0) return kvq8_num_parts(B, Hkv, rows, q8_tiles(max_prefix) * kTileKeys + max_len, d, num_sms);
+    const long long units = Hkv * (((long long)B * rows + 255) / 256);
+    return kvq8_num_parts(B, Hkv, rows, max_len, d, own_sms(units * splits, num_sms));
 }
 
 // Own summary, the runs' summaries, and what the own keys' parts take.
@@ -106,6 +148,8 @@ int launch_kvq8_prefix(const Kvq8AttnArgs &a, bool fp16) {
     own.lse = own_lse;
     own.workspace = reinterpret_cast<float *>(at);
     own.max_prefix = 0;
+    const long long head_rows = (long long)a.B * (a.H / a.c.Hkv) * a.Nq;
+    own.num_sms = own_sms((head_rows + 255) / 256 * a.c.Hkv * a.splits, a.num_sms);
     int rc = launch_kvq8_prefix_tc(a, fp16, o_part, lse_part);
     if (rc == 0) rc = launch_kvq8_prefix_own(own, fp16);
     if (rc != 0) return rc;
