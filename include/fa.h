@@ -321,7 +321,7 @@ int fa_fwd_kvq8_fp16(const void *q, const void *k_codes, const void *v_codes, co
  * of the lengths may be 0. Results are those of fa_fwd_kvq8 over the whole: causal counts positions over both parts,
  * so query i sees the first prefix_len[0] + kv_lens[b] - Nq + i + 1 of them.
  * With n_splits = 0 the prefix is read with every sequence's own keys, and n_parts and the workspace are those of
- * fa_fwd_kvq8. With n_splits > 0 (at most ceil(max_prefix / 128)) it is read once for the rows of all sequences, in
+ * fa_fwd_kvq8. With n_splits > 0 (at most ceil(max_prefix / 128), and 4096) it is read once for the rows of all sequences, in
  * n_splits runs of keys, and n_parts is for the sequences' own keys; the summaries (fp32) go through the workspace and are merged
  * as in fa_fwd_splitkv. fa_kvq8_prefix_plan chooses both. The workspace has at least
  * fa_kvq8_prefix_workspace_bytes bytes (256-byte aligned; it may be NULL where they are 0).

@@ -379,7 +379,7 @@ int splitkv_common(bool fp16, const void *q, const void *k, const void *v, void 
 
 // What the 8-bit cache's calls take, and their sizing helpers with them: positions and tiles stay below 2^31 with room to
 // add, and B * H * Nq rows fit an int.
-constexpr int kKvq8MaxLen = 1 << 30, kKvq8MaxTiles = 1 << 30, kKvq8MaxParts = 1 << 20;
+constexpr int kKvq8MaxLen = 1 << 30, kKvq8MaxTiles = 1 << 30, kKvq8MaxParts = 1 << 20, kKvq8MaxSplits = 4096;
 bool kvq8_rows_ok(int B, int H, int Hkv, int Nq) {
     if (H < 1 || Hkv < 1 || H % Hkv != 0 || Nq < 1 || Nq > fa::kKvq8MaxNq) return false;
     const int64_t bh = static_cast<int64_t>(B) * H;
@@ -1104,7 +1104,7 @@ int fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_l
 
 long long fa_kvq8_prefix_workspace_bytes(int B, int H, int Hkv, int Nq, int max_prefix, int d, int n_splits, int n_parts) {
     if (B < 1 || !kvq8_rows_ok(B, H, Hkv, Nq) || max_prefix < 1 || n_parts < 0 || n_parts > kKvq8MaxParts || n_splits < 0 ||
-        n_splits > (static_cast<int64_t>(max_prefix) + 127) / 128)
+        n_splits > kKvq8MaxSplits || n_splits > (static_cast<int64_t>(max_prefix) + 127) / 128)
         return FA_ERR_SHAPE;
     if (d != 64 && d != 128) return FA_ERR_UNSUPPORTED;
     return static_cast<long long>(fa::kvq8_prefix_workspace_bytes(B, Hkv, H / Hkv * Nq, d, n_splits, n_parts));

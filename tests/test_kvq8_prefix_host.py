@@ -59,7 +59,8 @@ def test_sizes_are_refused(fa):
         with pytest.raises(fa.FAError):
             fa.fa_kvq8_prefix_plan(*args)
     for args in ((0, 4, 2, 1, 10, 64, 0, 0), (1, 4, 3, 1, 10, 64, 0, 0), (1, 4, 2, 1, 10, 64, 2, 0), (1, 4, 2, 1, 10, 64, -1, 0),
-                 (1, 4, 2, 1, 10, 64, 0, -1), (1, 4, 2, 1, 0, 64, 0, 0), (1, 4, 2, 1, 10, 72, 0, 0)):
+                 (1, 4, 2, 1, 10, 64, 0, -1), (1, 4, 2, 1, 0, 64, 0, 0), (1, 4, 2, 1, 10, 72, 0, 0),
+                 (1, 4, 2, 1, 1 << 30, 64, 4097, 0)):
         with pytest.raises(fa.FAError):
             fa.fa_kvq8_prefix_workspace_bytes(*args)
     for B, Hkv, G, prefix, n, d in ((1, 1, 1, 1, 1, 64), (64, 8, 8, 32768, 2048, 128), (3, 8, 1, 1000, 100, 64), (300, 2, 4, 100, 9, 128)):
