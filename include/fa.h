@@ -323,11 +323,11 @@ int fa_fwd_kvq8_fp16(const void *q, const void *k_codes, const void *v_codes, co
  * With n_splits = 0 the prefix is read with every sequence's own keys, and n_parts and the workspace are those of
  * fa_fwd_kvq8. With n_splits > 0 (at most ceil(max_prefix / 128), and 4096) it is read once for the rows of all sequences, in
  * n_splits runs of keys, and n_parts is for the sequences' own keys; the summaries (fp32) go through the workspace and are merged
- * as in fa_fwd_splitkv. fa_kvq8_prefix_plan chooses both. The workspace has at least
- * fa_kvq8_prefix_workspace_bytes bytes (256-byte aligned; it may be NULL where they are 0).
+ * as in fa_fwd_splitkv. fa_kvq8_prefix_plan chooses both and returns the bytes of the workspace that they take, or a negative
+ * status. The workspace has at least fa_kvq8_prefix_workspace_bytes bytes (256-byte aligned; it may be NULL where they are 0).
  * Accuracy, errors and the device status as for fa_fwd_kvq8; a prefix length out of range counts as 0 and records
  * FA_ERR_SEQLENS. The result does not depend on timing. */
-int fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int *n_splits, int *n_parts);
+long long fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int *n_splits, int *n_parts);
 long long fa_kvq8_prefix_workspace_bytes(int B, int H, int Hkv, int Nq, int max_prefix, int d, int n_splits, int n_parts);
 int fa_fwd_kvq8_prefix(const void *q, const void *k_codes, const void *v_codes, const float *k_scale,
                        const float *v_scale, const int *prefix_table, int prefix_pages, const int *prefix_len,

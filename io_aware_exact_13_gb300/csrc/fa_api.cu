@@ -1091,7 +1091,7 @@ int fa_fwd_kvq8_fp16(FA_KVQ8_ARGS) {
 }
 #undef FA_KVQ8_ARGS
 
-int fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int *n_splits, int *n_parts) {
+long long fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_len, int d, int *n_splits, int *n_parts) {
     if (!n_splits || !n_parts) return FA_ERR_NULL;
     const int rc = check_kvq8_prefix(B, H, Hkv, Nq, max_prefix, max_len, d);
     if (rc != FA_OK) return rc;
@@ -1099,7 +1099,7 @@ int fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int max_l
     const int sms = di ? di->num_sms : kNominalSms, rows = H / Hkv * Nq;
     *n_splits = fa::kvq8_prefix_splits(B, Hkv, rows, max_prefix, max_len, d, sms);
     *n_parts = fa::kvq8_prefix_parts(B, Hkv, rows, max_prefix, max_len, d, *n_splits, sms);
-    return FA_OK;
+    return fa_kvq8_prefix_workspace_bytes(B, H, Hkv, Nq, max_prefix, d, *n_splits, *n_parts);
 }
 
 long long fa_kvq8_prefix_workspace_bytes(int B, int H, int Hkv, int Nq, int max_prefix, int d, int n_splits, int n_parts) {

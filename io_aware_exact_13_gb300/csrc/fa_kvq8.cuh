@@ -10,6 +10,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace fa {
 
 constexpr int kKvq8Int8 = 0, kKvq8E4m3 = 1;  // FA_KVQ8_INT8, FA_KVQ8_E4M3
@@ -100,6 +102,19 @@ int launch_kvq8_evict(const Kvq8EvictArgs &a);
 long long kvq8_tiles(int B, int Hkv, int rows, int max_len, int d);
 int kvq8_num_parts(int B, int Hkv, int rows, int max_len, int d, int num_sms);
 size_t kvq8_workspace_bytes(int rows, int d, int parts);
+
+// A kernel's dynamic shared memory allowed beyond 48 KB, once for each device (the driver's call costs half a microsecond).
+template <auto KERNEL>
+bool allow_smem(int bytes) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+}
 
 inline int kvq8_page_shift(int page) {
     int s = 0;

@@ -897,9 +897,7 @@ template <typename T, int D, int FMT, int NT, bool CAUSAL, int MODE>
 int launch_q8(const Kvq8AttnArgs &a) {
     using C = Q8Cfg<D, NT>;
     auto kern = fa_kvq8_partial<T, D, FMT, NT, CAUSAL, MODE>;
-    if (C::SMEM > 48 * 1024 &&
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) != cudaSuccess)
-        return -5;
+    if (C::SMEM > 48 * 1024 && !allow_smem<fa_kvq8_partial<T, D, FMT, NT, CAUSAL, MODE>>(C::SMEM)) return -5;
     Q8Params p;
     p.q = a.q;
     p.out = a.out;

@@ -459,9 +459,7 @@ int launch_move(const Kvq8EvictArgs &a, EvictParams p) {
     while (2 * p.cluster <= kMostCluster && 2 * p.cluster * units <= 4ll * a.num_sms && p.cluster * kMoveTokens < a.keep) p.cluster *= 2;
     const long long grid = units * p.cluster;
     if (grid > INT32_MAX) return -3;
-    if (kStages * kMoveTokens * D > 48 * 1024 &&
-        cudaFuncSetAttribute(fa_kvq8_move_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kStages * kMoveTokens * D) != cudaSuccess)
-        return -5;
+    if (!allow_smem<fa_kvq8_move_kernel<D, FMT>>(kStages * kMoveTokens * D)) return -5;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
     cfg.blockDim = dim3(kMoveThreads);
@@ -505,9 +503,7 @@ int launch_kvq8_evict(const Kvq8EvictArgs &a) {
     if (grid > INT32_MAX) return -3;
     const long long cap = (long long)a.c.max_pages * a.c.page;
     const int held = (int)(cap < kSelMost ? cap : kSelMost);
-    if (held * 4 > 32 * 1024 && cudaFuncSetAttribute(fa_kvq8_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                     kSelMost * 4) != cudaSuccess)
-        return -5;
+    if (!allow_smem<fa_kvq8_select_kernel>(kSelMost * 4)) return -5;  // (beside static shared memory: needed below 48 KB too)
     fa_kvq8_select_kernel<<<(unsigned)grid, kSelThreads, held * 4, a.stream>>>(p, held);
     if (cudaGetLastError() != cudaSuccess) return -5;
     const bool i8 = a.c.format == kKvq8Int8;

@@ -694,11 +694,10 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) fa_kvq8_prefix_kernel(const
 template <typename T, int D, int FMT>
 int launch_tc(const PrefixParams &p, cudaStream_t stream) {
     using S = PrefixCfg<D>;
-    auto kern = fa_kvq8_prefix_kernel<T, D, FMT>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM_BYTES) != cudaSuccess) return -5;
+    if (!allow_smem<fa_kvq8_prefix_kernel<T, D, FMT>>(S::SMEM_BYTES)) return -5;
     const long long grid = (long long)p.Hkv * p.row_tiles * p.splits;
     if (grid > INT32_MAX) return -3;
-    kern<<<(unsigned)grid, kPrefixThreads, S::SMEM_BYTES, stream>>>(p);
+    fa_kvq8_prefix_kernel<T, D, FMT><<<(unsigned)grid, kPrefixThreads, S::SMEM_BYTES, stream>>>(p);
     return cudaGetLastError() == cudaSuccess ? 0 : -5;
 }
 

@@ -125,7 +125,7 @@ for _suffix in ("", "_fp16"):
                                                [ctypes.c_float, ctypes.c_int, _vp])
     SIGNATURES["fa_rotary" + _suffix] = (ctypes.c_int, [_vp] * 3 + [ctypes.c_int] + [_vp] * 3 + [ctypes.c_int, _vp, ctypes.c_int] +
                                          [_vp] * 2 + [ctypes.c_int] * 5 + [_vp])
-SIGNATURES["fa_kvq8_prefix_plan"] = (ctypes.c_int, [ctypes.c_int] * 7 + [ctypes.POINTER(ctypes.c_int)] * 2)
+SIGNATURES["fa_kvq8_prefix_plan"] = (ctypes.c_longlong, [ctypes.c_int] * 7 + [ctypes.POINTER(ctypes.c_int)] * 2)
 SIGNATURES["fa_kvq8_prefix_workspace_bytes"] = (ctypes.c_longlong, [ctypes.c_int] * 8)
 SIGNATURES["fa_kvq8_evict"] = (ctypes.c_int, [_vp] * 5 + [ctypes.c_int] * 3 + [_vp] * 2 + [ctypes.c_int] * 2 + [_vp] * 3 +
                                [ctypes.c_int] * 4 + [_vp])
@@ -717,11 +717,16 @@ def attention_kvq8(q, cache, page_table, kv_lens, scale=None, causal=False, max_
 # ---------------------------------------------------------------- a prefix that all sequences share
 def fa_kvq8_prefix_plan(B, H, Hkv, Nq, max_prefix, max_len, d):
     """(n_splits, n_parts) for ``fa_fwd_kvq8_prefix``."""
+    return _kvq8_prefix_plan(int(B), int(H), int(Hkv), int(Nq), int(max_prefix), int(max_len), int(d))[:2]
+
+
+def _kvq8_prefix_plan(*sizes):
+    """(n_splits, n_parts, workspace bytes)"""
     splits, parts = ctypes.c_int(), ctypes.c_int()
-    rc = lib.fa_kvq8_prefix_plan(int(B), int(H), int(Hkv), int(Nq), int(max_prefix), int(max_len), int(d), splits, parts)
-    if rc != FA_OK:
-        raise FAError(rc, "fa_kvq8_prefix_plan")
-    return splits.value, parts.value
+    need = lib.fa_kvq8_prefix_plan(*sizes, splits, parts)
+    if need < 0:
+        raise FAError(need, "fa_kvq8_prefix_plan")
+    return splits.value, parts.value, need
 
 
 def fa_kvq8_prefix_workspace_bytes(B, H, Hkv, Nq, max_prefix, d, n_splits, n_parts) -> int:
@@ -743,16 +748,17 @@ def _raw_kvq8_prefix(fn_name, dtype, q, cache, prefix_table, prefix_len, page_ta
     B, H, Nq, dq = shape
     if dq != d or H % Hkv or nseq != B:
         raise ValueError("q: [B, H, Nq, d] with the cache's d, its Hkv dividing H and one page table row per b")
-    if prefix_table.dim() != 1:
+    prefix_pages = prefix_table.shape
+    if len(prefix_pages) != 1:
         raise ValueError("prefix_table must be int32 [prefix_pages]")
     if (n_splits is None) != (n_parts is None):
         raise ValueError("n_splits and n_parts are given together or not at all")
     _check_tensor("q", q, dtype, shape, index)
     _check_tensor("kv_lens", kv_lens, _I32, (B,), index)
-    _check_tensor("prefix_table", prefix_table, _I32, prefix_table.shape, index)
+    _check_tensor("prefix_table", prefix_table, _I32, prefix_pages, index)
     _check_tensor("prefix_len", prefix_len, _I32, (1,), index)
     max_len = max_pages * page if max_len is None else int(max_len)
-    max_prefix = prefix_table.shape[0] * page if max_prefix is None else int(max_prefix)
+    max_prefix = prefix_pages[0] * page if max_prefix is None else int(max_prefix)
     with _on(index, stream):
         if out is None:
             out = _empty4(B, H, Nq, d, dtype)
@@ -761,15 +767,19 @@ def _raw_kvq8_prefix(fn_name, dtype, q, cache, prefix_table, prefix_len, page_ta
             _check_tensor("out", out, dtype, shape, index)
             _check_tensor("lse", lse, _F32, shape[:3], index)
         if n_splits is None:
-            n_splits, n_parts = fa_kvq8_prefix_plan(B, H, Hkv, Nq, max_prefix, max_len, d)
-        if workspace is None:
+            n_splits, n_parts, need = _kvq8_prefix_plan(B, H, Hkv, Nq, max_prefix, max_len, d)
+        else:
+            n_splits, n_parts = int(n_splits), int(n_parts)
             need = fa_kvq8_prefix_workspace_bytes(B, H, Hkv, Nq, max_prefix, d, n_splits, n_parts)
-            workspace = _empty_bytes(need) if need else None
-        rc = getattr(lib, fn_name)(q.data_ptr(), *ptrs[:4], prefix_table.data_ptr(), prefix_table.shape[0],
+        room = 0
+        if workspace is not None:
+            room = _nbytes(workspace, index)
+        elif need:
+            workspace, room = _empty_bytes(need), need
+        rc = getattr(lib, fn_name)(q.data_ptr(), *ptrs[:4], prefix_table.data_ptr(), prefix_pages[0],
                                    prefix_len.data_ptr(), ptrs[4], n_pages, max_pages, page, kv_lens.data_ptr(),
                                    out.data_ptr(), lse.data_ptr(), B, H, Hkv, Nq, max_prefix, max_len, d, fmt, float(scale),
-                                   bool(causal), int(n_splits), int(n_parts),
-                                   None if workspace is None else workspace.data_ptr(), _nbytes(workspace, index),
+                                   bool(causal), n_splits, n_parts, None if workspace is None else workspace.data_ptr(), room,
                                    _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, fn_name)
@@ -885,67 +895,69 @@ _SixStrides = ctypes.c_longlong * 6
 
 
 def _rotary_strides(name, t, index, dtype, packed):
-    """(B, H, N, element strides of b, n, h) of a [total, H, d] or [B, H, N, d] tensor."""
+    """(shape, element strides of b, n, h) of a [total, H, d] or [B, H, N, d] tensor."""
     shape = t.shape
     if t.dtype is not dtype or t.get_device() != index or len(shape) != (3 if packed else 4):
         raise ValueError(f"{name} must be a {dtype} tensor {'[total, H, d]' if packed else '[B, H, N, d]'} on cuda:{index}")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name}: the head dimension must be contiguous")
     if packed:
-        (N, H, _), B, sb, sn, sh = shape, 1, 0, st[0], st[1]
+        sn, sh, one = t.stride()
+        strides = (0, sn if shape[0] > 1 else 0, sh if shape[1] > 1 else 0)
     else:
-        (B, H, N, _), (sb, sh, sn, _) = shape, st
-    return B, H, N, (sb if B > 1 else 0, sn if N > 1 else 0, sh if H > 1 else 0)
+        sb, sh, sn, one = t.stride()
+        strides = (sb if shape[0] > 1 else 0, sn if shape[2] > 1 else 0, sh if shape[1] > 1 else 0)
+    if one != 1:
+        raise ValueError(f"{name}: the head dimension must be contiguous")
+    return shape, strides
+
+
+def _rotary_out(t, shape, strides, dtype, packed, inplace):
+    """(tensor that the result goes to, its strides and the input's as the C call takes them)."""
+    if inplace:
+        if 0 in [s for s, n in zip(t.stride(), shape) if n > 1]:
+            raise ValueError("a tensor that repeats its rows cannot be turned in place")
+        return t, _SixStrides(*strides, *strides)
+    if packed:
+        N, H, d = shape
+        return _empty3(N, H, d, dtype), _SixStrides(*strides, 0, H * d, d)
+    B, H, N, d = shape
+    return _empty4(B, H, N, d, dtype), _SixStrides(*strides, H * N * d, d, N * d)
 
 
 def _rotary(q, k, positions, inv_freq, axis, inverse, inplace, stream):
-    packed, index, dtype = q.dim() == 3, q.get_device(), q.dtype
+    index, dtype = q.get_device(), q.dtype
     suffix = _FP16_SUFFIX.get(dtype)
     if suffix is None:
         raise ValueError(f"unsupported dtype {dtype}")
     if index < 0:
         raise ValueError("q must be on a CUDA device")
-    B, Hq, N, q_in = _rotary_strides("q", q, index, dtype, packed)
-    d, pairs = q.shape[-1], inv_freq.numel()
-    tokens = (N,) if packed else (B, N)
-    if positions.dim() != len(tokens) + 1:
+    packed = q.dim() == 3
+    sq, q_in = _rotary_strides("q", q, index, dtype, packed)
+    (N, Hq, d), B = (sq, 1) if packed else ((sq[2], sq[1], sq[3]), sq[0])
+    places, pairs = positions.shape, inv_freq.shape[0]
+    if places[1:] != ((N,) if packed else (B, N)):
         raise ValueError("positions must be [n_axes, total], or [n_axes, B, N] for q of four dimensions")
-    _check_tensor("positions", positions, _I32, (positions.shape[0], *tokens), index)
-    for name, t, want in (("inv_freq", inv_freq, torch.float64), ("axis", axis, _I32)):
-        if t.dtype is not want or t.is_cuda or t.dim() != 1 or t.numel() != pairs or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {want} tensor [pairs] on the CPU")
-    tensors = [(q, q_in)]
-    Hk = 0
+    _check_tensor("positions", positions, _I32, places, index)
+    if (inv_freq.dtype is not torch.float64 or axis.dtype is not _I32 or inv_freq.get_device() >= 0 or axis.get_device() >= 0
+            or inv_freq.dim() != 1 or axis.shape != inv_freq.shape or not inv_freq.is_contiguous() or not axis.is_contiguous()):
+        raise ValueError("inv_freq and axis must be contiguous tensors [pairs] on the CPU, float64 and int32")
     if k is not None:
-        Bk, Hk, Nk, k_in = _rotary_strides("k", k, index, dtype, packed)
-        if Bk != B or Nk != N or k.shape[-1] != d:
+        sk, k_in = _rotary_strides("k", k, index, dtype, packed)
+        Hk = sk[1]
+        if sk[-1] != d or (sk[0] != N if packed else sk[0] != B or sk[2] != N):
             raise ValueError("k must have q's tokens and d")
-        tensors.append((k, k_in))
     name = "fa_rotary" + suffix
-    args, outs = [], []
     with _on(index, stream):
-        for t, strides in tensors:
-            if inplace:
-                out, to = t, strides
-                if any(s == 0 for s, n in zip(t.stride(), t.shape) if n > 1):
-                    raise ValueError("a tensor that repeats its rows cannot be turned in place")
-            elif packed:
-                out = _empty3(N, t.shape[1], d, dtype)
-                to = (0, t.shape[1] * d, d)
-            else:
-                out = _empty4(B, t.shape[1], N, d, dtype)
-                to = (t.shape[1] * N * d, d, N * d)
-            outs.append(out)
-            args += [t.data_ptr(), out.data_ptr(), _SixStrides(*strides, *to), t.shape[1]]
-        if len(tensors) == 1:
-            outs.append(None)
-            args += [None, None, None, 0]
-        rc = getattr(lib, name)(*args, positions.data_ptr(), positions.shape[0], inv_freq.data_ptr(),
-                                axis.data_ptr(), pairs, B, N, d, bool(inverse), _raw_stream(index, stream))
+        q_out, q_six = _rotary_out(q, sq, q_in, dtype, packed, inplace)
+        if k is None:
+            k_out, of_k = None, (None, None, None, 0)
+        else:
+            k_out, k_six = _rotary_out(k, sk, k_in, dtype, packed, inplace)
+            of_k = (k.data_ptr(), k_out.data_ptr(), k_six, Hk)
+        rc = getattr(lib, name)(q.data_ptr(), q_out.data_ptr(), q_six, Hq, *of_k, positions.data_ptr(), places[0],
+                                inv_freq.data_ptr(), axis.data_ptr(), pairs, B, N, d, inverse, _raw_stream(index, stream))
     if rc != FA_OK:
         raise FAError(rc, name)
-    return outs[0], outs[1]
+    return q_out, k_out
 
 
 def rotary(q, k, positions, inv_freq, axis, inplace=False, stream=None):
