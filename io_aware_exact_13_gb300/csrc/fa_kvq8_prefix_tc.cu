@@ -335,11 +335,13 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) fa_kvq8_prefix_kernel(const
             uint32_t n_issued = 0;
             bool ok = true;
             for (int i = 0; ok && i < tiles; ++i) ok = wait_all(q_full(i), 0, abort_flag, p);
+            if (ok) ok = wait_all(k_full(0), 0, abort_flag, p);
             for (int j = 0; ok && j < nb; ++j) {
                 const int slot = j % RK;
-                ok = wait_all(k_full(slot), (uint32_t)(j / RK) & 1u, abort_flag, p);
                 for (int i = 0; ok && i < tiles; ++i) {
-                    if (n_issued > 0) ok = wait_all(s_free, (n_issued - 1) & 1u, abort_flag, p);
+                    // the next block's K is waited for while the last product still has the S buffer
+                    if (i == tiles - 1 && j + 1 < nb) ok = wait_all(k_full((j + 1) % RK), (uint32_t)((j + 1) / RK) & 1u, abort_flag, p);
+                    if (ok && n_issued > 0) ok = wait_all(s_free, (n_issued - 1) & 1u, abort_flag, p);
                     if (!ok) break;
                     ++n_issued;
                     tc_fence_after();

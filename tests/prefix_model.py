@@ -90,9 +90,11 @@ def simulate_prefix(blocks, tiles, raw, seed, dead=(), s_free=True, k_empty=True
         for t in range(tiles):
             yield ("wait", f"q_full{t}", 0)
         issued = 0
+        yield ("wait", "k_full0", 0)
         for j in range(blocks):
-            yield ("wait", f"k_full{j % 2}", j // 2)
             for t in range(tiles):
+                if t == tiles - 1 and j + 1 < blocks:
+                    yield ("wait", f"k_full{(j + 1) % 2}", (j + 1) // 2)
                 if issued and s_free:
                     yield ("wait", "s_free", issued - 1)
                 issued += 1
