@@ -619,10 +619,25 @@ bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
     return x < y + nb && y < x + na;
 }
 
-// Strides of one tensor of fa_rotary: input b, n, h, output b, n, h, in elements; whole 16-byte rows.
-bool rotary_tensor(const void *in, void *out, const long long *s, int heads, fa::RotaryTensor *t) {
+// Strides of one tensor of fa_rotary: input b, n, h, output b, n, h, in elements; whole 16-byte rows. The output's rows lie
+// apart, and where it is the input they are the input's.
+bool rotary_tensor(const void *in, void *out, const long long *s, int B, int N, int heads, int d, fa::RotaryTensor *t) {
+    const int count[3] = {B, N, heads};
     for (int i = 0; i < 6; ++i)
         if (s[i] % 8) return false;
+    for (int i = 0; in == out && i < 3; ++i)
+        if (count[i] > 1 && s[i] != s[3 + i]) return false;
+    bool taken[3] = {false, false, false};
+    int64_t reach = d;  // of the dimensions with smaller strides
+    for (int k = 0; k < 3; ++k) {
+        int at = -1;
+        for (int i = 0; i < 3; ++i)
+            if (!taken[i] && count[i] > 1 && (at < 0 || s[3 + i] < s[3 + at])) at = i;
+        if (at < 0) break;
+        taken[at] = true;
+        if (s[3 + at] < reach || s[3 + at] > (int64_t(1) << 40)) return false;
+        reach += (count[at] - 1) * s[3 + at];
+    }
     *t = {in, out, s[0], s[1], s[2], s[3], s[4], s[5], heads};
     return true;
 }
@@ -641,8 +656,10 @@ int rotary_common(bool fp16, const void *q, void *q_out, const long long *q_stri
     if (n_axes < 1 || n_axes > fa::kRotaryMaxAxes) return FA_ERR_ARG;
     fa::RotaryArgs a;
     a.x[1] = {nullptr, nullptr, 0, 0, 0, 0, 0, 0, 0};
-    if (!rotary_tensor(q, q_out, q_strides, Hq, &a.x[0]) || (Hk != 0 && !rotary_tensor(k, k_out, k_strides, Hk, &a.x[1])))
+    if (!rotary_tensor(q, q_out, q_strides, B, N, Hq, d, &a.x[0]) ||
+        (Hk != 0 && !rotary_tensor(k, k_out, k_strides, B, N, Hk, d, &a.x[1])))
         return FA_ERR_SHAPE;
+    if (Hk != 0 && (q_out == k_out || q_out == k || k_out == q)) return FA_ERR_ARG;
     for (int i = 0; i < pairs; ++i) {
         if (!std::isfinite(inv_freq[i]) || axis[i] < 0 || axis[i] >= n_axes) return FA_ERR_ARG;
         // the fraction of a turn in 2^-64; a negative frequency is the complement of its magnitude's
@@ -1154,9 +1171,15 @@ int fa_kvq8_evict(void *k_codes, void *v_codes, float *k_scale, float *v_scale, 
     if (nseq < 1 || static_cast<int64_t>(nseq) * Hkv > INT32_MAX / 2) return FA_ERR_SHAPE;
     if (keep < 1 || keep > kKvq8MaxLen || recent < 0 || recent > keep) return FA_ERR_ARG;
     const uint64_t heads = static_cast<uint64_t>(nseq) * Hkv, weights = heads * max_pages * page * 4;
-    if (overlap(weight, weights, weight_out, weights) || overlap(weight, weights, kept, heads * keep * 4) ||
-        overlap(weight_out, weights, kept, heads * keep * 4) || overlap(kv_lens, nseq * 4ull, lens_out, nseq * 4ull))
-        return FA_ERR_ARG;
+    const uint64_t scales = static_cast<uint64_t>(n_pages) * Hkv * 4, codes = scales / 4 * page * d, lens = nseq * 4ull;
+    const struct {
+        const void *at;
+        uint64_t bytes;
+    } all[] = {{lens_out, lens}, {kept, heads * keep * 4}, {weight_out, weights}, {weight, weights}, {kv_lens, lens},
+               {page_table, lens * max_pages}, {k_scale, scales}, {v_scale, scales}, {k_codes, codes}, {v_codes, codes}};
+    for (int out = 0; out < 3; ++out)
+        for (int i = out + 1; i < 10; ++i)
+            if (overlap(all[out].at, all[out].bytes, all[i].at, all[i].bytes)) return FA_ERR_ARG;
     DeviceInfo *di = device_info();
     if (!di) return FA_ERR_LAUNCH;
     fa::Kvq8EvictArgs a;

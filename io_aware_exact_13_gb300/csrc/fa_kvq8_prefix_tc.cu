@@ -23,6 +23,10 @@
 //   warps 12-19  converters: raw codes -> fp16 in the 128-byte swizzled K and V tiles
 // The own keys' kernel behind it is a programmatic dependent that needs nothing of it: it fills the SMs that this one leaves
 // free, and ends after it, so that the merge behind may rely on both.
+// Measured: 64 sequences of 64 / 8 heads of 128 behind 32768 int8 keys, 88 us (91 where the S issuer waited for K only once the S
+// buffer was free); a block of two tiles takes some 3700 cycles, of which the products need
+// 2048 and the softmax of a tile about 1500, a block of one tile 1750 to 2300, the first of a CTA 16000. Slower: converters in
+// two groups, one for K and one for V (a run of 6 blocks and one tile 28.8 us for 22.8).
 #include <float.h>
 
 #include "fa_fwd_bk128.cuh"

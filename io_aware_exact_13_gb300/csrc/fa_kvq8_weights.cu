@@ -9,6 +9,8 @@
 // Bound: HBM, the K codes once and eight bytes of weight for each key and head. As in the attention (fa_kvq8_attn.cuh) the
 // codes are the 16-row operand of 16x8x16 MMAs, cut from a lane's own 16-byte loads, and up to 32 query rows are the
 // columns; further rows go over the stretch again. bf16 queries enter in fp16 under a power of two for each row.
+// Measured: 64 sequences up to 8192 keys, 32 / 8 heads of 128, int8, 64 us (88 % of the copy rate); a CTA for each 256 keys of
+// a head 125, the same with all its codes requested at once 115. One sequence of 509 keys, 8 heads of 64: 6.2.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -72,6 +72,16 @@ def test_evict_sizes_and_overlaps_are_refused(fa):
         assert evict(fa, p) == fa.FA_ERR_ARG, (i, j, off)
 
 
+@pytest.mark.parametrize("out", [7, 8, 9])
+@pytest.mark.parametrize("other", range(10))
+def test_evict_outputs_on_any_other_tensor_are_refused(fa, out, other):
+    p = [0x1000000 * (i + 1) for i in range(10)]
+    if out == other:
+        return
+    p[out] = p[other]
+    assert evict(fa, p) == fa.FA_ERR_ARG
+
+
 def rotary(fa, ptrs=None, strides=(0, 128, 64, 0, 128, 64), Hq=2, Hk=1, n_axes=2, inv=None, axis=None, pairs=32, B=1, N=3, d=64,
            name="fa_rotary"):
     p = pointers(5, ptrs)
@@ -100,6 +110,25 @@ def test_rotary_arguments_are_refused(fa, name):
     for kw in (dict(n_axes=0), dict(n_axes=9), dict(n_axes=1), dict(axis=[-1] * 64), dict(inv=[float("nan")] * 64),
                dict(inv=[float("inf")] * 64)):
         assert rotary(fa, name=name, **kw) == fa.FA_ERR_ARG, kw
+
+
+@pytest.mark.parametrize("name", ["fa_rotary", "fa_rotary_fp16"])
+def test_rotary_outputs_that_collide_are_refused(fa, name):
+    base = [0x1000000 * (j + 1) for j in range(5)]
+    # output rows on each other: a repeated token or head, half a row apart, tokens within the heads' reach, far out
+    for s in ((0, 0, 64), (0, 128, 0), (0, 128, 32), (0, 64, 64), (0, 96, 64), (0, -128, 64), (0, 1 << 41, 64)):
+        assert rotary(fa, strides=(0, 128, 64, *s), name=name) == fa.FA_ERR_SHAPE, s
+    assert rotary(fa, strides=(384, 128, 64, 320, 128, 64), B=2, name=name) == fa.FA_ERR_SHAPE
+    for i, j in ((0, 1), (2, 3)):  # in place, under other strides
+        p = list(base)
+        p[j] = p[i]
+        assert rotary(fa, p, strides=(0, 128, 64, 0, 256, 64), name=name) == fa.FA_ERR_SHAPE
+    for i, j in ((3, 1), (1, 2), (3, 0)):  # one output for both, q's on k, k's on q
+        p = list(base)
+        p[i] = p[j]
+        assert rotary(fa, p, name=name) == fa.FA_ERR_ARG, (i, j)
+    p = [base[0], base[0], base[0], base[0], base[4]]  # the same tensor for q and k, in place
+    assert rotary(fa, p, Hq=1, name=name) == fa.FA_ERR_ARG
 
 
 def test_bindings_refuse(fa):
