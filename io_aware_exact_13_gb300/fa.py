@@ -11,13 +11,16 @@ Names follow the C ABI: ``fa_fwd`` (bf16), ``fa_fwd_fp16``, ``fa_fwd_fp32``,
 ``fa_fwd_splitkv`` / ``fa_fwd_splitkv_fp16`` (decoding), ``fa_bwd`` /
 ``fa_bwd_fp16`` (backward by recomputation), ``fa_fwd_varlen`` /
 ``fa_fwd_varlen_fp16`` (packed variable-length batches), ``fa_fwd_kvq8`` /
-``fa_fwd_kvq8_fp16`` (decoding over an 8-bit cache), ``fa_fwd_cross`` / ``fa_bwd_cross`` and their ``_fp16`` forms
+``fa_fwd_kvq8_fp16`` (decoding over an 8-bit cache), ``fa_fwd_kvq8_prefix`` / ``fa_fwd_kvq8_prefix_fp16`` (the same
+behind a prefix that all sequences share), ``fa_fwd_cross`` / ``fa_bwd_cross`` and their ``_fp16`` forms
 (keys of another length), their sizing helpers,
 ``fa_status_string``, ``fa_get_device_status``, ``fa_num_sms``. ``attention``,
-``attention_decode``, ``attention_varlen``, ``attention_kvq8``, ``attention_cross``,
+``attention_decode``, ``attention_varlen``, ``attention_kvq8``, ``attention_kvq8_prefix``, ``attention_cross``,
 ``attention_cross_backward`` and ``attention_backward`` are convenience wrappers
 that allocate outputs (and the workspaces) with torch and pick the entry point from the dtype; ``kvq8_append`` and
-``kvq8_read`` write and read the 8-bit cache (``KVCacheQ8``, allocated by ``kv_cache_q8``).
+``kvq8_read`` write and read the 8-bit cache (``KVCacheQ8``, allocated by ``kv_cache_q8``), ``kvq8_weights`` adds up the
+attention that its keys receive and ``kvq8_evict`` cuts it down by that. ``rotary`` turns queries and keys by positions
+along several axes (frequencies from ``rotary_frequencies``), ``rotary_backward`` their gradients.
 """
 from __future__ import annotations
 
@@ -964,7 +967,8 @@ def rotary(q, k, positions, inv_freq, axis, inplace=False, stream=None):
     """``q`` and ``k`` (or None) turned by rotary positions: packed [total, H, d] with ``positions`` [n_axes, total], or
     [B, H, N, d] with [n_axes, B, N] (int32 on the GPU), any strides that are multiples of 8 with contiguous rows. Pair i,
     dims i and pairs + i, is turned by positions[axis[i]] * inv_freq[i]; ``inv_freq`` (float64) and ``axis`` (int32) are
-    CPU tensors [pairs], as ``rotary_frequencies`` makes them. Returns (q, k), contiguous, or written in place."""
+    CPU tensors [pairs], as ``rotary_frequencies`` makes them. Returns (q, k), contiguous, or written in place (then no row
+    of either lies on another)."""
     return _rotary(q, k, positions, inv_freq, axis, False, inplace, stream)
 
 
