@@ -1114,8 +1114,7 @@ long long fa_kvq8_prefix_plan(int B, int H, int Hkv, int Nq, int max_prefix, int
     if (rc != FA_OK) return rc;
     DeviceInfo *di = device_info();
     const int sms = di ? di->num_sms : kNominalSms, rows = H / Hkv * Nq;
-    *n_splits = fa::kvq8_prefix_splits(B, Hkv, rows, max_prefix, max_len, d, sms);
-    *n_parts = fa::kvq8_prefix_parts(B, Hkv, rows, max_prefix, max_len, d, *n_splits, sms);
+    fa::kvq8_prefix_plan(B, Hkv, rows, max_prefix, max_len, d, sms, n_splits, n_parts);
     return fa_kvq8_prefix_workspace_bytes(B, H, Hkv, Nq, max_prefix, d, *n_splits, *n_parts);
 }
 

@@ -91,9 +91,9 @@ int launch_kvq8_append(const Kvq8AppendArgs &a, bool fp16);
 int launch_kvq8_read(const Kvq8ReadArgs &a, bool fp16);
 int launch_kvq8_attention(const Kvq8AttnArgs &a, bool fp16);
 int launch_kvq8_prefix(const Kvq8AttnArgs &a, bool fp16);
-// Runs of keys that a shared prefix is cut into (0: it is read with each sequence's own keys), and the workspace.
-int kvq8_prefix_splits(int B, int Hkv, int rows, int max_prefix, int max_len, int d, int num_sms);
-int kvq8_prefix_parts(int B, int Hkv, int rows, int max_prefix, int max_len, int d, int splits, int num_sms);
+// Runs of keys that a shared prefix is cut into (0: it is read with each sequence's own keys), the parts of the own keys,
+// and the workspace.
+void kvq8_prefix_plan(int B, int Hkv, int rows, int max_prefix, int max_len, int d, int num_sms, int *splits, int *parts);
 size_t kvq8_prefix_workspace_bytes(int B, int Hkv, int rows, int d, int splits, int parts);
 int launch_kvq8_weights(const Kvq8WeightsArgs &a, bool fp16);
 int launch_kvq8_evict(const Kvq8EvictArgs &a);
