@@ -35,6 +35,7 @@ WEIGHTS = [
     ("int8", "fp16", 128, 12, 2, 7, 64, [129, 6], True),
     ("e4m3", "bf16", 16, 40, 1, 16, 128, [15, 16, 700], True),
     ("int8", "bf16", 64, 5, 1, 3, 64, [2, 1, 1300], False),
+    ("e4m3", "fp16", 16, 4, 2, 2, 64, [3, 0, 40, 17, 1] * 30, True),
 ]
 
 
@@ -202,6 +203,21 @@ def test_evict_many_heads(fa):
     cache = filled(fa, rng, "e4m3", n_pages, 8, 32, 64)
     w = make_weights(rng, 90, 8, table.shape[1] * 32, "spread")
     want = run_evict(fa, cache, "e4m3", table, lens, w, 120, 30)
+    status_ok(fa)
+    check_cache(cache, want)
+
+
+@pytest.mark.parametrize("count", [128, 129, 300])
+@pytest.mark.parametrize("page", [16, 128])
+def test_evict_many_sequences(fa, count, page):
+    """Up to 128 sequences those that are cut come first, more go by their own place; none, some and long ones cut."""
+    rng = np.random.default_rng(count + page)
+    lens = [int(x) for x in rng.integers(0, 90, count)]
+    lens[:3] = [600, 40, 41]
+    table, n_pages = random_table(rng, [max(n, 1) for n in lens], page)
+    cache = filled(fa, rng, "int8", n_pages, 2, page, 64)
+    w = make_weights(rng, count, 2, table.shape[1] * page, "spread")
+    want = run_evict(fa, cache, "int8", table, lens, w, 40, 9)
     status_ok(fa)
     check_cache(cache, want)
 

@@ -91,6 +91,20 @@ def test_matches_the_definition(fa, fmt, dtype, page, H, Hkv, Nq, d, prefix, len
     check(q, cache, shared, prefix, table, lens, out, lse, 1 / math.sqrt(d), causal)
 
 
+@pytest.mark.parametrize("splits", [None, (0, 0), (0, 100), (1, 0), (2, 9), (7, 0)])
+@pytest.mark.parametrize("fmt,d", [("int8", 64), ("e4m3", 128)])
+def test_many_sequences(fa, fmt, d, splits):
+    """More rows than a few tiles, the last one partly filled; with seven runs more CTAs than SMs."""
+    rng = np.random.default_rng(d)
+    lens = [int(x) for x in rng.integers(0, 70, 301)]
+    shared, table, n_pages = tables(rng, 900, lens, 16)
+    cache = filled(fa, rng, fmt, n_pages, 2, 16, d)
+    q = torch.from_numpy(rng.standard_normal((301, 8, 3, d))).to(torch.bfloat16).to(DEV)
+    out, lse = call(fa, q, cache, shared, 900, table, lens, causal=True, splits=splits, max_prefix=900, max_len=max(lens))
+    status_ok(fa)
+    check(q, cache, shared, 900, table, lens, out, lse, 1 / math.sqrt(d), True)
+
+
 @pytest.mark.parametrize("splits", SPLITS)
 @pytest.mark.parametrize("fmt,d", [("int8", 128), ("e4m3", 64)])
 @pytest.mark.parametrize("scale", [0.0, -0.11, 0.4])
