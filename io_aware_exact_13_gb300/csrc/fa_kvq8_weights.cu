@@ -10,7 +10,8 @@
 // codes are the 16-row operand of 16x8x16 MMAs, cut from a lane's own 16-byte loads, and up to 32 query rows are the
 // columns; further rows go over the stretch again. bf16 queries enter in fp16 under a power of two for each row.
 // Measured: 64 sequences up to 8192 keys, 32 / 8 heads of 128, int8, 64 us (88 % of the copy rate); a CTA for each 256 keys of
-// a head 125, the same with all its codes requested at once 115. One sequence of 509 keys, 8 heads of 64: 6.2.
+// a head 125, the same with all its codes requested at once 115. One sequence of 509 keys, 8 heads of 64: 6.2. 12
+// sequences up to 6001 keys, 20 rows for each of 4 heads of 64: 10.4 (12.5 with four tiles of rows instead of three).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -26,7 +27,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kTileKeys = 16;
-__host__ __device__ constexpr int w_ctas(int NT) { return NT == 4 ? 3 : 4; }  // resident CTAs per SM: 168 or 128 registers
+__host__ __device__ constexpr int w_ctas(int NT) { return NT >= 3 ? 3 : 4; }  // resident CTAs per SM: 168 or 128 registers
 
 struct WeightParams {
     const void *q;
@@ -291,7 +292,12 @@ int launch_t(const Kvq8WeightsArgs &a) {
     p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
     if (p.rows <= 8) return launch_nt<T, D, FMT, 1>(a, p);
     if (p.rows <= 16) return launch_nt<T, D, FMT, 2>(a, p);
-    return launch_nt<T, D, FMT, 4>(a, p);
+    // Three or four tiles of eight rows for each pass over a stretch: the fewest that hold all, or three where that takes no more
+    // passes, or at d 128, where four spill. (64 sequences up to 4000 keys of 4 heads, three / four: d 64, 24 rows 23.4 / 27.0 us,
+    // 32 39.2 / 25.9, 48 39.2 / 43.4, 64 51.5 / 41.4, 80 70.0 / 62.0; d 128 29.1 / 40.0, 47.9 / 39.1, 53.7 / 80.0, 72.1 / 74.4,
+    // 89.5 / 102.7, 128 rows 148.5 / 152.6. With one tile 16 rows take 28.6 where two take 18.9.)
+    const bool three = p.rows <= 24 || (p.rows > 32 && (D == 128 || (p.rows + 23) / 24 == (p.rows + 31) / 32));
+    return three ? launch_nt<T, D, FMT, 3>(a, p) : launch_nt<T, D, FMT, 4>(a, p);
 }
 
 template <typename T>

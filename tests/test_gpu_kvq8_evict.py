@@ -36,6 +36,9 @@ WEIGHTS = [
     ("e4m3", "bf16", 16, 40, 1, 16, 128, [15, 16, 700], True),
     ("int8", "bf16", 64, 5, 1, 3, 64, [2, 1, 1300], False),
     ("e4m3", "fp16", 16, 4, 2, 2, 64, [3, 0, 40, 17, 1] * 30, True),
+    # rows that share a head: around each number of tiles of eight, and of passes
+    *[("int8", ("bf16", "fp16")[rows % 2], 16, 2 * rows, 2, 1, d, [37, 200], False)
+      for rows in (8, 9, 16, 17, 24, 25, 32, 33, 48, 49, 64, 72, 80, 129) for d in (64, 128)],
 ]
 
 
