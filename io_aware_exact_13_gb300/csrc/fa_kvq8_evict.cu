@@ -85,6 +85,8 @@ __device__ __forceinline__ uint32_t order_of(float w) {
 // And back; all NaN are one.
 __device__ __forceinline__ float weight_of(uint32_t v) { return __uint_as_float(v & 0x80000000u ? v ^ 0x80000000u : ~v); }
 
+// (With 1024 threads, whose registers spill at two CTAs on an SM, 8 sequences of 8 heads, 8192 tokens to 6144, take 85.1 us for 64.2
+// in all, 24 of 6000 to 4000 95.4 for 91.8.)
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelMost = 24576;  // positions whose weights are kept in shared memory (two CTAs on an SM)
 constexpr int kBins = 2048, kBinBits = 11;
