@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const Evict
         }
         __syncthreads();
         lo += (uint32_t)(top_bin - hit[0]) << shift;
-        hi = min(hi, lo + ((1u << shift) - 1u));
+        hi = lo + min(hi - lo, (1u << shift) - 1u);  // (the top bin's end may lie past 2^32, where NaN's integer is hi)
         above = hit[1];
         T = lo;
         if (above + hit[2] == need) {  // all that reach lo
