@@ -278,6 +278,7 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_
 }
 
 __device__ __forceinline__ __half2 half2_of(uint32_t h) { return *reinterpret_cast<const __half2 *>(&h); }
+constexpr float kMostRatio = 0x1p15f;  // the largest power of two in fp16
 // Four codes (as fp16) times the power of two r, rounded to codes once, where no product is past the largest code.
 // int8: code r + 1536 in one rounding is an integer whose low byte is the code's. e4m3: code r is exact in fp16, or below
 // 2^-20, where it becomes 0 either way.
@@ -442,11 +443,12 @@ __global__ void __launch_bounds__(kMoveThreads, 3) fa_kvq8_move_kernel(const __g
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
             const int t = i * PER + lane / LANES;
-            // (a token of zeros may have come under a scale far above the page's)
-            const float ratio = fminf(s[i] * inv, 512.0f);
+            // (at most 127 for a code of int8 that is not 0 and 2^18 for one of e4m3, whose smallest is 2^-9 and most often beside
+            // a larger one that has gone; a token of zeros may have come under any scale)
+            const float ratio = fminf(s[i] * inv, 0x1p18f);
             uint32_t w[4];
-            if (!slow) {
-                const __half2 r = __float2half2_rn(ratio);  // a power of two, or so small that every code becomes 0
+            if (!slow && (FMT == kKvq8Int8 || ratio <= kMostRatio || top_code[i] == 0.f)) {
+                const __half2 r = __float2half2_rn(fminf(ratio, kMostRatio));  // a power of two, or so small that every code becomes 0
 #pragma unroll
                 for (int e = 0; e < 4; ++e) w[e] = rescaled4<FMT>(half2_of(x[i][2 * e]), half2_of(x[i][2 * e + 1]), r);
             } else {
