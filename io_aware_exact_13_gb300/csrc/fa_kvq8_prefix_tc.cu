@@ -8,10 +8,14 @@
 //
 // Scales. A page's values are code * scale. Where all K scales of a run are powers of two (append writes no others) within
 // 2^20 of the largest, ks_max, the K tile holds code * 32 ks / ks_max, exact in fp16 (an int8 code and an e4m3 code are
-// multiples of 2^0 and 2^-9 of at most 448: 2^-24 is not undercut), so that one factor serves the whole row; V likewise. Any
-// other run (other scales, pages of zeros alone, a scale that is not positive, pages that are none) is done with the codes as
-// they are: each 16-key group of scores is multiplied by its own page's factor, and P carries 2^(log2 vs) under a
-// running maximum of its own, as in fa_kvq8_attn.cuh.
+// multiples of 2^0 and 2^-9 of at most 448: 2^-24 is not undercut), so that one factor serves the whole row; V likewise, within
+// 2^7: P, which then knows nothing of the V scales, is held 2^7 up, so that what fp16 loses of it (2^-25 at most) is no
+// more than 2^-25 of the row's largest contribution p vs, as in fa_kvq8_attn.cuh. (Not raised, and with V within 2^20,
+// weights of 2^-26 were lost whose V scale is 2^20 times that of the keys of weight 1.) Any other run (scales further apart
+// or no powers of two, K pages of zeros alone, pages that are none) is done with the codes as they are: each 16-key group of
+// scores is multiplied by its own page's factor, and P carries 2^(log2 vs) under a running maximum of its own, as there. (64
+// sequences of 64 / 8 heads of 128 behind 32768 int8 keys and 2048 of their own: 129 us with V scales up to 2^7 apart, 201
+// with 2^8 and more; 16 of 32 / 8 heads behind 8192: 23.6 and 37.)
 // Q is fp16, bf16 rows under a power of two that puts the row's largest magnitude into [2^15, 2^16).
 //
 // Bound: for few rows HBM (2 d bytes a key and head), from about 250 rows on the tensor cores, in effect the softmax's
@@ -38,7 +42,8 @@ namespace {
 constexpr int kConv = 256;          // converter threads
 constexpr int kPrefixThreads = 384 + kConv;
 
-constexpr int kSpread = 20;         // log2 of the scales' range that stays exact
+constexpr int kSpreadK = 20, kSpreadV = 7;  // log2 of the scales' ranges that one factor serves
+constexpr float kLift = (float)kSpreadV;    // log2 of what a weight of 1 is in P under such a factor: P is at most 2^(kLift + kTau)
 constexpr float kNone = -FLT_MAX;   // a running maximum that has seen no key
 
 template <int D>
@@ -407,8 +412,8 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) fa_kvq8_prefix_kernel(const
                 named_bar_sync(1, kConv);
                 if (tid == 0) {
                     // within 2^-110 .. 2^120, and K not all zeros (V may be)
-                    const bool k_ok = scan[0] >= 127 - 110 && scan[0] <= 127 + 120 && scan[0] - scan[1] <= kSpread;
-                    const bool v_ok = scan[2] == 0 || (scan[2] >= 127 - 110 && scan[2] <= 127 + 120 && scan[2] - scan[3] <= kSpread);
+                    const bool k_ok = scan[0] >= 127 - 110 && scan[0] <= 127 + 120 && scan[0] - scan[1] <= kSpreadK;
+                    const bool v_ok = scan[2] == 0 || (scan[2] >= 127 - 110 && scan[2] <= 127 + 120 && scan[2] - scan[3] <= kSpreadV);
                     if (!k_ok || !v_ok || !(p.scale_log2 > 0.f)) scan[4] = 1;
                 }
                 named_bar_sync(1, kConv);
@@ -563,8 +568,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) fa_kvq8_prefix_kernel(const
                         for (int i = 0; i < 128; ++i) x[i] *= sl2;
                         mul = 1.0f;
                     }
-                    const float m_new = fmaxf(m_ref, mb);
-                    const bool need = (m_new > m_ref + kTau) || (m_ref == -INFINITY && m_new != -INFINITY);
+                    // (the difference, not m_ref + kLift + kTau, which far out may round up and let P past fp16's range)
+                    const bool need = mb - m_ref > kLift + kTau;
+                    const float m_new = mb - kLift;
                     alpha = need ? ex2_approx(m_ref - m_new) : 1.0f;
                     rescale = __any_sync(0xffffffffu, need) && j > 0;
                     if (need) {
@@ -623,7 +629,9 @@ __global__ void __launch_bounds__(kPrefixThreads, 1) fa_kvq8_prefix_kernel(const
                         l *= ex2_approx(m_ref - mx);
                         m_ref = mx;
                     }
-                    const bool need = mv > mw + kTau;
+                    const float lift = regular ? kLift : 0.f;  // (lv is 0 where regular)
+                    const bool need = mv - mw > lift + kTau;
+                    if (need) mv -= lift;
                     alpha = need ? ex2_approx(mw - mv) : 1.0f;
                     rescale = __any_sync(0xffffffffu, need) && j > 0;
                     if (need) mw = mv;
