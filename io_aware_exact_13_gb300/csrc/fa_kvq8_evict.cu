@@ -95,7 +95,7 @@ constexpr int kBins = 2048, kBinBits = 11;
 // past the first `held` positions are read again for every count.
 __global__ void __launch_bounds__(kSelThreads) fa_kvq8_select_kernel(const EvictParams p, int held) {
     extern __shared__ uint4 order_sm[];  // [held / 4] integers of the weights' order
-    __shared__ int bins[kBins];  // from the top down
+    __shared__ __align__(16) int bins[kBins];  // from the top down; read four at a time
     __shared__ int sums[kSelWarps];
     __shared__ int2 found[kSelWarps];
     __shared__ int hit[3];
