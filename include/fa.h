@@ -386,13 +386,13 @@ int fa_kvq8_evict(void *k_codes, void *v_codes, float *k_scale, float *v_scale, 
  *              of b, n and h of the input, then of the output, multiples of 8; a row's d values are contiguous.
  *              (Packed tokens [total][H][d] are B = 1, N = total.) Hk = 0: no k. An output's rows do not
  *              overlap (its strides grow past each other's reach, in any order). An output may be its input, with the same
- *              strides, and must not overlap any tensor otherwise.
+ *              strides; otherwise none of its bytes may be another tensor's (FA_ERR_ARG), while rows that lie between
+ *              those of another tensor are fine (q and k of one packed buffer, in place).
  *   positions: int32 [n_axes][B][N] in DEVICE memory, of either sign, 1 <= n_axes <= 8
  *   inv_freq, axis: HOST arrays of `pairs` frequencies (finite) and axes (0 <= axis < n_axes), read during the call
  * Angles are formed modulo a turn in 64-bit integers (off by less than 2^-23 turns at any position for frequencies up to
  * 1, by no more than fp32's rounding at positions below 2^20); products and sums are fp32, results rounded once. Errors as
- * for fa_fwd; FA_ERR_SHAPE for strides or pairs, FA_ERR_ARG for axes, frequencies and one tensor's output given for the
- * other. */
+ * for fa_fwd; FA_ERR_SHAPE for strides or pairs, FA_ERR_ARG for axes, frequencies and outputs that overlap. */
 int fa_rotary(const void *q, void *q_out, const long long *q_strides, int Hq, const void *k, void *k_out,
               const long long *k_strides, int Hk, const int *positions, int n_axes, const double *inv_freq,
               const int *axis, int pairs, int B, int N, int d, int inverse, void *stream);

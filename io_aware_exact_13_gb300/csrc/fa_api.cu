@@ -18,6 +18,7 @@
 #include "fa_kvq8.cuh"
 #include "fa_rotary.cuh"
 #include "fa_splitkv.cuh"
+#include "rows.h"
 
 namespace fa {
 int launch_fwd_bf16(const LaunchArgs &a);
@@ -620,8 +621,9 @@ bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
 }
 
 // Strides of one tensor of fa_rotary: input b, n, h, output b, n, h, in elements; whole 16-byte rows. The output's rows lie
-// apart, and where it is the input they are the input's.
-bool rotary_tensor(const void *in, void *out, const long long *s, int B, int N, int heads, int d, fa::RotaryTensor *t) {
+// apart, and where it is the input they are the input's. What the rows take up in memory goes to `rows`, the input's and the output's.
+bool rotary_tensor(const void *in, void *out, const long long *s, int B, int N, int heads, int d, fa::RotaryTensor *t,
+                   fa::Rows *rows) {
     const int count[3] = {B, N, heads};
     for (int i = 0; i < 6; ++i)
         if (s[i] % 8) return false;
@@ -635,9 +637,11 @@ bool rotary_tensor(const void *in, void *out, const long long *s, int B, int N, 
             if (!taken[i] && count[i] > 1 && (at < 0 || s[3 + i] < s[3 + at])) at = i;
         if (at < 0) break;
         taken[at] = true;
-        if (s[3 + at] < reach || s[3 + at] > (int64_t(1) << 40)) return false;
+        if (s[3 + at] < reach || s[3 + at] > (int64_t(1) << 40) || !rows[1].add(2 * s[3 + at], count[at])) return false;
         reach += (count[at] - 1) * s[3 + at];
     }
+    for (int i = 0; i < 3; ++i)
+        if (count[i] > 1 && (s[i] > (int64_t(1) << 40) || s[i] < -(int64_t(1) << 40) || !rows[0].add(2 * s[i], count[i]))) return false;
     *t = {in, out, s[0], s[1], s[2], s[3], s[4], s[5], heads};
     return true;
 }
@@ -656,10 +660,16 @@ int rotary_common(bool fp16, const void *q, void *q_out, const long long *q_stri
     if (n_axes < 1 || n_axes > fa::kRotaryMaxAxes) return FA_ERR_ARG;
     fa::RotaryArgs a;
     a.x[1] = {nullptr, nullptr, 0, 0, 0, 0, 0, 0, 0};
-    if (!rotary_tensor(q, q_out, q_strides, B, N, Hq, d, &a.x[0]) ||
-        (Hk != 0 && !rotary_tensor(k, k_out, k_strides, B, N, Hk, d, &a.x[1])))
+    fa::Rows of_q[2] = {{q, 2 * d}, {q_out, 2 * d}}, of_k[2] = {{k, 2 * d}, {k_out, 2 * d}};
+    if (!rotary_tensor(q, q_out, q_strides, B, N, Hq, d, &a.x[0], of_q) ||
+        (Hk != 0 && !rotary_tensor(k, k_out, k_strides, B, N, Hk, d, &a.x[1], of_k)))
         return FA_ERR_SHAPE;
-    if (Hk != 0 && (q_out == k_out || q_out == k || k_out == q)) return FA_ERR_ARG;
+    // An output's rows lie on no other tensor's, nor between its own input's: what one thread has written another may read.
+    const fa::Rows of_positions(positions, static_cast<int64_t>(n_axes) * B * N * 4);
+    if ((q != q_out && rows_meet(of_q[0], of_q[1])) || rows_meet(of_positions, of_q[1])) return FA_ERR_ARG;
+    if (Hk != 0 && ((k != k_out && rows_meet(of_k[0], of_k[1])) || rows_meet(of_positions, of_k[1]) || rows_meet(of_q[1], of_k[1]) ||
+                    rows_meet(of_q[0], of_k[1]) || rows_meet(of_k[0], of_q[1])))
+        return FA_ERR_ARG;
     for (int i = 0; i < pairs; ++i) {
         if (!std::isfinite(inv_freq[i]) || axis[i] < 0 || axis[i] >= n_axes) return FA_ERR_ARG;
         // the fraction of a turn in 2^-64; a negative frequency is the complement of its magnitude's
