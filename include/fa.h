@@ -351,7 +351,10 @@ int fa_fwd_kvq8_prefix_fp16(const void *q, const void *k_codes, const void *v_co
  * with q [B][H][Nq][d] and lse [B][H][Nq] as fa_fwd_kvq8 takes and left them, and the same kv_lens, max_len and causal.
  * Rows with lse = -inf add nothing. (lse may be over more keys than these, as that of fa_fwd_kvq8_prefix.) Weights
  * of positions that a sequence does not hold are not touched, nor those on bad pages. Sums are fp32 and do not
- * depend on timing. v_codes and v_scale are not needed.
+ * depend on timing. An exponential is off by about 2^-21 (1 + |s_ij| + |lse_i|) of itself, beside what fp32 makes of the score's
+ * sum of d products: with scores in the thousands three digits are left, and past 2^20 a weight may be anything from 0 to
+ * infinity, where the attention, which takes scores against their own maximum, still has its result. A row whose lse is NaN makes
+ * the weights of all keys that it sees NaN. v_codes and v_scale are not needed.
  *
  * fa_kvq8_evict cuts every sequence of n = kv_lens[s] > keep tokens down to keep. Each K/V head keeps the last `recent`
  * positions (0 <= recent <= keep) and, of those before, the keep - recent of the greatest weight; of equal weights the

@@ -9,7 +9,8 @@
 // Angles: p f_i in 32 bits is off by 2^-24 of itself, 6e-3 at position 100000, more than bf16's rounding. So a frequency
 // is held as the fraction of a turn that one position makes, t_i = f_i / 2 pi mod 1 in 64 bits of fixed point. The integer
 // product p t_i mod 2^64 is then the angle's place on the circle with all whole turns taken out exactly, for any 32-bit
-// position of either sign (off by |p f_i| 2^-54 turns at most, from the 53 bits of f_i / 2 pi). It goes to sincospi in fp32.
+// position of either sign (off by |p| (f_i 2^-54 + 2^-64) turns at most, from the 53 bits of f_i / 2 pi and their cut to 64 of
+// fixed point). It goes to sincospi in fp32.
 // Products and sums are fp32, and each result is rounded once.
 //
 // Bound: HBM, each value read and written once. A thread turns the same 16 dims of up to ten heads by one set of eight
